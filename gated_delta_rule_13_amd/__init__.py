@@ -8,19 +8,27 @@ marshalling only -- every step of the computation runs in the HIP kernels of
 
 computes, for every (b, h) sequence and with S of shape [d_v, d_k],
     S_t = alpha_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,   o_t = S_t q_t.
+
+The operators around it in a layer are gdn_conv_* (the short causal
+convolution), gdn_ssm_* (the selective state space recurrence) and gdn_norm_*
+(the normalisation and gate of the heads), each for prompts, with its
+gradient, and the first two for single tokens.
 """
 from __future__ import annotations
 
 import ctypes
 
-from ._lib import (EXPORTS, GDN_BF16, GDN_F32, GdnError, GdnShape, check, load)
+from . import _layer
+from ._layer import *  # noqa: F401,F403
+from ._lib import (EXPORTS, GDN_BF16, GDN_F32, GdnConvShape, GdnError, GdnNormShape, GdnShape, GdnSsmShape,
+                   check, load)
 
 __all__ = ["gdn_chunk_fwd", "gdn_chunk_fwd_eta", "gdn_chunk_fwd_precise", "gdn_chunk_fwd_stages",
            "gdn_chunk_fwd_seq", "gdn_chunk_fwd_seq_workspace_bytes", "gdn_chunk_fwd_seq_noalloc",
            "gdn_chunk_prep", "gdn_chunk_fwd_workspace_bytes",
            "gdn_recurrent_fwd", "gdn_recurrent_fwd_eta",
            "gdn_status_string", "gdn_last_error", "gdn_version", "GdnError", "GdnShape",
-           "EXPORTS"]
+           "GdnConvShape", "GdnSsmShape", "GdnNormShape", "EXPORTS", *_layer.__all__]
 
 
 def _torch():

@@ -25,12 +25,34 @@ EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_eta"
            "gdn_chunk_fwd_seq_workspace_bytes", "gdn_chunk_fwd_seq", "gdn_chunk_fwd_seq_noalloc",
            "gdn_chunk_fwd_precise", "gdn_chunk_fwd_stages",
            "gdn_chunk_prep", "gdn_recurrent_fwd", "gdn_recurrent_fwd_eta",
+           "gdn_conv_fwd", "gdn_conv_step", "gdn_conv_bwd_workspace_bytes", "gdn_conv_bwd",
+           "gdn_ssm_fwd_workspace_bytes", "gdn_ssm_fwd", "gdn_ssm_step",
+           "gdn_ssm_bwd_workspace_bytes", "gdn_ssm_bwd",
+           "gdn_norm_fwd", "gdn_norm_bwd_workspace_bytes", "gdn_norm_bwd",
            "gdn_status_string", "gdn_last_error", "gdn_version")
 
 
 class GdnShape(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int32) for name in
                 ("B", "H", "T", "d_k", "d_v", "chunk_size", "qkv_dtype", "o_dtype")]
+
+
+class GdnConvShape(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int32) for name in ("B", "T", "D", "W", "H", "dtype", "silu")] +
+                [(name, ctypes.c_int64) for name in ("x_stride_b", "x_stride_t")])
+
+
+class GdnSsmShape(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int32) for name in ("B", "T", "D", "N", "G", "dtype", "dt_softplus")] +
+                [(f"{name}_stride_{dim}", ctypes.c_int64) for name in ("x", "dt", "z", "b", "c")
+                 for dim in "bt"])
+
+
+class GdnNormShape(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int32) for name in
+                 ("B", "T", "G", "d", "x_dtype", "o_dtype", "center", "w_per_group", "silu")] +
+                [("eps", ctypes.c_float)] +
+                [(f"{name}_stride_{dim}", ctypes.c_int64) for name in ("x", "z") for dim in "btg"])
 
 
 class GdnError(RuntimeError):
@@ -77,6 +99,23 @@ def load():
     lib.gdn_chunk_fwd_stages.restype = ctypes.c_int
     lib.gdn_recurrent_fwd_eta.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.gdn_recurrent_fwd_eta.restype = ctypes.c_int
+    cs, ss, ns = (ctypes.POINTER(t) for t in (GdnConvShape, GdnSsmShape, GdnNormShape))
+    size = ctypes.c_size_t
+    lib.gdn_conv_fwd.argtypes = [cs] + [vp] * 8
+    lib.gdn_conv_step.argtypes = [cs] + [vp] * 6
+    lib.gdn_conv_bwd.argtypes = [cs] + [vp] * 11 + [vp, size, vp]
+    lib.gdn_ssm_fwd.argtypes = [ss] + [vp] * 12 + [vp, size, vp]
+    lib.gdn_ssm_step.argtypes = [ss] + [vp] * 11
+    lib.gdn_ssm_bwd.argtypes = [ss] + [vp] * 21 + [vp, size, vp]
+    lib.gdn_norm_fwd.argtypes = [ns] + [vp] * 6
+    lib.gdn_norm_bwd.argtypes = [ns] + [vp] * 6 + [ctypes.c_int64] * 3 + [vp] * 3 + [vp, size, vp]
+    for entry in (lib.gdn_conv_fwd, lib.gdn_conv_step, lib.gdn_conv_bwd, lib.gdn_ssm_fwd, lib.gdn_ssm_step,
+                  lib.gdn_ssm_bwd, lib.gdn_norm_fwd, lib.gdn_norm_bwd):
+        entry.restype = ctypes.c_int
+    for entry, sp in ((lib.gdn_conv_bwd_workspace_bytes, cs), (lib.gdn_ssm_fwd_workspace_bytes, ss),
+                      (lib.gdn_ssm_bwd_workspace_bytes, ss), (lib.gdn_norm_bwd_workspace_bytes, ns)):
+        entry.argtypes = [sp]
+        entry.restype = size
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_last_error.argtypes = []

@@ -51,7 +51,12 @@ def units() -> list[tuple[str, str, list[str]]]:
            ("gdn_inst_generic_bf16.o", "gdn_inst_generic.hip", ["-DGDN_GEN_BF16=1"]),
            ("gdn_inst_generic_f32.o", "gdn_inst_generic.hip", ["-DGDN_GEN_BF16=0"]),
            ("gdn_inst_rec.o", "gdn_inst_rec.hip", []),
-           ("gdn_inst_seq.o", "gdn_inst_seq.hip", [])]
+           ("gdn_inst_seq.o", "gdn_inst_seq.hip", []),
+           ("gdn_api_layer.o", "gdn_api_layer.hip", []),
+           ("gdn_inst_conv.o", "gdn_inst_conv.hip", []),
+           ("gdn_inst_norm.o", "gdn_inst_norm.hip", []),
+           ("gdn_inst_ssm_bf16.o", "gdn_inst_ssm.hip", ["-DGDN_SSM_BF16=1"]),
+           ("gdn_inst_ssm_f32.o", "gdn_inst_ssm.hip", ["-DGDN_SSM_BF16=0"])]
     for c, d in FAST_PAIRS:
         out.append((f"gdn_inst_fast_c{c}_d{d}.o", "gdn_inst_fast.hip", [f"-DGDN_C={c}", f"-DGDN_DK={d}"]))
     return out

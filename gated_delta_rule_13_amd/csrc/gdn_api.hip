@@ -8,6 +8,7 @@
 #include <string>
 
 #include "gdn.h"
+#include "gdn_error.h"
 #include "gdn_launch.h"
 
 namespace {
@@ -262,6 +263,10 @@ gdn_status check_launch() {
 }  // namespace
 
 namespace gdn {
+void clear_error() { g_last_error.clear(); }
+gdn_status set_error(gdn_status st, const std::string& msg) { return fail(st, msg); }
+gdn_status launch_status() { return check_launch(); }
+
 FwdLauncher fast_launcher(int C, int dk, int ns, bool eta, bool seg) {
 #define GDN_FAST_PICK(CC, KK) \
     if (C == CC && dk == KK) return fast_launcher_c##CC##_d##KK(ns, eta, seg);
@@ -665,6 +670,6 @@ const char* gdn_status_string(gdn_status st) {
 
 const char* gdn_last_error(void) { return g_last_error.c_str(); }
 
-int32_t gdn_version(void) { return 200; }
+int32_t gdn_version(void) { return 300; }
 
 }  // extern "C"

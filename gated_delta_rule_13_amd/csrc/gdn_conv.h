@@ -1,0 +1,294 @@
+// gdn_conv.h -- the short causal convolution of each channel on gfx950.
+//
+//     p_t = bias + sum_{j < W} w_j x_{t-W+1+j},   y_t = silu(p_t)
+//
+// with the W-1 rows before the first token taken from the state.  Two passes
+// of x through memory (read once, y written once) bound it: a thread takes V
+// neighbouring channels (16 bytes of a row) down a tile of rows, holds the
+// last W-1 rows in registers, and has the next kRows rows in flight while it
+// works on the current ones.
+#pragma once
+#include "gdn_layer.h"
+
+namespace gdn {
+
+struct ConvParams {
+    const void* x;
+    const float* w;
+    const float* bias;      // may be null
+    const void* s0;         // may be null
+    const int32_t* lens;    // may be null
+    void* y;
+    void* s1;               // may be null; may be s0
+    int64_t sb, st;         // strides of x
+    int B, T, D;
+    int hd;                 // channels per head of y
+    int nv;                 // vectors per row
+    int tile, ntile;        // rows per thread, tiles per sequence
+    int silu;
+};
+
+constexpr int kConvThreads = 256;
+constexpr int kConvRows = 8;
+
+// weights of V neighbouring channels
+template <int W, int V>
+struct ConvWeights {
+    float w[W][V], b[V];
+    __device__ __forceinline__ void load(const float* wp, const float* bp, int c) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][v] = wp[(int64_t)(c + v) * W + j];
+            b[v] = bp ? bp[c + v] : 0.f;
+        }
+    }
+};
+
+// the row at time t of sequence b: x for t >= 0, the state for t < 0
+template <bool BF, int W, int V>
+__device__ __forceinline__ void conv_row(Raw<BF, V>& r, const ConvParams& p, int b, int t, int c) {
+    if (t >= 0) r.load(p.x, b * p.sb + t * p.st + c);
+    else if (p.s0) r.load(p.s0, ((int64_t)b * (W - 1) + (t + W - 1)) * p.D + c);
+    else r.zero();
+}
+
+template <bool BF, int W, int V>
+__global__ __launch_bounds__(kConvThreads) void gdn_conv_fwd_kernel(ConvParams p) {
+    const unsigned id = blockIdx.x * kConvThreads + threadIdx.x;
+    const unsigned row_tile = id / (unsigned)p.nv;
+    const int c = (int)(id % (unsigned)p.nv) * V;
+    const int b = (int)(row_tile / (unsigned)p.ntile);
+    if (b >= p.B) return;
+    const int t0 = (int)(row_tile % (unsigned)p.ntile) * p.tile;
+    const int n = seq_len(p.lens, b, p.T);
+    const int tz = t0 + p.tile < p.T ? t0 + p.tile : p.T;
+    const int t1 = tz < n ? tz : n;
+
+    ConvWeights<W, V> wt;
+    wt.load(p.w, p.bias, c);
+    const int head = c / p.hd;
+    const int64_t y0 = ((int64_t)b * (p.D / p.hd) + head) * p.T * p.hd + (c - head * p.hd);
+
+    // rows t0 - W + 1 .. t0 - 1, then the chunk's
+    Raw<BF, V> win[W - 1 + kConvRows], next[kConvRows];
+    if (t0 < n || t0 == 0) {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) conv_row<BF, W, V>(win[i], p, b, t0 - W + 1 + i, c);
+    }
+    // The thread of a sequence's first rows writes its final state too: it
+    // alone reads the initial one, and has read it by now, so the two may be
+    // the same buffer.
+    Raw<BF, V> last[W - 1];
+    if (t0 == 0 && p.s1) {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const int t = n - W + 1 + i;
+            last[i] = win[0];
+            if (t >= 0) last[i].load(p.x, b * p.sb + t * p.st + c);
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+                if (t + W - 1 == k) last[i] = win[k];
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            float f[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = last[i].get(v);
+            store_vec<BF, V>(p.s1, ((int64_t)b * (W - 1) + i) * p.D + c, f);
+        }
+    }
+    if (t0 < t1) {
+#pragma unroll
+        for (int i = 0; i < kConvRows; ++i) next[i].load(p.x, b * p.sb + (t0 + i < t1 ? t0 + i : t1 - 1) * p.st + c);
+    }
+    for (int t = t0; t < t1; t += kConvRows) {
+#pragma unroll
+        for (int i = 0; i < kConvRows; ++i) win[W - 1 + i] = next[i];
+        if (t + kConvRows < t1) {
+#pragma unroll
+            for (int i = 0; i < kConvRows; ++i) {
+                const int tt = t + kConvRows + i;
+                next[i].load(p.x, b * p.sb + (tt < t1 ? tt : t1 - 1) * p.st + c);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kConvRows; ++i) {
+            if (t + i < t1) {
+                float f[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float a = wt.b[v];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) a = fmaf(wt.w[j][v], win[i + j].get(v), a);
+                    f[v] = p.silu ? silu(a) : a;
+                }
+                store_vec<BF, V>(p.y, y0 + (int64_t)(t + i) * p.hd, f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) win[i] = win[kConvRows + i];
+    }
+    float zero[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) zero[v] = 0.f;
+    for (int t = t0 > t1 ? t0 : t1; t < tz; ++t) store_vec<BF, V>(p.y, y0 + (int64_t)t * p.hd, zero);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient.  With dp_t = dy_t silu'(p_t) (zero outside the sequence):
+//     dx_t = sum_j w_j dp_{t+W-1-j}   (t < 0: the initial state's rows)
+//     dw_j = sum_t dp_t x_{t-W+1+j},  dbias = sum_t dp_t
+// A thread takes V channels down `tile` rows and W-1 more, whose dp its last
+// rows need (computed again by the next tile's thread).  x and dy are read
+// once and dx written once, which bounds it.  The sums over rows stay in
+// registers, are added over the workgroup's tiles in LDS, and written as one
+// row of partial sums for each workgroup.
+struct ConvBwdParams {
+    ConvParams f;
+    const void* dy;
+    const void* ds1;        // gradient of the final state, may be null
+    void* dx;
+    void* ds0;              // may be null
+    float* part;            // [rows of workgroups][D * W + D]
+};
+
+constexpr int kConvBwdCv = 32;                               // vectors per workgroup
+constexpr int kConvBwdTiles = kConvThreads / kConvBwdCv;     // tiles per workgroup
+
+template <bool BF, int W, int V>
+__global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParams q) {
+    const ConvParams& p = q.f;
+    __shared__ float red[kConvBwdTiles][kConvBwdCv][(W + 1) * V + 1];
+    const int ncb = (p.nv + kConvBwdCv - 1) / kConvBwdCv;
+    const int cvl = threadIdx.x % kConvBwdCv, tl = threadIdx.x / kConvBwdCv;
+    const int cv = (int)(blockIdx.x % (unsigned)ncb) * kConvBwdCv + cvl;
+    const int64_t row_tile = (int64_t)(blockIdx.x / (unsigned)ncb) * kConvBwdTiles + tl;
+    const bool on = cv < p.nv && row_tile < (int64_t)p.B * p.ntile;
+
+    float acc[W + 1][V];
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
+
+    if (on) {
+        const int c = cv * V;
+        const int b = (int)(row_tile / p.ntile);
+        const int t0 = (int)(row_tile % p.ntile) * p.tile;
+        const int n = seq_len(p.lens, b, p.T);
+        const int tz = t0 + p.tile < p.T ? t0 + p.tile : p.T;   // dx rows [t0, tz)
+        const int t1 = tz < n ? tz : n;                         // tokens of its own
+        const int t2 = tz + W - 1 < n ? tz + W - 1 : n;         // tokens whose dp it needs
+        ConvWeights<W, V> wt;
+        wt.load(p.w, p.bias, c);
+        const int head = c / p.hd;
+        const int64_t dy0 = ((int64_t)b * (p.D / p.hd) + head) * p.T * p.hd + (c - head * p.hd);
+
+        Raw<BF, V> win[W - 1 + kConvRows], nx[kConvRows], ng[kConvRows];
+        float dp[W - 1 + kConvRows][V];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            if (t0 < t2) conv_row<BF, W, V>(win[i], p, b, t0 - W + 1 + i, c);
+            else win[i].zero();
+#pragma unroll
+            for (int v = 0; v < V; ++v) dp[i][v] = 0.f;
+        }
+        if (t0 < t2) {
+#pragma unroll
+            for (int i = 0; i < kConvRows; ++i) {
+                const int tt = t0 + i < t2 ? t0 + i : t2 - 1;
+                nx[i].load(p.x, b * p.sb + tt * p.st + c);
+                ng[i].load(q.dy, dy0 + (int64_t)tt * p.hd);
+            }
+        }
+        // dx rows t - W + 1 .. t - W + kConvRows follow from the dp up to t + kConvRows - 1
+        for (int t = t0; t < tz + W - 1; t += kConvRows) {
+            Raw<BF, V> g[kConvRows];
+#pragma unroll
+            for (int i = 0; i < kConvRows; ++i) {
+                win[W - 1 + i] = nx[i];
+                g[i] = ng[i];
+            }
+            if (t + kConvRows < t2) {
+#pragma unroll
+                for (int i = 0; i < kConvRows; ++i) {
+                    const int tt = t + kConvRows + i < t2 ? t + kConvRows + i : t2 - 1;
+                    nx[i].load(p.x, b * p.sb + tt * p.st + c);
+                    ng[i].load(q.dy, dy0 + (int64_t)tt * p.hd);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kConvRows; ++i) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) dp[W - 1 + i][v] = 0.f;
+                if (t + i < t2) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        float a = wt.b[v];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) a = fmaf(wt.w[j][v], win[i + j].get(v), a);
+                        float val, d = g[i].get(v);
+                        if (p.silu) {
+                            float slope;
+                            silu_both(a, val, slope);
+                            d *= slope;
+                        }
+                        dp[W - 1 + i][v] = d;
+                        if (t + i < t1) {
+#pragma unroll
+                            for (int j = 0; j < W; ++j) acc[j][v] = fmaf(d, win[i + j].get(v), acc[j][v]);
+                            acc[W][v] += d;
+                        }
+                    }
+                }
+                const int td = t + i - (W - 1);
+                float f[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    f[v] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) f[v] = fmaf(wt.w[j][v], dp[i + W - 1 - j][v], f[v]);
+                }
+                const bool state_row = td < 0;
+                if (td >= t0 ? td < tz : (state_row && t0 == 0)) {
+                    // the final state's rows are those at times n - W + 1 .. n - 1
+                    const int k = td - (n - (W - 1));
+                    if (q.ds1 && k >= 0 && td < n) {
+                        Raw<BF, V> e;
+                        e.load(q.ds1, ((int64_t)b * (W - 1) + k) * p.D + c);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) f[v] += e.get(v);
+                    }
+                    if (!state_row) store_vec<BF, V>(q.dx, ((int64_t)b * p.T + td) * p.D + c, f);
+                    else if (q.ds0) store_vec<BF, V>(q.ds0, ((int64_t)b * (W - 1) + td + W - 1) * p.D + c, f);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                win[i] = win[kConvRows + i];
+#pragma unroll
+                for (int v = 0; v < V; ++v) dp[i][v] = dp[kConvRows + i][v];
+            }
+        }
+    }
+    // [channel][tap], then the biases, summed over the workgroup's tiles
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j <= W; ++j) red[tl][cvl][v * (W + 1) + j] = acc[j][v];
+    __syncthreads();
+    float* out = q.part + (int64_t)(blockIdx.x / (unsigned)ncb) * p.D * (W + 1);
+    const int c0 = (int)(blockIdx.x % (unsigned)ncb) * kConvBwdCv * V;
+    for (int i = threadIdx.x; i < kConvBwdCv * V * (W + 1); i += kConvThreads) {
+        const int ch = i / (W + 1), j = i % (W + 1);
+        if (c0 + ch < p.D) {
+            float t = 0.f;
+#pragma unroll
+            for (int k = 0; k < kConvBwdTiles; ++k) t += red[k][ch / V][(ch % V) * (W + 1) + j];
+            out[j < W ? (int64_t)(c0 + ch) * W + j : (int64_t)p.D * W + c0 + ch] = t;
+        }
+    }
+}
+
+}  // namespace gdn

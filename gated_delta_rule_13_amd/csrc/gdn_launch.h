@@ -62,4 +62,34 @@ SeqLauncher seq_launcher(int dk);
 // workgroup covers.
 RecLauncher rec_launcher(int dk, bool bf16, int* rows_per_block);
 
+// ---- the operators around the recurrence ----
+struct ConvParams;
+struct ConvBwdParams;
+struct NormParams;
+struct NormBwdParams;
+struct SsmParams;
+struct SsmStepParams;
+
+// short convolution: W in {2, 3, 4}; wide: 16-byte pieces of a row
+using ConvLauncher = void (*)(const ConvParams&, hipStream_t);
+using ConvBwdLauncher = void (*)(const ConvBwdParams&, hipStream_t);
+ConvLauncher conv_launcher(bool bf16, int W, bool wide);
+ConvBwdLauncher conv_bwd_launcher(bool bf16, int W, bool wide);
+int64_t conv_bwd_part_rows(int64_t row_tiles);
+void conv_bwd_sum(const float* part, int64_t rows, int D, int W, float* dweight, float* dbias, hipStream_t st);
+
+// head normalisation: wide: 16-byte pieces of a row (else the plain kernels)
+using NormLauncher = void (*)(const NormParams&, hipStream_t);
+using NormBwdLauncher = void (*)(const NormBwdParams&, int nblk, hipStream_t);
+void norm_launchers(bool x_bf16, bool o_bf16, int d, bool wide, NormLauncher* fwd, NormBwdLauncher* bwd);
+void norm_bwd_sum(const NormBwdParams& q, int nblk, float* dweight, float* dbias, hipStream_t st);
+
+// selective state space recurrence; ssm_states: N rounded up to a built size
+int ssm_states(int N);
+void ssm_fwd_run(const SsmParams& p, bool bf16, hipStream_t st);
+void ssm_bwd_run(const SsmParams& p, bool bf16, float* dA, void* dBm, void* dC, float* dDskip, float* ddt_bias,
+                 hipStream_t st);
+void ssm_step_run(const SsmStepParams& q, bool bf16, hipStream_t st);
+int ssm_bwd_segment();
+
 }  // namespace gdn

@@ -1,0 +1,338 @@
+// gdn_norm.h -- normalisation of each head of each token with an activation
+// or a gate, on gfx950.
+//
+//     n = (x - mean) / sqrt(var + eps),  p = n w + b,  y = p act(z) | act(p)
+//
+// and its gradient, with dp = dy act(z) (or dy act'(p)), dn = dp w:
+//     dx = (dn - mean(dn) - n mean(dn n)) / sqrt(var + eps)
+// (without the mean(dn) where x is not centred), dw = sum dp n, db = sum dp,
+// dz = dy p act'(z).  One pass over x, z and y (and their gradients) bounds
+// it: a group of L lanes holds a row of d numbers in registers, K pieces of
+// four to a lane, so nothing is read twice; the row's sums are steps between
+// neighbouring lanes.  L and K are chosen so that L K pieces just cover the
+// row (d = 192: 16 lanes with 3 pieces each, no lane idle).  Rows whose size
+// or alignment does not allow 16-byte pieces, and rows over 2048 numbers,
+// take the plain kernels: one wave for a row, which it reads again for each
+// of its sums.
+#pragma once
+#include "gdn_layer.h"
+
+namespace gdn {
+
+struct NormParams {
+    const void* x;
+    const float* w;         // may be null
+    const float* b;         // may be null
+    const void* z;          // may be null
+    void* y;
+    int64_t xsb, xst, xsg;
+    int64_t zsb, zst, zsg;
+    int64_t rows;           // B T G
+    int T, G, d;
+    int x_bf16, o_bf16;
+    int center, per_group, silu;
+    float eps;
+};
+
+struct NormBwdParams {
+    NormParams f;
+    const void* dy;
+    void* dx;
+    void* dz;               // may be null
+    int64_t dsb, dst, dsg;  // strides of dx
+    float* part;            // [workgroups of a head][G][d] of w, then of b
+    int64_t part_b;         // offset of b's sums
+    int want_w, want_b;
+};
+
+constexpr int kNormThreads = 256;
+
+// Sum over aligned groups of L lanes, in every lane.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int m = 1; m < L; m *= 2) v += __shfl_xor(v, m, 64);
+    return v;
+}
+
+__device__ __forceinline__ void act_both(float x, int act, float& val, float& slope) {
+    if (act) {
+        silu_both(x, val, slope);
+    } else {
+        val = x;
+        slope = 1.f;
+    }
+}
+
+// The mean (0 if not centred) and 1 / sqrt(var + eps) of a row.
+template <int L, int K>
+__device__ __forceinline__ void row_stats(const float (&x)[K][4], const NormParams& p, int j, float& mean, float& r) {
+    const float inv = 1.f / (float)p.d;
+    mean = 0.f;
+    if (p.center) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s += x[k][e];     // (pieces behind the row hold 0)
+        mean = lanes_sum<L>(s) * inv;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const bool in = (k * L + j) * 4 < p.d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float c = in ? x[k][e] - mean : 0.f;
+            s = fmaf(c, c, s);
+        }
+    }
+    r = 1.f / sqrtf(lanes_sum<L>(s) * inv + p.eps);
+}
+
+template <bool XB, bool OB, int L, int K>
+__global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_kernel(NormParams p) {
+    const int j = threadIdx.x % L;
+    const int64_t row = (int64_t)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
+    if (row >= p.rows) return;      // (a whole group of lanes)
+    const int g = (int)(row % p.G);
+    const int64_t bt = row / p.G;
+    const int64_t b = bt / p.T, t = bt % p.T;
+    const int64_t x0 = b * p.xsb + t * p.xst + g * p.xsg, z0 = b * p.zsb + t * p.zst + g * p.zsg;
+    Raw<XB, 4> xr[K];
+    Raw<OB, 4> zr[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * L + j) * 4;
+        xr[k].zero();
+        zr[k].zero();
+        if (c < p.d) {
+            xr[k].load(p.x, x0 + c);
+            if (p.z) zr[k].load(p.z, z0 + c);
+        }
+    }
+    float x[K][4], mean, r;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[k][e] = xr[k].get(e);
+    row_stats<L, K>(x, p, j, mean, r);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * L + j) * 4;
+        if (c < p.d) {
+            const int wc = (p.per_group ? g * p.d : 0) + c;
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v = (x[k][e] - mean) * r;
+                if (p.w) v *= p.w[wc + e];
+                if (p.b) v += p.b[wc + e];
+                if (p.z) v *= p.silu ? silu(zr[k].get(e)) : zr[k].get(e);
+                else if (p.silu) v = silu(v);
+                f[e] = v;
+            }
+            store_vec<OB, 4>(p.y, row * p.d + c, f);
+        }
+    }
+}
+
+// A workgroup takes rows of one head, so that a lane's columns of the weight
+// stay the same and their sums stay in registers until the end.
+template <bool XB, bool OB, int L, int K>
+__global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParams q) {
+    const NormParams& p = q.f;
+    constexpr int kGroups = kNormThreads / L;
+    __shared__ float red[kGroups][L * K * 4];
+    const int j = threadIdx.x % L, grp = threadIdx.x / L;
+    const int g = blockIdx.x % p.G;
+    const int64_t blk = blockIdx.x / p.G, nblk = gridDim.x / p.G;
+    const int64_t bts = p.rows / p.G;
+    const float inv = 1.f / (float)p.d;
+    float w[K][4], b[K][4], sw[K][4], sb[K][4];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * L + j) * 4, wc = (p.per_group ? g * p.d : 0) + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[k][e] = p.w && c < p.d ? p.w[wc + e] : 1.f;
+            b[k][e] = p.b && c < p.d ? p.b[wc + e] : 0.f;
+            sw[k][e] = sb[k][e] = 0.f;
+        }
+    }
+    for (int64_t bt = blk * kGroups + grp; bt < bts; bt += nblk * kGroups) {
+        const int64_t bb = bt / p.T, t = bt % p.T;
+        const int64_t x0 = bb * p.xsb + t * p.xst + g * p.xsg, z0 = bb * p.zsb + t * p.zst + g * p.zsg;
+        const int64_t y0 = (bt * p.G + g) * p.d, d0 = bb * q.dsb + t * q.dst + g * q.dsg;
+        Raw<XB, 4> xr[K];
+        Raw<OB, 4> zr[K], yr[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + j) * 4;
+            xr[k].zero();
+            zr[k].zero();
+            yr[k].zero();
+            if (c < p.d) {
+                xr[k].load(p.x, x0 + c);
+                yr[k].load(q.dy, y0 + c);
+                if (p.z) zr[k].load(p.z, z0 + c);
+            }
+        }
+        float x[K][4], dn[K][4], mean, r;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[k][e] = xr[k].get(e);
+        row_stats<L, K>(x, p, j, mean, r);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + j) * 4;
+            if (c < p.d) {
+                float dz[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float n = (x[k][e] - mean) * r, pv = fmaf(n, w[k][e], b[k][e]), dy = yr[k].get(e);
+                    float val, slope;
+                    act_both(p.z ? zr[k].get(e) : pv, p.silu, val, slope);
+                    const float dp = dy * (p.z ? val : slope);
+                    dz[e] = dy * pv * slope;
+                    sw[k][e] = fmaf(dp, n, sw[k][e]);
+                    sb[k][e] += dp;
+                    x[k][e] = n;
+                    dn[k][e] = dp * w[k][e];
+                    s1 += dn[k][e];
+                    s2 = fmaf(dn[k][e], n, s2);
+                }
+                if (p.z && q.dz) store_vec<OB, 4>(q.dz, y0 + c, dz);
+            }
+        }
+        s1 = p.center ? lanes_sum<L>(s1) * inv : 0.f;
+        s2 = lanes_sum<L>(s2) * inv;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + j) * 4;
+            if (c < p.d) {
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = r * (dn[k][e] - s1 - x[k][e] * s2);
+                store_vec<XB, 4>(q.dx, d0 + c, f);
+            }
+        }
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        if (which == 0 ? !q.want_w : !q.want_b) continue;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[grp][(k * L + j) * 4 + e] = which ? sb[k][e] : sw[k][e];
+        __syncthreads();
+        float* out = q.part + (which ? q.part_b : 0) + (blk * p.G + g) * p.d;
+        for (int c = threadIdx.x; c < p.d; c += kNormThreads) {
+            float t = 0.f;
+            for (int k = 0; k < kGroups; ++k) t += red[k][c];
+            out[c] = t;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Any size, stride and alignment: one wave for a row.
+template <bool XB>
+__device__ __forceinline__ void plain_stats(const NormParams& p, int64_t x0, int lane, float& mean, float& r) {
+    const float inv = 1.f / (float)p.d;
+    mean = 0.f;
+    if (p.center) {
+        float s = 0.f;
+        for (int c = lane; c < p.d; c += 64) s += load_one<XB>(p.x, x0 + c);
+        mean = lanes_sum<64>(s) * inv;
+    }
+    float s = 0.f;
+    for (int c = lane; c < p.d; c += 64) {
+        const float v = load_one<XB>(p.x, x0 + c) - mean;
+        s = fmaf(v, v, s);
+    }
+    r = 1.f / sqrtf(lanes_sum<64>(s) * inv + p.eps);
+}
+
+template <bool XB, bool OB>
+__global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_plain_kernel(NormParams p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * (kNormThreads / 64) + (threadIdx.x >> 6);
+    if (row >= p.rows) return;
+    const int g = (int)(row % p.G);
+    const int64_t bt = row / p.G;
+    const int64_t b = bt / p.T, t = bt % p.T;
+    const int64_t x0 = b * p.xsb + t * p.xst + g * p.xsg, z0 = b * p.zsb + t * p.zst + g * p.zsg;
+    float mean, r;
+    plain_stats<XB>(p, x0, lane, mean, r);
+    for (int c = lane; c < p.d; c += 64) {
+        const int wc = (p.per_group ? g * p.d : 0) + c;
+        float v = (load_one<XB>(p.x, x0 + c) - mean) * r;
+        if (p.w) v *= p.w[wc];
+        if (p.b) v += p.b[wc];
+        if (p.z) {
+            const float z = load_one<OB>(p.z, z0 + c);
+            v *= p.silu ? silu(z) : z;
+        } else if (p.silu) {
+            v = silu(v);
+        }
+        store_one<OB>(p.y, row * p.d + c, v);
+    }
+}
+
+// One wave for a workgroup; the sums over rows in LDS, each column by the one
+// lane that owns it.
+constexpr int kNormMaxD = 4096;
+template <bool XB, bool OB>
+__global__ __launch_bounds__(64) void gdn_norm_bwd_plain_kernel(NormBwdParams q) {
+    const NormParams& p = q.f;
+    __shared__ float sw[kNormMaxD], sb[kNormMaxD];
+    const int lane = threadIdx.x;
+    const int g = blockIdx.x % p.G;
+    const int64_t blk = blockIdx.x / p.G, nblk = gridDim.x / p.G;
+    const int64_t bts = p.rows / p.G;
+    const float inv = 1.f / (float)p.d;
+    for (int c = lane; c < p.d; c += 64) sw[c] = sb[c] = 0.f;
+    for (int64_t bt = blk; bt < bts; bt += nblk) {
+        const int64_t bb = bt / p.T, t = bt % p.T;
+        const int64_t x0 = bb * p.xsb + t * p.xst + g * p.xsg, z0 = bb * p.zsb + t * p.zst + g * p.zsg;
+        const int64_t y0 = (bt * p.G + g) * p.d, d0 = bb * q.dsb + t * q.dst + g * q.dsg;
+        float mean, r, s1 = 0.f, s2 = 0.f;
+        plain_stats<XB>(p, x0, lane, mean, r);
+        for (int c = lane; c < p.d; c += 64) {
+            const int wc = (p.per_group ? g * p.d : 0) + c;
+            const float wv = p.w ? p.w[wc] : 1.f;
+            const float n = (load_one<XB>(p.x, x0 + c) - mean) * r, pv = fmaf(n, wv, p.b ? p.b[wc] : 0.f);
+            const float dy = load_one<OB>(q.dy, y0 + c);
+            float val, slope;
+            act_both(p.z ? load_one<OB>(p.z, z0 + c) : pv, p.silu, val, slope);
+            const float dp = dy * (p.z ? val : slope);
+            sw[c] = fmaf(dp, n, sw[c]);
+            sb[c] += dp;
+            s1 = fmaf(dp, wv, s1);
+            s2 = fmaf(dp * wv, n, s2);
+            if (p.z && q.dz) store_one<OB>(q.dz, y0 + c, dy * pv * slope);
+        }
+        s1 = p.center ? lanes_sum<64>(s1) * inv : 0.f;
+        s2 = lanes_sum<64>(s2) * inv;
+        for (int c = lane; c < p.d; c += 64) {
+            const int wc = (p.per_group ? g * p.d : 0) + c;
+            const float wv = p.w ? p.w[wc] : 1.f;
+            const float n = (load_one<XB>(p.x, x0 + c) - mean) * r, pv = fmaf(n, wv, p.b ? p.b[wc] : 0.f);
+            float val, slope;
+            act_both(p.z ? load_one<OB>(p.z, z0 + c) : pv, p.silu, val, slope);
+            const float dp = load_one<OB>(q.dy, y0 + c) * (p.z ? val : slope);
+            store_one<XB>(q.dx, d0 + c, r * (dp * wv - s1 - n * s2));
+        }
+    }
+    float* out = q.part + (blk * p.G + g) * p.d;
+    for (int c = lane; c < p.d; c += 64) {
+        if (q.want_w) out[c] = sw[c];
+        if (q.want_b) out[q.part_b + c] = sb[c];
+    }
+}
+
+}  // namespace gdn

@@ -1,0 +1,697 @@
+// gdn_ssm.h -- the selective state space recurrence on gfx950.
+//
+//     s_t = softplus(dt_t + dt_bias),  u_t = s_t x_t
+//     h_t = exp(s_t A) h_{t-1} + u_t Bm_t          (N numbers per channel)
+//     y_t = (C_t . h_t + Dskip x_t) silu(z_t)
+//
+// The decay differs for every channel and state, so a chunk of tokens is no
+// product of matrices (unlike the delta rule's): the work is one exponential
+// and four multiply-adds for each (token, channel, state), on the vector
+// units, against 8 bytes of memory for each (token, channel) in bf16.  With 16
+// states the vector units bound it.
+//
+// A lane holds one channel with all its states in registers, so the sum over
+// states needs no other lane.  Bm_t and C_t are the same for all channels of a
+// group: one wave stages them in LDS as fp32, kTok tokens ahead, and every
+// lane reads them at the same address.
+//
+// Few channels on long sequences leave the chip empty, so the tokens are cut
+// into segments.  The recurrence is linear in the state, and a segment acts
+// on the state that enters it as h -> exp(A sum s) h + E, with E its end
+// state from zero:
+//   gdn_ssm_sum_kernel      E and sum s of every segment (all at once)
+//   gdn_ssm_chain_kernel    the state that enters each segment, one after
+//                           another
+//   gdn_ssm_fwd_kernel      the outputs (all segments at once)
+// which costs the exponentials twice.
+#pragma once
+#include "gdn_layer.h"
+
+namespace gdn {
+
+struct SsmParams {
+    const void* x;
+    const void* dt;
+    const float* A;
+    const void* Bm;
+    const void* C;
+    const float* Dskip;     // may be null
+    const void* z;          // may be null
+    const float* dt_bias;   // may be null
+    const float* h0;        // may be null
+    const int32_t* lens;    // may be null
+    void* y;
+    float* h_final;         // may be null
+    int64_t xsb, xst, dsb, dst, zsb, zst, bsb, bst, csb, cst;
+    int B, T, D, N, G;
+    int Dg;                 // channels per group
+    int tpg;                // tiles of 64 channels per group
+    int softplus;
+    int seg_len, nseg;
+    // segment summaries, in units of (sequence, segment, tile):
+    float* sum_e;           // [unit][NS][64]: E, then the state that enters
+    float* sum_s;           // [unit][64]: sum of s
+    // gradient
+    const void* dy;
+    const float* dh_final;  // may be null
+    void* dx;
+    void* ddt;
+    void* dz;
+    float* dh0;             // may be null
+    float* sum_r;           // [unit][NS][64]: R, then the gradient that enters from behind
+    float* part_a;          // [sequence, segment][tile][NS][64]: dA
+    float* part_d;          // [sequence, segment][tile][2][64]: dDskip, ddt_bias
+    float* part_bc;         // [tile][sequence][token][2][NS]: dB, dC over a tile's channels
+};
+
+constexpr int kTok = 8;      // tokens staged at a time
+
+// Where a wave works: its sequence, segment and channels.
+struct SsmPlace {
+    int b, seg, tile, g, c;  // c: channel of the lane (clamped), of all D
+    bool on;                 // the lane has a channel of its own
+    int t0, t1, tz;          // tokens [t0, t1), padded rows [max(t0, t1), tz)
+    int64_t unit;
+};
+__device__ __forceinline__ SsmPlace ssm_place(const SsmParams& p, unsigned id, int nseg, int lane) {
+    SsmPlace w;
+    const unsigned tiles = (unsigned)(p.G * p.tpg);
+    w.tile = (int)(id % tiles);
+    const unsigned bs = id / tiles;
+    w.seg = (int)(bs % (unsigned)nseg);
+    w.b = (int)(bs / (unsigned)nseg);
+    w.g = w.tile / p.tpg;
+    const int c = (w.tile % p.tpg) * 64 + lane;
+    w.on = c < p.Dg;
+    w.c = w.g * p.Dg + (w.on ? c : p.Dg - 1);
+    const int n = seq_len(p.lens, w.b, p.T);
+    w.t0 = w.seg * p.seg_len;
+    w.tz = p.T - w.t0 < p.seg_len ? p.T : w.t0 + p.seg_len;
+    w.t1 = w.tz < n ? w.tz : n;
+    w.unit = ((int64_t)w.b * p.nseg + w.seg) * tiles + w.tile;
+    return w;
+}
+
+// Bm and C of kTok tokens, spread over the wave's lanes: value i of lane l is
+// number l + 64 i of [token][Bm | C][NS].
+template <bool BF, int NS>
+struct StagedBC {
+    static constexpr int kEach = kTok * 2 * NS / 64;
+    Raw<BF, 1> v[kEach];
+    __device__ __forceinline__ void load(const SsmParams& p, const SsmPlace& w, int t, int lane) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int k = lane + 64 * i, n = k % NS;
+            int tt = t + k / (2 * NS);
+            tt = tt < w.t1 ? tt : w.t1 - 1;
+            v[i].zero();
+            if (n < p.N) {
+                if ((k / NS) & 1) v[i].load(p.C, w.b * p.csb + tt * p.cst + w.g * p.N + n);
+                else v[i].load(p.Bm, w.b * p.bsb + tt * p.bst + w.g * p.N + n);
+            }
+        }
+    }
+    __device__ __forceinline__ void put(float* lds, int lane) const {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) lds[lane + 64 * i] = v[i].get(0);
+    }
+};
+
+// One number of kTok tokens of the lane's channel.
+template <bool BF>
+struct Column {
+    Raw<BF, 1> v[kTok];
+    __device__ __forceinline__ void load(const void* p, int64_t base, int64_t st, int t, int t1) {
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) v[i].load(p, base + (t + i < t1 ? t + i : t1 - 1) * st);
+    }
+};
+
+// A log2(e) of the lane's channel, 0 behind the N states (which then stay 0).
+template <int NS>
+__device__ __forceinline__ void load_decay(float (&a)[NS], const SsmParams& p, int c) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) a[n] = n < p.N ? p.A[(int64_t)c * p.N + n] * kLog2e : 0.f;
+}
+template <int NS>
+__device__ __forceinline__ void load_state(float (&h)[NS], const float* s, const SsmParams& p, int b, int c) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = s && n < p.N ? s[((int64_t)b * p.D + c) * p.N + n] : 0.f;
+}
+template <int NS>
+__device__ __forceinline__ void load_sum(float (&h)[NS], const float* s, int64_t unit, int lane) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = s[(unit * NS + n) * 64 + lane];
+}
+template <int NS>
+__device__ __forceinline__ void store_sum(float* s, const float (&h)[NS], int64_t unit, int lane) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) s[(unit * NS + n) * 64 + lane] = h[n];
+}
+
+__device__ __forceinline__ float ssm_step_size(float raw, bool soft) { return soft ? softplus(raw) : raw; }
+
+// Tokens behind t1 take the step size 0: they leave the state as it is.
+template <bool BF, int NS>
+__global__ __launch_bounds__(64) void gdn_ssm_fwd_kernel(SsmParams p) {
+    __shared__ __align__(16) float bc[2][kTok][2][NS];
+    const int lane = threadIdx.x;
+    const SsmPlace w = ssm_place(p, blockIdx.x, p.nseg, lane);
+    const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c, zb = w.b * p.zsb + w.c;
+    const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
+    float a[NS], h[NS];
+    load_decay<NS>(a, p, w.c);
+    if (p.nseg > 1) load_sum<NS>(h, p.sum_e, w.unit, lane);
+    else load_state<NS>(h, p.h0, p, w.b, w.c);
+    const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
+
+    if (w.t0 < w.t1) {
+        StagedBC<BF, NS> nbc;
+        Column<BF> nx, nd, nz;
+        nbc.load(p, w, w.t0, lane);
+        nx.load(p.x, xb, p.xst, w.t0, w.t1);
+        nd.load(p.dt, db, p.dst, w.t0, w.t1);
+        if (p.z) nz.load(p.z, zb, p.zst, w.t0, w.t1);
+        int buf = 0;
+        for (int t = w.t0; t < w.t1; t += kTok, buf ^= 1) {
+            nbc.put(&bc[buf][0][0][0], lane);
+            float x[kTok], s[kTok], gate[kTok];
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                x[i] = nx.v[i].get(0);
+                s[i] = t + i < w.t1 ? ssm_step_size(nd.v[i].get(0) + bias, p.softplus) : 0.f;
+                gate[i] = p.z ? silu(nz.v[i].get(0)) : 1.f;
+            }
+            if (t + kTok < w.t1) {
+                nbc.load(p, w, t + kTok, lane);
+                nx.load(p.x, xb, p.xst, t + kTok, w.t1);
+                nd.load(p.dt, db, p.dst, t + kTok, w.t1);
+                if (p.z) nz.load(p.z, zb, p.zst, t + kTok, w.t1);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                const float u = t + i < w.t1 ? s[i] * x[i] : 0.f;
+                float y = dskip * x[i];
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    h[n] = fmaf(exp2_hw(s[i] * a[n]), h[n], u * bc[buf][i][0][n]);
+                    y = fmaf(h[n], bc[buf][i][1][n], y);
+                }
+                if (w.on && t + i < w.t1) store_one<BF>(p.y, yb + (int64_t)(t + i) * p.D, y * gate[i]);
+            }
+        }
+    }
+    if (w.on) {
+        for (int t = w.t0 > w.t1 ? w.t0 : w.t1; t < w.tz; ++t) store_one<BF>(p.y, yb + (int64_t)t * p.D, 0.f);
+        if (p.h_final && w.seg == p.nseg - 1) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                if (n < p.N) p.h_final[((int64_t)w.b * p.D + w.c) * p.N + n] = h[n];
+        }
+    }
+}
+
+// Summaries of the segments.  E = sum_t P_end / P_t u_t Bm_t, with P_t the
+// product of the decays up to t, as the recurrence from zero.  For the
+// gradient also R = sum_t P_t C_t dyg_t: what the segment's outputs add to the
+// gradient of the state that enters it (dyg = dy silu(z)).
+template <bool BF, int NS, bool GRAD>
+__global__ __launch_bounds__(64) void gdn_ssm_sum_kernel(SsmParams p, int nseg) {
+    __shared__ __align__(16) float bc[2][kTok][2][NS];
+    const int lane = threadIdx.x;
+    const SsmPlace w = ssm_place(p, blockIdx.x, nseg, lane);
+    const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c, zb = w.b * p.zsb + w.c;
+    const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
+    float a[NS], h[NS], pr[NS], r[NS], total = 0.f;
+    load_decay<NS>(a, p, w.c);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = r[n] = 0.f, pr[n] = 1.f;
+    const float bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
+    if (w.t0 < w.t1) {
+        StagedBC<BF, NS> nbc;
+        Column<BF> nx, nd, nz, ng;
+        nbc.load(p, w, w.t0, lane);
+        nx.load(p.x, xb, p.xst, w.t0, w.t1);
+        nd.load(p.dt, db, p.dst, w.t0, w.t1);
+        if (GRAD) {
+            if (p.z) nz.load(p.z, zb, p.zst, w.t0, w.t1);
+            ng.load(p.dy, yb, p.D, w.t0, w.t1);
+        }
+        int buf = 0;
+        for (int t = w.t0; t < w.t1; t += kTok, buf ^= 1) {
+            nbc.put(&bc[buf][0][0][0], lane);
+            float u[kTok], s[kTok], g[kTok];
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                const bool in = t + i < w.t1;
+                s[i] = in ? ssm_step_size(nd.v[i].get(0) + bias, p.softplus) : 0.f;
+                u[i] = in ? s[i] * nx.v[i].get(0) : 0.f;
+                g[i] = 0.f;
+                if (GRAD && in) g[i] = p.z ? ng.v[i].get(0) * silu(nz.v[i].get(0)) : ng.v[i].get(0);
+                total += s[i];
+            }
+            if (t + kTok < w.t1) {
+                nbc.load(p, w, t + kTok, lane);
+                nx.load(p.x, xb, p.xst, t + kTok, w.t1);
+                nd.load(p.dt, db, p.dst, t + kTok, w.t1);
+                if (GRAD) {
+                    if (p.z) nz.load(p.z, zb, p.zst, t + kTok, w.t1);
+                    ng.load(p.dy, yb, p.D, t + kTok, w.t1);
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    const float d = exp2_hw(s[i] * a[n]);
+                    h[n] = fmaf(d, h[n], u[i] * bc[buf][i][0][n]);
+                    if (GRAD) {
+                        pr[n] *= d;
+                        r[n] = fmaf(pr[n], g[i] * bc[buf][i][1][n], r[n]);
+                    }
+                }
+            }
+        }
+    }
+    store_sum<NS>(p.sum_e, h, w.unit, lane);
+    p.sum_s[w.unit * 64 + lane] = total;
+    if (GRAD) store_sum<NS>(p.sum_r, r, w.unit, lane);
+}
+
+// From the summaries, in their place: sum_e becomes the state that enters
+// each segment; sum_r the gradient of the state that leaves it.  One thread
+// for a (sequence, tile, state, lane); kAhead segments' summaries are in
+// flight.
+constexpr int kChainThreads = 256;
+template <int NS, bool GRAD>
+__global__ __launch_bounds__(kChainThreads) void gdn_ssm_chain_kernel(SsmParams p) {
+    constexpr int kAhead = 8;
+    const unsigned tiles = (unsigned)(p.G * p.tpg);
+    const int64_t id = (int64_t)blockIdx.x * kChainThreads + threadIdx.x;
+    const int64_t per_seq = (int64_t)tiles * NS * 64;
+    if (id >= p.B * per_seq) return;
+    const int b = (int)(id / per_seq);
+    const int64_t in_seq = id % per_seq;
+    const int lane = (int)(in_seq % 64), n = (int)(in_seq / 64 % NS), tile = (int)(in_seq / (64 * NS));
+    const int c = (tile % p.tpg) * 64 + lane, g = tile / p.tpg;
+    const bool on = c < p.Dg && n < p.N;
+    const int64_t ch = g * p.Dg + c, at = ((int64_t)b * p.D + ch) * p.N + n;
+    const float a = on ? p.A[ch * p.N + n] * kLog2e : 0.f;
+    const int64_t se = per_seq, ss = (int64_t)tiles * 64;
+    float* e = p.sum_e + b * p.nseg * se + in_seq;
+    const float* s = p.sum_s + b * p.nseg * ss + tile * 64 + lane;
+    float h = p.h0 && on ? p.h0[at] : 0.f;
+    for (int k = 0; k < p.nseg; k += kAhead) {
+        float ev[kAhead], sv[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int j = k + i < p.nseg - 1 ? k + i : 0;     // (the last segment's own summary is not used)
+            ev[i] = e[j * se];
+            sv[i] = s[j * ss];
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (k + i < p.nseg) {
+                e[(k + i) * se] = h;
+                h = fmaf(exp2_hw(sv[i] * a), h, ev[i]);
+            }
+        }
+    }
+    if (GRAD) {
+        float* r = p.sum_r + b * p.nseg * se + in_seq;
+        float q = p.dh_final && on ? p.dh_final[at] : 0.f;
+        for (int k = p.nseg - 1; k >= 0; k -= kAhead) {
+            float rv[kAhead], sv[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int j = k - i >= 0 ? k - i : 0;
+                rv[i] = r[j * se];
+                sv[i] = s[j * ss];
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (k - i >= 0) {
+                    r[(k - i) * se] = q;
+                    q = fmaf(exp2_hw(sv[i] * a), q, rv[i]);
+                }
+            }
+        }
+        if (p.dh0 && on) p.dh0[at] = q;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sum over the 64 lanes of R registers at once (R a power of two, 2 .. 64):
+// each step between lanes halves the registers, a lane keeping the half that
+// its own number selects, while R > 1; then plain sums.  The result is value
+// lane / (64 / R) in every lane.  The first two steps are the lane-row swaps,
+// which exchange halves of two registers in one instruction.
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float swap32_add(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t r0 = r[0], r1 = r[1];     // (a bit cast of a vector's element takes element 0)
+    return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ float swap16_add(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t r0 = r[0], r1 = r[1];     // (a bit cast of a vector's element takes element 0)
+    return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+}
+// lanes whose `hi` is set keep b's sum with their partner, the others a's
+template <int CTRL>
+__device__ __forceinline__ float dpp_pair_add(float a, float b, bool hi) {
+    const float keep = hi ? b : a, give = hi ? a : b;
+    return keep + dpp_move<CTRL>(give);
+}
+template <int R>
+__device__ __forceinline__ float wave_sums(float (&v)[R], int lane) {
+    constexpr int R1 = R > 1 ? R / 2 : 1, R2 = R1 > 1 ? R1 / 2 : 1, R3 = R2 > 1 ? R2 / 2 : 1, R4 = R3 > 1 ? R3 / 2 : 1,
+                  R5 = R4 > 1 ? R4 / 2 : 1;
+    // partners: lane ^ 32, lane ^ 16 (of the same row half), the row rotated
+    // by 8, the half row mirrored (bits 0 to 2 flipped), lane ^ 2, lane ^ 1
+#pragma unroll
+    for (int i = 0; i < R1; ++i) v[i] = R > 1 ? swap32_add(v[i], v[(i + R1) % R]) : swap32_add(v[i], v[i]);
+#pragma unroll
+    for (int i = 0; i < R2; ++i) v[i] = R1 > 1 ? swap16_add(v[i], v[(i + R2) % R]) : swap16_add(v[i], v[i]);
+    const bool b3 = lane & 8, b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
+#pragma unroll
+    for (int i = 0; i < R3; ++i) v[i] = R2 > 1 ? dpp_pair_add<0x128>(v[i], v[(i + R3) % R], b3) : v[i] + dpp_move<0x128>(v[i]);
+#pragma unroll
+    for (int i = 0; i < R4; ++i) v[i] = R3 > 1 ? dpp_pair_add<0x141>(v[i], v[(i + R4) % R], b2) : v[i] + dpp_move<0x141>(v[i]);
+#pragma unroll
+    for (int i = 0; i < R5; ++i) v[i] = R4 > 1 ? dpp_pair_add<0x4E>(v[i], v[(i + R5) % R], b1) : v[i] + dpp_move<0x4E>(v[i]);
+    return R5 > 1 ? dpp_pair_add<0xB1>(v[0], v[1 % R], b0) : v[0] + dpp_move<0xB1>(v[0]);
+}
+
+// Gradient.  With g_t the gradient of h_t (g_t = C_t dyg_t + a_{t+1} g_{t+1},
+// a = exp(s A)), u = s x:
+//     dC_t = sum over channels of dyg_t h_t,  dB_t = sum over channels of g_t u_t
+//     du_t = sum over states of g_t Bm_t,     q_t = g_t a_t h_{t-1}
+//     dx_t = Dskip dyg_t + s_t du_t,          ds_t = x_t du_t + sum over states of q_t A
+//     ddt_t = ds_t sigmoid(dt_t + dt_bias),   dA = sum_t q_t s_t
+//     dz_t = dy_t silu'(z_t) (C_t . h_t + Dskip x_t)
+// A wave takes 64 channels of one segment.  It runs the recurrence forward
+// from the state that enters, keeping every kTok-th state in LDS, and then
+// goes through the groups of kTok tokens from the last to the first: the
+// group's states once more into registers, then the gradient backwards.
+// More than 16 states are split over the workgroup's NB waves, 16 each; what
+// sums over states (du, ds, y) is then added through LDS.
+constexpr int kGradGroups = 8;                       // groups of kTok tokens in a segment
+constexpr int kGradSeg = kGradGroups * kTok;
+
+template <bool BF, int NS, int NB>
+__global__ __launch_bounds__(64 * NB) void gdn_ssm_bwd_kernel(SsmParams p) {
+    constexpr int NSA = NS * NB;                     // states of the layout
+    __shared__ __align__(16) float bc_all[NB][kTok][2][NS];
+    __shared__ float keep_all[NB][kGradGroups - 1][NS][64];
+    __shared__ float cross[NB > 1 ? NB : 1][NB > 1 ? 3 * kTok : 1][64];
+    const int lane = threadIdx.x & 63, blk = NB > 1 ? threadIdx.x >> 6 : 0;
+    float(&bc)[kTok][2][NS] = bc_all[blk];
+    float(&keep)[kGradGroups - 1][NS][64] = keep_all[blk];
+    const SsmPlace w = ssm_place(p, blockIdx.x, p.nseg, lane);
+    const int n0 = blk * NS;
+    const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c, zb = w.b * p.zsb + w.c;
+    const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
+    const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
+    float a[NS], h[NS], g[NS], da[NS], dd = 0.f, dbias = 0.f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        a[n] = n0 + n < p.N ? p.A[(int64_t)w.c * p.N + n0 + n] * kLog2e : 0.f;
+        h[n] = p.sum_e[(w.unit * NSA + n0 + n) * 64 + lane];
+        g[n] = p.sum_r[(w.unit * NSA + n0 + n) * 64 + lane];
+        da[n] = 0.f;
+    }
+    // Bm and C of kTok tokens into the wave's part of LDS
+    auto stage = [&](int t) {
+        constexpr int kEach = kTok * 2 * NS / 64;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int k = lane + 64 * i, n = n0 + k % NS;
+            int tt = t + k / (2 * NS);
+            tt = tt < w.t1 ? tt : w.t1 - 1;
+            float v = 0.f;
+            if (n < p.N)
+                v = ((k / NS) & 1) ? load_one<BF>(p.C, w.b * p.csb + tt * p.cst + w.g * p.N + n)
+                                   : load_one<BF>(p.Bm, w.b * p.bsb + tt * p.bst + w.g * p.N + n);
+            (&bc[0][0][0])[k] = v;
+        }
+    };
+    const int groups = w.t1 > w.t0 ? (w.t1 - w.t0 + kTok - 1) / kTok : 0;
+    for (int k = 0; k + 1 < groups; ++k) {
+        const int t = w.t0 + k * kTok;      // (a full group: another follows)
+        __syncthreads();
+        stage(t);
+        float s[kTok], u[kTok];
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            s[i] = ssm_step_size(load_one<BF>(p.dt, db + (t + i) * p.dst) + bias, p.softplus);
+            u[i] = s[i] * load_one<BF>(p.x, xb + (t + i) * p.xst);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+#pragma unroll
+            for (int n = 0; n < NS; ++n) h[n] = fmaf(exp2_hw(s[i] * a[n]), h[n], u[i] * bc[i][0][n]);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) keep[k][n][lane] = h[n];
+    }
+    for (int k = groups - 1; k >= 0; --k) {
+        const int t = w.t0 + k * kTok;
+        __syncthreads();
+        stage(t);
+        if (k > 0) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n) h[n] = keep[k - 1][n][lane];
+        } else {
+#pragma unroll
+            for (int n = 0; n < NS; ++n) h[n] = p.sum_e[(w.unit * NSA + n0 + n) * 64 + lane];
+        }
+        float s[kTok], x[kTok], raw[kTok], gy[kTok], zs[kTok];
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            const bool in = t + i < w.t1;
+            const int tt = in ? t + i : w.t1 - 1;
+            raw[i] = load_one<BF>(p.dt, db + tt * p.dst) + bias;
+            s[i] = in ? ssm_step_size(raw[i], p.softplus) : 0.f;
+            x[i] = in ? load_one<BF>(p.x, xb + tt * p.xst) : 0.f;
+            const float dy = in ? load_one<BF>(p.dy, yb + (int64_t)tt * p.D) : 0.f;
+            gy[i] = dy;
+            zs[i] = 0.f;
+            if (p.z && in) {
+                float val, slope;
+                silu_both(load_one<BF>(p.z, zb + tt * p.zst), val, slope);
+                gy[i] = dy * val;
+                zs[i] = dy * slope;
+            }
+        }
+        __syncthreads();
+        float hs[kTok][NS], y[kTok], du[kTok], ds[kTok];
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            y[i] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                const float hp = i > 0 ? hs[i > 0 ? i - 1 : 0][n] : h[n];
+                hs[i][n] = fmaf(exp2_hw(s[i] * a[n]), hp, s[i] * x[i] * bc[i][0][n]);
+                y[i] = fmaf(hs[i][n], bc[i][1][n], y[i]);
+            }
+        }
+#pragma unroll
+        for (int i2 = kTok - 2; i2 >= 0; i2 -= 2) {
+            // two tokens' sums over the channels at once: [token][dB | dC][NS]
+            float v[4 * NS];
+#pragma unroll
+            for (int i = i2 + 1; i >= i2; --i) {
+                du[i] = ds[i] = 0.f;
+                const float u = s[i] * x[i];
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    g[n] = fmaf(bc[i][1][n], gy[i], g[n]);
+                    v[(i - i2) * 2 * NS + n] = w.on ? g[n] * u : 0.f;
+                    v[(i - i2) * 2 * NS + NS + n] = w.on ? gy[i] * hs[i][n] : 0.f;
+                    du[i] = fmaf(g[n], bc[i][0][n], du[i]);
+                    const float hp = i > 0 ? hs[i > 0 ? i - 1 : 0][n] : h[n];
+                    g[n] *= exp2_hw(s[i] * a[n]);
+                    const float q = g[n] * hp;
+                    ds[i] = fmaf(q, a[n], ds[i]);
+                    da[n] = fmaf(q, s[i], da[n]);
+                }
+            }
+            const float sum = wave_sums<4 * NS>(v, lane);
+            constexpr int kDup = 64 / (4 * NS) > 0 ? 64 / (4 * NS) : 1;
+            const int idx = lane / kDup, tt = t + i2 + idx / (2 * NS);
+            if (lane % kDup == 0 && tt < w.t1) {
+                const int which = (idx / NS) & 1, n = n0 + idx % NS;
+                p.part_bc[((((int64_t)w.tile * p.B + w.b) * p.T + tt) * 2 + which) * NSA + n] = sum;
+            }
+        }
+        if (NB > 1) {
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                cross[blk][i][lane] = y[i];
+                cross[blk][kTok + i][lane] = du[i];
+                cross[blk][2 * kTok + i][lane] = ds[i];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                y[i] = du[i] = ds[i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    y[i] += cross[j][i][lane];
+                    du[i] += cross[j][kTok + i][lane];
+                    ds[i] += cross[j][2 * kTok + i][lane];
+                }
+            }
+        }
+        if (NB == 1 || blk == 0) {
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                if (t + i < w.t1) {
+                    // (a holds A log2(e))
+                    float dr = fmaf(x[i], du[i], ds[i] * (1.f / kLog2e));
+                    if (p.softplus) dr *= sigmoid(raw[i]);
+                    dbias += dr;
+                    dd = fmaf(gy[i], x[i], dd);
+                    if (w.on) {
+                        const int64_t o = yb + (int64_t)(t + i) * p.D;
+                        store_one<BF>(p.dx, o, fmaf(dskip, gy[i], s[i] * du[i]));
+                        store_one<BF>(p.ddt, o, dr);
+                        if (p.z && p.dz) store_one<BF>(p.dz, o, zs[i] * fmaf(dskip, x[i], y[i]));
+                    }
+                }
+            }
+        }
+    }
+    const unsigned tiles = (unsigned)(p.G * p.tpg);
+    const int64_t at = ((int64_t)w.b * p.nseg + w.seg) * tiles + w.tile;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) p.part_a[(at * NSA + n0 + n) * 64 + lane] = da[n];
+    if (NB == 1 || blk == 0) {
+        p.part_d[(at * 2) * 64 + lane] = dd;
+        p.part_d[(at * 2 + 1) * 64 + lane] = dbias;
+        if (w.on) {
+            for (int t = w.t0 > w.t1 ? w.t0 : w.t1; t < w.tz; ++t) {
+                const int64_t o = yb + (int64_t)t * p.D;
+                store_one<BF>(p.dx, o, 0.f);
+                store_one<BF>(p.ddt, o, 0.f);
+                if (p.z && p.dz) store_one<BF>(p.dz, o, 0.f);
+            }
+        }
+    }
+}
+
+// dB and dC: the sum of the tiles' parts of a group, tiles ascending, rounded
+// once; zero behind a sequence's end.
+constexpr int kSumThreads = 256;
+template <bool BF>
+__global__ __launch_bounds__(kSumThreads) void gdn_ssm_bc_kernel(SsmParams p, void* dB, void* dC, int ns) {
+    const int64_t id = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
+    const int64_t per = (int64_t)p.B * p.T * p.G * 2 * ns;
+    if (id >= per) return;
+    const int n = (int)(id % ns), which = (int)(id / ns % 2);
+    const int64_t btg = id / (2 * ns);
+    const int g = (int)(btg % p.G);
+    const int64_t bt = btg / p.G;
+    if (n >= p.N) return;
+    float v = 0.f;
+    if (bt % p.T < seq_len(p.lens, (int)(bt / p.T), p.T)) {
+        const float* src = p.part_bc + (((int64_t)g * p.tpg * p.B * p.T + bt) * 2 + which) * ns + n;
+        const int64_t step = (int64_t)p.B * p.T * 2 * ns;
+#pragma unroll 4
+        for (int k = 0; k < p.tpg; ++k) v += src[k * step];
+    }
+    store_one<BF>(which ? dC : dB, (bt * p.G + g) * p.N + n, v);
+}
+
+// dA [D, N], dDskip [D], ddt_bias [D]: the sum over sequences and segments.
+template <bool BF>
+__global__ __launch_bounds__(kSumThreads) void gdn_ssm_param_kernel(SsmParams p, float* dA, float* dD, float* dbias, int ns) {
+    const int64_t id = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
+    const int tiles = p.G * p.tpg;
+    const int rows = ns + 2;
+    if (id >= (int64_t)tiles * rows * 64) return;
+    const int lane = (int)(id % 64), n = (int)(id / 64 % rows), tile = (int)(id / (64 * rows));
+    const int c = (tile % p.tpg) * 64 + lane, ch = tile / p.tpg * p.Dg + c;
+    if (c >= p.Dg) return;
+    const float* src = n < ns ? p.part_a + ((int64_t)tile * ns + n) * 64 + lane
+                              : p.part_d + ((int64_t)tile * 2 + n - ns) * 64 + lane;
+    const int64_t step = (int64_t)tiles * (n < ns ? ns : 2) * 64;
+    float v = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < p.B * p.nseg; ++k) v += src[k * step];
+    if (n < p.N) dA[(int64_t)ch * p.N + n] = v;
+    else if (n == ns && dD) dD[ch] = v;
+    else if (n == ns + 1 && dbias) dbias[ch] = v;
+}
+
+// ---------------------------------------------------------------------------
+// One token: the state passes through memory once, which bounds it.  LP lanes
+// share a channel, four states to a lane.
+struct SsmStepParams {
+    SsmParams f;
+    float* h;
+    int wide;               // states in 16-byte pieces (N a multiple of 4, aligned)
+};
+constexpr int kStepThreads = 256;
+
+template <bool BF, int LP>
+__global__ __launch_bounds__(kStepThreads) void gdn_ssm_step_kernel(SsmStepParams q) {
+    const SsmParams& p = q.f;
+    const int64_t id = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
+    const int64_t bd = id / LP;
+    const int n0 = (int)(id % LP) * 4;
+    const bool on = bd < (int64_t)p.B * p.D;
+    const int64_t bdc = on ? bd : (int64_t)p.B * p.D - 1;
+    const int b = (int)(bdc / p.D), d = (int)(bdc % p.D), g = d / p.Dg;
+    float h[4], a[4], bm[4], cm[4];
+    const int64_t hi = bdc * p.N + n0, ai = (int64_t)d * p.N + n0;
+    const int64_t bi = b * p.bsb + (int64_t)g * p.N + n0, ci = b * p.csb + (int64_t)g * p.N + n0;
+    const bool piece = q.wide && n0 < p.N;
+    if (piece) {
+        const f32x4 hv = *reinterpret_cast<const f32x4*>(q.h + hi), av = *reinterpret_cast<const f32x4*>(p.A + ai);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = hv[e], a[e] = av[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool in = n0 + e < p.N;
+        if (!piece) {
+            h[e] = in ? q.h[hi + e] : 0.f;
+            a[e] = in ? p.A[ai + e] : 0.f;
+        }
+        bm[e] = in ? load_one<BF>(p.Bm, bi + e) : 0.f;
+        cm[e] = in ? load_one<BF>(p.C, ci + e) : 0.f;
+    }
+    const float x = load_one<BF>(p.x, b * p.xsb + d);
+    const float s = ssm_step_size(load_one<BF>(p.dt, b * p.dsb + d) + (p.dt_bias ? p.dt_bias[d] : 0.f), p.softplus);
+    const float u = s * x;
+    float y = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = fmaf(exp2_hw(s * (a[e] * kLog2e)), h[e], u * bm[e]);
+        y = fmaf(h[e], cm[e], y);
+    }
+#pragma unroll
+    for (int m = 1; m < LP; m *= 2) y += __shfl_xor(y, m, 64);
+    if (!on) return;
+    if (piece) {
+        *reinterpret_cast<f32x4*>(q.h + hi) = f32x4{h[0], h[1], h[2], h[3]};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n0 + e < p.N) q.h[hi + e] = h[e];
+    }
+    if (n0 == 0) {
+        y = fmaf(p.Dskip ? p.Dskip[d] : 0.f, x, y);
+        if (p.z) y *= silu(load_one<BF>(p.z, b * p.zsb + d));
+        store_one<BF>(p.y, bd, y);
+    }
+}
+
+}  // namespace gdn

@@ -287,6 +287,174 @@ gdn_status gdn_recurrent_fwd_eta(const gdn_shape* s,
                                  const float* S0, void* O, float* S_final,
                                  void* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the recurrence of a mixing layer: the short causal
+ * convolution before it, the diagonal (selective state space) recurrence
+ * that takes the delta rule's place in some layers, and the normalisation
+ * and gate of the heads after it.  The conventions above hold, except that
+ * inputs whose strides are in a shape struct need only a contiguous last
+ * dimension (strides count elements, are >= 0, and may be 0: a broadcast
+ * input), that pointers need only the alignment of their type (16-byte
+ * aligned rows run the wide kernels), and that rows may be padded:
+ *   lens  [B] int32 or NULL (every sequence has T tokens): the number of
+ *         tokens of each sequence, clamped to [0, T].  Rows at and after it
+ *         are not read as tokens: their contents, NaN included, reach no
+ *         output; the output and gradient rows there are written as zero;
+ *         the final state is the one after the last token (the initial one
+ *         for a length of 0).
+ * Outputs may not overlap inputs or each other, except where stated.
+ * Gradients of parameters and of broadcast rows are sums in fp32 in a fixed
+ * order: the same call gives the same bits.
+ */
+
+/* Short causal convolution of each channel over W tokens. */
+typedef struct {
+    int32_t B, T, D;          /* sequences, tokens, channels                   */
+    int32_t W;                /* taps: 2, 3 or 4                               */
+    int32_t H;                /* heads of y and dy (D a multiple of H)         */
+    int32_t dtype;            /* gdn_dtype of x, y, the states, their gradients */
+    int32_t silu;             /* 1: y = SiLU(p), 0: y = p                      */
+    int64_t x_stride_b, x_stride_t;   /* x [B, T, D]                           */
+} gdn_conv_shape;
+
+/*
+ *     p_t = bias + sum_{j < W} weight_j x_{t-W+1+j},   y_t = p_t SiLU-ed
+ * per channel, with x_{-W+1} .. x_{-1} the rows of state0 (oldest first).
+ *   x          [B, T, D]        dtype, strided
+ *   weight     [D, W] float;  bias [D] float or NULL
+ *   state0     [B, W-1, D]      dtype, or NULL (zero)
+ *   y          [B, H, T, D/H]   dtype, contiguous (H = 1: [B, T, D]; H heads:
+ *                               q, k or v of gdn_chunk_fwd)
+ *   state_out  [B, W-1, D]      dtype or NULL; may be state0 (in place)
+ */
+gdn_status gdn_conv_fwd(const gdn_conv_shape* s, const void* x, const float* weight,
+                        const float* bias, const void* state0, const int32_t* lens,
+                        void* y, void* state_out, void* stream);
+
+/* One token of every sequence (T must be 1): gdn_conv_fwd with the state
+ * updated in place.  x [B, D] (rows x_stride_b apart), y [B, D]. */
+gdn_status gdn_conv_step(const gdn_conv_shape* s, const void* x, const float* weight,
+                         const float* bias, void* state, void* y, void* stream);
+
+/*
+ * Gradient of gdn_conv_fwd.  dy [B, H, T, D/H]; dstate_out (the gradient of
+ * state_out) [B, W-1, D] or NULL; dx [B, T, D] contiguous, all dtype;
+ * dweight [D, W], dbias [D] float (dbias may be NULL); dstate0 [B, W-1, D]
+ * dtype or NULL.  workspace: gdn_conv_bwd_workspace_bytes(s) bytes
+ * ((size_t)-1 for an invalid shape).
+ */
+size_t gdn_conv_bwd_workspace_bytes(const gdn_conv_shape* s);
+gdn_status gdn_conv_bwd(const gdn_conv_shape* s, const void* dy, const void* x,
+                        const float* weight, const float* bias, const void* state0,
+                        const void* dstate_out, const int32_t* lens,
+                        void* dx, float* dweight, float* dbias, void* dstate0,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Selective state space recurrence: a diagonal state of N numbers for every
+ * channel. */
+typedef struct {
+    int32_t B, T, D;          /* sequences, tokens, channels                   */
+    int32_t N;                /* states per channel: 1 .. 64                   */
+    int32_t G;                /* groups of B and C (D a multiple of G)         */
+    int32_t dtype;            /* gdn_dtype of x, dt, Bm, C, z, y and their gradients */
+    int32_t dt_softplus;      /* 1: dt passes through softplus, 0: as it is    */
+    int64_t x_stride_b, x_stride_t;     /* x  [B, T, D]                        */
+    int64_t dt_stride_b, dt_stride_t;   /* dt [B, T, D]                        */
+    int64_t z_stride_b, z_stride_t;     /* z  [B, T, D]                        */
+    int64_t b_stride_b, b_stride_t;     /* Bm [B, T, G, N] ([G, N] contiguous) */
+    int64_t c_stride_b, c_stride_t;     /* C  [B, T, G, N] ([G, N] contiguous) */
+} gdn_ssm_shape;
+
+/*
+ *     s_t = softplus(dt_t + dt_bias)      (dt_t + dt_bias with dt_softplus 0)
+ *     h_t = exp(s_t A) h_{t-1} + s_t x_t Bm_t
+ *     y_t = (C_t . h_t + Dskip x_t) SiLU(z_t)
+ * for every channel d, with A, h of N numbers and Bm_t, C_t those of the
+ * channel's group (channels [g D/G, (g+1) D/G) belong to group g).
+ *   A        [D, N] float (negative in a decaying state)
+ *   Dskip    [D] float or NULL (0);  dt_bias [D] float or NULL (0)
+ *   z        dtype or NULL (no gate)
+ *   h0       [B, D, N] float or NULL (zero)
+ *   y        [B, T, D] dtype, contiguous
+ *   h_final  [B, D, N] float or NULL; may be h0 (in place)
+ * The state is held in fp32.  Few channels on long sequences: the tokens are
+ * cut into segments that run at once, from summaries of the segments before
+ * them.  workspace: gdn_ssm_fwd_workspace_bytes(s) bytes (0 without segments;
+ * (size_t)-1 for an invalid shape).
+ */
+size_t gdn_ssm_fwd_workspace_bytes(const gdn_ssm_shape* s);
+gdn_status gdn_ssm_fwd(const gdn_ssm_shape* s, const void* x, const void* dt, const float* A,
+                       const void* Bm, const void* C, const float* Dskip, const void* z,
+                       const float* dt_bias, const float* h0, const int32_t* lens,
+                       void* y, float* h_final,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every sequence (T must be 1): gdn_ssm_fwd with the state h
+ * [B, D, N] updated in place.  x, dt, z [B, D], Bm, C [B, G, N], rows their
+ * stride_b apart; y [B, D]. */
+gdn_status gdn_ssm_step(const gdn_ssm_shape* s, const void* x, const void* dt, const float* A,
+                        const void* Bm, const void* C, const float* Dskip, const void* z,
+                        const float* dt_bias, float* h, void* y, void* stream);
+
+/*
+ * Gradient of gdn_ssm_fwd.  dy [B, T, D] dtype contiguous; dh_final
+ * [B, D, N] float or NULL (zero).  Written, all contiguous: dx, ddt, dz
+ * [B, T, D] and dBm, dC [B, T, G, N] in dtype (dz NULL without z); dA [D, N],
+ * dDskip [D], ddt_bias [D] float (the last two may be NULL); dh0 [B, D, N]
+ * float or NULL.  The states are computed again from the inputs.
+ * workspace: gdn_ssm_bwd_workspace_bytes(s) bytes ((size_t)-1 for an
+ * invalid shape).
+ */
+size_t gdn_ssm_bwd_workspace_bytes(const gdn_ssm_shape* s);
+gdn_status gdn_ssm_bwd(const gdn_ssm_shape* s, const void* dy, const void* x, const void* dt,
+                       const float* A, const void* Bm, const void* C, const float* Dskip,
+                       const void* z, const float* dt_bias, const float* h0,
+                       const float* dh_final, const int32_t* lens,
+                       void* dx, void* ddt, float* dA, void* dBm, void* dC, float* dDskip,
+                       void* dz, float* ddt_bias, float* dh0,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Normalisation of each head of each token, with an activation or a gate. */
+typedef struct {
+    int32_t B, T, G, d;       /* sequences, tokens, heads (groups), head size 1 .. 4096 */
+    int32_t x_dtype;          /* gdn_dtype of x and dx                         */
+    int32_t o_dtype;          /* gdn_dtype of y, dy, z and dz                  */
+    int32_t center;           /* 1: subtract the mean, 0: root mean square only */
+    int32_t w_per_group;      /* weight and bias: 0 [d] for all heads, 1 [G, d] */
+    int32_t silu;             /* 1: SiLU, 0: no activation                     */
+    float eps;                /* > 0                                           */
+    int64_t x_stride_b, x_stride_t, x_stride_g;   /* x [B, T, G, d]: the delta
+                                 rule's O [B, H, T, d] is read as it lies      */
+    int64_t z_stride_b, z_stride_t, z_stride_g;   /* z [B, T, G, d]            */
+} gdn_norm_shape;
+
+/*
+ *     n = (x - mean) / sqrt(var + eps)    over the d numbers of a head of a
+ *         token (mean = 0 and var = mean square where not centred)
+ *     p = n weight + bias
+ *     y = p act(z) with z, act(p) without  (act: SiLU or nothing)
+ * weight, bias float or NULL (1, 0); z o_dtype or NULL; y [B, T, G, d]
+ * o_dtype contiguous.  Statistics are taken in fp32 over the values in
+ * registers, the variance from the differences to the mean.
+ */
+gdn_status gdn_norm_fwd(const gdn_norm_shape* s, const void* x, const float* weight,
+                        const float* bias, const void* z, void* y, void* stream);
+
+/*
+ * Gradient of gdn_norm_fwd.  dy [B, T, G, d] o_dtype contiguous.  Written:
+ * dx x_dtype, with memory laid out by dx_stride_b, _t, _g (elements; its
+ * last dimension contiguous); dz [B, T, G, d] o_dtype contiguous (NULL
+ * without z); dweight, dbias float, shaped as weight (either may be NULL).
+ * workspace: gdn_norm_bwd_workspace_bytes(s) bytes ((size_t)-1 for an
+ * invalid shape).
+ */
+size_t gdn_norm_bwd_workspace_bytes(const gdn_norm_shape* s);
+gdn_status gdn_norm_bwd(const gdn_norm_shape* s, const void* dy, const void* x,
+                        const float* weight, const float* bias, const void* z,
+                        void* dx, int64_t dx_stride_b, int64_t dx_stride_t, int64_t dx_stride_g,
+                        float* dweight, float* dbias, void* dz,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* gdn_status_string(gdn_status st);
 
