@@ -18,8 +18,6 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _layer
-from ._layer import *  # noqa: F401,F403
 from ._lib import (EXPORTS, GDN_BF16, GDN_F32, GdnConvShape, GdnError, GdnNormShape, GdnShape, GdnSsmShape,
                    check, load)
 
@@ -28,7 +26,23 @@ __all__ = ["gdn_chunk_fwd", "gdn_chunk_fwd_eta", "gdn_chunk_fwd_precise", "gdn_c
            "gdn_chunk_prep", "gdn_chunk_fwd_workspace_bytes",
            "gdn_recurrent_fwd", "gdn_recurrent_fwd_eta",
            "gdn_status_string", "gdn_last_error", "gdn_version", "GdnError", "GdnShape",
-           "GdnConvShape", "GdnSsmShape", "GdnNormShape", "EXPORTS", *_layer.__all__]
+           "GdnConvShape", "GdnSsmShape", "GdnNormShape", "EXPORTS"]
+
+# the operators around the recurrence, from _layer.py at their first use (it
+# imports torch, which building and loading the library do without)
+_LAYER = ("gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step", "gdn_conv_bwd_workspace_bytes",
+          "gdn_ssm_fwd", "gdn_ssm_bwd", "gdn_ssm_step", "gdn_ssm_fwd_workspace_bytes",
+          "gdn_ssm_bwd_workspace_bytes",
+          "gdn_norm_fwd", "gdn_norm_bwd", "gdn_norm_bwd_workspace_bytes")
+__all__ += _LAYER
+
+
+def __getattr__(name):
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import _layer
+    globals().update({n: getattr(_layer, n) for n in _LAYER})
+    return globals()[name]
 
 
 def _torch():

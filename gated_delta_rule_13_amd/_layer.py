@@ -10,7 +10,10 @@ device by default), asynchronously.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+
+import torch
 
 from ._lib import GDN_BF16, GDN_F32, GdnConvShape, GdnError, GdnNormShape, GdnSsmShape, check, load
 
@@ -19,29 +22,45 @@ __all__ = ["gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step", "gdn_conv_bwd_worksp
            "gdn_ssm_bwd_workspace_bytes",
            "gdn_norm_fwd", "gdn_norm_bwd", "gdn_norm_bwd_workspace_bytes"]
 
-
-def _torch():
-    import torch
-    return torch
+_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 
 
 def _code(dt) -> int:
-    torch = _torch()
-    if dt == torch.bfloat16:
-        return GDN_BF16
-    if dt == torch.float32:
-        return GDN_F32
-    raise TypeError(f"unsupported dtype {dt}; use torch.bfloat16 or torch.float32")
+    code = _CODES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}; use torch.bfloat16 or torch.float32")
+    return code
 
 
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _device(name, t):
-    if t.device.type != "cuda":
+def _elsewhere(t, stream) -> bool:
+    """Whether a call has to move to another device or stream first."""
+    return stream is not None or not t.is_cuda or t.get_device() != torch.cuda.current_device()
+
+
+@contextlib.contextmanager
+def _moved(name, t, stream):
+    """The tensors' device and the call's stream made current, so that what
+    the call allocates belongs to that stream."""
+    if not t.is_cuda:
         raise ValueError(f"{name} runs on the GPU: tensors must be on a cuda device")
-    return t.device
+    if stream is None:
+        with torch.cuda.device(t.device):
+            yield
+    elif stream.device != t.device:
+        raise ValueError(f"the stream must be on {t.device}, got {stream.device}")
+    else:
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _stream(t) -> int:
+    """Handle of the current stream (the raw handle takes 0.1 us, a Stream
+    object 1.9 us: a single token's kernel runs for 3)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _check(name, t, shape, dtype, device, tail=None):
@@ -49,16 +68,16 @@ def _check(name, t, shape, dtype, device, tail=None):
     that its last `tail` dimensions are."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if tail is None:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    if t.is_contiguous():
         return
+    if tail is None:
+        raise ValueError(f"{name} must be contiguous")
     want = 1
     for dim in range(t.dim() - 1, t.dim() - 1 - tail, -1):
         if t.shape[dim] > 1 and t.stride(dim) != want:
@@ -75,12 +94,10 @@ def _rank(name, t, n):
 def _separate(name, out, **inputs):
     """An output of the caller's shares no memory with an input (as far as the
     ranges of their elements tell)."""
-    if out is None:
-        return
-    a0, a1 = _range(out)
+    base = out.untyped_storage().data_ptr()
     for other, t in inputs.items():
-        if t is not None and t.device == out.device and t.numel() and out.numel():
-            b0, b1 = _range(t)
+        if t is not None and t.untyped_storage().data_ptr() == base and t.numel() and out.numel():
+            (a0, a1), (b0, b1) = _range(out), _range(t)
             if a0 < b1 and b0 < a1:
                 raise ValueError(f"{name} may not overlap {other}")
 
@@ -90,47 +107,19 @@ def _range(t):
     return t.data_ptr(), t.data_ptr() + span * t.element_size()
 
 
-class _On:
-    """The device of the tensors made current, and the stream's handle."""
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream must be on {device}, got {stream.device}")
-        self.guard = torch.cuda.device(device)
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-
-    def __enter__(self):
-        self.guard.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
-
-
 def _query(entry, shape) -> int:
     n = getattr(load(), entry)(ctypes.byref(shape))
     if n == ctypes.c_size_t(-1).value:
         raise GdnError(4, load().gdn_last_error().decode())
-    return int(n)
+    return n
 
 
-def _workspace(nbytes, device, stream):
-    """(pointer, tensor): nbytes of device memory, 256-byte aligned, that the
-    call's stream owns."""
+def _workspace(nbytes, device):
+    """(256-byte aligned pointer, tensor that owns it) of nbytes."""
     if not nbytes:
         return None, None
-    torch = _torch()
-    with torch.cuda.stream(stream):
-        ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
     return (ws.data_ptr() + 255) // 256 * 256, ws
-
-
-def _outs(stream, device, **specs):
-    """Outputs made on the call's stream: name -> (shape, dtype) or None."""
-    torch = _torch()
-    with torch.cuda.stream(stream):
-        return {k: None if v is None else torch.empty(v[0], dtype=v[1], device=device) for k, v in specs.items()}
 
 
 def _silu(act) -> int:
@@ -152,7 +141,6 @@ def _conv_shape(x, weight, heads, act):
 
 
 def _conv_check(s, x, weight, bias, state, lens, dev):
-    torch = _torch()
     _check("x", x, x.shape, x.dtype, dev, tail=1)
     _check("weight", weight, (s.D, s.W), torch.float32, dev)
     _check("bias", bias, (s.D,), torch.float32, dev)
@@ -175,48 +163,49 @@ def gdn_conv_fwd(x, weight, bias=None, state0=None, lens=None, heads=None, act="
     [B,T,D], or [B,heads,T,D/heads] as gdn_chunk_fwd takes q, k and v;
     state_out [B,W-1,D], the last W-1 rows, which may be passed in and may be
     state0 (in place)."""
-    dev = _device("gdn_conv_fwd", x)
-    torch = _torch()
+    if _elsewhere(x, stream):
+        with _moved("gdn_conv_fwd", x, stream):
+            return gdn_conv_fwd(x, weight, bias, state0, lens, heads, act, y, state_out)
+    dev = x.device
     s = _conv_shape(x, weight, heads, act)
     _conv_check(s, x, weight, bias, state0, lens, dev)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    with _On(dev, stream) as hs:
-        made = _outs(st, dev, y=(_conv_out_shape(s, heads), x.dtype) if y is None else None,
-                     state_out=((s.B, s.W - 1, s.D), x.dtype) if state_out is None else None)
-        y = made["y"] if y is None else y
+    if y is None:
+        y = x.new_empty(_conv_out_shape(s, heads))
+    else:
         _check("y", y, _conv_out_shape(s, heads), x.dtype, dev)
-        if state_out is None:
-            state_out = made["state_out"]
-        else:
-            _check("state_out", state_out, (s.B, s.W - 1, s.D), x.dtype, dev)
-            same = state0 is not None and state_out.data_ptr() == state0.data_ptr()
-            _separate("state_out", state_out, x=x, y=y, state0=None if same else state0)
         _separate("y", y, x=x, state0=state0)
-        check(load().gdn_conv_fwd(ctypes.byref(s), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state0), _ptr(lens),
-                                  _ptr(y), _ptr(state_out), hs))
+    if state_out is None:
+        state_out = x.new_empty((s.B, s.W - 1, s.D))
+    else:
+        _check("state_out", state_out, (s.B, s.W - 1, s.D), x.dtype, dev)
+        same = state0 is not None and state_out.data_ptr() == state0.data_ptr()
+        _separate("state_out", state_out, x=x, y=y, state0=None if same else state0)
+    check(load().gdn_conv_fwd(ctypes.byref(s), x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state0), _ptr(lens),
+                              y.data_ptr(), state_out.data_ptr(), _stream(x)))
     return y, state_out
 
 
 def gdn_conv_step(x, weight, bias, state, act="silu", y=None, stream=None):
     """One token of every sequence: x [B,D] -> y [B,D], with state [B,W-1,D]
     updated in place.  Otherwise as gdn_conv_fwd."""
-    dev = _device("gdn_conv_step", x)
+    if _elsewhere(x, stream):
+        with _moved("gdn_conv_step", x, stream):
+            return gdn_conv_step(x, weight, bias, state, act, y)
+    dev = x.device
     _rank("x", x, 2)
-    torch = _torch()
-    row = x.unsqueeze(1)
-    s = _conv_shape(row, weight, None, act)
     if state is None:
         raise ValueError("gdn_conv_step needs the state")
+    row = x.unsqueeze(1)
+    s = _conv_shape(row, weight, None, act)
     _conv_check(s, row, weight, bias, state, None, dev)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    with _On(dev, stream) as hs:
-        if y is None:
-            y = _outs(st, dev, y=((s.B, s.D), x.dtype))["y"]
-        else:
-            _check("y", y, (s.B, s.D), x.dtype, dev)
-            _separate("y", y, x=x, state=state)
-        _separate("state", state, x=x)
-        check(load().gdn_conv_step(ctypes.byref(s), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), hs))
+    _separate("state", state, x=x)
+    if y is None:
+        y = x.new_empty((s.B, s.D))
+    else:
+        _check("y", y, (s.B, s.D), x.dtype, dev)
+        _separate("y", y, x=x, state=state)
+    check(load().gdn_conv_step(ctypes.byref(s), x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(),
+                               y.data_ptr(), _stream(x)))
     return y
 
 
@@ -229,8 +218,10 @@ def gdn_conv_bwd(dy, x, weight, bias=None, state0=None, lens=None, dstate_out=No
     contiguous), dstate_out [B,W-1,D] or None.  Returns a dict: dx [B,T,D] in
     x's dtype, dweight [D,W] and dbias [D] fp32 (dbias with a bias only),
     dstate0 [B,W-1,D] (with a state0 only)."""
-    dev = _device("gdn_conv_bwd", x)
-    torch = _torch()
+    if _elsewhere(x, stream):
+        with _moved("gdn_conv_bwd", x, stream):
+            return gdn_conv_bwd(dy, x, weight, bias, state0, lens, dstate_out, act)
+    dev = x.device
     if dy.dim() not in (3, 4):
         raise ValueError(f"dy must have 3 or 4 dimensions, got {dy.dim()}")
     heads = dy.shape[1] if dy.dim() == 4 else None
@@ -238,17 +229,17 @@ def gdn_conv_bwd(dy, x, weight, bias=None, state0=None, lens=None, dstate_out=No
     _conv_check(s, x, weight, bias, state0, lens, dev)
     _check("dy", dy, _conv_out_shape(s, heads), x.dtype, dev)
     _check("dstate_out", dstate_out, (s.B, s.W - 1, s.D), x.dtype, dev)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    with _On(dev, stream) as hs:
-        out = _outs(st, dev, dx=((s.B, s.T, s.D), x.dtype), dweight=((s.D, s.W), torch.float32),
-                    dbias=None if bias is None else ((s.D,), torch.float32),
-                    dstate0=None if state0 is None else ((s.B, s.W - 1, s.D), x.dtype))
-        nbytes = gdn_conv_bwd_workspace_bytes(s)
-        wp, ws = _workspace(nbytes, dev, st)
-        check(load().gdn_conv_bwd(ctypes.byref(s), _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state0),
-                                  _ptr(dstate_out), _ptr(lens), _ptr(out["dx"]), _ptr(out["dweight"]),
-                                  _ptr(out["dbias"]), _ptr(out["dstate0"]), wp, nbytes, hs))
-    return {k: v for k, v in out.items() if v is not None}
+    out = {"dx": x.new_empty((s.B, s.T, s.D)), "dweight": torch.empty_like(weight)}
+    if bias is not None:
+        out["dbias"] = torch.empty_like(bias)
+    if state0 is not None:
+        out["dstate0"] = torch.empty_like(state0)
+    nbytes = gdn_conv_bwd_workspace_bytes(s)
+    wp, ws = _workspace(nbytes, dev)
+    check(load().gdn_conv_bwd(ctypes.byref(s), dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state0),
+                              _ptr(dstate_out), _ptr(lens), out["dx"].data_ptr(), out["dweight"].data_ptr(),
+                              _ptr(out.get("dbias")), _ptr(out.get("dstate0")), wp, nbytes, _stream(x)))
+    return out
 
 
 # ---- selective state space recurrence ----
@@ -269,7 +260,6 @@ def _ssm_shape(x, dt, A, Bm, C, z, dt_softplus):
 
 
 def _ssm_check(s, x, dt, A, Bm, C, D, z, dt_bias, h, lens, dev):
-    torch = _torch()
     f32, io = torch.float32, x.dtype
     rows = (s.B, s.T, s.D)
     _check("x", x, rows, io, dev, tail=1)
@@ -299,52 +289,62 @@ def gdn_ssm_fwd(x, dt, A, Bm, C, D=None, z=None, dt_bias=None, h0=None, lens=Non
     [B] int32 or None (rows behind a sequence's length are written as zero);
     dt_softplus=False takes dt + dt_bias as it is.  Returns (y [B,T,D] in x's
     dtype, h_final [B,D,N] fp32), which may be passed in; h_final may be h0."""
-    dev = _device("gdn_ssm_fwd", x)
-    torch = _torch()
+    if _elsewhere(x, stream):
+        with _moved("gdn_ssm_fwd", x, stream):
+            return gdn_ssm_fwd(x, dt, A, Bm, C, D, z, dt_bias, h0, lens, dt_softplus, y, h_final)
+    dev = x.device
     s = _ssm_shape(x, dt, A, Bm, C, z, dt_softplus)
     _ssm_check(s, x, dt, A, Bm, C, D, z, dt_bias, h0, lens, dev)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    with _On(dev, stream) as hs:
-        made = _outs(st, dev, y=((s.B, s.T, s.D), x.dtype) if y is None else None,
-                     h=((s.B, s.D, s.N), torch.float32) if h_final is None else None)
-        if y is None:
-            y = made["y"]
-        else:
-            _check("y", y, (s.B, s.T, s.D), x.dtype, dev)
-            _separate("y", y, x=x, dt=dt, z=z, Bm=Bm, C=C)
-        if h_final is None:
-            h_final = made["h"]
-        else:
-            _check("h_final", h_final, (s.B, s.D, s.N), torch.float32, dev)
-            same = h0 is not None and h_final.data_ptr() == h0.data_ptr()
-            _separate("h_final", h_final, h0=None if same else h0, x=x, dt=dt, A=A, y=y)
-        nbytes = gdn_ssm_fwd_workspace_bytes(s)
-        wp, ws = _workspace(nbytes, dev, st)
-        check(load().gdn_ssm_fwd(ctypes.byref(s), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(C), _ptr(D), _ptr(z),
-                                 _ptr(dt_bias), _ptr(h0), _ptr(lens), _ptr(y), _ptr(h_final), wp, nbytes, hs))
+    if y is None:
+        y = x.new_empty((s.B, s.T, s.D))
+    else:
+        _check("y", y, (s.B, s.T, s.D), x.dtype, dev)
+        _separate("y", y, x=x, dt=dt, z=z, Bm=Bm, C=C)
+    if h_final is None:
+        h_final = A.new_empty((s.B, s.D, s.N))
+    else:
+        _check("h_final", h_final, (s.B, s.D, s.N), torch.float32, dev)
+        same = h0 is not None and h_final.data_ptr() == h0.data_ptr()
+        _separate("h_final", h_final, h0=None if same else h0, x=x, dt=dt, A=A, y=y)
+    nbytes = gdn_ssm_fwd_workspace_bytes(s)
+    wp, ws = _workspace(nbytes, dev)
+    check(load().gdn_ssm_fwd(ctypes.byref(s), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), C.data_ptr(),
+                             _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens), y.data_ptr(), h_final.data_ptr(),
+                             wp, nbytes, _stream(x)))
     return y, h_final
 
 
 def gdn_ssm_step(x, dt, A, Bm, C, D=None, z=None, dt_bias=None, h=None, dt_softplus=True, y=None, stream=None):
     """One token of every sequence: x, dt, z [B,D], Bm, C [B,G,N] -> y [B,D],
     with the state h [B,D,N] updated in place.  Otherwise as gdn_ssm_fwd."""
-    dev = _device("gdn_ssm_step", x)
-    torch = _torch()
+    if _elsewhere(x, stream):
+        with _moved("gdn_ssm_step", x, stream):
+            return gdn_ssm_step(x, dt, A, Bm, C, D, z, dt_bias, h, dt_softplus, y)
+    dev = x.device
     if h is None:
         raise ValueError("gdn_ssm_step needs the state h")
-    _rank("x", x, 2)
-    row = [None if t is None else t.unsqueeze(1) for t in (x, dt, Bm, C, z)]
-    s = _ssm_shape(row[0], row[1], A, row[2], row[3], row[4], dt_softplus)
-    _ssm_check(s, row[0], row[1], A, row[2], row[3], D, row[4], dt_bias, h, None, dev)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    with _On(dev, stream) as hs:
-        if y is None:
-            y = _outs(st, dev, y=((s.B, s.D), x.dtype))["y"]
-        else:
-            _check("y", y, (s.B, s.D), x.dtype, dev)
-            _separate("y", y, x=x, dt=dt, z=z, Bm=Bm, C=C, h=h)
-        check(load().gdn_ssm_step(ctypes.byref(s), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(C), _ptr(D), _ptr(z),
-                                  _ptr(dt_bias), _ptr(h), _ptr(y), hs))
+    for name, t, n in (("x", x, 2), ("dt", dt, 2), ("A", A, 2), ("Bm", Bm, 3), ("C", C, 3)):
+        _rank(name, t, n)
+    (B, Dc), (G, N), io = x.shape, Bm.shape[1:], x.dtype
+    if G < 1 or Dc % G:
+        raise ValueError(f"{Dc} channels do not divide into {G} groups")
+    for name, t, tail in (("x", x, 1), ("dt", dt, 1), ("z", z, 1)):
+        _check(name, t, (B, Dc), io, dev, tail)
+    _check("Bm", Bm, (B, G, N), io, dev, 2)
+    _check("C", C, (B, G, N), io, dev, 2)
+    _check("A", A, (Dc, N), torch.float32, dev)
+    _check("D", D, (Dc,), torch.float32, dev)
+    _check("dt_bias", dt_bias, (Dc,), torch.float32, dev)
+    _check("h", h, (B, Dc, N), torch.float32, dev)
+    s = GdnSsmShape(B, 1, Dc, N, G, _code(io), 1 if dt_softplus else 0, x.stride(0), 0, dt.stride(0), 0,
+                    0 if z is None else z.stride(0), 0, Bm.stride(0), 0, C.stride(0), 0)
+    if y is None:
+        y = x.new_empty((B, Dc))
+    else:
+        _check("y", y, (B, Dc), io, dev)
+        _separate("y", y, x=x, dt=dt, z=z, Bm=Bm, C=C, h=h)
+    check(load().gdn_ssm_step(ctypes.byref(s), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), C.data_ptr(),
+                              _ptr(D), _ptr(z), _ptr(dt_bias), h.data_ptr(), y.data_ptr(), _stream(x)))
     return y
 
 
@@ -358,27 +358,33 @@ def gdn_ssm_bwd(dy, x, dt, A, Bm, C, D=None, z=None, dt_bias=None, h0=None, lens
     or None.  Returns a dict: dx, ddt [B,T,D], dB, dC [B,T,G,N] in x's dtype, dA
     [D,N] fp32 and, with the inputs they belong to, dD, ddt_bias [D] fp32, dz
     [B,T,D], dh0 [B,D,N] fp32."""
-    dev = _device("gdn_ssm_bwd", x)
-    torch = _torch()
+    if _elsewhere(x, stream):
+        with _moved("gdn_ssm_bwd", x, stream):
+            return gdn_ssm_bwd(dy, x, dt, A, Bm, C, D, z, dt_bias, h0, lens, dh_final, dt_softplus)
+    dev = x.device
     s = _ssm_shape(x, dt, A, Bm, C, z, dt_softplus)
     _ssm_check(s, x, dt, A, Bm, C, D, z, dt_bias, h0, lens, dev)
-    rows, state, f32 = (s.B, s.T, s.D), (s.B, s.D, s.N), torch.float32
+    rows, bc = (s.B, s.T, s.D), (s.B, s.T, s.G, s.N)
     _check("dy", dy, rows, x.dtype, dev)
-    _check("dh_final", dh_final, state, f32, dev)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    with _On(dev, stream) as hs:
-        out = _outs(st, dev, dx=(rows, x.dtype), ddt=(rows, x.dtype), dA=((s.D, s.N), f32),
-                    dB=((s.B, s.T, s.G, s.N), x.dtype), dC=((s.B, s.T, s.G, s.N), x.dtype),
-                    dD=None if D is None else ((s.D,), f32), dz=None if z is None else (rows, x.dtype),
-                    ddt_bias=None if dt_bias is None else ((s.D,), f32), dh0=None if h0 is None else (state, f32))
-        nbytes = gdn_ssm_bwd_workspace_bytes(s)
-        wp, ws = _workspace(nbytes, dev, st)
-        check(load().gdn_ssm_bwd(ctypes.byref(s), _ptr(dy), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(C), _ptr(D),
-                                 _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(dh_final), _ptr(lens),
-                                 _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]),
-                                 _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]),
-                                 _ptr(out["dh0"]), wp, nbytes, hs))
-    return {k: v for k, v in out.items() if v is not None}
+    _check("dh_final", dh_final, (s.B, s.D, s.N), torch.float32, dev)
+    out = {"dx": x.new_empty(rows), "ddt": x.new_empty(rows), "dA": torch.empty_like(A), "dB": x.new_empty(bc),
+           "dC": x.new_empty(bc)}
+    if D is not None:
+        out["dD"] = torch.empty_like(D)
+    if z is not None:
+        out["dz"] = x.new_empty(rows)
+    if dt_bias is not None:
+        out["ddt_bias"] = torch.empty_like(dt_bias)
+    if h0 is not None:
+        out["dh0"] = torch.empty_like(h0)
+    nbytes = gdn_ssm_bwd_workspace_bytes(s)
+    wp, ws = _workspace(nbytes, dev)
+    check(load().gdn_ssm_bwd(ctypes.byref(s), dy.data_ptr(), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+                             C.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(dh_final), _ptr(lens),
+                             out["dx"].data_ptr(), out["ddt"].data_ptr(), out["dA"].data_ptr(), out["dB"].data_ptr(),
+                             out["dC"].data_ptr(), _ptr(out.get("dD")), _ptr(out.get("dz")),
+                             _ptr(out.get("ddt_bias")), _ptr(out.get("dh0")), wp, nbytes, _stream(x)))
+    return out
 
 
 # ---- head normalisation ----
@@ -395,7 +401,6 @@ def _norm_shape(x, weight, bias, z, act, center, eps, o_dtype):
 
 
 def _norm_check(s, x, weight, bias, z, o_dtype, dev):
-    torch = _torch()
     _check("x", x, x.shape, x.dtype, dev, tail=1)
     wshape = (s.G, s.d) if s.w_per_group else (s.d,)
     _check("weight", weight, wshape, torch.float32, dev)
@@ -412,20 +417,21 @@ def gdn_norm_fwd(x, weight=None, bias=None, z=None, act="silu", center=False, ep
     delta rule's O [B,H,T,d] as O.transpose(1, 2)); weight, bias fp32 [d] for
     all heads or [G,d], or None; z [B,T,G,d] in o_dtype, a view.  Returns y
     [B,T,G,d] contiguous in o_dtype (default: z's dtype, or x's)."""
-    dev = _device("gdn_norm_fwd", x)
-    torch = _torch()
+    if _elsewhere(x, stream):
+        with _moved("gdn_norm_fwd", x, stream):
+            return gdn_norm_fwd(x, weight, bias, z, act, center, eps, o_dtype, y)
+    dev = x.device
     if o_dtype is None:
         o_dtype = x.dtype if z is None else z.dtype
     s = _norm_shape(x, weight, bias, z, act, center, eps, o_dtype)
     _norm_check(s, x, weight, bias, z, o_dtype, dev)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    with _On(dev, stream) as hs:
-        if y is None:
-            y = _outs(st, dev, y=(tuple(x.shape), o_dtype))["y"]
-        else:
-            _check("y", y, x.shape, o_dtype, dev)
-            _separate("y", y, x=x, z=z)
-        check(load().gdn_norm_fwd(ctypes.byref(s), _ptr(x), _ptr(weight), _ptr(bias), _ptr(z), _ptr(y), hs))
+    if y is None:
+        y = torch.empty(x.shape, dtype=o_dtype, device=dev)
+    else:
+        _check("y", y, x.shape, o_dtype, dev)
+        _separate("y", y, x=x, z=z)
+    check(load().gdn_norm_fwd(ctypes.byref(s), x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z), y.data_ptr(),
+                              _stream(x)))
     return y
 
 
@@ -438,25 +444,28 @@ def gdn_norm_bwd(dy, x, weight=None, bias=None, z=None, act="silu", center=False
     Returns a dict: dx in x's dtype, and in x's order of dimensions in memory
     where x is dense, and, with the inputs they belong to, dweight and dbias
     fp32 (summed over the heads for weights [d]) and dz [B,T,G,d]."""
-    dev = _device("gdn_norm_bwd", x)
-    torch = _torch()
-    o_dtype = dy.dtype
+    if _elsewhere(x, stream):
+        with _moved("gdn_norm_bwd", x, stream):
+            return gdn_norm_bwd(dy, x, weight, bias, z, act, center, eps)
+    dev, o_dtype = x.device, dy.dtype
     s = _norm_shape(x, weight, bias, z, act, center, eps, o_dtype)
     _norm_check(s, x, weight, bias, z, o_dtype, dev)
     _check("dy", dy, x.shape, o_dtype, dev)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    with _On(dev, stream) as hs:
-        with torch.cuda.stream(st):
-            dx = torch.empty_like(x)        # (dense x: the same strides; else contiguous)
-            if dx.stride(-1) != 1 and dx.shape[-1] > 1 or any(
-                    n > 1 and v < s.d for n, v in zip(dx.shape[:3], dx.stride()[:3])):
-                dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        out = _outs(st, dev, dweight=None if weight is None else (tuple(weight.shape), torch.float32),
-                    dbias=None if bias is None else (tuple(bias.shape), torch.float32),
-                    dz=None if z is None else (tuple(x.shape), o_dtype))
-        nbytes = gdn_norm_bwd_workspace_bytes(s)
-        wp, ws = _workspace(nbytes, dev, st)
-        check(load().gdn_norm_bwd(ctypes.byref(s), _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(z), _ptr(dx),
-                                  *dx.stride()[:3], _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dz"]), wp,
-                                  nbytes, hs))
-    return {"dx": dx, **{k: v for k, v in out.items() if v is not None}}
+    dx = torch.empty_like(x)            # (dense x: the same strides; else torch's choice)
+    ds = dx.stride()
+    if (ds[3] != 1 and s.d > 1) or any(n > 1 and v < s.d for n, v in zip(dx.shape[:3], ds)):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        ds = dx.stride()
+    out = {"dx": dx}
+    if weight is not None:
+        out["dweight"] = torch.empty_like(weight)
+    if bias is not None:
+        out["dbias"] = torch.empty_like(bias)
+    if z is not None:
+        out["dz"] = torch.empty(x.shape, dtype=o_dtype, device=dev)
+    nbytes = gdn_norm_bwd_workspace_bytes(s)
+    wp, ws = _workspace(nbytes, dev)
+    check(load().gdn_norm_bwd(ctypes.byref(s), dy.data_ptr(), x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z),
+                              dx.data_ptr(), ds[0], ds[1], ds[2], _ptr(out.get("dweight")), _ptr(out.get("dbias")),
+                              _ptr(out.get("dz")), wp, nbytes, _stream(x)))
+    return out
