@@ -212,7 +212,7 @@ gdn_status ssm_check(const gdn_ssm_shape* s, const void* x, const void* dt, cons
 // Parts of the gradient's workspace, in bytes from its start.
 struct SsmGradPlan {
     int nseg;
-    size_t e, r, s, a, d, bc, bytes;
+    size_t e, r, s, kh, ks, a, d, bc, bytes;
 };
 SsmGradPlan ssm_bwd_plan(const gdn_ssm_shape& s) {
     SsmGradPlan g{};
@@ -222,7 +222,9 @@ SsmGradPlan ssm_bwd_plan(const gdn_ssm_shape& s) {
     g.e = 0;
     g.r = g.e + units * ns * 64 * 4;
     g.s = g.r + units * ns * 64 * 4;
-    g.a = g.s + units * 64 * 4;
+    g.kh = g.s + units * 64 * 4;
+    g.ks = g.kh + units * (gdn::kGradGroups - 1) * ns * 64 * 4;
+    g.a = g.ks + units * (gdn::kGradGroups - 1) * 64 * 4;
     g.d = g.a + units * ns * 64 * 4;
     g.bc = g.d + units * 2 * 64 * 4;
     g.bytes = g.bc + up256(tiles * s.B * s.T * 2 * ns * 4);
@@ -441,6 +443,8 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape* s, const void* dy, const void* x, co
     p.sum_e = reinterpret_cast<float*>(ws + pl.e);
     p.sum_r = reinterpret_cast<float*>(ws + pl.r);
     p.sum_s = reinterpret_cast<float*>(ws + pl.s);
+    p.keep_h = reinterpret_cast<float*>(ws + pl.kh);
+    p.keep_s = reinterpret_cast<float*>(ws + pl.ks);
     p.part_a = reinterpret_cast<float*>(ws + pl.a);
     p.part_d = reinterpret_cast<float*>(ws + pl.d);
     p.part_bc = reinterpret_cast<float*>(ws + pl.bc);

@@ -59,12 +59,16 @@ struct SsmParams {
     void* dz;
     float* dh0;             // may be null
     float* sum_r;           // [unit][NS][64]: R, then the gradient that enters from behind
+    float* keep_h;          // [unit][group 1 ..][NS][64]: state from zero at a group's start
+    float* keep_s;          // [unit][group 1 ..][64]: sum of s up to there
     float* part_a;          // [sequence, segment][tile][NS][64]: dA
     float* part_d;          // [sequence, segment][tile][2][64]: dDskip, ddt_bias
     float* part_bc;         // [tile][sequence][token][2][NS]: dB, dC over a tile's channels
 };
 
-constexpr int kTok = 8;      // tokens staged at a time
+constexpr int kTok = 8;                              // tokens staged at a time
+constexpr int kGradGroups = 8;                       // groups of kTok tokens in a segment of the gradient
+constexpr int kGradSeg = kGradGroups * kTok;
 
 // Where a wave works: its sequence, segment and channels.
 struct SsmPlace {
@@ -149,6 +153,18 @@ __device__ __forceinline__ void store_sum(float* s, const float (&h)[NS], int64_
     for (int n = 0; n < NS; ++n) s[(unit * NS + n) * 64 + lane] = h[n];
 }
 
+// Pins the registers of v where it stands.  The kernels go through their
+// staged tokens in an unrolled loop; without this the compiler reads every
+// token's Bm and C at once, computes every decay first, leaves sums that are
+// needed only at the end for last, and so holds hundreds of registers
+// (gradient kernel: 2.3 ms and spills where it now takes a fourth).  The
+// states of one token already are NS independent chains.
+template <int N>
+__device__ __forceinline__ void pin(float (&v)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) asm volatile("" : "+v"(v[n]) : : "memory");
+}
+
 __device__ __forceinline__ float ssm_step_size(float raw, bool soft) { return soft ? softplus(raw) : raw; }
 
 // Tokens behind t1 take the step size 0: they leave the state as it is.
@@ -199,6 +215,7 @@ __global__ __launch_bounds__(64) void gdn_ssm_fwd_kernel(SsmParams p) {
                     y = fmaf(h[n], bc[buf][i][1][n], y);
                 }
                 if (w.on && t + i < w.t1) store_one<BF>(p.y, yb + (int64_t)(t + i) * p.D, y * gate[i]);
+                pin(h);
             }
         }
     }
@@ -215,7 +232,9 @@ __global__ __launch_bounds__(64) void gdn_ssm_fwd_kernel(SsmParams p) {
 // Summaries of the segments.  E = sum_t P_end / P_t u_t Bm_t, with P_t the
 // product of the decays up to t, as the recurrence from zero.  For the
 // gradient also R = sum_t P_t C_t dyg_t: what the segment's outputs add to the
-// gradient of the state that enters it (dyg = dy silu(z)).
+// gradient of the state that enters it (dyg = dy silu(z)), and the state from
+// zero after each group of kTok tokens, from which the gradient kernel goes
+// on.
 template <bool BF, int NS, bool GRAD>
 __global__ __launch_bounds__(64) void gdn_ssm_sum_kernel(SsmParams p, int nseg) {
     __shared__ __align__(16) float bc[2][kTok][2][NS];
@@ -272,6 +291,16 @@ __global__ __launch_bounds__(64) void gdn_ssm_sum_kernel(SsmParams p, int nseg) 
                         r[n] = fmaf(pr[n], g[i] * bc[buf][i][1][n], r[n]);
                     }
                 }
+                pin(h);
+                if (GRAD) {
+                    pin(pr);
+                    pin(r);
+                }
+            }
+            if (GRAD && t + kTok < w.t1) {
+                const int64_t at = w.unit * (kGradGroups - 1) + (t - w.t0) / kTok;
+                store_sum<NS>(p.keep_h, h, at, lane);
+                p.keep_s[at * 64 + lane] = total;
             }
         }
     }
@@ -343,11 +372,13 @@ __global__ __launch_bounds__(kChainThreads) void gdn_ssm_chain_kernel(SsmParams 
 }
 
 // ---------------------------------------------------------------------------
-// Sum over the 64 lanes of R registers at once (R a power of two, 2 .. 64):
-// each step between lanes halves the registers, a lane keeping the half that
-// its own number selects, while R > 1; then plain sums.  The result is value
-// lane / (64 / R) in every lane.  The first two steps are the lane-row swaps,
-// which exchange halves of two registers in one instruction.
+// Sums over the lanes of many registers at once: each step between lanes
+// halves the registers, a lane keeping the half that its own number selects,
+// while there is more than one; then plain sums.  The steps between rows of 16
+// lanes are the lane-row swaps, which exchange halves of two registers in one
+// instruction: swap32_add(a, b) leaves a's sum over lane and lane ^ 32 in the
+// lower 32 lanes and b's in the upper, and row_sums of R registers leaves value
+// (lane % 32) / (32 / R) summed over the 32 lanes of each half.
 template <int CTRL>
 __device__ __forceinline__ float dpp_move(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
@@ -369,23 +400,21 @@ __device__ __forceinline__ float dpp_pair_add(float a, float b, bool hi) {
     return keep + dpp_move<CTRL>(give);
 }
 template <int R>
-__device__ __forceinline__ float wave_sums(float (&v)[R], int lane) {
-    constexpr int R1 = R > 1 ? R / 2 : 1, R2 = R1 > 1 ? R1 / 2 : 1, R3 = R2 > 1 ? R2 / 2 : 1, R4 = R3 > 1 ? R3 / 2 : 1,
-                  R5 = R4 > 1 ? R4 / 2 : 1;
-    // partners: lane ^ 32, lane ^ 16 (of the same row half), the row rotated
-    // by 8, the half row mirrored (bits 0 to 2 flipped), lane ^ 2, lane ^ 1
+__device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
+    static_assert(R >= 2 && R <= 32, "");
+    constexpr int R2 = R / 2, R3 = R2 > 1 ? R2 / 2 : 1, R4 = R3 > 1 ? R3 / 2 : 1, R5 = R4 > 1 ? R4 / 2 : 1;
+    // partners: lane ^ 16, the row rotated by 8, the half row mirrored (bits 0
+    // to 2 flipped), lane ^ 2, lane ^ 1
 #pragma unroll
-    for (int i = 0; i < R1; ++i) v[i] = R > 1 ? swap32_add(v[i], v[(i + R1) % R]) : swap32_add(v[i], v[i]);
-#pragma unroll
-    for (int i = 0; i < R2; ++i) v[i] = R1 > 1 ? swap16_add(v[i], v[(i + R2) % R]) : swap16_add(v[i], v[i]);
+    for (int i = 0; i < R2; ++i) v[i] = swap16_add(v[i], v[i + R2]);
     const bool b3 = lane & 8, b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
 #pragma unroll
-    for (int i = 0; i < R3; ++i) v[i] = R2 > 1 ? dpp_pair_add<0x128>(v[i], v[(i + R3) % R], b3) : v[i] + dpp_move<0x128>(v[i]);
+    for (int i = 0; i < R3; ++i) v[i] = R2 > 1 ? dpp_pair_add<0x128>(v[i], v[i + R3], b3) : v[i] + dpp_move<0x128>(v[i]);
 #pragma unroll
-    for (int i = 0; i < R4; ++i) v[i] = R3 > 1 ? dpp_pair_add<0x141>(v[i], v[(i + R4) % R], b2) : v[i] + dpp_move<0x141>(v[i]);
+    for (int i = 0; i < R4; ++i) v[i] = R3 > 1 ? dpp_pair_add<0x141>(v[i], v[i + R4], b2) : v[i] + dpp_move<0x141>(v[i]);
 #pragma unroll
-    for (int i = 0; i < R5; ++i) v[i] = R4 > 1 ? dpp_pair_add<0x4E>(v[i], v[(i + R5) % R], b1) : v[i] + dpp_move<0x4E>(v[i]);
-    return R5 > 1 ? dpp_pair_add<0xB1>(v[0], v[1 % R], b0) : v[0] + dpp_move<0xB1>(v[0]);
+    for (int i = 0; i < R5; ++i) v[i] = R4 > 1 ? dpp_pair_add<0x4E>(v[i], v[i + R5], b1) : v[i] + dpp_move<0x4E>(v[i]);
+    return R5 > 1 ? dpp_pair_add<0xB1>(v[0], v[1], b0) : v[0] + dpp_move<0xB1>(v[0]);
 }
 
 // Gradient.  With g_t the gradient of h_t (g_t = C_t dyg_t + a_{t+1} g_{t+1},
@@ -395,176 +424,152 @@ __device__ __forceinline__ float wave_sums(float (&v)[R], int lane) {
 //     dx_t = Dskip dyg_t + s_t du_t,          ds_t = x_t du_t + sum over states of q_t A
 //     ddt_t = ds_t sigmoid(dt_t + dt_bias),   dA = sum_t q_t s_t
 //     dz_t = dy_t silu'(z_t) (C_t . h_t + Dskip x_t)
-// A wave takes 64 channels of one segment.  It runs the recurrence forward
-// from the state that enters, keeping every kTok-th state in LDS, and then
-// goes through the groups of kTok tokens from the last to the first: the
-// group's states once more into registers, then the gradient backwards.
-// More than 16 states are split over the workgroup's NB waves, 16 each; what
-// sums over states (du, ds, y) is then added through LDS.
-constexpr int kGradGroups = 8;                       // groups of kTok tokens in a segment
-constexpr int kGradSeg = kGradGroups * kTok;
-
+// A wave takes 64 channels of one segment and goes through its groups of kTok
+// tokens from the last to the first: the state at the group's start (from zero,
+// as the summaries left it, and the decayed state that entered the segment),
+// the group's states into registers, then the gradient backwards.  The decays
+// are computed again on the way back: holding them too would leave room for
+// one wave on a vector unit instead of two.  More than 16 states are split
+// over the workgroup's NB waves, 16 each; what sums over states (du, ds, y) is
+// then added through LDS.
 template <bool BF, int NS, int NB>
-__global__ __launch_bounds__(64 * NB) void gdn_ssm_bwd_kernel(SsmParams p) {
+__global__ __launch_bounds__(64 * NB, 2) void gdn_ssm_bwd_kernel(SsmParams p) {
     constexpr int NSA = NS * NB;                     // states of the layout
     __shared__ __align__(16) float bc_all[NB][kTok][2][NS];
-    __shared__ float keep_all[NB][kGradGroups - 1][NS][64];
+    __shared__ float el[5][kTok][64];
+    __shared__ float start[NB][NS][64];
+    enum { kS, kX, kGy, kZs, kSg };                  // step size, x, dy silu(z), dy silu'(z), slope of softplus
     __shared__ float cross[NB > 1 ? NB : 1][NB > 1 ? 3 * kTok : 1][64];
     const int lane = threadIdx.x & 63, blk = NB > 1 ? threadIdx.x >> 6 : 0;
     float(&bc)[kTok][2][NS] = bc_all[blk];
-    float(&keep)[kGradGroups - 1][NS][64] = keep_all[blk];
     const SsmPlace w = ssm_place(p, blockIdx.x, p.nseg, lane);
     const int n0 = blk * NS;
     const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c, zb = w.b * p.zsb + w.c;
     const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
     const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
-    float a[NS], h[NS], g[NS], da[NS], dd = 0.f, dbias = 0.f;
+    float a[NS], g[NS], da[NS], dd = 0.f, dbias = 0.f;
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
         a[n] = n0 + n < p.N ? p.A[(int64_t)w.c * p.N + n0 + n] * kLog2e : 0.f;
-        h[n] = p.sum_e[(w.unit * NSA + n0 + n) * 64 + lane];
         g[n] = p.sum_r[(w.unit * NSA + n0 + n) * 64 + lane];
         da[n] = 0.f;
     }
-    // Bm and C of kTok tokens into the wave's part of LDS
-    auto stage = [&](int t) {
-        constexpr int kEach = kTok * 2 * NS / 64;
+    const int groups = w.t1 > w.t0 ? (w.t1 - w.t0 + kTok - 1) / kTok : 0;
+    for (int k = groups - 1; k >= 0; --k) {
+        const int t = w.t0 + k * kTok;
+        float h[NS];                                 // the state before the group (kept in LDS for its first token)
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int k = lane + 64 * i, n = n0 + k % NS;
-            int tt = t + k / (2 * NS);
+        for (int n = 0; n < NS; ++n) h[n] = p.sum_e[(w.unit * NSA + n0 + n) * 64 + lane];
+        if (k > 0) {
+            const int64_t at = w.unit * (kGradGroups - 1) + k - 1;
+            const float sk = p.keep_s[at * 64 + lane];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                h[n] = fmaf(exp2_hw(sk * a[n]), h[n], p.keep_h[(at * NSA + n0 + n) * 64 + lane]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kTok * 2 * NS / 64; ++i) {
+            const int e = lane + 64 * i, n = n0 + e % NS;
+            int tt = t + e / (2 * NS);
             tt = tt < w.t1 ? tt : w.t1 - 1;
             float v = 0.f;
             if (n < p.N)
-                v = ((k / NS) & 1) ? load_one<BF>(p.C, w.b * p.csb + tt * p.cst + w.g * p.N + n)
+                v = ((e / NS) & 1) ? load_one<BF>(p.C, w.b * p.csb + tt * p.cst + w.g * p.N + n)
                                    : load_one<BF>(p.Bm, w.b * p.bsb + tt * p.bst + w.g * p.N + n);
-            (&bc[0][0][0])[k] = v;
+            (&bc[0][0][0])[e] = v;
         }
-    };
-    const int groups = w.t1 > w.t0 ? (w.t1 - w.t0 + kTok - 1) / kTok : 0;
-    for (int k = 0; k + 1 < groups; ++k) {
-        const int t = w.t0 + k * kTok;      // (a full group: another follows)
-        __syncthreads();
-        stage(t);
-        float s[kTok], u[kTok];
+        // What the tokens' channels need besides the states goes through LDS,
+        // for the registers' sake, and so that each wave computes its share.
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
-            s[i] = ssm_step_size(load_one<BF>(p.dt, db + (t + i) * p.dst) + bias, p.softplus);
-            u[i] = s[i] * load_one<BF>(p.x, xb + (t + i) * p.xst);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kTok; ++i)
-#pragma unroll
-            for (int n = 0; n < NS; ++n) h[n] = fmaf(exp2_hw(s[i] * a[n]), h[n], u[i] * bc[i][0][n]);
-#pragma unroll
-        for (int n = 0; n < NS; ++n) keep[k][n][lane] = h[n];
-    }
-    for (int k = groups - 1; k >= 0; --k) {
-        const int t = w.t0 + k * kTok;
-        __syncthreads();
-        stage(t);
-        if (k > 0) {
-#pragma unroll
-            for (int n = 0; n < NS; ++n) h[n] = keep[k - 1][n][lane];
-        } else {
-#pragma unroll
-            for (int n = 0; n < NS; ++n) h[n] = p.sum_e[(w.unit * NSA + n0 + n) * 64 + lane];
-        }
-        float s[kTok], x[kTok], raw[kTok], gy[kTok], zs[kTok];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
+            if (i % NB != blk) continue;
             const bool in = t + i < w.t1;
             const int tt = in ? t + i : w.t1 - 1;
-            raw[i] = load_one<BF>(p.dt, db + tt * p.dst) + bias;
-            s[i] = in ? ssm_step_size(raw[i], p.softplus) : 0.f;
-            x[i] = in ? load_one<BF>(p.x, xb + tt * p.xst) : 0.f;
+            const float raw = load_one<BF>(p.dt, db + tt * p.dst) + bias;
             const float dy = in ? load_one<BF>(p.dy, yb + (int64_t)tt * p.D) : 0.f;
-            gy[i] = dy;
-            zs[i] = 0.f;
-            if (p.z && in) {
-                float val, slope;
-                silu_both(load_one<BF>(p.z, zb + tt * p.zst), val, slope);
-                gy[i] = dy * val;
-                zs[i] = dy * slope;
-            }
+            float val = 1.f, slope = 0.f;
+            if (p.z) silu_both(load_one<BF>(p.z, zb + tt * p.zst), val, slope);
+            el[kS][i][lane] = in ? ssm_step_size(raw, p.softplus) : 0.f;
+            el[kX][i][lane] = in ? load_one<BF>(p.x, xb + tt * p.xst) : 0.f;
+            el[kGy][i][lane] = in ? dy * val : 0.f;
+            el[kZs][i][lane] = in ? dy * slope : 0.f;
+            el[kSg][i][lane] = p.softplus ? sigmoid(raw) : 1.f;
         }
         __syncthreads();
-        float hs[kTok][NS], y[kTok], du[kTok], ds[kTok];
+        float hs[kTok][NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) start[blk][n][lane] = h[n];
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
-            y[i] = 0.f;
+            const float si = el[kS][i][lane], u = si * el[kX][i][lane];
 #pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                const float hp = i > 0 ? hs[i > 0 ? i - 1 : 0][n] : h[n];
-                hs[i][n] = fmaf(exp2_hw(s[i] * a[n]), hp, s[i] * x[i] * bc[i][0][n]);
-                y[i] = fmaf(hs[i][n], bc[i][1][n], y[i]);
-            }
+            for (int n = 0; n < NS; ++n)
+                hs[i][n] = fmaf(exp2_hw(si * a[n]), i > 0 ? hs[i > 0 ? i - 1 : 0][n] : h[n], u * bc[i][0][n]);
+            pin(hs[i]);
         }
-#pragma unroll
-        for (int i2 = kTok - 2; i2 >= 0; i2 -= 2) {
-            // two tokens' sums over the channels at once: [token][dB | dC][NS]
-            float v[4 * NS];
-#pragma unroll
-            for (int i = i2 + 1; i >= i2; --i) {
-                du[i] = ds[i] = 0.f;
-                const float u = s[i] * x[i];
-#pragma unroll
-                for (int n = 0; n < NS; ++n) {
-                    g[n] = fmaf(bc[i][1][n], gy[i], g[n]);
-                    v[(i - i2) * 2 * NS + n] = w.on ? g[n] * u : 0.f;
-                    v[(i - i2) * 2 * NS + NS + n] = w.on ? gy[i] * hs[i][n] : 0.f;
-                    du[i] = fmaf(g[n], bc[i][0][n], du[i]);
-                    const float hp = i > 0 ? hs[i > 0 ? i - 1 : 0][n] : h[n];
-                    g[n] *= exp2_hw(s[i] * a[n]);
-                    const float q = g[n] * hp;
-                    ds[i] = fmaf(q, a[n], ds[i]);
-                    da[n] = fmaf(q, s[i], da[n]);
+        // the outputs of token i of the lane's channel
+        auto finish = [&](int i, float y, float du, float ds) {
+            if (t + i < w.t1) {
+                const float x = el[kX][i][lane], gy = el[kGy][i][lane];
+                // (a holds A log2(e))
+                const float dr = fmaf(x, du, ds * (1.f / kLog2e)) * el[kSg][i][lane];
+                dbias += dr;
+                dd = fmaf(gy, x, dd);
+                if (w.on) {
+                    const int64_t o = yb + (int64_t)(t + i) * p.D;
+                    store_one<BF>(p.dx, o, fmaf(dskip, gy, el[kS][i][lane] * du));
+                    store_one<BF>(p.ddt, o, dr);
+                    if (p.z) store_one<BF>(p.dz, o, el[kZs][i][lane] * fmaf(dskip, x, y));
                 }
             }
-            const float sum = wave_sums<4 * NS>(v, lane);
-            constexpr int kDup = 64 / (4 * NS) > 0 ? 64 / (4 * NS) : 1;
-            const int idx = lane / kDup, tt = t + i2 + idx / (2 * NS);
-            if (lane % kDup == 0 && tt < w.t1) {
-                const int which = (idx / NS) & 1, n = n0 + idx % NS;
-                p.part_bc[((((int64_t)w.tile * p.B + w.b) * p.T + tt) * 2 + which) * NSA + n] = sum;
+        };
+#pragma unroll
+        for (int i = kTok - 1; i >= 0; --i) {
+            // sums over the channels: the terms of dB in the lower half of the
+            // wave and of dC in the upper after the first step between lanes
+            float v[NS], y = 0.f, du = 0.f, ds = 0.f;
+            const float si = el[kS][i][lane], gy = el[kGy][i][lane], u = si * el[kX][i][lane];
+            const float ul = w.on ? u : 0.f, gl = w.on ? gy : 0.f;
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                const float c = bc[i][1][n];
+                g[n] = fmaf(c, gy, g[n]);
+                v[n] = swap32_add(g[n] * ul, gl * hs[i][n]);
+                y = fmaf(hs[i][n], c, y);
+                du = fmaf(g[n], bc[i][0][n], du);
+                g[n] *= exp2_hw(si * a[n]);
+                const float q = g[n] * (i > 0 ? hs[i > 0 ? i - 1 : 0][n] : start[blk][n][lane]);
+                ds = fmaf(q, a[n], ds);
+                da[n] = fmaf(q, si, da[n]);
+            }
+            pin(g);
+            pin(da);
+            const float sum = row_sums<NS>(v, lane);
+            constexpr int kDup = 32 / NS;
+            if (lane % kDup == 0 && t + i < w.t1)
+                p.part_bc[((((int64_t)w.tile * p.B + w.b) * p.T + t + i) * 2 + lane / 32) * NSA + n0 + lane % 32 / kDup] = sum;
+            if (NB > 1) {
+                cross[blk][i][lane] = y;
+                cross[blk][kTok + i][lane] = du;
+                cross[blk][2 * kTok + i][lane] = ds;
+            } else {
+                finish(i, y, du, ds);
             }
         }
         if (NB > 1) {
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                cross[blk][i][lane] = y[i];
-                cross[blk][kTok + i][lane] = du[i];
-                cross[blk][2 * kTok + i][lane] = ds[i];
-            }
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
-                y[i] = du[i] = ds[i] = 0.f;
+                if (i % NB != blk) continue;
+                float y = 0.f, du = 0.f, ds = 0.f;
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    y[i] += cross[j][i][lane];
-                    du[i] += cross[j][kTok + i][lane];
-                    ds[i] += cross[j][2 * kTok + i][lane];
+                    y += cross[j][i][lane];
+                    du += cross[j][kTok + i][lane];
+                    ds += cross[j][2 * kTok + i][lane];
                 }
-            }
-        }
-        if (NB == 1 || blk == 0) {
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                if (t + i < w.t1) {
-                    // (a holds A log2(e))
-                    float dr = fmaf(x[i], du[i], ds[i] * (1.f / kLog2e));
-                    if (p.softplus) dr *= sigmoid(raw[i]);
-                    dbias += dr;
-                    dd = fmaf(gy[i], x[i], dd);
-                    if (w.on) {
-                        const int64_t o = yb + (int64_t)(t + i) * p.D;
-                        store_one<BF>(p.dx, o, fmaf(dskip, gy[i], s[i] * du[i]));
-                        store_one<BF>(p.ddt, o, dr);
-                        if (p.z && p.dz) store_one<BF>(p.dz, o, zs[i] * fmaf(dskip, x[i], y[i]));
-                    }
-                }
+                finish(i, y, du, ds);
             }
         }
     }
@@ -572,6 +577,18 @@ __global__ __launch_bounds__(64 * NB) void gdn_ssm_bwd_kernel(SsmParams p) {
     const int64_t at = ((int64_t)w.b * p.nseg + w.seg) * tiles + w.tile;
 #pragma unroll
     for (int n = 0; n < NS; ++n) p.part_a[(at * NSA + n0 + n) * 64 + lane] = da[n];
+    if (NB > 1) {                                    // (each wave finished some of the tokens)
+        __syncthreads();
+        cross[blk][0][lane] = dd;
+        cross[blk][1][lane] = dbias;
+        __syncthreads();
+        dd = dbias = 0.f;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            dd += cross[j][0][lane];
+            dbias += cross[j][1][lane];
+        }
+    }
     if (NB == 1 || blk == 0) {
         p.part_d[(at * 2) * 64 + lane] = dd;
         p.part_d[(at * 2 + 1) * 64 + lane] = dbias;
@@ -580,7 +597,7 @@ __global__ __launch_bounds__(64 * NB) void gdn_ssm_bwd_kernel(SsmParams p) {
                 const int64_t o = yb + (int64_t)t * p.D;
                 store_one<BF>(p.dx, o, 0.f);
                 store_one<BF>(p.ddt, o, 0.f);
-                if (p.z && p.dz) store_one<BF>(p.dz, o, 0.f);
+                if (p.z) store_one<BF>(p.dz, o, 0.f);
             }
         }
     }
