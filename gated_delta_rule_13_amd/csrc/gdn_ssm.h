@@ -444,7 +444,7 @@ __global__ __launch_bounds__(64 * NB, 2) void gdn_ssm_bwd_kernel(SsmParams p) {
     float(&bc)[kTok][2][NS] = bc_all[blk];
     const SsmPlace w = ssm_place(p, blockIdx.x, p.nseg, lane);
     const int n0 = blk * NS;
-    const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c, zb = w.b * p.zsb + w.c;
+    const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c;
     const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
     const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
     float a[NS], g[NS], da[NS], dd = 0.f, dbias = 0.f;
@@ -454,6 +454,9 @@ __global__ __launch_bounds__(64 * NB, 2) void gdn_ssm_bwd_kernel(SsmParams p) {
         g[n] = p.sum_r[(w.unit * NSA + n0 + n) * 64 + lane];
         da[n] = 0.f;
     }
+    // (without a gate z's loads read dy instead, and are not used)
+    const void* zsrc = p.z ? p.z : p.dy;
+    const int64_t zb = p.z ? w.b * p.zsb + w.c : yb, zst = p.z ? p.zst : p.D;
     const int groups = w.t1 > w.t0 ? (w.t1 - w.t0 + kTok - 1) / kTok : 0;
     for (int k = groups - 1; k >= 0; --k) {
         const int t = w.t0 + k * kTok;
@@ -480,21 +483,31 @@ __global__ __launch_bounds__(64 * NB, 2) void gdn_ssm_bwd_kernel(SsmParams p) {
             (&bc[0][0][0])[e] = v;
         }
         // What the tokens' channels need besides the states goes through LDS,
-        // for the registers' sake, and so that each wave computes its share.
+        // for the registers' sake, and so that each wave computes its share
+        // of the tokens.
+        constexpr int kMine = kTok / NB;
+        Raw<BF, 1> rx[kMine], rd[kMine], rg[kMine], rz[kMine];
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            if (i % NB != blk) continue;
+        for (int j = 0; j < kMine; ++j) {
+            const int tt = t + j * NB + blk < w.t1 ? t + j * NB + blk : w.t1 - 1;
+            rx[j].load(p.x, xb + tt * p.xst);
+            rd[j].load(p.dt, db + tt * p.dst);
+            rg[j].load(p.dy, yb + (int64_t)tt * p.D);
+            rz[j].load(zsrc, zb + tt * zst);
+        }
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+            const int i = j * NB + blk;
             const bool in = t + i < w.t1;
-            const int tt = in ? t + i : w.t1 - 1;
-            const float raw = load_one<BF>(p.dt, db + tt * p.dst) + bias;
-            const float dy = in ? load_one<BF>(p.dy, yb + (int64_t)tt * p.D) : 0.f;
-            float val = 1.f, slope = 0.f;
-            if (p.z) silu_both(load_one<BF>(p.z, zb + tt * p.zst), val, slope);
-            el[kS][i][lane] = in ? ssm_step_size(raw, p.softplus) : 0.f;
-            el[kX][i][lane] = in ? load_one<BF>(p.x, xb + tt * p.xst) : 0.f;
-            el[kGy][i][lane] = in ? dy * val : 0.f;
+            const float raw = rd[j].get(0) + bias, dy = rg[j].get(0);
+            const float soft = softplus(raw), slope_soft = sigmoid(raw);
+            float val, slope;
+            silu_both(rz[j].get(0), val, slope);
+            el[kS][i][lane] = in ? (p.softplus ? soft : raw) : 0.f;
+            el[kX][i][lane] = in ? rx[j].get(0) : 0.f;
+            el[kGy][i][lane] = in ? (p.z ? dy * val : dy) : 0.f;
             el[kZs][i][lane] = in ? dy * slope : 0.f;
-            el[kSg][i][lane] = p.softplus ? sigmoid(raw) : 1.f;
+            el[kSg][i][lane] = p.softplus ? slope_soft : 1.f;
         }
         __syncthreads();
         float hs[kTok][NS];
