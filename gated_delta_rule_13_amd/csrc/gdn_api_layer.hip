@@ -44,6 +44,14 @@ bool rows16(const void* p, int dtype, std::initializer_list<int64_t> strides) {
         if (s % (dtype == GDN_BF16 ? 8 : 4) != 0) return false;
     return true;
 }
+// 16-byte pieces of fp32 rows and 8-byte ones of bf16 rows: four numbers.
+bool rows4(const void* p, int dtype, std::initializer_list<int64_t> strides) {
+    if (!p) return true;
+    if (!aligned(p, dtype == GDN_BF16 ? 8 : 16)) return false;
+    for (int64_t s : strides)
+        if (s % 4 != 0) return false;
+    return true;
+}
 gdn_status check_workspace(const void* ws, size_t given, size_t need, const char* query) {
     if (need == 0) return GDN_OK;
     if (!ws || given < need) return set_error(GDN_ERR_WORKSPACE, std::string("workspace smaller than ") + query);
@@ -81,7 +89,7 @@ int conv_fwd_tile(const gdn_conv_shape& s) { return conv_rows(s, 131072); }
 int conv_bwd_tile(const gdn_conv_shape& s) { return conv_rows(s, 65536) - (s.W - 1); }
 
 gdn::ConvParams conv_params(const gdn_conv_shape& s, const void* x, const float* w, const float* bias, const void* s0,
-                            const int32_t* lens, int tile, bool wide) {
+                            const int32_t* lens, int tile, int vec) {
     gdn::ConvParams p{};
     p.x = x;
     p.w = w;
@@ -94,7 +102,7 @@ gdn::ConvParams conv_params(const gdn_conv_shape& s, const void* x, const float*
     p.T = s.T;
     p.D = s.D;
     p.hd = s.D / s.H;
-    p.nv = wide ? s.D / (s.dtype == GDN_BF16 ? 8 : 4) : s.D;
+    p.nv = s.D / vec;
     p.tile = tile;
     p.ntile = (int)ceil_div(s.T, tile);
     p.silu = s.silu;
@@ -110,7 +118,8 @@ gdn_status conv_forward(const gdn_conv_shape* s, const void* x, const float* wei
     const int64_t hd = s->D / s->H;
     const bool wide = rows16(x, s->dtype, {s->x_stride_b, s->x_stride_t, hd}) && rows16(y, s->dtype, {hd}) &&
                       rows16(state0, s->dtype, {hd}) && rows16(state_out, s->dtype, {hd});
-    gdn::ConvParams p = conv_params(*s, x, weight, bias, state0, lens, conv_fwd_tile(*s), wide);
+    gdn::ConvParams p = conv_params(*s, x, weight, bias, state0, lens, conv_fwd_tile(*s),
+                                    !wide ? 1 : s->dtype == GDN_BF16 ? 8 : 4);
     p.y = y;
     p.s1 = state_out;
     if ((int64_t)p.B * p.ntile * p.nv > kMaxGrid) return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
@@ -271,14 +280,6 @@ gdn::NormParams norm_params(const gdn_norm_shape& s, const void* x, const float*
     p.eps = s.eps;
     return p;
 }
-// 16-byte pieces of fp32 rows and 8-byte ones of bf16 rows: four numbers.
-bool rows4(const void* p, int dtype, std::initializer_list<int64_t> strides) {
-    if (!p) return true;
-    if (!aligned(p, dtype == GDN_BF16 ? 8 : 16)) return false;
-    for (int64_t s : strides)
-        if (s % 4 != 0) return false;
-    return true;
-}
 // Workgroups that share a head's rows in the gradient, at most: eight
 // workgroups for each of the chip's 256 compute units over all heads.
 int64_t norm_bwd_blocks(const gdn_norm_shape& s) {
@@ -330,11 +331,11 @@ gdn_status gdn_conv_bwd(const gdn_conv_shape* s, const void* dy, const void* x, 
     st = check_workspace(workspace, workspace_bytes, gdn_conv_bwd_workspace_bytes(s), "gdn_conv_bwd_workspace_bytes");
     if (st != GDN_OK) return st;
     const int64_t hd = s->D / s->H;
-    const bool wide = rows16(x, s->dtype, {s->x_stride_b, s->x_stride_t, hd}) && rows16(dy, s->dtype, {hd}) &&
-                      rows16(dx, s->dtype, {hd}) && rows16(state0, s->dtype, {hd}) &&
-                      rows16(dstate_out, s->dtype, {hd}) && rows16(dstate0, s->dtype, {hd});
+    const bool wide = rows4(x, s->dtype, {s->x_stride_b, s->x_stride_t, hd}) && rows4(dy, s->dtype, {hd}) &&
+                      rows4(dx, s->dtype, {hd}) && rows4(state0, s->dtype, {hd}) &&
+                      rows4(dstate_out, s->dtype, {hd}) && rows4(dstate0, s->dtype, {hd});
     gdn::ConvBwdParams q{};
-    q.f = conv_params(*s, x, weight, bias, state0, lens, conv_bwd_tile(*s), wide);
+    q.f = conv_params(*s, x, weight, bias, state0, lens, conv_bwd_tile(*s), wide ? gdn::kConvBwdV : 1);
     q.dy = dy;
     q.ds1 = dstate_out;
     q.dx = dx;

@@ -153,6 +153,7 @@ struct ConvBwdParams {
     float* part;            // [rows of workgroups][D * W + D]
 };
 
+constexpr int kConvBwdV = 4;                                 // channels per thread (wide)
 constexpr int kConvBwdCv = 32;                               // vectors per workgroup
 constexpr int kConvBwdTiles = kConvThreads / kConvBwdCv;     // tiles per workgroup
 
@@ -201,6 +202,12 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
                 nx[i].load(p.x, b * p.sb + tt * p.st + c);
                 ng[i].load(q.dy, dy0 + (int64_t)tt * p.hd);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kConvRows; ++i) {
+                nx[i].zero();
+                ng[i].zero();
+            }
         }
         // dx rows t - W + 1 .. t - W + kConvRows follow from the dp up to t + kConvRows - 1
         for (int t = t0; t < tz + W - 1; t += kConvRows) {
@@ -220,32 +227,25 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
             }
 #pragma unroll
             for (int i = 0; i < kConvRows; ++i) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) dp[W - 1 + i][v] = 0.f;
-                if (t + i < t2) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float a = wt.b[v];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) a = fmaf(wt.w[j][v], win[i + j].get(v), a);
-                        float val, d = g[i].get(v);
-                        if (p.silu) {
-                            float slope;
-                            silu_both(a, val, slope);
-                            d *= slope;
-                        }
-                        dp[W - 1 + i][v] = d;
-                        if (t + i < t1) {
-#pragma unroll
-                            for (int j = 0; j < W; ++j) acc[j][v] = fmaf(d, win[i + j].get(v), acc[j][v]);
-                            acc[W][v] += d;
-                        }
-                    }
-                }
                 const int td = t + i - (W - 1);
+                // (rows behind t2 repeat the last one: their dp is 0)
+                const bool live = t + i < t2, mine = t + i < t1;
                 float f[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
+                    float d = g[i].get(v);
+                    if (p.silu) {
+                        float a = wt.b[v], val, slope;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) a = fmaf(wt.w[j][v], win[i + j].get(v), a);
+                        silu_both(a, val, slope);
+                        d *= slope;
+                    }
+                    dp[W - 1 + i][v] = live ? d : 0.f;
+                    const float own = mine ? d : 0.f;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) acc[j][v] = fmaf(own, win[i + j].get(v), acc[j][v]);
+                    acc[W][v] += own;
                     f[v] = 0.f;
 #pragma unroll
                     for (int j = 0; j < W; ++j) f[v] = fmaf(wt.w[j][v], dp[i + W - 1 - j][v], f[v]);

@@ -19,16 +19,16 @@ void bwd(const ConvBwdParams& q, hipStream_t st) {
 }
 }  // namespace
 
-#define GDN_CONV_PICK(FN)                                                 \
-    switch (W) {                                                          \
-        case 2: return bf ? (wide ? FN<true, 2, 8> : FN<true, 2, 1>) : (wide ? FN<false, 2, 4> : FN<false, 2, 1>); \
-        case 3: return bf ? (wide ? FN<true, 3, 8> : FN<true, 3, 1>) : (wide ? FN<false, 3, 4> : FN<false, 3, 1>); \
-        case 4: return bf ? (wide ? FN<true, 4, 8> : FN<true, 4, 1>) : (wide ? FN<false, 4, 4> : FN<false, 4, 1>); \
-    }                                                                     \
+#define GDN_CONV_PICK(FN, VB, VF)                                                                                  \
+    switch (W) {                                                                                                   \
+        case 2: return bf ? (wide ? FN<true, 2, VB> : FN<true, 2, 1>) : (wide ? FN<false, 2, VF> : FN<false, 2, 1>); \
+        case 3: return bf ? (wide ? FN<true, 3, VB> : FN<true, 3, 1>) : (wide ? FN<false, 3, VF> : FN<false, 3, 1>); \
+        case 4: return bf ? (wide ? FN<true, 4, VB> : FN<true, 4, 1>) : (wide ? FN<false, 4, VF> : FN<false, 4, 1>); \
+    }                                                                                                              \
     return nullptr;
 
-ConvLauncher conv_launcher(bool bf, int W, bool wide) { GDN_CONV_PICK(fwd) }
-ConvBwdLauncher conv_bwd_launcher(bool bf, int W, bool wide) { GDN_CONV_PICK(bwd) }
+ConvLauncher conv_launcher(bool bf, int W, bool wide) { GDN_CONV_PICK(fwd, 8, 4) }
+ConvBwdLauncher conv_bwd_launcher(bool bf, int W, bool wide) { GDN_CONV_PICK(bwd, kConvBwdV, kConvBwdV) }
 #undef GDN_CONV_PICK
 
 int64_t conv_bwd_part_rows(int64_t row_tiles) { return (row_tiles + kConvBwdTiles - 1) / kConvBwdTiles; }

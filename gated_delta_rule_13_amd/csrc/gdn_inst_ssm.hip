@@ -68,7 +68,7 @@ void GDN_SSM_NAME(ssm_bwd_run)(const SsmParams& p, float* dA, void* dBm, void* d
     switch (ssm_states(p.N)) {
         case 4: return bwd<4, 1>(p, dA, dBm, dC, dD, dbias, st);
         case 8: return bwd<8, 1>(p, dA, dBm, dC, dD, dbias, st);
-        case 16: return bwd<8, 2>(p, dA, dBm, dC, dD, dbias, st);
+        case 16: return bwd<4, 4>(p, dA, dBm, dC, dD, dbias, st);
         case 32: return bwd<8, 4>(p, dA, dBm, dC, dD, dbias, st);
         default: return bwd<8, 8>(p, dA, dBm, dC, dD, dbias, st);
     }
