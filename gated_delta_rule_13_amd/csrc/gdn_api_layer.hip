@@ -73,7 +73,10 @@ gdn_status validate(const gdn_conv_shape* s) {
     if (s->W < 2 || s->W > 4) return set_error(GDN_ERR_UNSUPPORTED, "W must be 2, 3 or 4");
     if (s->silu != 0 && s->silu != 1) return set_error(GDN_ERR_UNSUPPORTED, "silu must be 0 or 1");
     if (s->x_stride_b < 0 || s->x_stride_t < 0) return set_error(GDN_ERR_BAD_SHAPE, "strides must be >= 0");
-    return check_counts(s->B, s->T, s->D);
+    const gdn_status st = check_counts(s->B, s->T, s->D);
+    if (st != GDN_OK) return st;
+    if (s->D > (1 << 29)) return set_error(GDN_ERR_UNSUPPORTED, "D must be at most 2^29");
+    return GDN_OK;
 }
 
 // Rows per thread: long tiles read the W - 1 rows before them less often, but
@@ -86,7 +89,7 @@ int conv_rows(const gdn_conv_shape& s, int64_t threads) {
     return rows;
 }
 int conv_fwd_tile(const gdn_conv_shape& s) { return conv_rows(s, 131072); }
-int conv_bwd_tile(const gdn_conv_shape& s) { return conv_rows(s, 65536) - (s.W - 1); }
+int conv_bwd_tile(const gdn_conv_shape& s) { return conv_rows(s, 200000) - (s.W - 1); }
 
 gdn::ConvParams conv_params(const gdn_conv_shape& s, const void* x, const float* w, const float* bias, const void* s0,
                             const int32_t* lens, int tile, int vec) {
@@ -331,7 +334,8 @@ gdn_status gdn_conv_bwd(const gdn_conv_shape* s, const void* dy, const void* x, 
     st = check_workspace(workspace, workspace_bytes, gdn_conv_bwd_workspace_bytes(s), "gdn_conv_bwd_workspace_bytes");
     if (st != GDN_OK) return st;
     const int64_t hd = s->D / s->H;
-    const bool wide = rows4(x, s->dtype, {s->x_stride_b, s->x_stride_t, hd}) && rows4(dy, s->dtype, {hd}) &&
+    // (under 256 channels pieces of four would leave lanes of the wave idle)
+    const bool wide = s->D >= 256 && rows4(x, s->dtype, {s->x_stride_b, s->x_stride_t, hd}) && rows4(dy, s->dtype, {hd}) &&
                       rows4(dx, s->dtype, {hd}) && rows4(state0, s->dtype, {hd}) &&
                       rows4(dstate_out, s->dtype, {hd}) && rows4(dstate0, s->dtype, {hd});
     gdn::ConvBwdParams q{};
@@ -342,7 +346,7 @@ gdn_status gdn_conv_bwd(const gdn_conv_shape* s, const void* dy, const void* x, 
     q.ds0 = dstate0;
     q.part = static_cast<float*>(workspace);
     const int64_t rows = gdn::conv_bwd_part_rows((int64_t)q.f.B * q.f.ntile);
-    if ((long double)rows * (ceil_div(q.f.nv, gdn::kConvBwdCv)) > kMaxGrid)
+    if ((long double)rows * ceil_div(q.f.nv, 64) > kMaxGrid || (int64_t)q.f.B * q.f.ntile > kMaxGrid)
         return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     gdn::conv_bwd_launcher(s->dtype == GDN_BF16, s->W, wide)(q, hs);

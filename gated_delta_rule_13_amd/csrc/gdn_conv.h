@@ -29,7 +29,7 @@ struct ConvParams {
 };
 
 constexpr int kConvThreads = 256;
-constexpr int kConvRows = 8;
+constexpr int kConvRows = 4;
 
 // weights of V neighbouring channels
 template <int W, int V>
@@ -139,8 +139,8 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_fwd_kernel(ConvParams p
 // Gradient.  With dp_t = dy_t silu'(p_t) (zero outside the sequence):
 //     dx_t = sum_j w_j dp_{t+W-1-j}   (t < 0: the initial state's rows)
 //     dw_j = sum_t dp_t x_{t-W+1+j},  dbias = sum_t dp_t
-// A thread takes V channels down `tile` rows and W-1 more, whose dp its last
-// rows need (computed again by the next tile's thread).  x and dy are read
+// A wave takes 64 V channels down `tile` rows and W-1 more, whose dp its last
+// rows need (computed again by the next tile's wave).  x and dy are read
 // once and dx written once, which bounds it.  The sums over rows stay in
 // registers, are added over the workgroup's tiles in LDS, and written as one
 // row of partial sums for each workgroup.
@@ -153,19 +153,18 @@ struct ConvBwdParams {
     float* part;            // [rows of workgroups][D * W + D]
 };
 
-constexpr int kConvBwdV = 4;                                 // channels per thread (wide)
-constexpr int kConvBwdCv = 32;                               // vectors per workgroup
-constexpr int kConvBwdTiles = kConvThreads / kConvBwdCv;     // tiles per workgroup
+constexpr int kConvBwdV = 2;                                 // channels per thread (wide)
+constexpr int kConvBwdTiles = kConvThreads / 64;             // tiles per workgroup, one for each wave
 
 template <bool BF, int W, int V>
 __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParams q) {
     const ConvParams& p = q.f;
-    __shared__ float red[kConvBwdTiles][kConvBwdCv][(W + 1) * V + 1];
-    const int ncb = (p.nv + kConvBwdCv - 1) / kConvBwdCv;
-    const int cvl = threadIdx.x % kConvBwdCv, tl = threadIdx.x / kConvBwdCv;
-    const int cv = (int)(blockIdx.x % (unsigned)ncb) * kConvBwdCv + cvl;
-    const int64_t row_tile = (int64_t)(blockIdx.x / (unsigned)ncb) * kConvBwdTiles + tl;
-    const bool on = cv < p.nv && row_tile < (int64_t)p.B * p.ntile;
+    constexpr uint32_t E = BF ? 2 : 4;
+    __shared__ float red[kConvBwdTiles][64][(W + 1) * V + 1];
+    const int ncb = (p.nv + 63) / 64;
+    const int lane = threadIdx.x & 63, tl = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c0 = (int)(blockIdx.x % (unsigned)ncb) * 64 * V, c = c0 + lane * V;
+    const int row_tile = (int)(blockIdx.x / (unsigned)ncb) * kConvBwdTiles + tl;
 
     float acc[W + 1][V];
 #pragma unroll
@@ -173,10 +172,9 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
 
-    if (on) {
-        const int c = cv * V;
-        const int b = (int)(row_tile / p.ntile);
-        const int t0 = (int)(row_tile % p.ntile) * p.tile;
+    if (c < p.D && row_tile < p.B * p.ntile) {
+        const int b = row_tile / p.ntile;
+        const int t0 = row_tile % p.ntile * p.tile;
         const int n = seq_len(p.lens, b, p.T);
         const int tz = t0 + p.tile < p.T ? t0 + p.tile : p.T;   // dx rows [t0, tz)
         const int t1 = tz < n ? tz : n;                         // tokens of its own
@@ -184,7 +182,14 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
         ConvWeights<W, V> wt;
         wt.load(p.w, p.bias, c);
         const int head = c / p.hd;
-        const int64_t dy0 = ((int64_t)b * (p.D / p.hd) + head) * p.T * p.hd + (c - head * p.hd);
+        const uint32_t off = (uint32_t)c * E;                   // (rows of 2 GiB are refused)
+        const char* xr = row_at<BF>(p.x, b * p.sb);
+        const int64_t xs = p.st * E;
+        // dy: the lane's head starts p.T * p.hd elements after the one before
+        const char* gr = row_at<BF>(q.dy, (int64_t)b * p.T * p.D);
+        const int64_t goff = ((int64_t)head * p.T * p.hd + (c - head * p.hd)) * E;
+        char* dr = row_at<BF>(q.dx, (int64_t)b * p.T * p.D);
+        const int64_t gs = (int64_t)p.hd * E, ds = (int64_t)p.D * E;
 
         Raw<BF, V> win[W - 1 + kConvRows], nx[kConvRows], ng[kConvRows];
         float dp[W - 1 + kConvRows][V];
@@ -195,16 +200,13 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
 #pragma unroll
             for (int v = 0; v < V; ++v) dp[i][v] = 0.f;
         }
-        if (t0 < t2) {
 #pragma unroll
-            for (int i = 0; i < kConvRows; ++i) {
+        for (int i = 0; i < kConvRows; ++i) {
+            if (t0 < t2) {
                 const int tt = t0 + i < t2 ? t0 + i : t2 - 1;
-                nx[i].load(p.x, b * p.sb + tt * p.st + c);
-                ng[i].load(q.dy, dy0 + (int64_t)tt * p.hd);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kConvRows; ++i) {
+                nx[i].load_at(xr + tt * xs, off);
+                ng[i].load(gr + tt * gs + goff, 0);
+            } else {
                 nx[i].zero();
                 ng[i].zero();
             }
@@ -221,8 +223,8 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
 #pragma unroll
                 for (int i = 0; i < kConvRows; ++i) {
                     const int tt = t + kConvRows + i < t2 ? t + kConvRows + i : t2 - 1;
-                    nx[i].load(p.x, b * p.sb + tt * p.st + c);
-                    ng[i].load(q.dy, dy0 + (int64_t)tt * p.hd);
+                    nx[i].load_at(xr + tt * xs, off);
+                    ng[i].load(gr + tt * gs + goff, 0);
                 }
             }
 #pragma unroll
@@ -260,7 +262,7 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
 #pragma unroll
                         for (int v = 0; v < V; ++v) f[v] += e.get(v);
                     }
-                    if (!state_row) store_vec<BF, V>(q.dx, ((int64_t)b * p.T + td) * p.D + c, f);
+                    if (!state_row) store_at<BF, V>(dr + td * ds, off, f);
                     else if (q.ds0) store_vec<BF, V>(q.ds0, ((int64_t)b * (W - 1) + td + W - 1) * p.D + c, f);
                 }
             }
@@ -276,11 +278,10 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int j = 0; j <= W; ++j) red[tl][cvl][v * (W + 1) + j] = acc[j][v];
+        for (int j = 0; j <= W; ++j) red[tl][lane][v * (W + 1) + j] = acc[j][v];
     __syncthreads();
     float* out = q.part + (int64_t)(blockIdx.x / (unsigned)ncb) * p.D * (W + 1);
-    const int c0 = (int)(blockIdx.x % (unsigned)ncb) * kConvBwdCv * V;
-    for (int i = threadIdx.x; i < kConvBwdCv * V * (W + 1); i += kConvThreads) {
+    for (int i = threadIdx.x; i < 64 * V * (W + 1); i += kConvThreads) {
         const int ch = i / (W + 1), j = i % (W + 1);
         if (c0 + ch < p.D) {
             float t = 0.f;

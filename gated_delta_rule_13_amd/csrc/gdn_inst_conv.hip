@@ -13,7 +13,7 @@ void fwd(const ConvParams& p, hipStream_t st) {
 }
 template <bool BF, int W, int V>
 void bwd(const ConvBwdParams& q, hipStream_t st) {
-    const int64_t ncb = (q.f.nv + kConvBwdCv - 1) / kConvBwdCv;
+    const int64_t ncb = (q.f.nv + 63) / 64;
     const int64_t rows = ((int64_t)q.f.B * q.f.ntile + kConvBwdTiles - 1) / kConvBwdTiles;
     hipLaunchKernelGGL((gdn_conv_bwd_kernel<BF, W, V>), dim3((unsigned)(ncb * rows)), dim3(kConvThreads), 0, st, q);
 }

@@ -32,6 +32,11 @@ struct Raw {
             }
         }
     }
+    // the elements at byte `off` of a row that the whole wave shares (its
+    // address stays in scalar registers, and so does all arithmetic on it)
+    __device__ __forceinline__ void load_at(const void* row, uint32_t off) {
+        load(reinterpret_cast<const char*>(row) + off, 0);
+    }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (!BF) return __builtin_bit_cast(float, w[i]);
         return __builtin_bit_cast(float, (i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
@@ -55,6 +60,20 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&f)[V
     }
 }
 
+template <bool BF, int V>
+__device__ __forceinline__ void store_at(void* row, uint32_t off, const float (&f)[V]) {
+    store_vec<BF, V>(reinterpret_cast<char*>(row) + off, 0, f);
+}
+// Element i of a tensor as the address of a row.
+template <bool BF>
+__device__ __forceinline__ const char* row_at(const void* p, int64_t i) {
+    return reinterpret_cast<const char*>(p) + i * (BF ? 2 : 4);
+}
+template <bool BF>
+__device__ __forceinline__ char* row_at(void* p, int64_t i) {
+    return reinterpret_cast<char*>(p) + i * (BF ? 2 : 4);
+}
+
 template <bool BF>
 __device__ __forceinline__ float load_one(const void* p, int64_t i) {
     if constexpr (BF) return (float)reinterpret_cast<const __bf16*>(p)[i];
@@ -73,40 +92,61 @@ __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(
 // 1 / (1 + e^-x); e^-x overflows to infinity for x < -88.7, whose reciprocal
 // is the right 0.
 __device__ __forceinline__ float sigmoid(float x) { return rcp_hw(1.f + exp2_hw(-kLog2e * x)); }
-// x sigmoid(x).  At x = -infinity the limit 0 (the product would be NaN).
-__device__ __forceinline__ float silu(float x) {
-    return x == -__builtin_inff() ? 0.f : x * sigmoid(x);
-}
+// x sigmoid(x).  The bound keeps -infinity times 0 from being NaN; a NaN comes
+// through sigmoid.
+__device__ __forceinline__ float silu(float x) { return __builtin_fmaxf(x, -__FLT_MAX__) * sigmoid(x); }
 // silu(x) and silu'(x) = s + x s (1 - s), s = sigmoid(x), from e = e^-|x| and
 // r = 1 / (1 + e): s is r or e r by x's sign, and s (1 - s) = e r^2 either way,
 // with no cancellation.  At the infinities the limits (0 or x, 0 or 1).
 __device__ __forceinline__ void silu_both(float x, float& val, float& slope) {
     const float e = exp2_hw(-kLog2e * __builtin_fabsf(x));
-    const float r = rcp_hw(1.f + e);
-    const float s = x < 0.f ? e * r : r;
-    const bool inf = __builtin_isinf(x);
-    val = inf && x < 0.f ? 0.f : x * s;
-    slope = inf ? s : fmaf(x, e * r * r, s);
+    const float r = rcp_hw(1.f + e), er = e * r;
+    const float s = x < 0.f ? er : r;
+    val = __builtin_fmaxf(x, -__FLT_MAX__) * s;
+    slope = fmaf(__builtin_amdgcn_fmed3f(x, -__FLT_MAX__, __FLT_MAX__), er * r, s);
 }
-// ln(1 + e^x) = max(x, 0) + ln(1 + e), e = e^-|x| <= 1, and
-// ln(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3: the odd series in s to
-// s^17 leaves 2 (1/3)^19 / 19 (1 - 1/9) < 1e-10 of the sum, and keeps the
-// relative accuracy of small results (1 + e rounded first would not: steps of
-// 1e-3 would be off by 6e-5).
+// ln(1 + e^x) = max(x, 0) + ln(1 + e), e = e^-|x| <= 1.  With w = 1 + e as it
+// was rounded and d = e - (w - 1) what that lost (exact), ln(1 + e) is ln(w) +
+// d / w, and d / w is d to 2^-24 of the sum: small results keep their relative
+// accuracy (ln(w) alone would leave steps of 1e-3 off by 6e-5).  v_log_f32 is
+// accurate to its last bit near 1 too (measured: 1.9 x 2^-24 at most from 1 to
+// 2), and the whole to the rounding of the exponent, 2^-24 |x| log2(e).
 __device__ __forceinline__ float softplus(float x) {
     const float e = exp2_hw(-kLog2e * __builtin_fabsf(x));
-    const float s = e * rcp_hw(2.f + e);
-    const float q = s * s;
-    float r = 1.f / 17.f;
-    r = fmaf(r, q, 1.f / 15.f);
-    r = fmaf(r, q, 1.f / 13.f);
-    r = fmaf(r, q, 1.f / 11.f);
-    r = fmaf(r, q, 1.f / 9.f);
-    r = fmaf(r, q, 1.f / 7.f);
-    r = fmaf(r, q, 1.f / 5.f);
-    r = fmaf(r, q, 1.f / 3.f);
-    r = fmaf(r, q, 1.f);
-    return __builtin_fmaxf(x, 0.f) + 2.f * s * r;
+    const float w = 1.f + e, d = e - (w - 1.f);
+    return __builtin_fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(w), 1.f / kLog2e, d);
+}
+
+// Moves and sums between lanes without LDS: DPP within a row of 16 lanes, and
+// the lane-row swaps, which exchange halves of two registers in one
+// instruction.  swap32_add(a, b) leaves a's sum over lane and lane ^ 32 in the
+// lower 32 lanes and b's in the upper; swap16_add the same of lane ^ 16.
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float swap32_add(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t r0 = r[0], r1 = r[1];     // (a bit cast of a vector's element takes element 0)
+    return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ float swap16_add(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t r0 = r[0], r1 = r[1];     // (a bit cast of a vector's element takes element 0)
+    return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+}
+// Sum over aligned groups of L lanes, in every lane (partners: lane ^ 1, lane ^
+// 2, the half row mirrored, the row mirrored, then the other rows).
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+    static_assert(L == 8 || L == 16 || L == 32 || L == 64, "");
+    v += dpp_move<0xB1>(v);
+    v += dpp_move<0x4E>(v);
+    v += dpp_move<0x141>(v);
+    if constexpr (L >= 16) v += dpp_move<0x140>(v);
+    if constexpr (L >= 32) v = swap16_add(v, v);
+    if constexpr (L >= 64) v = swap32_add(v, v);
+    return v;
 }
 
 // The length of sequence b.

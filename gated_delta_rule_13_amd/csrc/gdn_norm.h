@@ -47,14 +47,6 @@ struct NormBwdParams {
 
 constexpr int kNormThreads = 256;
 
-// Sum over aligned groups of L lanes, in every lane.
-template <int L>
-__device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-    for (int m = 1; m < L; m *= 2) v += __shfl_xor(v, m, 64);
-    return v;
-}
-
 __device__ __forceinline__ void act_both(float x, int act, float& val, float& slope) {
     if (act) {
         silu_both(x, val, slope);

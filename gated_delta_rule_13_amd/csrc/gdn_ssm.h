@@ -374,25 +374,8 @@ __global__ __launch_bounds__(kChainThreads) void gdn_ssm_chain_kernel(SsmParams 
 // ---------------------------------------------------------------------------
 // Sums over the lanes of many registers at once: each step between lanes
 // halves the registers, a lane keeping the half that its own number selects,
-// while there is more than one; then plain sums.  The steps between rows of 16
-// lanes are the lane-row swaps, which exchange halves of two registers in one
-// instruction: swap32_add(a, b) leaves a's sum over lane and lane ^ 32 in the
-// lower 32 lanes and b's in the upper, and row_sums of R registers leaves value
-// (lane % 32) / (32 / R) summed over the 32 lanes of each half.
-template <int CTRL>
-__device__ __forceinline__ float dpp_move(float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float swap32_add(float a, float b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
-    const uint32_t r0 = r[0], r1 = r[1];     // (a bit cast of a vector's element takes element 0)
-    return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
-}
-__device__ __forceinline__ float swap16_add(float a, float b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
-    const uint32_t r0 = r[0], r1 = r[1];     // (a bit cast of a vector's element takes element 0)
-    return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
-}
+// while there is more than one; then plain sums.  row_sums of R registers
+// leaves value (lane % 32) / (32 / R) summed over the 32 lanes of each half.
 // lanes whose `hi` is set keep b's sum with their partner, the others a's
 template <int CTRL>
 __device__ __forceinline__ float dpp_pair_add(float a, float b, bool hi) {
