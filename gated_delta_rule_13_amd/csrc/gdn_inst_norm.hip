@@ -5,11 +5,16 @@
 
 namespace gdn {
 namespace {
+// About four waves for each of the chip's 1024 vector units, all resident
+// (measured at 4 x 4096 x 16 x 128, fp32 to bf16: 55 us; 8192 waves 60, 2048
+// 58, one wave for every eight rows without the next row in flight 70).
+constexpr int64_t kNormWaves = 4096;
 template <bool XB, bool OB, int L, int K>
 void fwd(const NormParams& p, hipStream_t st) {
-    const int64_t per = kNormThreads / L;
-    hipLaunchKernelGGL((gdn_norm_fwd_kernel<XB, OB, L, K>), dim3((unsigned)((p.rows + per - 1) / per)),
-                       dim3(kNormThreads), 0, st, p);
+    const int64_t per = kNormThreads / L, bts = p.rows / p.G, most = (kNormWaves * (64 / L) + p.G - 1) / p.G;
+    const int64_t tokens = bts < most ? bts : most;
+    hipLaunchKernelGGL((gdn_norm_fwd_kernel<XB, OB, L, K>), dim3((unsigned)((tokens * p.G + per - 1) / per)),
+                       dim3(kNormThreads), 0, st, p, tokens);
 }
 template <bool XB, bool OB>
 void fwd_plain(const NormParams& p, hipStream_t st) {
@@ -65,7 +70,6 @@ void norm_bwd_sum(const NormBwdParams& q, int nblk, float* dweight, float* dbias
     const NormParams& p = q.f;
     const int64_t rows = p.per_group ? nblk : (int64_t)nblk * p.G;
     const int64_t cols = p.per_group ? (int64_t)p.G * p.d : p.d;
-    if (dweight) launch_colsum(q.part, rows, dweight, cols, nullptr, 0, st);
-    if (dbias) launch_colsum(q.part + q.part_b, rows, dbias, cols, nullptr, 0, st);
+    if (dweight || dbias) launch_colsum(q.part, rows, dweight, cols, dbias, cols, st);
 }
 }  // namespace gdn

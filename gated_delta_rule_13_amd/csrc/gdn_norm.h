@@ -40,12 +40,18 @@ struct NormBwdParams {
     void* dx;
     void* dz;               // may be null
     int64_t dsb, dst, dsg;  // strides of dx
-    float* part;            // [workgroups of a head][G][d] of w, then of b
-    int64_t part_b;         // offset of b's sums
-    int want_w, want_b;
+    float* part;            // sums of a head's workgroups: rows of [w | b], see norm_partial
 };
 
 constexpr int kNormThreads = 256;
+
+// Where workgroup blk leaves head g's sums for the weight (which 0) or the
+// bias: rows [blk][w of all heads | b of all heads] for weights [G, d], and
+// [blk, g][w | b] for weights [d], which are summed over the heads too.
+__device__ __forceinline__ float* norm_partial(const NormBwdParams& q, int64_t blk, int g, int which) {
+    const int64_t G = q.f.G, d = q.f.d;
+    return q.part + (q.f.per_group ? (blk * 2 + which) * G + g : (blk * G + g) * 2 + which) * d;
+}
 
 __device__ __forceinline__ void act_both(float x, int act, float& val, float& slope) {
     if (act) {
@@ -82,49 +88,76 @@ __device__ __forceinline__ void row_stats(const float (&x)[K][4], const NormPara
     r = 1.f / sqrtf(lanes_sum<L>(s) * inv + p.eps);
 }
 
+// One row as it lies in memory.
 template <bool XB, bool OB, int L, int K>
-__global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_kernel(NormParams p) {
-    const int j = threadIdx.x % L;
-    const int64_t row = (int64_t)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
-    if (row >= p.rows) return;      // (a whole group of lanes)
-    const int g = (int)(row % p.G);
-    const int64_t bt = row / p.G;
-    const int64_t b = bt / p.T, t = bt % p.T;
-    const int64_t x0 = b * p.xsb + t * p.xst + g * p.xsg, z0 = b * p.zsb + t * p.zst + g * p.zsg;
-    Raw<XB, 4> xr[K];
-    Raw<OB, 4> zr[K];
+struct NormRow {
+    Raw<XB, 4> x[K];
+    Raw<OB, 4> z[K], dy[K];
+    __device__ __forceinline__ void load(const NormParams& p, const void* dyp, int64_t bt, int g, int j) {
+        const int64_t b = bt / p.T, t = bt - b * p.T;
+        const int64_t x0 = b * p.xsb + t * p.xst + g * p.xsg, z0 = b * p.zsb + t * p.zst + g * p.zsg;
+        const int64_t y0 = (bt * p.G + g) * p.d;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (k * L + j) * 4;
-        xr[k].zero();
-        zr[k].zero();
-        if (c < p.d) {
-            xr[k].load(p.x, x0 + c);
-            if (p.z) zr[k].load(p.z, z0 + c);
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + j) * 4;
+            x[k].zero();
+            z[k].zero();
+            dy[k].zero();
+            if (c < p.d) {
+                x[k].load(p.x, x0 + c);
+                if (p.z) z[k].load(p.z, z0 + c);
+                if (dyp) dy[k].load(dyp, y0 + c);
+            }
         }
     }
-    float x[K][4], mean, r;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[k][e] = xr[k].get(e);
-    row_stats<L, K>(x, p, j, mean, r);
+};
+template <int L, int K>
+__device__ __forceinline__ void load_columns(float (&w)[K][4], const float* src, const NormParams& p, int g, int j, float none) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * L + j) * 4;
-        if (c < p.d) {
-            const int wc = (p.per_group ? g * p.d : 0) + c;
-            float f[4];
+        const int c = (k * L + j) * 4, wc = (p.per_group ? g * p.d : 0) + c;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float v = (x[k][e] - mean) * r;
-                if (p.w) v *= p.w[wc + e];
-                if (p.b) v += p.b[wc + e];
-                if (p.z) v *= p.silu ? silu(zr[k].get(e)) : zr[k].get(e);
-                else if (p.silu) v = silu(v);
-                f[e] = v;
+        for (int e = 0; e < 4; ++e) w[k][e] = src && c < p.d ? src[wc + e] : none;
+    }
+}
+
+// A group of lanes takes every `tokens`-th token of one head, so that its
+// columns of the weight stay in registers, with the next row in flight.
+template <bool XB, bool OB, int L, int K>
+__global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_kernel(NormParams p, int64_t tokens) {
+    const int j = threadIdx.x % L;
+    const int64_t grp = (int64_t)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
+    const int g = (int)(grp % p.G);
+    const int64_t bts = p.rows / p.G;
+    int64_t bt = grp / p.G;
+    if (bt >= tokens || bt >= bts) return;      // (a whole group of lanes)
+    float w[K][4], b[K][4];
+    load_columns<L, K>(w, p.w, p, g, j, 1.f);
+    load_columns<L, K>(b, p.b, p, g, j, 0.f);
+    NormRow<XB, OB, L, K> cur, next;
+    next.load(p, nullptr, bt, g, j);
+    for (; bt < bts; bt += tokens) {
+        cur = next;
+        if (bt + tokens < bts) next.load(p, nullptr, bt + tokens, g, j);
+        float x[K][4], mean, r;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[k][e] = cur.x[k].get(e);
+        row_stats<L, K>(x, p, j, mean, r);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + j) * 4;
+            if (c < p.d) {
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = fmaf((x[k][e] - mean) * r, w[k][e], b[k][e]), gate = cur.z[k].get(e);
+                    if (p.z) f[e] = v * (p.silu ? silu(gate) : gate);
+                    else f[e] = p.silu ? silu(v) : v;
+                }
+                store_vec<OB, 4>(p.y, (bt * p.G + g) * p.d + c, f);
             }
-            store_vec<OB, 4>(p.y, row * p.d + c, f);
         }
     }
 }
@@ -139,42 +172,28 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParam
     const int j = threadIdx.x % L, grp = threadIdx.x / L;
     const int g = blockIdx.x % p.G;
     const int64_t blk = blockIdx.x / p.G, nblk = gridDim.x / p.G;
-    const int64_t bts = p.rows / p.G;
+    const int64_t bts = p.rows / p.G, step = nblk * kGroups;
     const float inv = 1.f / (float)p.d;
     float w[K][4], b[K][4], sw[K][4], sb[K][4];
+    load_columns<L, K>(w, p.w, p, g, j, 1.f);
+    load_columns<L, K>(b, p.b, p, g, j, 0.f);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (k * L + j) * 4, wc = (p.per_group ? g * p.d : 0) + c;
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            w[k][e] = p.w && c < p.d ? p.w[wc + e] : 1.f;
-            b[k][e] = p.b && c < p.d ? p.b[wc + e] : 0.f;
-            sw[k][e] = sb[k][e] = 0.f;
-        }
-    }
-    for (int64_t bt = blk * kGroups + grp; bt < bts; bt += nblk * kGroups) {
-        const int64_t bb = bt / p.T, t = bt % p.T;
-        const int64_t x0 = bb * p.xsb + t * p.xst + g * p.xsg, z0 = bb * p.zsb + t * p.zst + g * p.zsg;
+        for (int e = 0; e < 4; ++e) sw[k][e] = sb[k][e] = 0.f;
+    int64_t bt = blk * kGroups + grp;
+    NormRow<XB, OB, L, K> cur, next;
+    if (bt < bts) next.load(p, q.dy, bt, g, j);
+    for (; bt < bts; bt += step) {
+        cur = next;
+        if (bt + step < bts) next.load(p, q.dy, bt + step, g, j);
+        const int64_t bb = bt / p.T, t = bt - bb * p.T;
         const int64_t y0 = (bt * p.G + g) * p.d, d0 = bb * q.dsb + t * q.dst + g * q.dsg;
-        Raw<XB, 4> xr[K];
-        Raw<OB, 4> zr[K], yr[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (k * L + j) * 4;
-            xr[k].zero();
-            zr[k].zero();
-            yr[k].zero();
-            if (c < p.d) {
-                xr[k].load(p.x, x0 + c);
-                yr[k].load(q.dy, y0 + c);
-                if (p.z) zr[k].load(p.z, z0 + c);
-            }
-        }
         float x[K][4], dn[K][4], mean, r;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[k][e] = xr[k].get(e);
+            for (int e = 0; e < 4; ++e) x[k][e] = cur.x[k].get(e);
         row_stats<L, K>(x, p, j, mean, r);
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -184,9 +203,9 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParam
                 float dz[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float n = (x[k][e] - mean) * r, pv = fmaf(n, w[k][e], b[k][e]), dy = yr[k].get(e);
+                    const float n = (x[k][e] - mean) * r, pv = fmaf(n, w[k][e], b[k][e]), dy = cur.dy[k].get(e);
                     float val, slope;
-                    act_both(p.z ? zr[k].get(e) : pv, p.silu, val, slope);
+                    act_both(p.z ? cur.z[k].get(e) : pv, p.silu, val, slope);
                     const float dp = dy * (p.z ? val : slope);
                     dz[e] = dy * pv * slope;
                     sw[k][e] = fmaf(dp, n, sw[k][e]);
@@ -214,16 +233,16 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParam
     }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        if (which == 0 ? !q.want_w : !q.want_b) continue;
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) red[grp][(k * L + j) * 4 + e] = which ? sb[k][e] : sw[k][e];
         __syncthreads();
-        float* out = q.part + (which ? q.part_b : 0) + (blk * p.G + g) * p.d;
+        float* out = norm_partial(q, blk, g, which);
         for (int c = threadIdx.x; c < p.d; c += kNormThreads) {
             float t = 0.f;
+#pragma unroll
             for (int k = 0; k < kGroups; ++k) t += red[k][c];
             out[c] = t;
         }
@@ -320,10 +339,10 @@ __global__ __launch_bounds__(64) void gdn_norm_bwd_plain_kernel(NormBwdParams q)
             store_one<XB>(q.dx, d0 + c, r * (dp * wv - s1 - n * s2));
         }
     }
-    float* out = q.part + (blk * p.G + g) * p.d;
+    float *out_w = norm_partial(q, blk, g, 0), *out_b = norm_partial(q, blk, g, 1);
     for (int c = lane; c < p.d; c += 64) {
-        if (q.want_w) out[c] = sw[c];
-        if (q.want_b) out[q.part_b + c] = sb[c];
+        out_w[c] = sw[c];
+        out_b[c] = sb[c];
     }
 }
 
