@@ -416,7 +416,7 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // over the workgroup's NB waves, 16 each; what sums over states (du, ds, y) is
 // then added through LDS.
 template <bool BF, int NS, int NB>
-__global__ __launch_bounds__(64 * NB, 3) void gdn_ssm_bwd_kernel(SsmParams p) {
+__global__ __launch_bounds__(64 * NB, NS <= 4 ? 4 : 3) void gdn_ssm_bwd_kernel(SsmParams p) {
     constexpr int NSA = NS * NB;                     // states of the layout
     __shared__ __align__(16) float bc_all[NB][kTok][2][NS];
     __shared__ float el[5][kTok][64];
