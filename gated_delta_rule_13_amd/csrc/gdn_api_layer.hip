@@ -142,6 +142,10 @@ gdn_status validate(const gdn_ssm_shape* s) {
     for (int64_t v : {s->x_stride_b, s->x_stride_t, s->dt_stride_b, s->dt_stride_t, s->z_stride_b, s->z_stride_t,
                       s->b_stride_b, s->b_stride_t, s->c_stride_b, s->c_stride_t})
         if (v < 0) return set_error(GDN_ERR_BAD_SHAPE, "strides must be >= 0");
+    // (the kernels address the rows of a group of tokens by 32-bit offsets)
+    constexpr int64_t kMaxRow = 1 << 24;
+    for (int64_t v : {(int64_t)s->D, s->x_stride_t, s->dt_stride_t, s->z_stride_t, s->b_stride_t, s->c_stride_t})
+        if (v > kMaxRow) return set_error(GDN_ERR_UNSUPPORTED, "D and the strides of tokens must be at most 2^24");
     gdn_status st = check_counts(s->B, s->T, (int64_t)s->D * s->N);
     if (st != GDN_OK) return st;
     // (sequences x segments of at least 8 tokens x tiles of 64 channels, and

@@ -74,6 +74,23 @@ __device__ __forceinline__ char* row_at(void* p, int64_t i) {
     return reinterpret_cast<char*>(p) + i * (BF ? 2 : 4);
 }
 
+// One element through a buffer resource (gdn_device.h): at or behind its end,
+// as kOutside is, a load gives 0 and a store writes nothing, so that neither
+// needs a branch (one around a prefetch makes the compiler wait for it where
+// the branch ends).
+constexpr uint32_t kOutside = 0x80000000u;
+__device__ __forceinline__ buf_t buffer_from(const void* base) { return buffer_over(base, 0x7fffffffu); }
+template <bool BF>
+__device__ __forceinline__ void buf_load_one(Raw<BF, 1>& r, buf_t b, uint32_t off) {
+    if constexpr (BF) r.w[0] = buf_load_bf16_bits(b, off);
+    else r.w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0);
+}
+template <bool BF>
+__device__ __forceinline__ void buf_store_one(buf_t b, uint32_t off, float v) {
+    if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)v), b, (int)off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), b, (int)off, 0, 0);
+}
+
 template <bool BF>
 __device__ __forceinline__ float load_one(const void* p, int64_t i) {
     if constexpr (BF) return (float)reinterpret_cast<const __bf16*>(p)[i];

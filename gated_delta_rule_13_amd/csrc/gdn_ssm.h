@@ -73,6 +73,7 @@ constexpr int kGradSeg = kGradGroups * kTok;
 // Where a wave works: its sequence, segment and channels.
 struct SsmPlace {
     int b, seg, tile, g, c;  // c: channel of the lane (clamped), of all D
+    int c0;                  // the wave's first channel
     bool on;                 // the lane has a channel of its own
     int t0, t1, tz;          // tokens [t0, t1), padded rows [max(t0, t1), tz)
     int64_t unit;
@@ -88,6 +89,7 @@ __device__ __forceinline__ SsmPlace ssm_place(const SsmParams& p, unsigned id, i
     const int c = (w.tile % p.tpg) * 64 + lane;
     w.on = c < p.Dg;
     w.c = w.g * p.Dg + (w.on ? c : p.Dg - 1);
+    w.c0 = w.g * p.Dg + (w.tile % p.tpg) * 64;
     const int n = seq_len(p.lens, w.b, p.T);
     w.t0 = w.seg * p.seg_len;
     w.tz = p.T - w.t0 < p.seg_len ? p.T : w.t0 + p.seg_len;
@@ -97,21 +99,29 @@ __device__ __forceinline__ SsmPlace ssm_place(const SsmParams& p, unsigned id, i
 }
 
 // Bm and C of kTok tokens, spread over the wave's lanes: value i of lane l is
-// number l + 64 i of [token][Bm | C][NS].
+// number l + 64 i of [token][Bm | C][NS]; 0 behind the N states and behind t1.
 template <bool BF, int NS>
 struct StagedBC {
     static constexpr int kEach = kTok * 2 * NS / 64;
     Raw<BF, 1> v[kEach];
     __device__ __forceinline__ void load(const SsmParams& p, const SsmPlace& w, int t, int lane) {
+        constexpr uint32_t E = BF ? 2 : 4;
+        const buf_t bb = buffer_from(row_at<BF>(p.Bm, w.b * p.bsb + t * p.bst + w.g * p.N));
+        const buf_t cb = buffer_from(row_at<BF>(p.C, w.b * p.csb + t * p.cst + w.g * p.N));
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int k = lane + 64 * i, n = k % NS;
-            int tt = t + k / (2 * NS);
-            tt = tt < w.t1 ? tt : w.t1 - 1;
-            v[i].zero();
-            if (n < p.N) {
-                if ((k / NS) & 1) v[i].load(p.C, w.b * p.csb + tt * p.cst + w.g * p.N + n);
-                else v[i].load(p.Bm, w.b * p.bsb + tt * p.bst + w.g * p.N + n);
+            const int k = lane + 64 * i, n = k % NS, tok = k / (2 * NS);
+            const bool in = n < p.N && t + tok < w.t1, c = (k / NS) & 1;
+            // (strides are below 2^24 elements)
+            const uint32_t bo = ((uint32_t)tok * (uint32_t)p.bst + n) * E, co = ((uint32_t)tok * (uint32_t)p.cst + n) * E;
+            if constexpr (NS >= 64) {            // (a value of all lanes is of one of them)
+                if (((64 * i) / NS) & 1) buf_load_one<BF>(v[i], cb, in ? co : kOutside);
+                else buf_load_one<BF>(v[i], bb, in ? bo : kOutside);
+            } else {
+                Raw<BF, 1> other;
+                buf_load_one<BF>(v[i], bb, in && !c ? bo : kOutside);
+                buf_load_one<BF>(other, cb, in && c ? co : kOutside);
+                v[i].w[0] |= other.w[0];
             }
         }
     }
@@ -121,13 +131,14 @@ struct StagedBC {
     }
 };
 
-// One number of kTok tokens of the lane's channel.
+// One number of kTok tokens of the lane's channel; behind t1 the last one again.
 template <bool BF>
 struct Column {
     Raw<BF, 1> v[kTok];
-    __device__ __forceinline__ void load(const void* p, int64_t base, int64_t st, int t, int t1) {
+    // base: element of the wave's first channel, off: the lane's byte offset
+    __device__ __forceinline__ void load(const void* p, int64_t base, int64_t st, uint32_t off, int t, int t1) {
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) v[i].load(p, base + (t + i < t1 ? t + i : t1 - 1) * st);
+        for (int i = 0; i < kTok; ++i) v[i].load_at(row_at<BF>(p, base + (t + i < t1 ? t + i : t1 - 1) * st), off);
     }
 };
 
@@ -173,8 +184,12 @@ __global__ __launch_bounds__(64) void gdn_ssm_fwd_kernel(SsmParams p) {
     __shared__ __align__(16) float bc[2][kTok][2][NS];
     const int lane = threadIdx.x;
     const SsmPlace w = ssm_place(p, blockIdx.x, p.nseg, lane);
-    const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c, zb = w.b * p.zsb + w.c;
-    const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
+    const int64_t xb = w.b * p.xsb + w.c0, db = w.b * p.dsb + w.c0;
+    const int64_t yb = (int64_t)w.b * p.T * p.D + w.c, y0 = (int64_t)w.b * p.T * p.D + w.c0;
+    // (without a gate x is loaded in its place, and not used)
+    const void* zsrc = p.z ? p.z : p.x;
+    const int64_t zb = p.z ? w.b * p.zsb + w.c0 : xb, zst = p.z ? p.zst : p.xst;
+    const uint32_t off = (uint32_t)(w.c - w.c0) * (BF ? 2 : 4);
     float a[NS], h[NS];
     load_decay<NS>(a, p, w.c);
     if (p.nseg > 1) load_sum<NS>(h, p.sum_e, w.unit, lane);
@@ -184,37 +199,38 @@ __global__ __launch_bounds__(64) void gdn_ssm_fwd_kernel(SsmParams p) {
     if (w.t0 < w.t1) {
         StagedBC<BF, NS> nbc;
         Column<BF> nx, nd, nz;
-        nbc.load(p, w, w.t0, lane);
-        nx.load(p.x, xb, p.xst, w.t0, w.t1);
-        nd.load(p.dt, db, p.dst, w.t0, w.t1);
-        if (p.z) nz.load(p.z, zb, p.zst, w.t0, w.t1);
+        auto load = [&](int t) {
+            nbc.load(p, w, t, lane);
+            nx.load(p.x, xb, p.xst, off, t, w.t1);
+            nd.load(p.dt, db, p.dst, off, t, w.t1);
+            nz.load(zsrc, zb, zst, off, t, w.t1);
+        };
+        load(w.t0);
         int buf = 0;
         for (int t = w.t0; t < w.t1; t += kTok, buf ^= 1) {
             nbc.put(&bc[buf][0][0][0], lane);
             float x[kTok], s[kTok], gate[kTok];
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
+                const float raw = nd.v[i].get(0) + bias, soft = softplus(raw), open = silu(nz.v[i].get(0));
                 x[i] = nx.v[i].get(0);
-                s[i] = t + i < w.t1 ? ssm_step_size(nd.v[i].get(0) + bias, p.softplus) : 0.f;
-                gate[i] = p.z ? silu(nz.v[i].get(0)) : 1.f;
+                s[i] = t + i < w.t1 ? (p.softplus ? soft : raw) : 0.f;
+                gate[i] = p.z ? open : 1.f;
             }
-            if (t + kTok < w.t1) {
-                nbc.load(p, w, t + kTok, lane);
-                nx.load(p.x, xb, p.xst, t + kTok, w.t1);
-                nd.load(p.dt, db, p.dst, t + kTok, w.t1);
-                if (p.z) nz.load(p.z, zb, p.zst, t + kTok, w.t1);
-            }
+            load(t + kTok < w.t1 ? t + kTok : w.t0);      // (the last time for nothing)
             __syncthreads();
+            const buf_t yr = buffer_from(row_at<BF>(p.y, y0 + (int64_t)t * p.D));
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
-                const float u = t + i < w.t1 ? s[i] * x[i] : 0.f;
+                const float u = s[i] == 0.f ? 0.f : s[i] * x[i];
                 float y = dskip * x[i];
 #pragma unroll
                 for (int n = 0; n < NS; ++n) {
                     h[n] = fmaf(exp2_hw(s[i] * a[n]), h[n], u * bc[buf][i][0][n]);
                     y = fmaf(h[n], bc[buf][i][1][n], y);
                 }
-                if (w.on && t + i < w.t1) store_one<BF>(p.y, yb + (int64_t)(t + i) * p.D, y * gate[i]);
+                buf_store_one<BF>(yr, w.on && t + i < w.t1 ? (uint32_t)i * (uint32_t)p.D * (BF ? 2 : 4) + off : kOutside,
+                                  y * gate[i]);
                 pin(h);
             }
         }
@@ -240,8 +256,10 @@ __global__ __launch_bounds__(64) void gdn_ssm_sum_kernel(SsmParams p, int nseg) 
     __shared__ __align__(16) float bc[2][kTok][2][NS];
     const int lane = threadIdx.x;
     const SsmPlace w = ssm_place(p, blockIdx.x, nseg, lane);
-    const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c, zb = w.b * p.zsb + w.c;
-    const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
+    const int64_t xb = w.b * p.xsb + w.c0, db = w.b * p.dsb + w.c0, y0 = (int64_t)w.b * p.T * p.D + w.c0;
+    const void* zsrc = p.z ? p.z : p.x;
+    const int64_t zb = p.z ? w.b * p.zsb + w.c0 : xb, zst = p.z ? p.zst : p.xst;
+    const uint32_t off = (uint32_t)(w.c - w.c0) * (BF ? 2 : 4);
     float a[NS], h[NS], pr[NS], r[NS], total = 0.f;
     load_decay<NS>(a, p, w.c);
 #pragma unroll
@@ -250,13 +268,16 @@ __global__ __launch_bounds__(64) void gdn_ssm_sum_kernel(SsmParams p, int nseg) 
     if (w.t0 < w.t1) {
         StagedBC<BF, NS> nbc;
         Column<BF> nx, nd, nz, ng;
-        nbc.load(p, w, w.t0, lane);
-        nx.load(p.x, xb, p.xst, w.t0, w.t1);
-        nd.load(p.dt, db, p.dst, w.t0, w.t1);
-        if (GRAD) {
-            if (p.z) nz.load(p.z, zb, p.zst, w.t0, w.t1);
-            ng.load(p.dy, yb, p.D, w.t0, w.t1);
-        }
+        auto load = [&](int t) {
+            nbc.load(p, w, t, lane);
+            nx.load(p.x, xb, p.xst, off, t, w.t1);
+            nd.load(p.dt, db, p.dst, off, t, w.t1);
+            if (GRAD) {
+                nz.load(zsrc, zb, zst, off, t, w.t1);
+                ng.load(p.dy, y0, p.D, off, t, w.t1);
+            }
+        };
+        load(w.t0);
         int buf = 0;
         for (int t = w.t0; t < w.t1; t += kTok, buf ^= 1) {
             nbc.put(&bc[buf][0][0][0], lane);
@@ -264,21 +285,17 @@ __global__ __launch_bounds__(64) void gdn_ssm_sum_kernel(SsmParams p, int nseg) 
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
                 const bool in = t + i < w.t1;
-                s[i] = in ? ssm_step_size(nd.v[i].get(0) + bias, p.softplus) : 0.f;
+                const float raw = nd.v[i].get(0) + bias, soft = softplus(raw);
+                s[i] = in ? (p.softplus ? soft : raw) : 0.f;
                 u[i] = in ? s[i] * nx.v[i].get(0) : 0.f;
                 g[i] = 0.f;
-                if (GRAD && in) g[i] = p.z ? ng.v[i].get(0) * silu(nz.v[i].get(0)) : ng.v[i].get(0);
+                if (GRAD) {
+                    const float dy = ng.v[i].get(0), open = silu(nz.v[i].get(0));
+                    g[i] = in ? (p.z ? dy * open : dy) : 0.f;
+                }
                 total += s[i];
             }
-            if (t + kTok < w.t1) {
-                nbc.load(p, w, t + kTok, lane);
-                nx.load(p.x, xb, p.xst, t + kTok, w.t1);
-                nd.load(p.dt, db, p.dst, t + kTok, w.t1);
-                if (GRAD) {
-                    if (p.z) nz.load(p.z, zb, p.zst, t + kTok, w.t1);
-                    ng.load(p.dy, yb, p.D, t + kTok, w.t1);
-                }
-            }
+            load(t + kTok < w.t1 ? t + kTok : w.t0);      // (the last time for nothing)
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
