@@ -158,9 +158,10 @@ gdn_status validate(const gdn_ssm_shape* s) {
 }
 
 // Segments of the forward pass.  One wave takes 64 channels of a segment; the
-// chip has 1024 vector units, which two waves each keep busy.  Segments cost
+// chip has 1024 vector units, which hold three such waves each.  Segments cost
 // the decays a second time, so there are none when the channels alone give
-// that many waves, and as few as do otherwise.
+// that many waves, and as few as do otherwise; of 16 tokens at least, where
+// what a segment costs besides its tokens is a fifth of it.
 struct SsmPlan {
     int seg_len, nseg;
     size_t off_s, bytes;
@@ -168,10 +169,10 @@ struct SsmPlan {
 SsmPlan ssm_fwd_plan(const gdn_ssm_shape& s) {
     const int64_t tiles = (int64_t)s.G * ceil_div(s.D / s.G, 64), waves = s.B * tiles;
     SsmPlan pl{s.T, 1, 0, 0};
-    const int64_t want = ceil_div(2048, waves);
-    if (want > 1 && s.T >= 128) {
+    const int64_t want = ceil_div(3072, waves);
+    if (want > 1 && s.T >= 64) {
         const int64_t len = ceil_div(ceil_div(s.T, want), gdn::kTok) * gdn::kTok;
-        pl.seg_len = (int)(len < 64 ? 64 : len);
+        pl.seg_len = (int)(len < 16 ? 16 : len);
         pl.nseg = (int)ceil_div(s.T, pl.seg_len);
     }
     if (pl.nseg > 1) {
@@ -227,20 +228,24 @@ gdn_status ssm_check(const gdn_ssm_shape* s, const void* x, const void* dt, cons
 
 // Parts of the gradient's workspace, in bytes from its start.
 struct SsmGradPlan {
-    int nseg;
+    int seg_len, nseg;
     size_t e, r, s, kh, ks, a, d, bc, bytes;
 };
 SsmGradPlan ssm_bwd_plan(const gdn_ssm_shape& s) {
     SsmGradPlan g{};
     const size_t tiles = (size_t)s.G * ceil_div(s.D / s.G, 64);
-    g.nseg = (int)ceil_div(s.T, gdn::ssm_bwd_segment());
+    // segments of 64 tokens, or 32 or 16 where those leave fewer than 1024 waves
+    // of summaries (one for each vector unit)
+    g.seg_len = 64;
+    while (g.seg_len > 16 && (int64_t)s.B * tiles * ceil_div(s.T, g.seg_len) < 1024) g.seg_len /= 2;
+    g.nseg = (int)ceil_div(s.T, g.seg_len);
     const size_t units = (size_t)s.B * g.nseg * tiles, ns = gdn::ssm_states(s.N);
     g.e = 0;
     g.r = g.e + units * ns * 64 * 4;
     g.s = g.r + units * ns * 64 * 4;
     g.kh = g.s + units * 64 * 4;
-    g.ks = g.kh + units * (gdn::kGradGroups - 1) * ns * 64 * 4;
-    g.a = g.ks + units * (gdn::kGradGroups - 1) * 64 * 4;
+    g.ks = g.kh + units * (g.seg_len / gdn::kTok - 1) * ns * 64 * 4;
+    g.a = g.ks + units * (g.seg_len / gdn::kTok - 1) * 64 * 4;
     g.d = g.a + units * ns * 64 * 4;
     g.bc = g.d + units * 2 * 64 * 4;
     g.bytes = g.bc + up256(tiles * s.B * s.T * 2 * ns * 4);
@@ -443,7 +448,7 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape* s, const void* dy, const void* x, co
     if (st != GDN_OK) return st;
     gdn::SsmParams p = ssm_params(*s, x, dt, A, Bm, C, Dskip, z, dt_bias, h0, lens);
     char* ws = static_cast<char*>(workspace);
-    p.seg_len = gdn::ssm_bwd_segment();
+    p.seg_len = pl.seg_len;
     p.nseg = pl.nseg;
     p.dy = dy;
     p.dh_final = dh_final;

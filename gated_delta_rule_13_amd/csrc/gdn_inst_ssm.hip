@@ -19,7 +19,7 @@ void summaries(const SsmParams& p, int nseg_summed, hipStream_t st) {
     if (nseg_summed > 0)
         hipLaunchKernelGGL((gdn_ssm_sum_kernel<kBF, NS, GRAD>), dim3((unsigned)(p.B * nseg_summed * tiles)), dim3(64), 0,
                            st, p, nseg_summed);
-    hipLaunchKernelGGL((gdn_ssm_chain_kernel<NS, GRAD>), dim3(blocks(p.B * tiles * NS * 64, kChainThreads)),
+    hipLaunchKernelGGL((gdn_ssm_chain_kernel<NS, GRAD>), dim3(blocks((GRAD ? 2 : 1) * p.B * tiles * NS * 64, kChainThreads)),
                        dim3(kChainThreads), 0, st, p);
 }
 
@@ -38,8 +38,8 @@ void bwd(const SsmParams& p, float* dA, void* dBm, void* dC, float* dD, float* d
     hipLaunchKernelGGL((gdn_ssm_bwd_kernel<kBF, NS, NB>), dim3((unsigned)(p.B * p.nseg * tiles)), dim3(64 * NB), 0, st, p);
     hipLaunchKernelGGL((gdn_ssm_bc_kernel<kBF>), dim3(blocks((int64_t)p.B * p.T * p.G * 2 * NSA, kSumThreads)),
                        dim3(kSumThreads), 0, st, p, dBm, dC, NSA);
-    hipLaunchKernelGGL((gdn_ssm_param_kernel<kBF>), dim3(blocks(tiles * (NSA + 2) * 64, kSumThreads)), dim3(kSumThreads), 0, st,
-                       p, dA, dD, dbias, NSA);
+    hipLaunchKernelGGL((gdn_ssm_param_kernel<kBF>), dim3((unsigned)(tiles * (NSA + 2))), dim3(64 * kParamSlices), 0, st, p,
+                       dA, dD, dbias, NSA);
 }
 
 template <int LP>
@@ -85,7 +85,6 @@ void GDN_SSM_NAME(ssm_step_run)(const SsmStepParams& q, hipStream_t st) {
 
 #if GDN_SSM_BF16
 int ssm_states(int N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
-int ssm_bwd_segment() { return kGradSeg; }
 void ssm_fwd_run_f32(const SsmParams& p, hipStream_t st);
 void ssm_bwd_run_f32(const SsmParams& p, float* dA, void* dBm, void* dC, float* dD, float* dbias, hipStream_t st);
 void ssm_step_run_f32(const SsmStepParams& q, hipStream_t st);

@@ -90,6 +90,5 @@ void ssm_fwd_run(const SsmParams& p, bool bf16, hipStream_t st);
 void ssm_bwd_run(const SsmParams& p, bool bf16, float* dA, void* dBm, void* dC, float* dDskip, float* ddt_bias,
                  hipStream_t st);
 void ssm_step_run(const SsmStepParams& q, bool bf16, hipStream_t st);
-int ssm_bwd_segment();
 
 }  // namespace gdn

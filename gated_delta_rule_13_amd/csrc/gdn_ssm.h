@@ -47,7 +47,7 @@ struct SsmParams {
     int Dg;                 // channels per group
     int tpg;                // tiles of 64 channels per group
     int softplus;
-    int seg_len, nseg;
+    int seg_len, nseg;      // with segments a multiple of kTok
     // segment summaries, in units of (sequence, segment, tile):
     float* sum_e;           // [unit][NS][64]: E, then the state that enters
     float* sum_s;           // [unit][64]: sum of s
@@ -66,9 +66,7 @@ struct SsmParams {
     float* part_bc;         // [tile][sequence][token][2][NS]: dB, dC over a tile's channels
 };
 
-constexpr int kTok = 8;                              // tokens staged at a time
-constexpr int kGradGroups = 8;                       // groups of kTok tokens in a segment of the gradient
-constexpr int kGradSeg = kGradGroups * kTok;
+constexpr int kTok = 8;                              // tokens staged at a time (a group)
 
 // Where a wave works: its sequence, segment and channels.
 struct SsmPlace {
@@ -180,7 +178,7 @@ __device__ __forceinline__ float ssm_step_size(float raw, bool soft) { return so
 
 // Tokens behind t1 take the step size 0: they leave the state as it is.
 template <bool BF, int NS>
-__global__ __launch_bounds__(64) void gdn_ssm_fwd_kernel(SsmParams p) {
+__global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmParams p) {
     __shared__ __align__(16) float bc[2][kTok][2][NS];
     const int lane = threadIdx.x;
     const SsmPlace w = ssm_place(p, blockIdx.x, p.nseg, lane);
@@ -252,7 +250,7 @@ __global__ __launch_bounds__(64) void gdn_ssm_fwd_kernel(SsmParams p) {
 // zero after each group of kTok tokens, from which the gradient kernel goes
 // on.
 template <bool BF, int NS, bool GRAD>
-__global__ __launch_bounds__(64) void gdn_ssm_sum_kernel(SsmParams p, int nseg) {
+__global__ __launch_bounds__(64, NS <= 16 && !GRAD ? 3 : 1) void gdn_ssm_sum_kernel(SsmParams p, int nseg) {
     __shared__ __align__(16) float bc[2][kTok][2][NS];
     const int lane = threadIdx.x;
     const SsmPlace w = ssm_place(p, blockIdx.x, nseg, lane);
@@ -315,7 +313,7 @@ __global__ __launch_bounds__(64) void gdn_ssm_sum_kernel(SsmParams p, int nseg) 
                 }
             }
             if (GRAD && t + kTok < w.t1) {
-                const int64_t at = w.unit * (kGradGroups - 1) + (t - w.t0) / kTok;
+                const int64_t at = w.unit * (p.seg_len / kTok - 1) + (t - w.t0) / kTok;
                 store_sum<NS>(p.keep_h, h, at, lane);
                 p.keep_s[at * 64 + lane] = total;
             }
@@ -327,17 +325,19 @@ __global__ __launch_bounds__(64) void gdn_ssm_sum_kernel(SsmParams p, int nseg) 
 }
 
 // From the summaries, in their place: sum_e becomes the state that enters
-// each segment; sum_r the gradient of the state that leaves it.  One thread
-// for a (sequence, tile, state, lane); kAhead segments' summaries are in
-// flight.
+// each segment; sum_r the gradient of the state that leaves it, from the last
+// segment to the first (by the second half of the threads).  One thread for a
+// (sequence, tile, state, lane); kAhead segments' summaries are in flight.
 constexpr int kChainThreads = 256;
 template <int NS, bool GRAD>
 __global__ __launch_bounds__(kChainThreads) void gdn_ssm_chain_kernel(SsmParams p) {
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     const unsigned tiles = (unsigned)(p.G * p.tpg);
-    const int64_t id = (int64_t)blockIdx.x * kChainThreads + threadIdx.x;
-    const int64_t per_seq = (int64_t)tiles * NS * 64;
-    if (id >= p.B * per_seq) return;
+    const int64_t per_seq = (int64_t)tiles * NS * 64, all = p.B * per_seq;
+    int64_t id = (int64_t)blockIdx.x * kChainThreads + threadIdx.x;
+    if (id >= (GRAD ? 2 : 1) * all) return;
+    const bool back = GRAD && id >= all;
+    if (back) id -= all;
     const int b = (int)(id / per_seq);
     const int64_t in_seq = id % per_seq;
     const int lane = (int)(in_seq % 64), n = (int)(in_seq / 64 % NS), tile = (int)(in_seq / (64 * NS));
@@ -345,15 +345,19 @@ __global__ __launch_bounds__(kChainThreads) void gdn_ssm_chain_kernel(SsmParams 
     const bool on = c < p.Dg && n < p.N;
     const int64_t ch = g * p.Dg + c, at = ((int64_t)b * p.D + ch) * p.N + n;
     const float a = on ? p.A[ch * p.N + n] * kLog2e : 0.f;
-    const int64_t se = per_seq, ss = (int64_t)tiles * 64;
-    float* e = p.sum_e + b * p.nseg * se + in_seq;
-    const float* s = p.sum_s + b * p.nseg * ss + tile * 64 + lane;
-    float h = p.h0 && on ? p.h0[at] : 0.f;
+    // segment j of the way: j, or from the end
+    const int64_t first = back ? p.nseg - 1 : 0, dir = back ? -1 : 1;
+    const int64_t se = dir * per_seq, ss = dir * (int64_t)tiles * 64;
+    float* e = (back ? p.sum_r : p.sum_e) + (b * p.nseg + first) * per_seq + in_seq;
+    const float* s = p.sum_s + (b * p.nseg + first) * (int64_t)tiles * 64 + tile * 64 + lane;
+    const float* start = back ? p.dh_final : p.h0;
+    float h = start && on ? start[at] : 0.f;
     for (int k = 0; k < p.nseg; k += kAhead) {
         float ev[kAhead], sv[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int j = k + i < p.nseg - 1 ? k + i : 0;     // (the last segment's own summary is not used)
+            // (forward alone, the last segment has no summary: none is used)
+            const int j = k + i < p.nseg - (GRAD ? 0 : 1) ? k + i : 0;
             ev[i] = e[j * se];
             sv[i] = s[j * ss];
         }
@@ -365,27 +369,7 @@ __global__ __launch_bounds__(kChainThreads) void gdn_ssm_chain_kernel(SsmParams 
             }
         }
     }
-    if (GRAD) {
-        float* r = p.sum_r + b * p.nseg * se + in_seq;
-        float q = p.dh_final && on ? p.dh_final[at] : 0.f;
-        for (int k = p.nseg - 1; k >= 0; k -= kAhead) {
-            float rv[kAhead], sv[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int j = k - i >= 0 ? k - i : 0;
-                rv[i] = r[j * se];
-                sv[i] = s[j * ss];
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (k - i >= 0) {
-                    r[(k - i) * se] = q;
-                    q = fmaf(exp2_hw(sv[i] * a), q, rv[i]);
-                }
-            }
-        }
-        if (p.dh0 && on) p.dh0[at] = q;
-    }
+    if (back && p.dh0 && on) p.dh0[at] = h;
 }
 
 // ---------------------------------------------------------------------------
@@ -464,7 +448,7 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 ? 4 : 3) void gdn_ssm_bwd_kernel(S
 #pragma unroll
         for (int n = 0; n < NS; ++n) h[n] = p.sum_e[(w.unit * NSA + n0 + n) * 64 + lane];
         if (k > 0) {
-            const int64_t at = w.unit * (kGradGroups - 1) + k - 1;
+            const int64_t at = w.unit * (p.seg_len / kTok - 1) + k - 1;
             const float sk = p.keep_s[at * 64 + lane];
 #pragma unroll
             for (int n = 0; n < NS; ++n)
@@ -639,23 +623,32 @@ __global__ __launch_bounds__(kSumThreads) void gdn_ssm_bc_kernel(SsmParams p, vo
     store_one<BF>(which ? dC : dB, (bt * p.G + g) * p.N + n, v);
 }
 
-// dA [D, N], dDskip [D], ddt_bias [D]: the sum over sequences and segments.
+// dA [D, N], dDskip [D], ddt_bias [D]: the sum over sequences and segments, in
+// kParamSlices slices of them (ascending) and the slices in order.
+constexpr int kParamSlices = 8;
 template <bool BF>
-__global__ __launch_bounds__(kSumThreads) void gdn_ssm_param_kernel(SsmParams p, float* dA, float* dD, float* dbias, int ns) {
-    const int64_t id = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
-    const int tiles = p.G * p.tpg;
-    const int rows = ns + 2;
-    if (id >= (int64_t)tiles * rows * 64) return;
-    const int lane = (int)(id % 64), n = (int)(id / 64 % rows), tile = (int)(id / (64 * rows));
-    const int c = (tile % p.tpg) * 64 + lane, ch = tile / p.tpg * p.Dg + c;
-    if (c >= p.Dg) return;
+__global__ __launch_bounds__(64 * kParamSlices) void gdn_ssm_param_kernel(SsmParams p, float* dA, float* dD, float* dbias, int ns) {
+    __shared__ float sum[kParamSlices][64];
+    const int tiles = p.G * p.tpg, rows = ns + 2;
+    const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+    const int n = (int)(blockIdx.x % (unsigned)rows), tile = (int)(blockIdx.x / (unsigned)rows);
     const float* src = n < ns ? p.part_a + ((int64_t)tile * ns + n) * 64 + lane
                               : p.part_d + ((int64_t)tile * 2 + n - ns) * 64 + lane;
     const int64_t step = (int64_t)tiles * (n < ns ? ns : 2) * 64;
+    const int64_t all = (int64_t)p.B * p.nseg, per = (all + kParamSlices - 1) / kParamSlices;
+    const int64_t end = (slice + 1) * per < all ? (slice + 1) * per : all;
     float v = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < p.B * p.nseg; ++k) v += src[k * step];
-    if (n < p.N) dA[(int64_t)ch * p.N + n] = v;
+    for (int64_t k = slice * per; k < end; ++k) v += src[k * step];
+    sum[slice][lane] = v;
+    __syncthreads();
+    const int c = (tile % p.tpg) * 64 + lane;
+    if (slice > 0 || c >= p.Dg) return;
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kParamSlices; ++k) v += sum[k][lane];
+    const int64_t ch = (int64_t)(tile / p.tpg) * p.Dg + c;
+    if (n < p.N) dA[ch * p.N + n] = v;
     else if (n == ns && dD) dD[ch] = v;
     else if (n == ns + 1 && dbias) dbias[ch] = v;
 }
