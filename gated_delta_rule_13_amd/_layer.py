@@ -65,25 +65,23 @@ def _stream(t) -> int:
 
 def _check(name, t, shape, dtype, device, tail=None):
     """Shape, dtype and device of t, and that it is contiguous (tail None) or
-    that its last `tail` dimensions are."""
+    that its last dimension (tail 1) or two dimensions (tail 2) are."""
     if t is None:
         return
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.is_contiguous():
-        return
     if tail is None:
-        raise ValueError(f"{name} must be contiguous")
-    want = 1
-    for dim in range(t.dim() - 1, t.dim() - 1 - tail, -1):
-        if t.shape[dim] > 1 and t.stride(dim) != want:
-            raise ValueError(f"the last {'dimension' if tail == 1 else f'{tail} dimensions'} of {name} "
-                             "must be contiguous")
-        want *= t.shape[dim]
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if tail == 2 and t.stride(-2) != shape[-1] and shape[-2] > 1:
+        raise ValueError(f"the last 2 dimensions of {name} must be contiguous")
 
 
 def _rank(name, t, n):
@@ -96,7 +94,7 @@ def _separate(name, out, **inputs):
     ranges of their elements tell)."""
     base = out.untyped_storage().data_ptr()
     for other, t in inputs.items():
-        if t is not None and t.untyped_storage().data_ptr() == base and t.numel() and out.numel():
+        if t is not None and t.untyped_storage().data_ptr() == base:
             (a0, a1), (b0, b1) = _range(out), _range(t)
             if a0 < b1 and b0 < a1:
                 raise ValueError(f"{name} may not overlap {other}")
@@ -191,18 +189,22 @@ def gdn_conv_step(x, weight, bias, state, act="silu", y=None, stream=None):
     if _elsewhere(x, stream):
         with _moved("gdn_conv_step", x, stream):
             return gdn_conv_step(x, weight, bias, state, act, y)
-    dev = x.device
-    _rank("x", x, 2)
+    dev, io = x.device, x.dtype
     if state is None:
         raise ValueError("gdn_conv_step needs the state")
-    row = x.unsqueeze(1)
-    s = _conv_shape(row, weight, None, act)
-    _conv_check(s, row, weight, bias, state, None, dev)
+    _rank("x", x, 2)
+    _rank("weight", weight, 2)
+    (B, D), W = x.shape, weight.shape[1]
+    _check("x", x, (B, D), io, dev, 1)
+    _check("weight", weight, (D, W), torch.float32, dev)
+    _check("bias", bias, (D,), torch.float32, dev)
+    _check("state", state, (B, W - 1, D), io, dev)
     _separate("state", state, x=x)
+    s = GdnConvShape(B, 1, D, W, 1, _code(io), _silu(act), x.stride(0), 0)
     if y is None:
-        y = x.new_empty((s.B, s.D))
+        y = x.new_empty((B, D))
     else:
-        _check("y", y, (s.B, s.D), x.dtype, dev)
+        _check("y", y, (B, D), io, dev)
         _separate("y", y, x=x, state=state)
     check(load().gdn_conv_step(ctypes.byref(s), x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(),
                                y.data_ptr(), _stream(x)))
@@ -245,33 +247,38 @@ def gdn_conv_bwd(dy, x, weight, bias=None, state0=None, lens=None, dstate_out=No
 # ---- selective state space recurrence ----
 
 def _ssm_shape(x, dt, A, Bm, C, z, dt_softplus):
-    for name, t, n in (("x", x, 3), ("dt", dt, 3), ("A", A, 2), ("Bm", Bm, 4), ("C", C, 4)):
-        _rank(name, t, n)
-    if z is not None:
-        _rank("z", z, 3)
+    _rank("x", x, 3)
+    _rank("dt", dt, 3)
+    _rank("Bm", Bm, 4)
+    _rank("C", C, 4)
     B, T, D = x.shape
-    G, N = Bm.shape[2:]
+    _, _, G, N = Bm.shape
     if G < 1 or D % G:
         raise ValueError(f"{D} channels do not divide into {G} groups")
-    strides = []
-    for t in (x, dt, z, Bm, C):
-        strides += [0, 0] if t is None else [t.stride(0), t.stride(1)]
-    return GdnSsmShape(B, T, D, N, G, _code(x.dtype), 1 if dt_softplus else 0, *strides)
+    if z is None:
+        zs = (0, 0)
+    else:
+        _rank("z", z, 3)
+        zs = z.stride()
+    xs, ds, bs, cs = x.stride(), dt.stride(), Bm.stride(), C.stride()
+    return GdnSsmShape(B, T, D, N, G, _code(x.dtype), 1 if dt_softplus else 0, xs[0], xs[1], ds[0], ds[1],
+                       zs[0], zs[1], bs[0], bs[1], cs[0], cs[1])
 
 
 def _ssm_check(s, x, dt, A, Bm, C, D, z, dt_bias, h, lens, dev):
     f32, io = torch.float32, x.dtype
-    rows = (s.B, s.T, s.D)
-    _check("x", x, rows, io, dev, tail=1)
-    _check("dt", dt, rows, io, dev, tail=1)
-    _check("z", z, rows, io, dev, tail=1)
-    _check("A", A, (s.D, s.N), f32, dev)
-    _check("Bm", Bm, (s.B, s.T, s.G, s.N), io, dev, tail=2)
-    _check("C", C, (s.B, s.T, s.G, s.N), io, dev, tail=2)
-    _check("D", D, (s.D,), f32, dev)
-    _check("dt_bias", dt_bias, (s.D,), f32, dev)
-    _check("h0", h, (s.B, s.D, s.N), f32, dev)
-    _check("lens", lens, (s.B,), torch.int32, dev)
+    B, T, Dc, N, G = s.B, s.T, s.D, s.N, s.G
+    rows, bc, each = (B, T, Dc), (B, T, G, N), (Dc,)
+    _check("x", x, rows, io, dev, 1)
+    _check("dt", dt, rows, io, dev, 1)
+    _check("z", z, rows, io, dev, 1)
+    _check("A", A, (Dc, N), f32, dev)
+    _check("Bm", Bm, bc, io, dev, 2)
+    _check("C", C, bc, io, dev, 2)
+    _check("D", D, each, f32, dev)
+    _check("dt_bias", dt_bias, each, f32, dev)
+    _check("h0", h, (B, Dc, N), f32, dev)
+    _check("lens", lens, (B,), torch.int32, dev)
 
 
 def gdn_ssm_fwd_workspace_bytes(shape: GdnSsmShape) -> int:
@@ -323,21 +330,30 @@ def gdn_ssm_step(x, dt, A, Bm, C, D=None, z=None, dt_bias=None, h=None, dt_softp
     dev = x.device
     if h is None:
         raise ValueError("gdn_ssm_step needs the state h")
-    for name, t, n in (("x", x, 2), ("dt", dt, 2), ("A", A, 2), ("Bm", Bm, 3), ("C", C, 3)):
-        _rank(name, t, n)
-    (B, Dc), (G, N), io = x.shape, Bm.shape[1:], x.dtype
+    _rank("x", x, 2)
+    _rank("Bm", Bm, 3)
+    (B, Dc), (_, G, N), io = x.shape, Bm.shape, x.dtype
     if G < 1 or Dc % G:
         raise ValueError(f"{Dc} channels do not divide into {G} groups")
-    for name, t, tail in (("x", x, 1), ("dt", dt, 1), ("z", z, 1)):
-        _check(name, t, (B, Dc), io, dev, tail)
-    _check("Bm", Bm, (B, G, N), io, dev, 2)
-    _check("C", C, (B, G, N), io, dev, 2)
-    _check("A", A, (Dc, N), torch.float32, dev)
-    _check("D", D, (Dc,), torch.float32, dev)
-    _check("dt_bias", dt_bias, (Dc,), torch.float32, dev)
-    _check("h", h, (B, Dc, N), torch.float32, dev)
-    s = GdnSsmShape(B, 1, Dc, N, G, _code(io), 1 if dt_softplus else 0, x.stride(0), 0, dt.stride(0), 0,
-                    0 if z is None else z.stride(0), 0, Bm.stride(0), 0, C.stride(0), 0)
+    row, bc, f32 = (B, Dc), (B, G, N), torch.float32
+    # (one expression where all is well, 3 us less than the checks one by one,
+    # which say what is wrong)
+    xs, ds, bs, cs = x.stride(), dt.stride(), Bm.stride(), C.stride()
+    if not (dt.shape == row and Bm.shape == bc and C.shape == bc and A.shape == (Dc, N) and h.shape == (B, Dc, N)
+            and io is dt.dtype is Bm.dtype is C.dtype and A.dtype is h.dtype is f32
+            and dev == dt.device == Bm.device == C.device == A.device == h.device
+            and xs[1] == ds[1] == bs[2] == cs[2] == 1 and bs[1] == cs[1] == N and A.is_contiguous() and h.is_contiguous()):
+        _check("x", x, row, io, dev, 1)
+        _check("dt", dt, row, io, dev, 1)
+        _check("Bm", Bm, bc, io, dev, 2)
+        _check("C", C, bc, io, dev, 2)
+        _check("A", A, (Dc, N), f32, dev)
+        _check("h", h, (B, Dc, N), f32, dev)
+    _check("z", z, row, io, dev, 1)
+    _check("D", D, (Dc,), f32, dev)
+    _check("dt_bias", dt_bias, (Dc,), f32, dev)
+    s = GdnSsmShape(B, 1, Dc, N, G, _code(io), 1 if dt_softplus else 0, xs[0], 0, ds[0], 0,
+                    0 if z is None else z.stride(0), 0, bs[0], 0, cs[0], 0)
     if y is None:
         y = x.new_empty((B, Dc))
     else:

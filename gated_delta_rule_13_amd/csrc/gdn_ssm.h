@@ -655,7 +655,9 @@ __global__ __launch_bounds__(64 * kParamSlices) void gdn_ssm_param_kernel(SsmPar
 
 // ---------------------------------------------------------------------------
 // One token: the state passes through memory once, which bounds it.  LP lanes
-// share a channel, four states to a lane.
+// share a channel, four states to a lane; a thread takes its channel's states
+// in R sequences, so that their loads are in flight together and A is read
+// once for them.
 struct SsmStepParams {
     SsmParams f;
     float* h;
@@ -663,57 +665,71 @@ struct SsmStepParams {
 };
 constexpr int kStepThreads = 256;
 
-template <bool BF, int LP>
+template <bool BF, int LP, int R>
 __global__ __launch_bounds__(kStepThreads) void gdn_ssm_step_kernel(SsmStepParams q) {
     const SsmParams& p = q.f;
-    const int64_t id = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
-    const int64_t bd = id / LP;
-    const int n0 = (int)(id % LP) * 4;
-    const bool on = bd < (int64_t)p.B * p.D;
-    const int64_t bdc = on ? bd : (int64_t)p.B * p.D - 1;
-    const int b = (int)(bdc / p.D), d = (int)(bdc % p.D), g = d / p.Dg;
-    float h[4], a[4], bm[4], cm[4];
-    const int64_t hi = bdc * p.N + n0, ai = (int64_t)d * p.N + n0;
-    const int64_t bi = b * p.bsb + (int64_t)g * p.N + n0, ci = b * p.csb + (int64_t)g * p.N + n0;
+    const unsigned id = blockIdx.x * kStepThreads + threadIdx.x;
+    const int d0 = (int)(id / LP), n0 = (int)(id % LP) * 4;
+    const bool on = d0 < p.D;
+    const int d = on ? d0 : p.D - 1, g = d / p.Dg;
     const bool piece = q.wide && n0 < p.N;
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, dskip = p.Dskip ? p.Dskip[d] : 0.f;
+    f32x4 a = zero4(), h[R];
+    float bm[R][4], cm[R][4], x[R], raw[R], z[R];
+    const int64_t ai = (int64_t)d * p.N + n0;
     if (piece) {
-        const f32x4 hv = *reinterpret_cast<const f32x4*>(q.h + hi), av = *reinterpret_cast<const f32x4*>(p.A + ai);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = hv[e], a[e] = av[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const bool in = n0 + e < p.N;
-        if (!piece) {
-            h[e] = in ? q.h[hi + e] : 0.f;
-            a[e] = in ? p.A[ai + e] : 0.f;
-        }
-        bm[e] = in ? load_one<BF>(p.Bm, bi + e) : 0.f;
-        cm[e] = in ? load_one<BF>(p.C, ci + e) : 0.f;
-    }
-    const float x = load_one<BF>(p.x, b * p.xsb + d);
-    const float s = ssm_step_size(load_one<BF>(p.dt, b * p.dsb + d) + (p.dt_bias ? p.dt_bias[d] : 0.f), p.softplus);
-    const float u = s * x;
-    float y = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        h[e] = fmaf(exp2_hw(s * (a[e] * kLog2e)), h[e], u * bm[e]);
-        y = fmaf(h[e], cm[e], y);
-    }
-#pragma unroll
-    for (int m = 1; m < LP; m *= 2) y += __shfl_xor(y, m, 64);
-    if (!on) return;
-    if (piece) {
-        *reinterpret_cast<f32x4*>(q.h + hi) = f32x4{h[0], h[1], h[2], h[3]};
+        a = *reinterpret_cast<const f32x4*>(p.A + ai);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n0 + e < p.N) q.h[hi + e] = h[e];
+        for (int e = 0; e < 4; ++e) a[e] = n0 + e < p.N ? p.A[ai + e] : 0.f;
     }
-    if (n0 == 0) {
-        y = fmaf(p.Dskip ? p.Dskip[d] : 0.f, x, y);
-        if (p.z) y *= silu(load_one<BF>(p.z, b * p.zsb + d));
-        store_one<BF>(p.y, bd, y);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t b = blockIdx.y * R + r < (unsigned)p.B ? blockIdx.y * R + r : p.B - 1;
+        const int64_t hi = (b * p.D + d) * p.N + n0;
+        const int64_t bi = b * p.bsb + (int64_t)g * p.N + n0, ci = b * p.csb + (int64_t)g * p.N + n0;
+        if (piece) {
+            h[r] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(q.h + hi));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[r][e] = n0 + e < p.N ? q.h[hi + e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = n0 + e < p.N;
+            bm[r][e] = in ? load_one<BF>(p.Bm, bi + e) : 0.f;
+            cm[r][e] = in ? load_one<BF>(p.C, ci + e) : 0.f;
+        }
+        x[r] = load_one<BF>(p.x, b * p.xsb + d);
+        raw[r] = load_one<BF>(p.dt, b * p.dsb + d) + bias;
+        z[r] = p.z ? load_one<BF>(p.z, b * p.zsb + d) : 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float s = ssm_step_size(raw[r], p.softplus), u = s * x[r];
+        float y = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            h[r][e] = fmaf(exp2_hw(s * (a[e] * kLog2e)), h[r][e], u * bm[r][e]);
+            y = fmaf(h[r][e], cm[r][e], y);
+        }
+#pragma unroll
+        for (int m = 1; m < LP; m *= 2) y += __shfl_xor(y, m, 64);
+        const int64_t b = blockIdx.y * R + r;
+        if (!on || b >= p.B) continue;
+        const int64_t hi = (b * p.D + d) * p.N + n0;
+        if (piece) {
+            __builtin_nontemporal_store(h[r], reinterpret_cast<f32x4*>(q.h + hi));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n0 + e < p.N) q.h[hi + e] = h[r][e];
+        }
+        if (n0 == 0) {
+            y = fmaf(dskip, x[r], y);
+            if (p.z) y *= silu(z[r]);
+            store_one<BF>(p.y, b * p.D + d, y);
+        }
     }
 }
 
