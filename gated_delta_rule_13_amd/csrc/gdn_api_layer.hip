@@ -415,7 +415,8 @@ gdn_status gdn_ssm_step(const gdn_ssm_shape* s, const void* x, const void* dt, c
     q.f.y = y;
     q.h = h;
     q.wide = s->N % 4 == 0 && aligned(h, 16) && aligned(A, 16);
-    // (the grid's second dimension counts sequences, or fours of them)
+    q.wide_bc = s->N % 4 == 0 && rows4(Bm, s->dtype, {s->b_stride_b}) && rows4(C, s->dtype, {s->c_stride_b});
+    // (the grid's second dimension counts sequences)
     if (s->B > 65535) return set_error(GDN_ERR_UNSUPPORTED, "B must be at most 65535");
     gdn::ssm_step_run(q, s->dtype == GDN_BF16, reinterpret_cast<hipStream_t>(stream));
     return gdn::launch_status();

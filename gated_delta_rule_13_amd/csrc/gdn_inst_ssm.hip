@@ -42,17 +42,10 @@ void bwd(const SsmParams& p, float* dA, void* dBm, void* dC, float* dD, float* d
                        dA, dD, dbias, NSA);
 }
 
-// Four sequences to a thread where that leaves the chip's 256 compute units a
-// workgroup each.
-template <int LP, int R>
-void step_rows(const SsmStepParams& q, hipStream_t st) {
-    hipLaunchKernelGGL((gdn_ssm_step_kernel<kBF, LP, R>), dim3(blocks((int64_t)q.f.D * LP, kStepThreads), blocks(q.f.B, R)),
-                       dim3(kStepThreads), 0, st, q);
-}
 template <int LP>
 void step(const SsmStepParams& q, hipStream_t st) {
-    if ((int64_t)blocks((int64_t)q.f.D * LP, kStepThreads) * blocks(q.f.B, 4) >= 256) step_rows<LP, 4>(q, st);
-    else step_rows<LP, 1>(q, st);
+    hipLaunchKernelGGL((gdn_ssm_step_kernel<kBF, LP>), dim3(blocks((int64_t)q.f.D * LP, kStepThreads), (unsigned)q.f.B),
+                       dim3(kStepThreads), 0, st, q);
 }
 }  // namespace
 

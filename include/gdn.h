@@ -356,6 +356,7 @@ typedef struct {
     int32_t B, T, D;          /* sequences, tokens, channels                   */
     int32_t N;                /* states per channel: 1 .. 64                   */
     int32_t G;                /* groups of B and C (D a multiple of G)         */
+                              /* (D and the strides of tokens: up to 2^24)     */
     int32_t dtype;            /* gdn_dtype of x, dt, Bm, C, z, y and their gradients */
     int32_t dt_softplus;      /* 1: dt passes through softplus, 0: as it is    */
     int64_t x_stride_b, x_stride_t;     /* x  [B, T, D]                        */
@@ -389,8 +390,8 @@ gdn_status gdn_ssm_fwd(const gdn_ssm_shape* s, const void* x, const void* dt, co
                        void* y, float* h_final,
                        void* workspace, size_t workspace_bytes, void* stream);
 
-/* One token of every sequence (T must be 1): gdn_ssm_fwd with the state h
- * [B, D, N] updated in place.  x, dt, z [B, D], Bm, C [B, G, N], rows their
+/* One token of every sequence (T must be 1, B at most 65535): gdn_ssm_fwd with
+ * the state h [B, D, N] updated in place.  x, dt, z [B, D], Bm, C [B, G, N], rows their
  * stride_b apart; y [B, D]. */
 gdn_status gdn_ssm_step(const gdn_ssm_shape* s, const void* x, const void* dt, const float* A,
                         const void* Bm, const void* C, const float* Dskip, const void* z,
