@@ -36,10 +36,9 @@ void bwd(const SsmParams& p, float* dA, void* dBm, void* dC, float* dD, float* d
     const int64_t tiles = (int64_t)p.G * p.tpg;
     summaries<NSA, true>(p, p.nseg, st);
     hipLaunchKernelGGL((gdn_ssm_bwd_kernel<kBF, NS, NB>), dim3((unsigned)(p.B * p.nseg * tiles)), dim3(64 * NB), 0, st, p);
-    hipLaunchKernelGGL((gdn_ssm_bc_kernel<kBF>), dim3(blocks((int64_t)p.B * p.T * p.G * 2 * NSA, kSumThreads)),
-                       dim3(kSumThreads), 0, st, p, dBm, dC, NSA);
-    hipLaunchKernelGGL((gdn_ssm_param_kernel<kBF>), dim3((unsigned)(tiles * (NSA + 2))), dim3(64 * kParamSlices), 0, st, p,
-                       dA, dD, dbias, NSA);
+    SsmSumParams q{p, dBm, dC, dA, dD, dbias, NSA, blocks((int64_t)p.B * p.T * p.G * 2 * NSA, kSumThreads)};
+    hipLaunchKernelGGL((gdn_ssm_grad_sum_kernel<kBF>), dim3(q.bc + (unsigned)(tiles * (NSA + 2))), dim3(kSumThreads), 0, st,
+                       q);
 }
 
 template <int LP>

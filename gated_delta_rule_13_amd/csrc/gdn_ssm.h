@@ -600,42 +600,55 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 ? 4 : 3) void gdn_ssm_bwd_kernel(S
     }
 }
 
-// dB and dC: the sum of the tiles' parts of a group, tiles ascending, rounded
-// once; zero behind a sequence's end.
-constexpr int kSumThreads = 256;
-template <bool BF>
-__global__ __launch_bounds__(kSumThreads) void gdn_ssm_bc_kernel(SsmParams p, void* dB, void* dC, int ns) {
-    const int64_t id = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
-    const int64_t per = (int64_t)p.B * p.T * p.G * 2 * ns;
-    if (id >= per) return;
-    const int n = (int)(id % ns), which = (int)(id / ns % 2);
-    const int64_t btg = id / (2 * ns);
-    const int g = (int)(btg % p.G);
-    const int64_t bt = btg / p.G;
-    if (n >= p.N) return;
-    float v = 0.f;
-    if (bt % p.T < seq_len(p.lens, (int)(bt / p.T), p.T)) {
-        const float* src = p.part_bc + (((int64_t)g * p.tpg * p.B * p.T + bt) * 2 + which) * ns + n;
-        const int64_t step = (int64_t)p.B * p.T * 2 * ns;
-#pragma unroll 4
-        for (int k = 0; k < p.tpg; ++k) v += src[k * step];
-    }
-    store_one<BF>(which ? dC : dB, (bt * p.G + g) * p.N + n, v);
-}
+// The gradients that sum over what the waves above share, in one launch.
+//   Workgroups [0, bc): dB and dC, the sum of the tiles' parts of a group,
+//     tiles ascending, rounded once; zero behind a sequence's end.
+//   The others, one for a (tile, state) and two for a tile's dDskip and
+//     ddt_bias: dA [D, N], dDskip [D], ddt_bias [D], the sum over sequences and
+//     segments, in kSumSlices slices of them (ascending) and the slices in
+//     order.
+struct SsmSumParams {
+    SsmParams f;
+    void *dB, *dC;
+    float *dA, *dD, *dbias;
+    int ns;                 // states of the layout
+    unsigned bc;
+};
+constexpr int kSumSlices = 8;
+constexpr int kSumThreads = 64 * kSumSlices;
 
-// dA [D, N], dDskip [D], ddt_bias [D]: the sum over sequences and segments, in
-// kParamSlices slices of them (ascending) and the slices in order.
-constexpr int kParamSlices = 8;
 template <bool BF>
-__global__ __launch_bounds__(64 * kParamSlices) void gdn_ssm_param_kernel(SsmParams p, float* dA, float* dD, float* dbias, int ns) {
-    __shared__ float sum[kParamSlices][64];
-    const int tiles = p.G * p.tpg, rows = ns + 2;
+__global__ __launch_bounds__(kSumThreads) void gdn_ssm_grad_sum_kernel(SsmSumParams q) {
+    const SsmParams& p = q.f;
+    const int ns = q.ns;
+    if (blockIdx.x < q.bc) {
+        const int64_t id = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
+        const int64_t per = (int64_t)p.B * p.T * p.G * 2 * ns;
+        if (id >= per) return;
+        const int n = (int)(id % ns), which = (int)(id / ns % 2);
+        const int64_t btg = id / (2 * ns);
+        const int g = (int)(btg % p.G);
+        const int64_t bt = btg / p.G;
+        if (n >= p.N) return;
+        float v = 0.f;
+        if (bt % p.T < seq_len(p.lens, (int)(bt / p.T), p.T)) {
+            const float* src = p.part_bc + (((int64_t)g * p.tpg * p.B * p.T + bt) * 2 + which) * ns + n;
+            const int64_t step = (int64_t)p.B * p.T * 2 * ns;
+#pragma unroll 8
+            for (int k = 0; k < p.tpg; ++k) v += src[k * step];
+        }
+        store_one<BF>(which ? q.dC : q.dB, (bt * p.G + g) * p.N + n, v);
+        return;
+    }
+    __shared__ float sum[kSumSlices][64];
+    const unsigned rows = (unsigned)ns + 2, id = blockIdx.x - q.bc;
+    const int tiles = p.G * p.tpg;
     const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
-    const int n = (int)(blockIdx.x % (unsigned)rows), tile = (int)(blockIdx.x / (unsigned)rows);
+    const int n = (int)(id % rows), tile = (int)(id / rows);
     const float* src = n < ns ? p.part_a + ((int64_t)tile * ns + n) * 64 + lane
                               : p.part_d + ((int64_t)tile * 2 + n - ns) * 64 + lane;
     const int64_t step = (int64_t)tiles * (n < ns ? ns : 2) * 64;
-    const int64_t all = (int64_t)p.B * p.nseg, per = (all + kParamSlices - 1) / kParamSlices;
+    const int64_t all = (int64_t)p.B * p.nseg, per = (all + kSumSlices - 1) / kSumSlices;
     const int64_t end = (slice + 1) * per < all ? (slice + 1) * per : all;
     float v = 0.f;
 #pragma unroll 8
@@ -646,11 +659,11 @@ __global__ __launch_bounds__(64 * kParamSlices) void gdn_ssm_param_kernel(SsmPar
     if (slice > 0 || c >= p.Dg) return;
     v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kParamSlices; ++k) v += sum[k][lane];
+    for (int k = 0; k < kSumSlices; ++k) v += sum[k][lane];
     const int64_t ch = (int64_t)(tile / p.tpg) * p.Dg + c;
-    if (n < p.N) dA[ch * p.N + n] = v;
-    else if (n == ns && dD) dD[ch] = v;
-    else if (n == ns + 1 && dbias) dbias[ch] = v;
+    if (n < p.N) q.dA[ch * p.N + n] = v;
+    else if (n == ns && q.dD) q.dD[ch] = v;
+    else if (n == ns + 1 && q.dbias) q.dbias[ch] = v;
 }
 
 // ---------------------------------------------------------------------------
