@@ -80,15 +80,17 @@ __device__ __forceinline__ char* row_at(void* p, int64_t i) {
 // the branch ends).
 constexpr uint32_t kOutside = 0x80000000u;
 __device__ __forceinline__ buf_t buffer_from(const void* base) { return buffer_over(base, 0x7fffffffu); }
+// (row: a byte offset that the whole wave shares, which costs no vector
+// instruction; off + row stays below 2^30)
 template <bool BF>
-__device__ __forceinline__ void buf_load_one(Raw<BF, 1>& r, buf_t b, uint32_t off) {
-    if constexpr (BF) r.w[0] = buf_load_bf16_bits(b, off);
-    else r.w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0);
+__device__ __forceinline__ void buf_load_one(Raw<BF, 1>& r, buf_t b, uint32_t off, uint32_t row = 0) {
+    if constexpr (BF) r.w[0] = (uint32_t)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(b, (int)off, (int)row, 0);
+    else r.w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, (int)row, 0);
 }
 template <bool BF>
-__device__ __forceinline__ void buf_store_one(buf_t b, uint32_t off, float v) {
-    if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)v), b, (int)off, 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), b, (int)off, 0, 0);
+__device__ __forceinline__ void buf_store_one(buf_t b, uint32_t off, uint32_t row, float v) {
+    if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)v), b, (int)off, (int)row, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), b, (int)off, (int)row, 0);
 }
 
 template <bool BF>
@@ -109,9 +111,12 @@ __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(
 // 1 / (1 + e^-x); e^-x overflows to infinity for x < -88.7, whose reciprocal
 // is the right 0.
 __device__ __forceinline__ float sigmoid(float x) { return rcp_hw(1.f + exp2_hw(-kLog2e * x)); }
+// x, with -infinity as the lowest number (a NaN becomes a number: it is for
+// products with what is NaN then too).
+__device__ __forceinline__ float above_inf(float x) { return __builtin_amdgcn_fmed3f(x, -__FLT_MAX__, __builtin_inff()); }
 // x sigmoid(x).  The bound keeps -infinity times 0 from being NaN; a NaN comes
 // through sigmoid.
-__device__ __forceinline__ float silu(float x) { return __builtin_fmaxf(x, -__FLT_MAX__) * sigmoid(x); }
+__device__ __forceinline__ float silu(float x) { return above_inf(x) * sigmoid(x); }
 // silu(x) and silu'(x) = s + x s (1 - s), s = sigmoid(x), from e = e^-|x| and
 // r = 1 / (1 + e): s is r or e r by x's sign, and s (1 - s) = e r^2 either way,
 // with no cancellation.  At the infinities the limits (0 or x, 0 or 1).
@@ -119,7 +124,7 @@ __device__ __forceinline__ void silu_both(float x, float& val, float& slope) {
     const float e = exp2_hw(-kLog2e * __builtin_fabsf(x));
     const float r = rcp_hw(1.f + e), er = e * r;
     const float s = x < 0.f ? er : r;
-    val = __builtin_fmaxf(x, -__FLT_MAX__) * s;
+    val = above_inf(x) * s;
     slope = fmaf(__builtin_amdgcn_fmed3f(x, -__FLT_MAX__, __FLT_MAX__), er * r, s);
 }
 // ln(1 + e^x) = max(x, 0) + ln(1 + e), e = e^-|x| <= 1.  With w = 1 + e as it
@@ -131,7 +136,9 @@ __device__ __forceinline__ void silu_both(float x, float& val, float& slope) {
 __device__ __forceinline__ float softplus(float x) {
     const float e = exp2_hw(-kLog2e * __builtin_fabsf(x));
     const float w = 1.f + e, d = e - (w - 1.f);
-    return __builtin_fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(w), 1.f / kLog2e, d);
+    // (max(x, 0) as integers: one instruction; a NaN is in d)
+    const int bits = __builtin_bit_cast(int, x), top = bits > 0 ? bits : 0;
+    return __builtin_bit_cast(float, top) + fmaf(__builtin_amdgcn_logf(w), 1.f / kLog2e, d);
 }
 
 // Moves and sums between lanes without LDS: DPP within a row of 16 lanes, and

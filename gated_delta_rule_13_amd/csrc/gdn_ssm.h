@@ -133,10 +133,13 @@ struct StagedBC {
 template <bool BF>
 struct Column {
     Raw<BF, 1> v[kTok];
-    // base: element of the wave's first channel, off: the lane's byte offset
+    // base: element of the sequence's first row and the wave's first channel,
+    // off: the lane's byte offset
     __device__ __forceinline__ void load(const void* p, int64_t base, int64_t st, uint32_t off, int t, int t1) {
+        const buf_t rows = buffer_from(row_at<BF>(p, base + t * st));
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) v[i].load_at(row_at<BF>(p, base + (t + i < t1 ? t + i : t1 - 1) * st), off);
+        for (int i = 0; i < kTok; ++i)
+            buf_load_one<BF>(v[i], rows, off, (uint32_t)(t + i < t1 ? i : t1 - 1 - t) * (uint32_t)st * (BF ? 2 : 4));
     }
 };
 
@@ -187,7 +190,7 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
     // (without a gate x is loaded in its place, and not used)
     const void* zsrc = p.z ? p.z : p.x;
     const int64_t zb = p.z ? w.b * p.zsb + w.c0 : xb, zst = p.z ? p.zst : p.xst;
-    const uint32_t off = (uint32_t)(w.c - w.c0) * (BF ? 2 : 4);
+    const uint32_t off = (uint32_t)(w.c - w.c0) * (BF ? 2 : 4), out = w.on ? off : kOutside;
     float a[NS], h[NS];
     load_decay<NS>(a, p, w.c);
     if (p.nseg > 1) load_sum<NS>(h, p.sum_e, w.unit, lane);
@@ -220,15 +223,14 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
             const buf_t yr = buffer_from(row_at<BF>(p.y, y0 + (int64_t)t * p.D));
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
-                const float u = s[i] == 0.f ? 0.f : s[i] * x[i];
+                const float u = s[i] * x[i];
                 float y = dskip * x[i];
 #pragma unroll
                 for (int n = 0; n < NS; ++n) {
                     h[n] = fmaf(exp2_hw(s[i] * a[n]), h[n], u * bc[buf][i][0][n]);
                     y = fmaf(h[n], bc[buf][i][1][n], y);
                 }
-                buf_store_one<BF>(yr, w.on && t + i < w.t1 ? (uint32_t)i * (uint32_t)p.D * (BF ? 2 : 4) + off : kOutside,
-                                  y * gate[i]);
+                buf_store_one<BF>(yr, t + i < w.t1 ? out : kOutside, (uint32_t)i * (uint32_t)p.D * (BF ? 2 : 4), y * gate[i]);
                 pin(h);
             }
         }
@@ -285,7 +287,7 @@ __global__ __launch_bounds__(64, NS <= 16 && !GRAD ? 3 : 1) void gdn_ssm_sum_ker
                 const bool in = t + i < w.t1;
                 const float raw = nd.v[i].get(0) + bias, soft = softplus(raw);
                 s[i] = in ? (p.softplus ? soft : raw) : 0.f;
-                u[i] = in ? s[i] * nx.v[i].get(0) : 0.f;
+                u[i] = s[i] * nx.v[i].get(0);
                 g[i] = 0.f;
                 if (GRAD) {
                     const float dy = ng.v[i].get(0), open = silu(nz.v[i].get(0));
