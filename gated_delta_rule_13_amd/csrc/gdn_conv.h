@@ -2,12 +2,15 @@
 //
 //     p_t = bias + sum_{j < W} w_j x_{t-W+1+j},   y_t = silu(p_t)
 //
-// with the W-1 rows before the first token taken from the state.  Two passes
-// of x through memory (read once, y written once) bound it: a thread takes V
-// neighbouring channels (16 bytes of a row) down a tile of rows, holds the
-// last W-1 rows in registers, and has the next kRows rows in flight while it
-// works on the current ones.
+// with the W-1 rows before the first token taken from the state.  Memory bounds
+// it (x read once, y written once): a thread takes V neighbouring channels (16
+// bytes of a row) down a tile of rows, holds the last W-1 rows in registers,
+// and has the next kConvRows rows in flight while it works on the current ones.
+// Measured at 4 x 4096 x 2048 in bf16, 4 taps: 30 us for 134 MB (4.5 TB/s, where
+// a large copy reaches 5.1).
 #pragma once
+#include <type_traits>
+
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -121,7 +124,8 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_fwd_kernel(ConvParams p
                     float a = wt.b[v];
 #pragma unroll
                     for (int j = 0; j < W; ++j) a = fmaf(wt.w[j][v], win[i + j].get(v), a);
-                    f[v] = p.silu ? silu(a) : a;
+                    const float act = silu(a);
+                    f[v] = p.silu ? act : a;
                 }
                 store_vec<BF, V>(p.y, y0 + (int64_t)(t + i) * p.hd, f);
             }
@@ -143,7 +147,13 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_fwd_kernel(ConvParams p
 // rows need (computed again by the next tile's wave).  x and dy are read
 // once and dx written once, which bounds it.  The sums over rows stay in
 // registers, are added over the workgroup's tiles in LDS, and written as one
-// row of partial sums for each workgroup.
+// row of partial sums for each workgroup.  Measured at 4 x 4096 x 2048 in bf16,
+// 4 taps: 52 us for 201 MB (3.9 TB/s) and 5 us for the sum of the partial rows.
+// About 31 vector instructions an element take as long as the memory, so the
+// waves matter: two channels to a thread (117 registers, four waves on a
+// vector unit) took 52 us where four (205 registers) took 59 and eight spilled;
+// branches on the activation and at the ends of tiles inside the row loop cost
+// 8 us more.
 struct ConvBwdParams {
     ConvParams f;
     const void* dy;
@@ -227,45 +237,49 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
                     ng[i].load(gr + tt * gs + goff, 0);
                 }
             }
+            // EDGE: rows at the ends of the tile or the sequence are among them
+            auto rows = [&](auto edge) {
+                constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
-            for (int i = 0; i < kConvRows; ++i) {
-                const int td = t + i - (W - 1);
-                // (rows behind t2 repeat the last one: their dp is 0)
-                const bool live = t + i < t2, mine = t + i < t1;
-                float f[V];
+                for (int i = 0; i < kConvRows; ++i) {
+                    const int td = t + i - (W - 1);
+                    // (rows behind t2 repeat the last one: their dp is 0)
+                    const bool live = !EDGE || t + i < t2, mine = !EDGE || t + i < t1;
+                    float f[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float d = g[i].get(v);
-                    if (p.silu) {
+                    for (int v = 0; v < V; ++v) {
                         float a = wt.b[v], val, slope;
 #pragma unroll
                         for (int j = 0; j < W; ++j) a = fmaf(wt.w[j][v], win[i + j].get(v), a);
                         silu_both(a, val, slope);
-                        d *= slope;
+                        const float d = g[i].get(v) * (p.silu ? slope : 1.f);
+                        dp[W - 1 + i][v] = live ? d : 0.f;
+                        const float own = mine ? d : 0.f;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) acc[j][v] = fmaf(own, win[i + j].get(v), acc[j][v]);
+                        acc[W][v] += own;
+                        f[v] = 0.f;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) f[v] = fmaf(wt.w[j][v], dp[i + W - 1 - j][v], f[v]);
                     }
-                    dp[W - 1 + i][v] = live ? d : 0.f;
-                    const float own = mine ? d : 0.f;
+                    if (!EDGE) {
+                        store_at<BF, V>(dr + td * ds, off, f);
+                    } else if (td >= t0 ? td < tz : (td < 0 && t0 == 0)) {
+                        // the final state's rows are those at times n - W + 1 .. n - 1
+                        const int k = td - (n - (W - 1));
+                        if (q.ds1 && k >= 0 && td < n) {
+                            Raw<BF, V> e;
+                            e.load(q.ds1, ((int64_t)b * (W - 1) + k) * p.D + c);
 #pragma unroll
-                    for (int j = 0; j < W; ++j) acc[j][v] = fmaf(own, win[i + j].get(v), acc[j][v]);
-                    acc[W][v] += own;
-                    f[v] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) f[v] = fmaf(wt.w[j][v], dp[i + W - 1 - j][v], f[v]);
-                }
-                const bool state_row = td < 0;
-                if (td >= t0 ? td < tz : (state_row && t0 == 0)) {
-                    // the final state's rows are those at times n - W + 1 .. n - 1
-                    const int k = td - (n - (W - 1));
-                    if (q.ds1 && k >= 0 && td < n) {
-                        Raw<BF, V> e;
-                        e.load(q.ds1, ((int64_t)b * (W - 1) + k) * p.D + c);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) f[v] += e.get(v);
+                            for (int v = 0; v < V; ++v) f[v] += e.get(v);
+                        }
+                        if (td >= 0) store_at<BF, V>(dr + td * ds, off, f);
+                        else if (q.ds0) store_vec<BF, V>(q.ds0, ((int64_t)b * (W - 1) + td + W - 1) * p.D + c, f);
                     }
-                    if (!state_row) store_at<BF, V>(dr + td * ds, off, f);
-                    else if (q.ds0) store_vec<BF, V>(q.ds0, ((int64_t)b * (W - 1) + td + W - 1) * p.D + c, f);
                 }
-            }
+            };
+            if (t >= t0 + W - 1 && t + kConvRows <= t1 && (!q.ds1 || t + kConvRows <= n - (W - 1))) rows(std::false_type());
+            else rows(std::true_type());
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) {
                 win[i] = win[kConvRows + i];

@@ -6,14 +6,18 @@
 //
 // The decay differs for every channel and state, so a chunk of tokens is no
 // product of matrices (unlike the delta rule's): the work is one exponential
-// and four multiply-adds for each (token, channel, state), on the vector
-// units, against 8 bytes of memory for each (token, channel) in bf16.  With 16
-// states the vector units bound it.
+// (two issue slots) and four multiply-adds for each (token, channel, state),
+// on the vector units, against 8 bytes of memory for each (token, channel) in
+// bf16.  With 16 states the vector units bound it: 96 issue slots a (token,
+// channel) for the states and about 35 for the step size, gate and skip.
 //
 // A lane holds one channel with all its states in registers, so the sum over
 // states needs no other lane.  Bm_t and C_t are the same for all channels of a
-// group: one wave stages them in LDS as fp32, kTok tokens ahead, and every
-// lane reads them at the same address.
+// group: the wave stages them in LDS as fp32, kTok tokens ahead, and every lane
+// reads them at the same address (reading none of them changes nothing in the
+// time).  A lane for each state instead (16 lanes a channel, no segments below)
+// was built and took 231 us or more for what follows in 135, for the moves
+// between lanes.
 //
 // Few channels on long sequences leave the chip empty, so the tokens are cut
 // into segments.  The recurrence is linear in the state, and a segment acts
@@ -23,7 +27,10 @@
 //   gdn_ssm_chain_kernel    the state that enters each segment, one after
 //                           another
 //   gdn_ssm_fwd_kernel      the outputs (all segments at once)
-// which costs the exponentials twice.
+// which costs the exponentials twice.  Measured at 4 x 4096 x 2048 with 16
+// states, bf16, gated: 101 + 8 + 135 us (24 segments), the last two thirds of
+// what the vector units' issue rate would allow at 2.4 GHz, and at 1 x 32768 x
+// 1024: 101 + 17 + 135 us.
 #pragma once
 #include "gdn_layer.h"
 
@@ -330,10 +337,10 @@ __global__ __launch_bounds__(64, NS <= 16 && !GRAD ? 3 : 1) void gdn_ssm_sum_ker
 // each segment; sum_r the gradient of the state that leaves it, from the last
 // segment to the first (by the second half of the threads).  One thread for a
 // (sequence, tile, state, lane); kAhead segments' summaries are in flight.
-constexpr int kChainThreads = 256;
+constexpr int kChainThreads = 64;
 template <int NS, bool GRAD>
 __global__ __launch_bounds__(kChainThreads) void gdn_ssm_chain_kernel(SsmParams p) {
-    constexpr int kAhead = 16;
+    constexpr int kAhead = 32;
     const unsigned tiles = (unsigned)(p.G * p.tpg);
     const int64_t per_seq = (int64_t)tiles * NS * 64, all = p.B * per_seq;
     int64_t id = (int64_t)blockIdx.x * kChainThreads + threadIdx.x;
@@ -414,10 +421,15 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // tokens from the last to the first: the state at the group's start (from zero,
 // as the summaries left it, and the decayed state that entered the segment),
 // the group's states into registers, then the gradient backwards.  The decays
-// are computed again on the way back: holding them too would leave room for
-// one wave on a vector unit instead of two.  More than 16 states are split
-// over the workgroup's NB waves, 16 each; what sums over states (du, ds, y) is
-// then added through LDS.
+// are computed again on the way back: holding them too costs a wave on each
+// vector unit (277 us for 251 below).  The states are split over the
+// workgroup's NB waves, NS each; what sums over states (du, ds, y) is added
+// through LDS.  Measured at 2 x 4096 x 2048 with 16 states, bf16, gated, all
+// launches 380 us: summaries 103, chain 16, this kernel 251 (four states to a
+// wave; eight took 299, all 16 in one wave 322 and spilled), the sums over
+// tiles and segments 11.  About 27 issue slots for a (token, channel, state)
+// with its share of the rest bound it, two fifths of them in the sums over
+// channels.
 template <bool BF, int NS, int NB>
 __global__ __launch_bounds__(64 * NB, NS <= 4 ? 4 : 3) void gdn_ssm_bwd_kernel(SsmParams p) {
     constexpr int NSA = NS * NB;                     // states of the layout
