@@ -145,15 +145,18 @@ gdn_status validate(const gdn_ssm_shape* s) {
         if (v < 0) return set_error(GDN_ERR_BAD_SHAPE, "strides must be >= 0");
     // (the kernels address the rows of a group of tokens by 32-bit offsets)
     constexpr int64_t kMaxRow = 1 << 24;
-    for (int64_t v : {(int64_t)s->D, s->x_stride_t, s->dt_stride_t, s->z_stride_t, s->b_stride_t, s->c_stride_t})
-        if (v > kMaxRow) return set_error(GDN_ERR_UNSUPPORTED, "D and the strides of tokens must be at most 2^24");
+    if (s->D > kMaxRow) return set_error(GDN_ERR_UNSUPPORTED, "D must be at most 2^24");
+    if (s->T > 1)
+        for (int64_t v : {s->x_stride_t, s->dt_stride_t, s->z_stride_t, s->b_stride_t, s->c_stride_t})
+            if (v > kMaxRow) return set_error(GDN_ERR_UNSUPPORTED, "strides of tokens must be at most 2^24");
     gdn_status st = check_counts(s->B, s->T, (int64_t)s->D * s->N);
     if (st != GDN_OK) return st;
-    // (sequences x segments of at least 8 tokens x tiles of 64 channels, and
-    // the threads of the sums over tiles)
+    // the largest grids: sequences x segments of at least 8 tokens x tiles of
+    // 64 channels; the chains, a workgroup for 64 states of a tile, both ways;
+    // the sums over tiles and segments
     const int64_t tiles = (int64_t)s->G * ceil_div(s->D / s->G, 64);
-    if ((long double)s->B * ceil_div(s->T, 8) * tiles > kMaxGrid ||
-        (long double)s->B * s->T * s->G * 2 * 64 / 256 > kMaxGrid)
+    if ((long double)s->B * ceil_div(s->T, 8) * tiles > kMaxGrid || (long double)s->B * tiles * 2 * 64 > kMaxGrid ||
+        (long double)s->B * s->T * s->G * 2 * 64 / gdn::kSumThreads + (long double)tiles * 66 > kMaxGrid)
         return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
     return GDN_OK;
 }

@@ -176,7 +176,7 @@ __device__ __forceinline__ void store_sum(float* s, const float (&h)[NS], int64_
 // staged tokens in an unrolled loop; without this the compiler reads every
 // token's Bm and C at once, computes every decay first, leaves sums that are
 // needed only at the end for last, and so holds hundreds of registers
-// (gradient kernel: 2.3 ms and spills where it now takes a fourth).  The
+// (the gradient's summaries: 403 registers and 178 us for 177 and 107).  The
 // states of one token already are NS independent chains.
 template <int N>
 __device__ __forceinline__ void pin(float (&v)[N]) {

@@ -76,7 +76,8 @@ BAD_CONV = [(dict(B=0), 2), (dict(T=0), 2), (dict(D=0), 2), (dict(H=0), 2), (dic
             (dict(B=2 ** 31 - 1, T=2 ** 31 - 1, D=2 ** 31 - 2), 2)]
 BAD_SSM = [(dict(B=0), 2), (dict(T=-1), 2), (dict(D=0), 2), (dict(N=0), 2), (dict(G=0), 2), (dict(G=3), 2),
            (dict(dtype=-1), 3), (dict(N=65), 4), (dict(dt_softplus=3), 4), (dict(z_stride_b=-1), 2),
-           (dict(c_stride_t=-5), 2), (dict(B=2 ** 30, T=2 ** 20, D=2), 2)]
+           (dict(c_stride_t=-5), 2), (dict(B=2 ** 30, T=2 ** 20, D=2), 2), (dict(D=2 ** 25), 4),
+           (dict(G=2 ** 22, D=2 ** 22, B=1000), 4)]
 BAD_NORM = [(dict(B=0), 2), (dict(T=0), 2), (dict(G=0), 2), (dict(d=0), 2), (dict(x_dtype=5), 3), (dict(o_dtype=-1), 3),
             (dict(d=4097), 4), (dict(center=2), 4), (dict(w_per_group=-1), 4), (dict(silu=4), 4), (dict(eps=0.0), 2),
             (dict(eps=float("nan")), 2), (dict(x_stride_g=-1), 2), (dict(z_stride_t=-1), 2)]
@@ -103,6 +104,16 @@ def test_missing_and_misaligned_arguments(lib_nogpu, entry):  # noqa: F811
         assert call(lib_nogpu, entry, shape(), **{name: ODD}) == 4, name
     if "step" in entry:
         assert call(lib_nogpu, entry, shape(T=2), x=ODD) == 2
+
+
+def test_far_rows(lib_nogpu):  # noqa: F811
+    """Strides of tokens past what a group's 32-bit offsets reach."""
+    for name in ("x", "dt", "z", "b", "c"):
+        kw = {name + "_stride_t": 2 ** 24 + 1}
+        assert call(lib_nogpu, "gdn_ssm_fwd", ssm_shape(**kw), x=ODD) == 4
+        assert "strides" in lib_nogpu.gdn_last_error().decode()
+        assert lib_nogpu.gdn_ssm_fwd_workspace_bytes(ctypes.byref(ssm_shape(T=1, **kw))) == 0
+    assert call(lib_nogpu, "gdn_ssm_step", ssm_shape(T=1, B=65536)) == 4
 
 
 def test_gradient_of_the_gate_goes_with_the_gate(lib_nogpu):  # noqa: F811

@@ -161,6 +161,54 @@ def test_two_graphs_at_once_and_streams():
     assert torch.equal(y, gdn.gdn_conv_fwd(a["proj"][:, :, :D], a["w"], a["b"])[0])
 
 
+def test_every_entry_on_another_stream():
+    """Calls with a stream argument, while another stream is current: the same
+    bits, and the outputs belong to that stream."""
+    a = layer_args(9, T=70)
+    D = a["w"].shape[0]
+    x, z = a["proj"][:, :, :D], a["proj"][:, :, D:].unflatten(2, (-1, 32))
+    Bm, C = a["bc"][:, :, :1], a["bc"][:, :, 1:]
+    u, st = gdn.gdn_conv_fwd(x, a["w"], a["b"])
+    s, h = gdn.gdn_ssm_fwd(u, a["dt"], a["A"], Bm, C, a["D"], None, a["bias"])
+    heads = s.unflatten(2, (-1, 32))
+    calls = [
+        lambda **k: gdn.gdn_conv_fwd(x, a["w"], a["b"], **k),
+        lambda **k: gdn.gdn_conv_bwd(u, x, a["w"], a["b"], **k),
+        lambda **k: gdn.gdn_conv_step(x[:, 0], a["w"], a["b"], st.clone(), **k),
+        lambda **k: gdn.gdn_ssm_fwd(u, a["dt"], a["A"], Bm, C, a["D"], None, a["bias"], **k),
+        lambda **k: gdn.gdn_ssm_bwd(s, u, a["dt"], a["A"], Bm, C, a["D"], None, a["bias"], **k),
+        lambda **k: gdn.gdn_ssm_step(u[:, 0], a["dt"][:, 0], a["A"], Bm[:, 0], C[:, 0], a["D"], None, a["bias"],
+                                     h=h.clone(), **k),
+        lambda **k: gdn.gdn_norm_fwd(heads, a["norm"], None, z, **k),
+        lambda **k: gdn.gdn_norm_bwd(a["dy"], heads, a["norm"], None, z, **k),
+    ]
+    side = torch.cuda.Stream()
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        got = call(stream=side)
+        side.synchronize()
+        flat = lambda r: list(r.values()) if isinstance(r, dict) else list(r) if isinstance(r, tuple) else [r]  # noqa: E731
+        for g, w in zip(flat(got), flat(want)):
+            assert torch.equal(g, w)
+
+
+def test_not_a_number_stays_in_its_sequence():
+    """NaN and infinity in one sequence's inputs reach that sequence's outputs
+    only (and the parameters' gradients, which sum over all)."""
+    a = layer_args(10, B=3, T=70)
+    D = a["w"].shape[0]
+    bad = dict(a, proj=a["proj"].clone(), dt=a["dt"].clone(), bc=a["bc"].clone())
+    bad["proj"][1, 20] = float("nan")
+    bad["bc"][1, 30] = float("inf")
+    got, want = layer(bad), layer(a)
+    for k in ("y", "h", "st", "dz", "sdx", "sddt", "sdB", "sdC", "cdx"):
+        for i in (0, 2):
+            assert torch.equal(got[k][i], want[k][i]), k
+    assert not torch.isfinite(got["y"][1].float()).all()
+    assert torch.equal(got["y"][1, :17], want["y"][1, :17])       # (rows before it, too)
+
+
 def test_prompt_then_tokens_of_a_state_space_layer():
     """A padded batch's prompt, then tokens on the states it left: as the
     reference on each sequence's own tokens."""

@@ -158,6 +158,15 @@ def test_step(dtype, B, D, N, G, full):
     ref.close("h", state, wh)
 
 
+def test_strides_of_a_single_row():
+    """With one token the stride between tokens is never used: any will do."""
+    a = ref.dev(inputs(2, 1, 20, 16, 1, F32, 3))
+    y, h = gdn.gdn_ssm_fwd(**a)
+    far = a["x"].as_strided((2, 1, 20), (20, 1 << 30, 1))
+    y2, h2 = gdn.gdn_ssm_fwd(**{**a, "x": far})
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+
+
 def test_step_unaligned_state():
     """A state at an odd address takes the narrow loads."""
     a = inputs(3, 1, 20, 16, 1, F32, 3)
