@@ -66,7 +66,7 @@ void GDN_SSM_NAME(ssm_fwd_run)(const SsmParams& p, hipStream_t st) {
 void GDN_SSM_NAME(ssm_bwd_run)(const SsmParams& p, float* dA, void* dBm, void* dC, float* dD, float* dbias, hipStream_t st) {
     switch (ssm_states(p.N)) {
         case 4: return bwd<4, 1>(p, dA, dBm, dC, dD, dbias, st);
-        case 8: return bwd<8, 1>(p, dA, dBm, dC, dD, dbias, st);
+        case 8: return bwd<4, 2>(p, dA, dBm, dC, dD, dbias, st);
         case 16: return bwd<4, 4>(p, dA, dBm, dC, dD, dbias, st);
         case 32: return bwd<8, 4>(p, dA, dBm, dC, dD, dbias, st);
         default: return bwd<8, 8>(p, dA, dBm, dC, dD, dbias, st);

@@ -502,8 +502,9 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 ? 4 : 3) void gdn_ssm_bwd_kernel(S
             float val, slope;
             silu_both(rz[j].get(0), val, slope);
             el[kS][i][lane] = in ? (p.softplus ? soft : raw) : 0.f;
-            el[kX][i][lane] = in ? rx[j].get(0) : 0.f;
-            el[kGy][i][lane] = in ? (p.z ? dy * val : dy) : 0.f;
+            // (lanes without a channel add nothing to the sums over channels)
+            el[kX][i][lane] = in && w.on ? rx[j].get(0) : 0.f;
+            el[kGy][i][lane] = in && w.on ? (p.z ? dy * val : dy) : 0.f;
             el[kZs][i][lane] = in ? dy * slope : 0.f;
             el[kSg][i][lane] = p.softplus ? slope_soft : 1.f;
         }
@@ -535,38 +536,43 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 ? 4 : 3) void gdn_ssm_bwd_kernel(S
                 }
             }
         };
+        // kSum tokens' sums over the channels at once: 16 registers, after the
+        // first step between lanes the terms of dB in the lower half of the
+        // wave and of dC in the upper
+        constexpr int kSum = 16 / NS;
 #pragma unroll
-        for (int i = kTok - 1; i >= 0; --i) {
-            // sums over the channels: the terms of dB in the lower half of the
-            // wave and of dC in the upper after the first step between lanes
-            float v[NS], y = 0.f, du = 0.f, ds = 0.f;
-            const float si = el[kS][i][lane], gy = el[kGy][i][lane], u = si * el[kX][i][lane];
-            const float ul = w.on ? u : 0.f, gl = w.on ? gy : 0.f;
+        for (int i0 = kTok - kSum; i0 >= 0; i0 -= kSum) {
+            float v[16];
 #pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                const float c = bc[i][1][n];
-                g[n] = fmaf(c, gy, g[n]);
-                v[n] = swap32_add(g[n] * ul, gl * hs[i][n]);
-                y = fmaf(hs[i][n], c, y);
-                du = fmaf(g[n], bc[i][0][n], du);
-                g[n] *= exp2_hw(si * a[n]);
-                const float q = g[n] * (i > 0 ? hs[i > 0 ? i - 1 : 0][n] : start[blk][n][lane]);
-                ds = fmaf(q, a[n], ds);
-                da[n] = fmaf(q, si, da[n]);
+            for (int i = i0 + kSum - 1; i >= i0; --i) {
+                float y = 0.f, du = 0.f, ds = 0.f;
+                const float si = el[kS][i][lane], gy = el[kGy][i][lane], u = si * el[kX][i][lane];
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    const float c = bc[i][1][n];
+                    g[n] = fmaf(c, gy, g[n]);
+                    v[(i - i0) * NS + n] = swap32_add(g[n] * u, gy * hs[i][n]);
+                    y = fmaf(hs[i][n], c, y);
+                    du = fmaf(g[n], bc[i][0][n], du);
+                    g[n] *= exp2_hw(si * a[n]);
+                    const float q = g[n] * (i > 0 ? hs[i > 0 ? i - 1 : 0][n] : start[blk][n][lane]);
+                    ds = fmaf(q, a[n], ds);
+                    da[n] = fmaf(q, si, da[n]);
+                }
+                pin(g);
+                pin(da);
+                if (NB > 1) {
+                    cross[blk][i][lane] = y;
+                    cross[blk][kTok + i][lane] = du;
+                    cross[blk][2 * kTok + i][lane] = ds;
+                } else {
+                    finish(i, y, du, ds);
+                }
             }
-            pin(g);
-            pin(da);
-            const float sum = row_sums<NS>(v, lane);
-            constexpr int kDup = 32 / NS;
-            if (lane % kDup == 0 && t + i < w.t1)
-                p.part_bc[((((int64_t)w.tile * p.B + w.b) * p.T + t + i) * 2 + lane / 32) * NSA + n0 + lane % 32 / kDup] = sum;
-            if (NB > 1) {
-                cross[blk][i][lane] = y;
-                cross[blk][kTok + i][lane] = du;
-                cross[blk][2 * kTok + i][lane] = ds;
-            } else {
-                finish(i, y, du, ds);
-            }
+            const float sum = row_sums<16>(v, lane);
+            const int k = lane % 32 / 2, tt = t + i0 + k / NS;
+            if (lane % 2 == 0 && tt < w.t1)
+                p.part_bc[((((int64_t)w.tile * p.B + w.b) * p.T + tt) * 2 + lane / 32) * NSA + n0 + k % NS] = sum;
         }
         if (NB > 1) {
             __syncthreads();
