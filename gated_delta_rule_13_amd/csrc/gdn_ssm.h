@@ -420,19 +420,19 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // A wave takes 64 channels of one segment and goes through its groups of kTok
 // tokens from the last to the first: the state at the group's start (from zero,
 // as the summaries left it, and the decayed state that entered the segment),
-// the group's states into registers, then the gradient backwards.  The decays
-// are computed again on the way back: holding them too costs a wave on each
-// vector unit (277 us for 251 below).  The states are split over the
-// workgroup's NB waves, NS each; what sums over states (du, ds, y) is added
-// through LDS.  Measured at 2 x 4096 x 2048 with 16 states, bf16, gated, all
-// launches 380 us: summaries 103, chain 16, this kernel 251 (four states to a
-// wave; eight took 299, all 16 in one wave 322 and spilled), the sums over
-// tiles and segments 11.  About 27 issue slots for a (token, channel, state)
-// with its share of the rest bound it, two fifths of them in the sums over
-// channels.
+// the group's states and decays into registers, then the gradient backwards.
+// The states are split over the workgroup's NB waves, NS each; what sums over
+// states (du, ds, y) is added through LDS.  Measured at 2 x 4096 x 2048 with 16
+// states, bf16, gated, all launches 363 us: summaries 103, chain 16, this
+// kernel 229 (four states to a wave, held decays; computed again 238; eight
+// states to a wave took 299 when four took 256, all 16 in one wave 322), the
+// sums over tiles and segments 11.  The vector units are busy nine tenths of
+// the time: about 26 issue slots for a (token, channel, state) with its share
+// of the rest, two fifths of them in the sums over channels.
 template <bool BF, int NS, int NB>
-__global__ __launch_bounds__(64 * NB, NS <= 4 ? 4 : 3) void gdn_ssm_bwd_kernel(SsmParams p) {
+__global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 ? 4 : 3) void gdn_ssm_bwd_kernel(SsmParams p) {
     constexpr int NSA = NS * NB;                     // states of the layout
+    constexpr bool HOLD = NS <= 4;                   // the group's decays stay in registers too
     __shared__ __align__(16) float bc_all[NB][kTok][2][NS];
     __shared__ float el[5][kTok][64];
     __shared__ float start[NB][NS][64];
@@ -509,15 +509,18 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 ? 4 : 3) void gdn_ssm_bwd_kernel(S
             el[kSg][i][lane] = p.softplus ? slope_soft : 1.f;
         }
         __syncthreads();
-        float hs[kTok][NS];
+        float hs[kTok][NS], decays[kTok][HOLD ? NS : 1];
 #pragma unroll
         for (int n = 0; n < NS; ++n) start[blk][n][lane] = h[n];
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
             const float si = el[kS][i][lane], u = si * el[kX][i][lane];
 #pragma unroll
-            for (int n = 0; n < NS; ++n)
-                hs[i][n] = fmaf(exp2_hw(si * a[n]), i > 0 ? hs[i > 0 ? i - 1 : 0][n] : h[n], u * bc[i][0][n]);
+            for (int n = 0; n < NS; ++n) {
+                const float decay = exp2_hw(si * a[n]);
+                hs[i][n] = fmaf(decay, i > 0 ? hs[i > 0 ? i - 1 : 0][n] : h[n], u * bc[i][0][n]);
+                if (HOLD) decays[i][HOLD ? n : 0] = decay;
+            }
             pin(hs[i]);
         }
         // the outputs of token i of the lane's channel
@@ -554,7 +557,7 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 ? 4 : 3) void gdn_ssm_bwd_kernel(S
                     v[(i - i0) * NS + n] = swap32_add(g[n] * u, gy * hs[i][n]);
                     y = fmaf(hs[i][n], c, y);
                     du = fmaf(g[n], bc[i][0][n], du);
-                    g[n] *= exp2_hw(si * a[n]);
+                    g[n] *= HOLD ? decays[i][HOLD ? n : 0] : exp2_hw(si * a[n]);
                     const float q = g[n] * (i > 0 ? hs[i > 0 ? i - 1 : 0][n] : start[blk][n][lane]);
                     ds = fmaf(q, a[n], ds);
                     da[n] = fmaf(q, si, da[n]);
