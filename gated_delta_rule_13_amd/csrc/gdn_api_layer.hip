@@ -19,6 +19,8 @@ namespace {
 
 constexpr size_t kInvalid = (size_t)-1;
 constexpr int64_t kMaxGrid = 0x7fffffff;
+// A launch counts its threads in 32 bits.
+bool threads_ok(long double n) { return n <= 4294967295.0L; }
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool dtype_ok(int t) { return t == GDN_BF16 || t == GDN_F32; }
@@ -75,7 +77,7 @@ gdn_status validate(const gdn_conv_shape* s) {
     if (s->x_stride_b < 0 || s->x_stride_t < 0) return set_error(GDN_ERR_BAD_SHAPE, "strides must be >= 0");
     const gdn_status st = check_counts(s->B, s->T, s->D);
     if (st != GDN_OK) return st;
-    if (s->D > (1 << 29)) return set_error(GDN_ERR_UNSUPPORTED, "D must be at most 2^29");
+    if (s->D > (1 << 25)) return set_error(GDN_ERR_UNSUPPORTED, "D must be at most 2^25");
     return GDN_OK;
 }
 
@@ -126,7 +128,7 @@ gdn_status conv_forward(const gdn_conv_shape* s, const void* x, const float* wei
                                     !wide ? 1 : s->dtype == GDN_BF16 ? 8 : 4);
     p.y = y;
     p.s1 = state_out;
-    if ((int64_t)p.B * p.ntile * p.nv > kMaxGrid) return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
+    if ((long double)p.B * p.ntile * p.nv > kMaxGrid) return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
     gdn::conv_launcher(s->dtype == GDN_BF16, s->W, wide)(p, reinterpret_cast<hipStream_t>(stream));
     return gdn::launch_status();
 }
@@ -151,12 +153,7 @@ gdn_status validate(const gdn_ssm_shape* s) {
             if (v > kMaxRow) return set_error(GDN_ERR_UNSUPPORTED, "strides of tokens must be at most 2^24");
     gdn_status st = check_counts(s->B, s->T, (int64_t)s->D * s->N);
     if (st != GDN_OK) return st;
-    // the largest grids: sequences x segments of at least 8 tokens x tiles of
-    // 64 channels; the chains, a workgroup for 64 states of a tile, both ways;
-    // the sums over tiles and segments
-    const int64_t tiles = (int64_t)s->G * ceil_div(s->D / s->G, 64);
-    if ((long double)s->B * ceil_div(s->T, 8) * tiles > kMaxGrid || (long double)s->B * tiles * 2 * 64 > kMaxGrid ||
-        (long double)s->B * s->T * s->G * 2 * 64 / gdn::kSumThreads + (long double)tiles * 66 > kMaxGrid)
+    if (!threads_ok((long double)s->B * s->G * ceil_div(s->D / s->G, 64) * 64 * 2 * gdn::ssm_states(s->N)))
         return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
     return GDN_OK;
 }
@@ -255,6 +252,17 @@ SsmGradPlan ssm_bwd_plan(const gdn_ssm_shape& s) {
     g.bytes = g.bc + up256(tiles * s.B * s.T * 2 * ns * 4);
     return g;
 }
+// Whether the launches of a plan fit: a wave for each segment of 64 channels,
+// in the gradient up to eight, and a thread for each number of dB and dC.
+gdn_status ssm_fits(const gdn_ssm_shape& s, int nseg, bool grad) {
+    const long double units = (long double)s.B * nseg * s.G * ceil_div(s.D / s.G, 64);
+    const int ns = gdn::ssm_states(s.N);
+    const long double sums = (long double)s.B * s.T * s.G * 2 * ns +
+                             (long double)s.G * ceil_div(s.D / s.G, 64) * (ns + 2) * gdn::kSumThreads + gdn::kSumThreads;
+    if (!threads_ok(units * 64 * (grad ? 8 : 1)) || (grad && !threads_ok(sums)))
+        return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
+    return GDN_OK;
+}
 
 // ---- head normalisation ----
 gdn_status validate(const gdn_norm_shape* s) {
@@ -271,7 +279,9 @@ gdn_status validate(const gdn_norm_shape* s) {
         if (v < 0) return set_error(GDN_ERR_BAD_SHAPE, "strides must be >= 0");
     gdn_status st = check_counts((int64_t)s->B * s->T, s->G, s->d);
     if (st != GDN_OK) return st;
-    if ((long double)s->B * s->T * s->G / 4 > kMaxGrid) return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
+    // (a workgroup for each head, and the gradient's sums over w and b of all)
+    if (s->G >= (1 << 24) || (s->w_per_group && (int64_t)s->G * s->d > (1 << 27)))
+        return set_error(GDN_ERR_UNSUPPORTED, "G must be below 2^24, and G d at most 2^27 for weights [G, d]");
     return GDN_OK;
 }
 gdn::NormParams norm_params(const gdn_norm_shape& s, const void* x, const float* w, const float* b, const void* z) {
@@ -361,7 +371,7 @@ gdn_status gdn_conv_bwd(const gdn_conv_shape* s, const void* dy, const void* x, 
     q.ds0 = dstate0;
     q.part = static_cast<float*>(workspace);
     const int64_t rows = gdn::conv_bwd_part_rows((int64_t)q.f.B * q.f.ntile);
-    if ((long double)rows * ceil_div(q.f.nv, 64) > kMaxGrid || (int64_t)q.f.B * q.f.ntile > kMaxGrid)
+    if (!threads_ok((long double)rows * ceil_div(q.f.nv, 64) * gdn::kConvThreads))
         return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     gdn::conv_bwd_launcher(s->dtype == GDN_BF16, s->W, wide)(q, hs);
@@ -372,7 +382,8 @@ gdn_status gdn_conv_bwd(const gdn_conv_shape* s, const void* dy, const void* x, 
 size_t gdn_ssm_fwd_workspace_bytes(const gdn_ssm_shape* s) {
     gdn::clear_error();
     if (validate(s) != GDN_OK) return kInvalid;
-    return ssm_fwd_plan(*s).bytes;
+    const SsmPlan pl = ssm_fwd_plan(*s);
+    return ssm_fits(*s, pl.nseg, false) == GDN_OK ? pl.bytes : kInvalid;
 }
 
 gdn_status gdn_ssm_fwd(const gdn_ssm_shape* s, const void* x, const void* dt, const float* A, const void* Bm,
@@ -382,12 +393,14 @@ gdn_status gdn_ssm_fwd(const gdn_ssm_shape* s, const void* x, const void* dt, co
     gdn::clear_error();
     gdn_status st = validate(s);
     if (st != GDN_OK) return st;
+    const SsmPlan pl = ssm_fwd_plan(*s);
+    st = ssm_fits(*s, pl.nseg, false);
+    if (st != GDN_OK) return st;
     if (!x || !dt || !A || !Bm || !C || !y) return set_error(GDN_ERR_NULL_ARG, "x, dt, A, Bm, C and y are required");
     st = ssm_check(s, x, dt, A, Bm, C, Dskip, z, dt_bias, h0, lens);
     if (st != GDN_OK) return st;
     st = check_aligned({{y, s->dtype}, {h_final, GDN_F32}});
     if (st != GDN_OK) return st;
-    const SsmPlan pl = ssm_fwd_plan(*s);
     st = check_workspace(workspace, workspace_bytes, pl.bytes, "gdn_ssm_fwd_workspace_bytes");
     if (st != GDN_OK) return st;
     gdn::SsmParams p = ssm_params(*s, x, dt, A, Bm, C, Dskip, z, dt_bias, h0, lens);
@@ -429,7 +442,8 @@ gdn_status gdn_ssm_step(const gdn_ssm_shape* s, const void* x, const void* dt, c
 size_t gdn_ssm_bwd_workspace_bytes(const gdn_ssm_shape* s) {
     gdn::clear_error();
     if (validate(s) != GDN_OK) return kInvalid;
-    return ssm_bwd_plan(*s).bytes;
+    const SsmGradPlan pl = ssm_bwd_plan(*s);
+    return ssm_fits(*s, pl.nseg, true) == GDN_OK ? pl.bytes : kInvalid;
 }
 
 gdn_status gdn_ssm_bwd(const gdn_ssm_shape* s, const void* dy, const void* x, const void* dt, const float* A,
@@ -440,6 +454,9 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape* s, const void* dy, const void* x, co
     gdn::clear_error();
     gdn_status st = validate(s);
     if (st != GDN_OK) return st;
+    const SsmGradPlan pl = ssm_bwd_plan(*s);
+    st = ssm_fits(*s, pl.nseg, true);
+    if (st != GDN_OK) return st;
     if (!dy || !x || !dt || !A || !Bm || !C || !dx || !ddt || !dA || !dBm || !dC)
         return set_error(GDN_ERR_NULL_ARG, "dy, x, dt, A, Bm, C, dx, ddt, dA, dBm and dC are required");
     if ((z != nullptr) != (dz != nullptr)) return set_error(GDN_ERR_NULL_ARG, "dz goes with z");
@@ -449,7 +466,6 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape* s, const void* dy, const void* x, co
                         {dBm, s->dtype}, {dC, s->dtype}, {dDskip, GDN_F32}, {dz, s->dtype}, {ddt_bias, GDN_F32},
                         {dh0, GDN_F32}});
     if (st != GDN_OK) return st;
-    const SsmGradPlan pl = ssm_bwd_plan(*s);
     st = check_workspace(workspace, workspace_bytes, pl.bytes, "gdn_ssm_bwd_workspace_bytes");
     if (st != GDN_OK) return st;
     gdn::SsmParams p = ssm_params(*s, x, dt, A, Bm, C, Dskip, z, dt_bias, h0, lens);

@@ -18,9 +18,10 @@ void fwd(const NormParams& p, hipStream_t st) {
 }
 template <bool XB, bool OB>
 void fwd_plain(const NormParams& p, hipStream_t st) {
-    const int64_t per = kNormThreads / 64;
-    hipLaunchKernelGGL((gdn_norm_fwd_plain_kernel<XB, OB>), dim3((unsigned)((p.rows + per - 1) / per)),
-                       dim3(kNormThreads), 0, st, p);
+    const int64_t per = kNormThreads / 64, most = 1 << 20;
+    const int64_t all = (p.rows + per - 1) / per;
+    hipLaunchKernelGGL((gdn_norm_fwd_plain_kernel<XB, OB>), dim3((unsigned)(all < most ? all : most)), dim3(kNormThreads),
+                       0, st, p);
 }
 template <bool XB, bool OB, int L, int K>
 void bwd(const NormBwdParams& q, int nblk, hipStream_t st) {

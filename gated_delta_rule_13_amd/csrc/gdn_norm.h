@@ -32,7 +32,6 @@ struct NormParams {
     int64_t zsb, zst, zsg;
     int64_t rows;           // B T G
     int T, G, d;
-    int x_bf16, o_bf16;
     int center, per_group, silu;
     float eps;
 };
@@ -118,7 +117,8 @@ template <int L, int K>
 __device__ __forceinline__ void load_columns(float (&w)[K][4], const float* src, const NormParams& p, int g, int j, float none) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * L + j) * 4, wc = (p.per_group ? g * p.d : 0) + c;
+        const int c = (k * L + j) * 4;
+        const int wc = (p.per_group ? g * p.d : 0) + c;   // (weights [G, d] have 2^27 numbers at most)
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[k][e] = src && c < p.d ? src[wc + e] : none;
     }
@@ -274,26 +274,27 @@ __device__ __forceinline__ void plain_stats(const NormParams& p, int64_t x0, int
 template <bool XB, bool OB>
 __global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_plain_kernel(NormParams p) {
     const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * (kNormThreads / 64) + (threadIdx.x >> 6);
-    if (row >= p.rows) return;
-    const int g = (int)(row % p.G);
-    const int64_t bt = row / p.G;
-    const int64_t b = bt / p.T, t = bt % p.T;
-    const int64_t x0 = b * p.xsb + t * p.xst + g * p.xsg, z0 = b * p.zsb + t * p.zst + g * p.zsg;
-    float mean, r;
-    plain_stats<XB>(p, x0, lane, mean, r);
-    for (int c = lane; c < p.d; c += 64) {
-        const int wc = (p.per_group ? g * p.d : 0) + c;
-        float v = (load_one<XB>(p.x, x0 + c) - mean) * r;
-        if (p.w) v *= p.w[wc];
-        if (p.b) v += p.b[wc];
-        if (p.z) {
-            const float z = load_one<OB>(p.z, z0 + c);
-            v *= p.silu ? silu(z) : z;
-        } else if (p.silu) {
-            v = silu(v);
+    const int64_t step = (int64_t)gridDim.x * (kNormThreads / 64);
+    for (int64_t row = (int64_t)blockIdx.x * (kNormThreads / 64) + (threadIdx.x >> 6); row < p.rows; row += step) {
+        const int g = (int)(row % p.G);
+        const int64_t bt = row / p.G;
+        const int64_t b = bt / p.T, t = bt % p.T;
+        const int64_t x0 = b * p.xsb + t * p.xst + g * p.xsg, z0 = b * p.zsb + t * p.zst + g * p.zsg;
+        float mean, r;
+        plain_stats<XB>(p, x0, lane, mean, r);
+        for (int c = lane; c < p.d; c += 64) {
+            const int wc = (p.per_group ? g * p.d : 0) + c;
+            float v = (load_one<XB>(p.x, x0 + c) - mean) * r;
+            if (p.w) v *= p.w[wc];
+            if (p.b) v += p.b[wc];
+            if (p.z) {
+                const float z = load_one<OB>(p.z, z0 + c);
+                v *= p.silu ? silu(z) : z;
+            } else if (p.silu) {
+                v = silu(v);
+            }
+            store_one<OB>(p.y, row * p.d + c, v);
         }
-        store_one<OB>(p.y, row * p.d + c, v);
     }
 }
 
