@@ -153,8 +153,6 @@ gdn_status validate(const gdn_ssm_shape* s) {
             if (v > kMaxRow) return set_error(GDN_ERR_UNSUPPORTED, "strides of tokens must be at most 2^24");
     gdn_status st = check_counts(s->B, s->T, (int64_t)s->D * s->N);
     if (st != GDN_OK) return st;
-    if (!threads_ok((long double)s->B * s->G * ceil_div(s->D / s->G, 64) * 64 * 2 * gdn::ssm_states(s->N)))
-        return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
     return GDN_OK;
 }
 
@@ -253,13 +251,16 @@ SsmGradPlan ssm_bwd_plan(const gdn_ssm_shape& s) {
     return g;
 }
 // Whether the launches of a plan fit: a wave for each segment of 64 channels,
-// in the gradient up to eight, and a thread for each number of dB and dC.
+// in the gradient up to eight; the chains, if there are any, a thread for each
+// state of a lane, in the gradient both ways; and the gradient's sums, one for
+// each number of dB and dC and a workgroup for 64 of the others.
 gdn_status ssm_fits(const gdn_ssm_shape& s, int nseg, bool grad) {
-    const long double units = (long double)s.B * nseg * s.G * ceil_div(s.D / s.G, 64);
     const int ns = gdn::ssm_states(s.N);
-    const long double sums = (long double)s.B * s.T * s.G * 2 * ns +
-                             (long double)s.G * ceil_div(s.D / s.G, 64) * (ns + 2) * gdn::kSumThreads + gdn::kSumThreads;
-    if (!threads_ok(units * 64 * (grad ? 8 : 1)) || (grad && !threads_ok(sums)))
+    const long double tiles = (long double)s.G * ceil_div(s.D / s.G, 64), lanes = tiles * s.B * 64;
+    const bool waves = threads_ok(lanes * nseg * (grad ? 8 : 1));
+    const bool chains = (nseg == 1 && !grad) || threads_ok(lanes * ns * (grad ? 2 : 1));
+    const bool sums = !grad || threads_ok((long double)s.B * s.T * s.G * 2 * ns + (tiles * (ns + 2) + 1) * gdn::kSumThreads);
+    if (!waves || !chains || !sums)
         return set_error(GDN_ERR_UNSUPPORTED, "tensor too large");
     return GDN_OK;
 }

@@ -117,7 +117,8 @@ def test_far_rows(lib_nogpu):  # noqa: F811
 
 
 @pytest.mark.parametrize("entry,kw", [
-    ("gdn_conv_bwd", dict(D=2 ** 25 + 2)), ("gdn_ssm_fwd", dict(B=4096, T=2 ** 20, D=4096, G=2 ** 10)),
+    ("gdn_conv_bwd", dict(D=2 ** 25 + 2)), ("gdn_ssm_bwd", dict(B=1100, T=1, D=32768, N=64, G=1)),
+    ("gdn_ssm_fwd", dict(B=2 ** 16, D=2 ** 11, G=2 ** 11)),
     ("gdn_ssm_bwd", dict(B=64, T=2 ** 24, D=4096)), ("gdn_ssm_bwd", dict(B=64, T=2 ** 20, D=64, N=64, G=2)),
     ("gdn_norm_bwd", dict(G=2 ** 24)), ("gdn_norm_bwd", dict(G=2 ** 20, d=256, w_per_group=1))])
 def test_launch_limits(lib_nogpu, entry, kw):  # noqa: F811
@@ -125,6 +126,14 @@ def test_launch_limits(lib_nogpu, entry, kw):  # noqa: F811
     assert getattr(lib_nogpu, entry + "_workspace_bytes")(ctypes.byref(CALLS[entry][0](**kw))) == BIG
     assert call(lib_nogpu, entry, CALLS[entry][0](**kw), dx=ODD, y=ODD) == 4
     assert "aligned" not in lib_nogpu.gdn_last_error().decode()
+
+
+def test_large_states(lib_nogpu):  # noqa: F811
+    """What one pass over the tokens takes, where chains of segments would not fit."""
+    big = dict(B=1100, D=32768, N=64, G=1)
+    assert lib_nogpu.gdn_ssm_fwd_workspace_bytes(ctypes.byref(ssm_shape(T=1, **big))) == 0
+    assert call(lib_nogpu, "gdn_ssm_step", ssm_shape(T=1, **big), x=ODD) == 4
+    assert "aligned" in lib_nogpu.gdn_last_error().decode()
 
 
 def test_gradient_of_the_gate_goes_with_the_gate(lib_nogpu):  # noqa: F811
