@@ -214,6 +214,7 @@ gdn::SsmParams ssm_params(const gdn_ssm_shape& s, const void* x, const void* dt,
     p.Dg = s.D / s.G;
     p.tpg = (int)ceil_div(p.Dg, 64);
     p.softplus = s.dt_softplus;
+    p.wide = s.N % 4 == 0 && aligned(A, 16) && aligned(h0, 16);
     p.seg_len = s.T;
     p.nseg = 1;
     return p;
@@ -407,6 +408,7 @@ gdn_status gdn_ssm_fwd(const gdn_ssm_shape* s, const void* x, const void* dt, co
     gdn::SsmParams p = ssm_params(*s, x, dt, A, Bm, C, Dskip, z, dt_bias, h0, lens);
     p.y = y;
     p.h_final = h_final;
+    p.wide_out = s->N % 4 == 0 && aligned(h_final, 16);
     p.seg_len = pl.seg_len;
     p.nseg = pl.nseg;
     p.sum_e = static_cast<float*>(workspace);

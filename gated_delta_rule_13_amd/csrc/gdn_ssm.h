@@ -16,7 +16,7 @@
 // group: the wave stages them in LDS as fp32, kTok tokens ahead, and every lane
 // reads them at the same address (reading none of them changes nothing in the
 // time).  A lane for each state instead (16 lanes a channel, no segments below)
-// was built and took 231 us or more for what follows in 135, for the moves
+// was built and took 231 us or more for what follows in 129, for the moves
 // between lanes.
 //
 // Few channels on long sequences leave the chip empty, so the tokens are cut
@@ -28,9 +28,9 @@
 //                           another
 //   gdn_ssm_fwd_kernel      the outputs (all segments at once)
 // which costs the exponentials twice.  Measured at 4 x 4096 x 2048 with 16
-// states, bf16, gated: 101 + 8 + 135 us (24 segments), the last two thirds of
+// states, bf16, gated: 97 + 8 + 129 us (24 segments), the last two thirds of
 // what the vector units' issue rate would allow at 2.4 GHz, and at 1 x 32768 x
-// 1024: 101 + 17 + 135 us.
+// 1024: 97 + 17 + 129 us.
 #pragma once
 #include "gdn_layer.h"
 
@@ -54,6 +54,7 @@ struct SsmParams {
     int Dg;                 // channels per group
     int tpg;                // tiles of 64 channels per group
     int softplus;
+    int wide, wide_out;     // A and h0, h_final in 16-byte pieces (N a multiple of 4, aligned)
     int seg_len, nseg;      // with segments a multiple of kTok
     // segment summaries, in units of (sequence, segment, tile):
     float* sum_e;           // [unit][NS][64]: E, then the state that enters
@@ -150,16 +151,31 @@ struct Column {
     }
 };
 
-// A log2(e) of the lane's channel, 0 behind the N states (which then stay 0).
+// NS states from n0 on of row `row` of A or h0 [.][N], 0 behind the N states.
+// Lanes read rows of N numbers each, a cache line or more apart, so that a load
+// costs by the lines it touches: 16-byte pieces take a quarter of the time
+// (number by number, and before the first tokens' loads, the passes below took
+// 101 and 135 us for 97 and 129, and 18 and 20 for 15 and 15 at 24 states).
 template <int NS>
-__device__ __forceinline__ void load_decay(float (&a)[NS], const SsmParams& p, int c) {
+__device__ __forceinline__ void load_states(float (&v)[NS], const float* s, const SsmParams& p, int64_t row, int n0 = 0) {
+    if (p.wide) {
 #pragma unroll
-    for (int n = 0; n < NS; ++n) a[n] = n < p.N ? p.A[(int64_t)c * p.N + n] * kLog2e : 0.f;
+        for (int n = 0; n < NS; n += 4) {
+            const f32x4 q = n0 + n < p.N ? *reinterpret_cast<const f32x4*>(s + row * p.N + n0 + n) : zero4();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[n + e] = q[e];
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) v[n] = n0 + n < p.N ? s[row * p.N + n0 + n] : 0.f;
+    }
 }
+// A log2(e) (0 behind the N states, which then stay 0)
 template <int NS>
-__device__ __forceinline__ void load_state(float (&h)[NS], const float* s, const SsmParams& p, int b, int c) {
+__device__ __forceinline__ void load_decay(float (&a)[NS], const SsmParams& p, int c, int n0 = 0) {
+    load_states<NS>(a, p.A, p, c, n0);
 #pragma unroll
-    for (int n = 0; n < NS; ++n) h[n] = s && n < p.N ? s[((int64_t)b * p.D + c) * p.N + n] : 0.f;
+    for (int n = 0; n < NS; ++n) a[n] *= kLog2e;
 }
 template <int NS>
 __device__ __forceinline__ void load_sum(float (&h)[NS], const float* s, int64_t unit, int lane) {
@@ -199,9 +215,14 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
     const int64_t zb = p.z ? w.b * p.zsb + w.c0 : xb, zst = p.z ? p.zst : p.xst;
     const uint32_t off = (uint32_t)(w.c - w.c0) * (BF ? 2 : 4), out = w.on ? off : kOutside;
     float a[NS], h[NS];
-    load_decay<NS>(a, p, w.c);
-    if (p.nseg > 1) load_sum<NS>(h, p.sum_e, w.unit, lane);
-    else load_state<NS>(h, p.h0, p, w.b, w.c);
+    if (p.nseg > 1) {
+        load_sum<NS>(h, p.sum_e, w.unit, lane);
+    } else if (p.h0) {
+        load_states<NS>(h, p.h0, p, (int64_t)w.b * p.D + w.c);
+    } else {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) h[n] = 0.f;
+    }
     const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
 
     if (w.t0 < w.t1) {
@@ -214,6 +235,7 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
             nz.load(zsrc, zb, zst, off, t, w.t1);
         };
         load(w.t0);
+        load_decay<NS>(a, p, w.c);
         int buf = 0;
         for (int t = w.t0; t < w.t1; t += kTok, buf ^= 1) {
             nbc.put(&bc[buf][0][0][0], lane);
@@ -245,9 +267,16 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
     if (w.on) {
         for (int t = w.t0 > w.t1 ? w.t0 : w.t1; t < w.tz; ++t) store_one<BF>(p.y, yb + (int64_t)t * p.D, 0.f);
         if (p.h_final && w.seg == p.nseg - 1) {
+            float* out_h = p.h_final + ((int64_t)w.b * p.D + w.c) * p.N;
+            if (p.wide_out) {
 #pragma unroll
-            for (int n = 0; n < NS; ++n)
-                if (n < p.N) p.h_final[((int64_t)w.b * p.D + w.c) * p.N + n] = h[n];
+                for (int n = 0; n < NS; n += 4)
+                    if (n < p.N) *reinterpret_cast<f32x4*>(out_h + n) = f32x4{h[n], h[n + 1], h[n + 2], h[n + 3]};
+            } else {
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    if (n < p.N) out_h[n] = h[n];
+            }
         }
     }
 }
@@ -268,7 +297,6 @@ __global__ __launch_bounds__(64, NS <= 16 && !GRAD ? 3 : 1) void gdn_ssm_sum_ker
     const int64_t zb = p.z ? w.b * p.zsb + w.c0 : xb, zst = p.z ? p.zst : p.xst;
     const uint32_t off = (uint32_t)(w.c - w.c0) * (BF ? 2 : 4);
     float a[NS], h[NS], pr[NS], r[NS], total = 0.f;
-    load_decay<NS>(a, p, w.c);
 #pragma unroll
     for (int n = 0; n < NS; ++n) h[n] = r[n] = 0.f, pr[n] = 1.f;
     const float bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
@@ -285,6 +313,7 @@ __global__ __launch_bounds__(64, NS <= 16 && !GRAD ? 3 : 1) void gdn_ssm_sum_ker
             }
         };
         load(w.t0);
+        load_decay<NS>(a, p, w.c);
         int buf = 0;
         for (int t = w.t0; t < w.t1; t += kTok, buf ^= 1) {
             nbc.put(&bc[buf][0][0][0], lane);
@@ -423,8 +452,8 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // the group's states and decays into registers, then the gradient backwards.
 // The states are split over the workgroup's NB waves, NS each; what sums over
 // states (du, ds, y) is added through LDS.  Measured at 2 x 4096 x 2048 with 16
-// states, bf16, gated, all launches 363 us: summaries 103, chain 16, this
-// kernel 229 (four states to a wave, held decays; computed again 238; eight
+// states, bf16, gated, all launches 347 us: summaries 97, chain 16, this
+// kernel 221 (four states to a wave, held decays; computed again 238; eight
 // states to a wave took 299 when four took 256, all 16 in one wave 322), the
 // sums over tiles and segments 11.  The vector units are busy nine tenths of
 // the time: about 26 issue slots for a (token, channel, state) with its share
@@ -446,9 +475,9 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 ? 4 : 3) void gdn_ssm_b
     const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
     const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
     float a[NS], g[NS], da[NS], dd = 0.f, dbias = 0.f;
+    load_decay<NS>(a, p, w.c, n0);
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-        a[n] = n0 + n < p.N ? p.A[(int64_t)w.c * p.N + n0 + n] * kLog2e : 0.f;
         g[n] = p.sum_r[(w.unit * NSA + n0 + n) * 64 + lane];
         da[n] = 0.f;
     }
