@@ -7,16 +7,15 @@
 //     dx = (dn - mean(dn) - n mean(dn n)) / sqrt(var + eps)
 // (without the mean(dn) where x is not centred), dw = sum dp n, db = sum dp,
 // dz = dy p act'(z).  One pass over x, z and y (and their gradients) bounds
-// it: a group of L lanes holds a row of d numbers in registers, K pieces of
-// four to a lane, so nothing is read twice; the row's sums are steps between
-// neighbouring lanes.  L and K are chosen so that L K pieces just cover the
-// row (d = 192: 16 lanes with 3 pieces each, no lane idle).  Rows whose size
-// or alignment does not allow 16-byte pieces, and rows over 2048 numbers,
-// take the plain kernels: one wave for a row, which it reads again for each
-// of its sums.  Measured: 4 x 4096 x 16 x 128 from fp32 to bf16 with a gate, 55
-// us for 268 MB (4.9 TB/s, where a large copy reaches 5.1); the gradient at 2 x
-// 1031 x 30 x 192 in bf16, 27 us for 119 MB (4.4 TB/s) and 4 us for the sum of
-// the partial rows.
+// it: a group of L lanes holds a row of d numbers in registers, K pieces of V
+// to a lane, so nothing is read twice; the row's sums are steps between
+// neighbouring lanes (and between the waves, where the group is the whole
+// workgroup).  L and K are chosen so that the pieces just cover the row (d =
+// 192: 16 lanes with 3 pieces of four each, no lane idle); V is 4, or 1 where
+// the size or the alignment of rows does not allow pieces.  Measured: 4 x 4096 x
+// 16 x 128 from fp32 to bf16 with a gate, 55 us for 268 MB (4.9 TB/s, where a
+// large copy reaches 5.1); the gradient at 2 x 1031 x 30 x 192 in bf16, 27 us
+// for 119 MB (4.4 TB/s) and 4 us for the sum of the partial rows.
 #pragma once
 #include "gdn_layer.h"
 
@@ -46,6 +45,7 @@ struct NormBwdParams {
 };
 
 constexpr int kNormThreads = 256;
+constexpr int kNormMaxD = 4096;
 
 // Where workgroup blk leaves head g's sums for the weight (which 0) or the
 // bias: rows [blk][w of all heads | b of all heads] for weights [G, d], and
@@ -64,9 +64,32 @@ __device__ __forceinline__ void act_both(float x, int act, float& val, float& sl
     }
 }
 
+// Sum over a group's lanes, in every lane.  Where the group is the workgroup
+// the waves' sums are added in order, through two slots in turn: a wave that
+// writes one again has passed the barrier behind the other, and so have all
+// that read it.
+template <int L>
+struct GroupSum {
+    float (*slots)[kNormThreads / 64];
+    int turn = 0;
+    __device__ __forceinline__ float operator()(float v) {
+        if constexpr (L <= 64) return lanes_sum<L>(v);
+        v = lanes_sum<64>(v);
+        float* s = slots[turn];
+        turn ^= 1;
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kNormThreads / 64; ++i) v += s[i];
+        return v;
+    }
+};
+
 // The mean (0 if not centred) and 1 / sqrt(var + eps) of a row.
-template <int L, int K>
-__device__ __forceinline__ void row_stats(const float (&x)[K][4], const NormParams& p, int j, float& mean, float& r) {
+template <int L, int K, int V>
+__device__ __forceinline__ void row_stats(const float (&x)[K][V], const NormParams& p, int j, GroupSum<L>& sum, float& mean,
+                                          float& r) {
     const float inv = 1.f / (float)p.d;
     mean = 0.f;
     if (p.center) {
@@ -74,34 +97,34 @@ __device__ __forceinline__ void row_stats(const float (&x)[K][4], const NormPara
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s += x[k][e];     // (pieces behind the row hold 0)
-        mean = lanes_sum<L>(s) * inv;
+            for (int e = 0; e < V; ++e) s += x[k][e];     // (pieces behind the row hold 0)
+        mean = sum(s) * inv;
     }
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const bool in = (k * L + j) * 4 < p.d;
+        const bool in = (k * L + j) * V < p.d;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < V; ++e) {
             const float c = in ? x[k][e] - mean : 0.f;
             s = fmaf(c, c, s);
         }
     }
-    r = 1.f / sqrtf(lanes_sum<L>(s) * inv + p.eps);
+    r = 1.f / sqrtf(sum(s) * inv + p.eps);
 }
 
 // One row as it lies in memory.
-template <bool XB, bool OB, int L, int K>
+template <bool XB, bool OB, int L, int K, int V>
 struct NormRow {
-    Raw<XB, 4> x[K];
-    Raw<OB, 4> z[K], dy[K];
+    Raw<XB, V> x[K];
+    Raw<OB, V> z[K], dy[K];
     __device__ __forceinline__ void load(const NormParams& p, const void* dyp, int64_t bt, int g, int j) {
         const int64_t b = bt / p.T, t = bt - b * p.T;
         const int64_t x0 = b * p.xsb + t * p.xst + g * p.xsg, z0 = b * p.zsb + t * p.zst + g * p.zsg;
         const int64_t y0 = (bt * p.G + g) * p.d;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * L + j) * 4;
+            const int c = (k * L + j) * V;
             x[k].zero();
             z[k].zero();
             dy[k].zero();
@@ -113,53 +136,55 @@ struct NormRow {
         }
     }
 };
-template <int L, int K>
-__device__ __forceinline__ void load_columns(float (&w)[K][4], const float* src, const NormParams& p, int g, int j, float none) {
+template <int L, int K, int V>
+__device__ __forceinline__ void load_columns(float (&w)[K][V], const float* src, const NormParams& p, int g, int j, float none) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * L + j) * 4;
+        const int c = (k * L + j) * V;
         const int wc = (p.per_group ? g * p.d : 0) + c;   // (weights [G, d] have 2^27 numbers at most)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[k][e] = src && c < p.d ? src[wc + e] : none;
+        for (int e = 0; e < V; ++e) w[k][e] = src && c < p.d ? src[wc + e] : none;
     }
 }
 
 // A group of lanes takes every `tokens`-th token of one head, so that its
 // columns of the weight stay in registers, with the next row in flight.
-template <bool XB, bool OB, int L, int K>
+template <bool XB, bool OB, int L, int K, int V>
 __global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_kernel(NormParams p, int64_t tokens) {
+    __shared__ float slots[2][kNormThreads / 64];
+    GroupSum<L> sum{slots};
     const int j = threadIdx.x % L;
     const int64_t grp = (int64_t)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
     const int g = (int)(grp % p.G);
     const int64_t bts = p.rows / p.G;
     int64_t bt = grp / p.G;
     if (bt >= tokens || bt >= bts) return;      // (a whole group of lanes)
-    float w[K][4], b[K][4];
-    load_columns<L, K>(w, p.w, p, g, j, 1.f);
-    load_columns<L, K>(b, p.b, p, g, j, 0.f);
-    NormRow<XB, OB, L, K> cur, next;
+    float w[K][V], b[K][V];
+    load_columns<L, K, V>(w, p.w, p, g, j, 1.f);
+    load_columns<L, K, V>(b, p.b, p, g, j, 0.f);
+    NormRow<XB, OB, L, K, V> cur, next;
     next.load(p, nullptr, bt, g, j);
     for (; bt < bts; bt += tokens) {
         cur = next;
         if (bt + tokens < bts) next.load(p, nullptr, bt + tokens, g, j);
-        float x[K][4], mean, r;
+        float x[K][V], mean, r;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[k][e] = cur.x[k].get(e);
-        row_stats<L, K>(x, p, j, mean, r);
+            for (int e = 0; e < V; ++e) x[k][e] = cur.x[k].get(e);
+        row_stats<L, K, V>(x, p, j, sum, mean, r);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * L + j) * 4;
+            const int c = (k * L + j) * V;
             if (c < p.d) {
-                float f[4];
+                float f[V];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < V; ++e) {
                     const float v = fmaf((x[k][e] - mean) * r, w[k][e], b[k][e]), gate = cur.z[k].get(e);
                     if (p.z) f[e] = v * (p.silu ? silu(gate) : gate);
                     else f[e] = p.silu ? silu(v) : v;
                 }
-                store_vec<OB, 4>(p.y, (bt * p.G + g) * p.d + c, f);
+                store_vec<OB, V>(p.y, (bt * p.G + g) * p.d + c, f);
             }
         }
     }
@@ -167,45 +192,47 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_kernel(NormParams p
 
 // A workgroup takes rows of one head, so that a lane's columns of the weight
 // stay the same and their sums stay in registers until the end.
-template <bool XB, bool OB, int L, int K>
+template <bool XB, bool OB, int L, int K, int V>
 __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParams q) {
     const NormParams& p = q.f;
     constexpr int kGroups = kNormThreads / L;
-    __shared__ float red[kGroups][L * K * 4];
+    __shared__ float red[kGroups][L * K * V];
+    __shared__ float slots[2][kNormThreads / 64];
+    GroupSum<L> sum{slots};
     const int j = threadIdx.x % L, grp = threadIdx.x / L;
     const int g = blockIdx.x % p.G;
     const int64_t blk = blockIdx.x / p.G, nblk = gridDim.x / p.G;
     const int64_t bts = p.rows / p.G, step = nblk * kGroups;
     const float inv = 1.f / (float)p.d;
-    float w[K][4], b[K][4], sw[K][4], sb[K][4];
-    load_columns<L, K>(w, p.w, p, g, j, 1.f);
-    load_columns<L, K>(b, p.b, p, g, j, 0.f);
+    float w[K][V], b[K][V], sw[K][V], sb[K][V];
+    load_columns<L, K, V>(w, p.w, p, g, j, 1.f);
+    load_columns<L, K, V>(b, p.b, p, g, j, 0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sw[k][e] = sb[k][e] = 0.f;
+        for (int e = 0; e < V; ++e) sw[k][e] = sb[k][e] = 0.f;
     int64_t bt = blk * kGroups + grp;
-    NormRow<XB, OB, L, K> cur, next;
+    NormRow<XB, OB, L, K, V> cur, next;
     if (bt < bts) next.load(p, q.dy, bt, g, j);
     for (; bt < bts; bt += step) {
         cur = next;
         if (bt + step < bts) next.load(p, q.dy, bt + step, g, j);
         const int64_t bb = bt / p.T, t = bt - bb * p.T;
         const int64_t y0 = (bt * p.G + g) * p.d, d0 = bb * q.dsb + t * q.dst + g * q.dsg;
-        float x[K][4], dn[K][4], mean, r;
+        float x[K][V], dn[K][V], mean, r;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[k][e] = cur.x[k].get(e);
-        row_stats<L, K>(x, p, j, mean, r);
+            for (int e = 0; e < V; ++e) x[k][e] = cur.x[k].get(e);
+        row_stats<L, K, V>(x, p, j, sum, mean, r);
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * L + j) * 4;
+            const int c = (k * L + j) * V;
             if (c < p.d) {
-                float dz[4];
+                float dz[V];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < V; ++e) {
                     const float n = (x[k][e] - mean) * r, pv = fmaf(n, w[k][e], b[k][e]), dy = cur.dy[k].get(e);
                     float val, slope;
                     act_both(p.z ? cur.z[k].get(e) : pv, p.silu, val, slope);
@@ -218,19 +245,19 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParam
                     s1 += dn[k][e];
                     s2 = fmaf(dn[k][e], n, s2);
                 }
-                if (p.z && q.dz) store_vec<OB, 4>(q.dz, y0 + c, dz);
+                if (p.z && q.dz) store_vec<OB, V>(q.dz, y0 + c, dz);
             }
         }
-        s1 = p.center ? lanes_sum<L>(s1) * inv : 0.f;
-        s2 = lanes_sum<L>(s2) * inv;
+        s1 = p.center ? sum(s1) * inv : 0.f;
+        s2 = sum(s2) * inv;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * L + j) * 4;
+            const int c = (k * L + j) * V;
             if (c < p.d) {
-                float f[4];
+                float f[V];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = r * (dn[k][e] - s1 - x[k][e] * s2);
-                store_vec<XB, 4>(q.dx, d0 + c, f);
+                for (int e = 0; e < V; ++e) f[e] = r * (dn[k][e] - s1 - x[k][e] * s2);
+                store_vec<XB, V>(q.dx, d0 + c, f);
             }
         }
     }
@@ -240,7 +267,7 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParam
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) red[grp][(k * L + j) * 4 + e] = which ? sb[k][e] : sw[k][e];
+            for (int e = 0; e < V; ++e) red[grp][(k * L + j) * V + e] = which ? sb[k][e] : sw[k][e];
         __syncthreads();
         float* out = norm_partial(q, blk, g, which);
         for (int c = threadIdx.x; c < p.d; c += kNormThreads) {
@@ -249,104 +276,6 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParam
             for (int k = 0; k < kGroups; ++k) t += red[k][c];
             out[c] = t;
         }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Any size, stride and alignment: one wave for a row.
-template <bool XB>
-__device__ __forceinline__ void plain_stats(const NormParams& p, int64_t x0, int lane, float& mean, float& r) {
-    const float inv = 1.f / (float)p.d;
-    mean = 0.f;
-    if (p.center) {
-        float s = 0.f;
-        for (int c = lane; c < p.d; c += 64) s += load_one<XB>(p.x, x0 + c);
-        mean = lanes_sum<64>(s) * inv;
-    }
-    float s = 0.f;
-    for (int c = lane; c < p.d; c += 64) {
-        const float v = load_one<XB>(p.x, x0 + c) - mean;
-        s = fmaf(v, v, s);
-    }
-    r = 1.f / sqrtf(lanes_sum<64>(s) * inv + p.eps);
-}
-
-template <bool XB, bool OB>
-__global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_plain_kernel(NormParams p) {
-    const int lane = threadIdx.x & 63;
-    const int64_t step = (int64_t)gridDim.x * (kNormThreads / 64);
-    for (int64_t row = (int64_t)blockIdx.x * (kNormThreads / 64) + (threadIdx.x >> 6); row < p.rows; row += step) {
-        const int g = (int)(row % p.G);
-        const int64_t bt = row / p.G;
-        const int64_t b = bt / p.T, t = bt % p.T;
-        const int64_t x0 = b * p.xsb + t * p.xst + g * p.xsg, z0 = b * p.zsb + t * p.zst + g * p.zsg;
-        float mean, r;
-        plain_stats<XB>(p, x0, lane, mean, r);
-        for (int c = lane; c < p.d; c += 64) {
-            const int wc = (p.per_group ? g * p.d : 0) + c;
-            float v = (load_one<XB>(p.x, x0 + c) - mean) * r;
-            if (p.w) v *= p.w[wc];
-            if (p.b) v += p.b[wc];
-            if (p.z) {
-                const float z = load_one<OB>(p.z, z0 + c);
-                v *= p.silu ? silu(z) : z;
-            } else if (p.silu) {
-                v = silu(v);
-            }
-            store_one<OB>(p.y, row * p.d + c, v);
-        }
-    }
-}
-
-// One wave for a workgroup; the sums over rows in LDS, each column by the one
-// lane that owns it.
-constexpr int kNormMaxD = 4096;
-template <bool XB, bool OB>
-__global__ __launch_bounds__(64) void gdn_norm_bwd_plain_kernel(NormBwdParams q) {
-    const NormParams& p = q.f;
-    __shared__ float sw[kNormMaxD], sb[kNormMaxD];
-    const int lane = threadIdx.x;
-    const int g = blockIdx.x % p.G;
-    const int64_t blk = blockIdx.x / p.G, nblk = gridDim.x / p.G;
-    const int64_t bts = p.rows / p.G;
-    const float inv = 1.f / (float)p.d;
-    for (int c = lane; c < p.d; c += 64) sw[c] = sb[c] = 0.f;
-    for (int64_t bt = blk; bt < bts; bt += nblk) {
-        const int64_t bb = bt / p.T, t = bt % p.T;
-        const int64_t x0 = bb * p.xsb + t * p.xst + g * p.xsg, z0 = bb * p.zsb + t * p.zst + g * p.zsg;
-        const int64_t y0 = (bt * p.G + g) * p.d, d0 = bb * q.dsb + t * q.dst + g * q.dsg;
-        float mean, r, s1 = 0.f, s2 = 0.f;
-        plain_stats<XB>(p, x0, lane, mean, r);
-        for (int c = lane; c < p.d; c += 64) {
-            const int wc = (p.per_group ? g * p.d : 0) + c;
-            const float wv = p.w ? p.w[wc] : 1.f;
-            const float n = (load_one<XB>(p.x, x0 + c) - mean) * r, pv = fmaf(n, wv, p.b ? p.b[wc] : 0.f);
-            const float dy = load_one<OB>(q.dy, y0 + c);
-            float val, slope;
-            act_both(p.z ? load_one<OB>(p.z, z0 + c) : pv, p.silu, val, slope);
-            const float dp = dy * (p.z ? val : slope);
-            sw[c] = fmaf(dp, n, sw[c]);
-            sb[c] += dp;
-            s1 = fmaf(dp, wv, s1);
-            s2 = fmaf(dp * wv, n, s2);
-            if (p.z && q.dz) store_one<OB>(q.dz, y0 + c, dy * pv * slope);
-        }
-        s1 = p.center ? lanes_sum<64>(s1) * inv : 0.f;
-        s2 = lanes_sum<64>(s2) * inv;
-        for (int c = lane; c < p.d; c += 64) {
-            const int wc = (p.per_group ? g * p.d : 0) + c;
-            const float wv = p.w ? p.w[wc] : 1.f;
-            const float n = (load_one<XB>(p.x, x0 + c) - mean) * r, pv = fmaf(n, wv, p.b ? p.b[wc] : 0.f);
-            float val, slope;
-            act_both(p.z ? load_one<OB>(p.z, z0 + c) : pv, p.silu, val, slope);
-            const float dp = load_one<OB>(q.dy, y0 + c) * (p.z ? val : slope);
-            store_one<XB>(q.dx, d0 + c, r * (dp * wv - s1 - n * s2));
-        }
-    }
-    float *out_w = norm_partial(q, blk, g, 0), *out_b = norm_partial(q, blk, g, 1);
-    for (int c = lane; c < p.d; c += 64) {
-        out_w[c] = sw[c];
-        out_b[c] = sb[c];
     }
 }
 
