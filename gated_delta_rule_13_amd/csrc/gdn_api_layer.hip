@@ -308,12 +308,12 @@ gdn::NormParams norm_params(const gdn_norm_shape& s, const void* x, const float*
     p.eps = s.eps;
     return p;
 }
-// Workgroups that share a head's rows in the gradient, at most: three for each
-// of the chip's 256 compute units over all heads, as many as are resident at
-// once (measured at 2 x 1031 x 30 x 192 in bf16: 28.5 us; 2048 workgroups,
-// which leave a last round half empty, 32.3; 512, 29.8).
-int64_t norm_bwd_blocks(const gdn_norm_shape& s) {
-    const int64_t bts = (int64_t)s.B * s.T, most = s.G < 768 ? 768 / s.G : 1;
+// Workgroups that share a head's rows in the gradient, at most: over all heads
+// as many as are resident at once on the chip's 256 compute units (measured at
+// 2 x 1031 x 30 x 192 in bf16, three on each: 28.5 us; 2048 workgroups, which
+// leave a last round half empty, 32.3; 512, 29.8).
+int64_t norm_bwd_blocks(const gdn_norm_shape& s, int resident) {
+    const int64_t bts = (int64_t)s.B * s.T, all = 256 * resident, most = s.G < all ? all / s.G : 1;
     return bts < most ? bts : most;
 }
 
@@ -508,7 +508,8 @@ gdn_status gdn_norm_fwd(const gdn_norm_shape* s, const void* x, const float* wei
                       rows4(z, s->o_dtype, {s->z_stride_b, s->z_stride_t, s->z_stride_g});
     gdn::NormLauncher fwd = nullptr;
     gdn::NormBwdLauncher bwd = nullptr;
-    gdn::norm_launchers(s->x_dtype == GDN_BF16, s->o_dtype == GDN_BF16, s->d, wide, &fwd, &bwd);
+    int resident = 0;
+    gdn::norm_launchers(s->x_dtype == GDN_BF16, s->o_dtype == GDN_BF16, s->d, wide, &fwd, &bwd, &resident);
     fwd(p, reinterpret_cast<hipStream_t>(stream));
     return gdn::launch_status();
 }
@@ -516,7 +517,7 @@ gdn_status gdn_norm_fwd(const gdn_norm_shape* s, const void* x, const float* wei
 size_t gdn_norm_bwd_workspace_bytes(const gdn_norm_shape* s) {
     gdn::clear_error();
     if (validate(s) != GDN_OK) return kInvalid;
-    return up256((size_t)norm_bwd_blocks(*s) * 2 * s->G * s->d * 4);
+    return up256((size_t)norm_bwd_blocks(*s, gdn::kNormResident) * 2 * s->G * s->d * 4);
 }
 
 gdn_status gdn_norm_bwd(const gdn_norm_shape* s, const void* dy, const void* x, const float* weight, const float* bias,
@@ -549,8 +550,9 @@ gdn_status gdn_norm_bwd(const gdn_norm_shape* s, const void* dy, const void* x, 
                       rows4(z, s->o_dtype, {s->z_stride_b, s->z_stride_t, s->z_stride_g});
     gdn::NormLauncher fwd = nullptr;
     gdn::NormBwdLauncher bwd = nullptr;
-    gdn::norm_launchers(s->x_dtype == GDN_BF16, s->o_dtype == GDN_BF16, s->d, wide, &fwd, &bwd);
-    const int nblk = (int)norm_bwd_blocks(*s);
+    int resident = 0;
+    gdn::norm_launchers(s->x_dtype == GDN_BF16, s->o_dtype == GDN_BF16, s->d, wide, &fwd, &bwd, &resident);
+    const int nblk = (int)norm_bwd_blocks(*s, resident);
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     bwd(q, nblk, hs);
     gdn::norm_bwd_sum(q, nblk, dweight, dbias, hs);

@@ -24,10 +24,12 @@ void bwd(const NormBwdParams& q, int nblk, hipStream_t st) {
 struct Pick {
     NormLauncher* f;
     NormBwdLauncher* b;
+    int* resident;
     template <bool XB, bool OB, int L, int K, int V>
     void set() const {
         *f = fwd<XB, OB, L, K, V>;
         *b = bwd<XB, OB, L, K, V>;
+        *resident = norm_resident(XB && OB, K, V);
     }
 };
 template <bool XB, bool OB, int L>
@@ -51,23 +53,25 @@ void pick_row(int d, bool wide, const Pick& to) {
         if (pieces <= 512) return to.set<XB, OB, 64, 8, 4>();
         return to.set<XB, OB, 256, 4, 4>();
     }
-    // likewise with at most 16 numbers each, in steps of four
+    // likewise with at most eight numbers each, while there are lanes (16
+    // numbers to a lane: the gradient at 4 heads of 509 in bf16 143 us for 96)
     if (d <= 32) return to.set<XB, OB, 8, 4, 1>();
     if (d <= 64) return to.set<XB, OB, 16, 4, 1>();
+    if (d <= 96) return to.set<XB, OB, 16, 6, 1>();
     if (d <= 128) return to.set<XB, OB, 16, 8, 1>();
-    if (d <= 192) return to.set<XB, OB, 16, 12, 1>();
-    if (d <= 256) return to.set<XB, OB, 16, 16, 1>();
-    if (d <= 384) return to.set<XB, OB, 32, 12, 1>();
-    if (d <= 512) return to.set<XB, OB, 32, 16, 1>();
-    if (d <= 768) return to.set<XB, OB, 64, 12, 1>();
-    if (d <= 1024) return to.set<XB, OB, 64, 16, 1>();
+    if (d <= 192) return to.set<XB, OB, 32, 6, 1>();
+    if (d <= 256) return to.set<XB, OB, 32, 8, 1>();
+    if (d <= 384) return to.set<XB, OB, 64, 6, 1>();
+    if (d <= 512) return to.set<XB, OB, 64, 8, 1>();
+    if (d <= 1024) return to.set<XB, OB, 256, 4, 1>();
     if (d <= 2048) return to.set<XB, OB, 256, 8, 1>();
     return to.set<XB, OB, 256, 16, 1>();
 }
 }  // namespace
 
-void norm_launchers(bool x_bf16, bool o_bf16, int d, bool wide, NormLauncher* fwd, NormBwdLauncher* bwd) {
-    const Pick to{fwd, bwd};
+void norm_launchers(bool x_bf16, bool o_bf16, int d, bool wide, NormLauncher* fwd, NormBwdLauncher* bwd,
+                    int* resident) {
+    const Pick to{fwd, bwd, resident};
     if (x_bf16) o_bf16 ? pick_row<true, true>(d, wide, to) : pick_row<true, false>(d, wide, to);
     else o_bf16 ? pick_row<false, true>(d, wide, to) : pick_row<false, false>(d, wide, to);
 }

@@ -81,7 +81,8 @@ void conv_bwd_sum(const float* part, int64_t rows, int D, int W, float* dweight,
 // head normalisation: wide: 16-byte pieces of a row (else the plain kernels)
 using NormLauncher = void (*)(const NormParams&, hipStream_t);
 using NormBwdLauncher = void (*)(const NormBwdParams&, int nblk, hipStream_t);
-void norm_launchers(bool x_bf16, bool o_bf16, int d, bool wide, NormLauncher* fwd, NormBwdLauncher* bwd);
+void norm_launchers(bool x_bf16, bool o_bf16, int d, bool wide, NormLauncher* fwd, NormBwdLauncher* bwd,
+                    int* resident);
 void norm_bwd_sum(const NormBwdParams& q, int nblk, float* dweight, float* dbias, hipStream_t st);
 
 // selective state space recurrence; ssm_states: N rounded up to a built size

@@ -15,7 +15,9 @@
 // the size or the alignment of rows does not allow pieces.  Measured: 4 x 4096 x
 // 16 x 128 from fp32 to bf16 with a gate, 55 us for 268 MB (4.9 TB/s, where a
 // large copy reaches 5.1); the gradient at 2 x 1031 x 30 x 192 in bf16, 27 us
-// for 119 MB (4.4 TB/s) and 4 us for the sum of the partial rows.
+// for 119 MB (4.4 TB/s) and 4 us for the sum of the partial rows.  Number by
+// number, in bf16 with a gate, 32M numbers in heads of 127 take 43 us where
+// those of 128 take 34, and their gradient 102 for 66.
 #pragma once
 #include "gdn_layer.h"
 
@@ -46,6 +48,14 @@ struct NormBwdParams {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormMaxD = 4096;
+
+// Workgroups of the gradient that a compute unit holds at once, by the numbers
+// in a lane (V K), where they lie two to a register or one, and their types: it
+// is launched with as many.
+constexpr int kNormResident = 4;
+constexpr int norm_resident(bool bf16, int k, int v) {
+    return k * v <= 6 || (k * v <= 8 && v == 4 && bf16) ? kNormResident : 3;
+}
 
 // Where workgroup blk leaves head g's sums for the weight (which 0) or the
 // bias: rows [blk][w of all heads | b of all heads] for weights [G, d], and
@@ -113,15 +123,59 @@ __device__ __forceinline__ void row_stats(const float (&x)[K][V], const NormPara
     r = 1.f / sqrtf(sum(s) * inv + p.eps);
 }
 
+// Where the rows of a group lie: it takes every `step`-th token of one head,
+// token bt = b T + t, by additions (a division a row instead: 59 us for 52 at 30
+// heads of 61 in bf16).
+struct NormAt {
+    int64_t bt, x, z, y, d; // elements of the row in x, z, y (dy, dz) and dx
+    unsigned t;
+    __device__ __forceinline__ NormAt(const NormParams& p, int64_t dsb, int64_t dst, int64_t dsg, int64_t token, int g) {
+        const int64_t b = token / p.T;
+        bt = token;
+        t = (unsigned)(token - b * p.T);
+        x = b * p.xsb + (int64_t)t * p.xst + g * p.xsg;
+        z = b * p.zsb + (int64_t)t * p.zst + g * p.zsg;
+        d = b * dsb + (int64_t)t * dst + g * dsg;
+        y = (token * p.G + g) * p.d;
+    }
+};
+struct NormStep {
+    int64_t bt, x, z, y, d, wx, wz, wd;     // wx, wz, wd: where a sequence ends, on top
+    unsigned t, T;
+    __device__ __forceinline__ NormStep(const NormParams& p, int64_t dsb, int64_t dst, int64_t step) {
+        const int64_t b = step / p.T, tt = step - b * p.T;
+        bt = step;
+        t = (unsigned)tt;
+        T = (unsigned)p.T;
+        x = b * p.xsb + tt * p.xst;
+        z = b * p.zsb + tt * p.zst;
+        d = b * dsb + tt * dst;
+        y = step * p.G * p.d;
+        wx = p.xsb - p.T * p.xst;
+        wz = p.zsb - p.T * p.zst;
+        wd = dsb - p.T * dst;
+    }
+    __device__ __forceinline__ void operator()(NormAt& r) const {
+        r.bt += bt;
+        r.t += t;
+        const bool wrap = r.t >= T;
+        r.t -= wrap ? T : 0;
+        r.x += x + (wrap ? wx : 0);
+        r.z += z + (wrap ? wz : 0);
+        r.d += d + (wrap ? wd : 0);
+        r.y += y;
+    }
+};
+
 // One row as it lies in memory.
 template <bool XB, bool OB, int L, int K, int V>
 struct NormRow {
     Raw<XB, V> x[K];
     Raw<OB, V> z[K], dy[K];
-    __device__ __forceinline__ void load(const NormParams& p, const void* dyp, int64_t bt, int g, int j) {
-        const int64_t b = bt / p.T, t = bt - b * p.T;
-        const int64_t x0 = b * p.xsb + t * p.xst + g * p.xsg, z0 = b * p.zsb + t * p.zst + g * p.zsg;
-        const int64_t y0 = (bt * p.G + g) * p.d;
+    int64_t y0, d0;
+    __device__ __forceinline__ void load(const NormParams& p, const void* dyp, const NormAt& at, int j) {
+        y0 = at.y;
+        d0 = at.d;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * L + j) * V;
@@ -129,9 +183,9 @@ struct NormRow {
             z[k].zero();
             dy[k].zero();
             if (c < p.d) {
-                x[k].load(p.x, x0 + c);
-                if (p.z) z[k].load(p.z, z0 + c);
-                if (dyp) dy[k].load(dyp, y0 + c);
+                x[k].load(p.x, at.x + c);
+                if (p.z) z[k].load(p.z, at.z + c);
+                if (dyp) dy[k].load(dyp, at.y + c);
             }
         }
     }
@@ -163,10 +217,13 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_kernel(NormParams p
     load_columns<L, K, V>(w, p.w, p, g, j, 1.f);
     load_columns<L, K, V>(b, p.b, p, g, j, 0.f);
     NormRow<XB, OB, L, K, V> cur, next;
-    next.load(p, nullptr, bt, g, j);
+    NormAt at(p, 0, 0, 0, bt, g);
+    const NormStep ahead(p, 0, 0, tokens);
+    next.load(p, nullptr, at, j);
     for (; bt < bts; bt += tokens) {
         cur = next;
-        if (bt + tokens < bts) next.load(p, nullptr, bt + tokens, g, j);
+        ahead(at);
+        if (at.bt < bts) next.load(p, nullptr, at, j);
         float x[K][V], mean, r;
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -184,7 +241,7 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_kernel(NormParams p
                     if (p.z) f[e] = v * (p.silu ? silu(gate) : gate);
                     else f[e] = p.silu ? silu(v) : v;
                 }
-                store_vec<OB, V>(p.y, (bt * p.G + g) * p.d + c, f);
+                store_vec<OB, V>(p.y, cur.y0 + c, f);
             }
         }
     }
@@ -193,7 +250,7 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_fwd_kernel(NormParams p
 // A workgroup takes rows of one head, so that a lane's columns of the weight
 // stay the same and their sums stay in registers until the end.
 template <bool XB, bool OB, int L, int K, int V>
-__global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParams q) {
+__global__ __launch_bounds__(kNormThreads, K * V <= 12 ? norm_resident(XB && OB, K, V) : 1) void gdn_norm_bwd_kernel(NormBwdParams q) {
     const NormParams& p = q.f;
     constexpr int kGroups = kNormThreads / L;
     __shared__ float red[kGroups][L * K * V];
@@ -213,12 +270,13 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParam
         for (int e = 0; e < V; ++e) sw[k][e] = sb[k][e] = 0.f;
     int64_t bt = blk * kGroups + grp;
     NormRow<XB, OB, L, K, V> cur, next;
-    if (bt < bts) next.load(p, q.dy, bt, g, j);
+    NormAt at(p, q.dsb, q.dst, q.dsg, bt, g);
+    const NormStep ahead(p, q.dsb, q.dst, step);
+    if (bt < bts) next.load(p, q.dy, at, j);
     for (; bt < bts; bt += step) {
         cur = next;
-        if (bt + step < bts) next.load(p, q.dy, bt + step, g, j);
-        const int64_t bb = bt / p.T, t = bt - bb * p.T;
-        const int64_t y0 = (bt * p.G + g) * p.d, d0 = bb * q.dsb + t * q.dst + g * q.dsg;
+        ahead(at);
+        if (at.bt < bts) next.load(p, q.dy, at, j);
         float x[K][V], dn[K][V], mean, r;
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -245,7 +303,7 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParam
                     s1 += dn[k][e];
                     s2 = fmaf(dn[k][e], n, s2);
                 }
-                if (p.z && q.dz) store_vec<OB, V>(q.dz, y0 + c, dz);
+                if (p.z && q.dz) store_vec<OB, V>(q.dz, cur.y0 + c, dz);
             }
         }
         s1 = p.center ? sum(s1) * inv : 0.f;
@@ -257,7 +315,7 @@ __global__ __launch_bounds__(kNormThreads) void gdn_norm_bwd_kernel(NormBwdParam
                 float f[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) f[e] = r * (dn[k][e] - s1 - x[k][e] * s2);
-                store_vec<XB, V>(q.dx, d0 + c, f);
+                store_vec<XB, V>(q.dx, cur.d0 + c, f);
             }
         }
     }

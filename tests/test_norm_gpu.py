@@ -75,6 +75,42 @@ def test_gradient(xdt, odt, B, T, G, d, weight, gate, heads_first, center, act):
         assert got["dx"].stride() == d_["x"].stride()
 
 
+@pytest.mark.parametrize("xdt,odt", [(F32, BF), (BF, BF)])
+@pytest.mark.parametrize("d", [7, 33, 63, 65, 97, 127, 129, 191, 193, 255, 257, 383, 385, 511, 513, 1023, 1025, 2047, 2049])
+def test_odd_rows(xdt, odt, d):
+    """Rows that no piece of four divides, at the ends of the kernels' ranges."""
+    say(f"case: norm odd rows {xdt} -> {odt} d{d}")
+    a = inputs(2, 5, 3, d, xdt, odt, d, "Gd", True, True)
+    y = torch.full((2, 5, 3, d), float("nan"), dtype=odt, device="cuda")
+    d_ = on_gpu(a)
+    gdn.gdn_norm_fwd(**d_, center=True, y=y)
+    ref.close("y", y, ref.norm(**ref.wide(a), center=True))
+    dy = ref.rand(ref.gen(d + 1), 2, 5, 3, d, dtype=odt)
+    got = gdn.gdn_norm_bwd(dy.cuda(), **d_, center=True)
+    names = ("x", "weight", "bias", "z")
+    want = ref.gradients(lambda **k: ref.norm(**k, center=True), ref.wide(a), names, (dy,))
+    for n in names:
+        ref.close("d" + n, got["d" + n], want[n])
+
+
+@pytest.mark.parametrize("B,T,G,d", [(700, 3, 2, 64), (1, 5000, 1, 24), (5000, 1, 3, 21), (37, 61, 7, 128), (2, 900, 1, 2052)])
+def test_walk_over_sequences(B, T, G, d):
+    """Groups whose next row lies in a later sequence, or several on: sliced
+    rows, as dense ones to the bit."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    wide = torch.randn(B, T + 2, G, d + 4, generator=g, device="cuda")
+    x, z = wide[:, 1:-1, :, :d], torch.randn(B, G, T, d, generator=g, device="cuda").transpose(1, 2)
+    w = torch.randn(d, generator=g, device="cuda")
+    dense = (x.contiguous(), w, w, z.contiguous())
+    y, want = gdn.gdn_norm_fwd(x, w, w, z), gdn.gdn_norm_fwd(*dense)
+    ref.close("y", want, ref.norm(*[t.cpu().double() for t in dense]))
+    assert torch.equal(y, want)
+    a, b = gdn.gdn_norm_bwd(want, x, w, w, z), gdn.gdn_norm_bwd(want, *dense)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
 def test_strides_and_alignment():
     """Slices of wider rows, aligned or not, and a broadcast x: as dense ones.
     The plain kernels sum a row in another order than the wide ones, so the
