@@ -168,7 +168,7 @@ struct SsmPlan {
 SsmPlan ssm_fwd_plan(const gdn_ssm_shape& s) {
     const int64_t tiles = (int64_t)s.G * ceil_div(s.D / s.G, 64), waves = s.B * tiles;
     SsmPlan pl{s.T, 1, 0, 0};
-    const int64_t want = ceil_div(3072, waves);
+    const int64_t want = ceil_div(3 * 1024, waves);
     if (want > 1 && s.T >= 64) {
         const int64_t len = ceil_div(ceil_div(s.T, want), gdn::kTok) * gdn::kTok;
         pl.seg_len = (int)(len < 16 ? 16 : len);

@@ -113,7 +113,7 @@ def test_walk_over_sequences(B, T, G, d):
 
 def test_strides_and_alignment():
     """Slices of wider rows, aligned or not, and a broadcast x: as dense ones.
-    The plain kernels sum a row in another order than the wide ones, so the
+    The kernels of unaligned rows sum in another order than the others, so the
     two agree within the tolerance, not to the bit."""
     a = inputs(2, 9, 3, 64, F32, F32, 3)
     want = ref.norm(**ref.wide(a))
