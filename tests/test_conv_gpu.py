@@ -165,6 +165,27 @@ def test_gradient(dtype, B, T, D, W, heads, state, act, lens):
     assert all(torch.equal(got[k], again[k]) for k in got)      # sums in a fixed order
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,heads", [(262, None), (300, 2), (300, 50), (262, 2), (257, None), (640, 5)])
+def test_gradient_pairs_and_slices(dtype, D, heads):
+    """Channels that pairs divide, or do not, and slices of wider rows that
+    leave the pairs aligned, or not."""
+    say(f"case: conv bwd pairs {dtype} D{D} heads {heads}")
+    a = inputs(2, 40, D, 4, dtype, D, True, True, [40, 29])
+    g = ref.gen(D)
+    dy = ref.rand(g, *((2, 40, D) if heads is None else (2, heads, 40, D // heads)), dtype=dtype)
+    ds = ref.rand(g, 2, 3, D, dtype=dtype)
+    names = ("x", "weight", "bias", "state0")
+    want = ref.gradients(lambda **k: ref.conv(**k, heads=heads), ref.wide(a), names, (dy, ds))
+    d = ref.dev(a)
+    for off in (0, 1, 2):
+        rows = torch.full((2, 40, D + 4 + D % 2), float("nan"), dtype=dtype, device="cuda")
+        rows[:, :, off:off + D] = d["x"]
+        got = gdn.gdn_conv_bwd(dy.cuda(), **{**d, "x": rows[:, :, off:off + D]}, dstate_out=ds.cuda())
+        for n in names:
+            ref.close("d" + n, got["d" + n], want[n])
+
+
 def test_gradient_against_differences():
     a = inputs(2, 23, 8, 4, F32, 21)
     g = ref.gen(1)
