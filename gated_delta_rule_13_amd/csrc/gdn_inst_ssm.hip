@@ -19,7 +19,7 @@ void summaries(const SsmParams& p, int nseg_summed, hipStream_t st) {
     if (nseg_summed > 0)
         hipLaunchKernelGGL((gdn_ssm_sum_kernel<kBF, NS, GRAD>), dim3((unsigned)(p.B * nseg_summed * tiles)), dim3(64), 0,
                            st, p, nseg_summed);
-    hipLaunchKernelGGL((gdn_ssm_chain_kernel<NS, GRAD>), dim3(blocks((GRAD ? 2 : 1) * p.B * tiles * NS * 64, kChainThreads)),
+    hipLaunchKernelGGL((gdn_ssm_chain_kernel<NS, GRAD>), dim3((unsigned)((GRAD ? 2 : 1) * p.B * tiles * NS)),
                        dim3(kChainThreads), 0, st, p);
 }
 

@@ -32,6 +32,8 @@
 // what the vector units' issue rate would allow at 2.4 GHz, and at 1 x 32768 x
 // 1024: 97 + 17 + 129 us.
 #pragma once
+#include <type_traits>
+
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -364,49 +366,51 @@ __global__ __launch_bounds__(64, NS <= 16 && !GRAD ? 3 : 1) void gdn_ssm_sum_ker
 
 // From the summaries, in their place: sum_e becomes the state that enters
 // each segment; sum_r the gradient of the state that leaves it, from the last
-// segment to the first (by the second half of the threads).  One thread for a
-// (sequence, tile, state, lane); kAhead segments' summaries are in flight.
+// segment to the first (by the second half of the workgroups).  One wave for a
+// (sequence, tile, state); the summaries of up to 32 segments are in flight, of
+// 4 where there are no more (the gradient at 8 x 20 x 4000 with 16 states, one
+// segment: 10 us, with 32 all the same 29).
 constexpr int kChainThreads = 64;
 template <int NS, bool GRAD>
 __global__ __launch_bounds__(kChainThreads) void gdn_ssm_chain_kernel(SsmParams p) {
-    constexpr int kAhead = 32;
-    const unsigned tiles = (unsigned)(p.G * p.tpg);
-    const int64_t per_seq = (int64_t)tiles * NS * 64, all = p.B * per_seq;
-    int64_t id = (int64_t)blockIdx.x * kChainThreads + threadIdx.x;
-    if (id >= (GRAD ? 2 : 1) * all) return;
-    const bool back = GRAD && id >= all;
-    if (back) id -= all;
-    const int b = (int)(id / per_seq);
-    const int64_t in_seq = id % per_seq;
-    const int lane = (int)(in_seq % 64), n = (int)(in_seq / 64 % NS), tile = (int)(in_seq / (64 * NS));
+    const unsigned tiles = (unsigned)(p.G * p.tpg), all = (unsigned)p.B * tiles * NS;
+    const int lane = threadIdx.x;
+    const bool back = GRAD && blockIdx.x >= all;
+    const unsigned id = back ? blockIdx.x - all : blockIdx.x;
+    const int n = (int)(id % NS), tile = (int)(id / NS % tiles), b = (int)(id / NS / tiles);
     const int c = (tile % p.tpg) * 64 + lane, g = tile / p.tpg;
     const bool on = c < p.Dg && n < p.N;
     const int64_t ch = g * p.Dg + c, at = ((int64_t)b * p.D + ch) * p.N + n;
     const float a = on ? p.A[ch * p.N + n] * kLog2e : 0.f;
     // segment j of the way: j, or from the end
-    const int64_t first = back ? p.nseg - 1 : 0, dir = back ? -1 : 1;
-    const int64_t se = dir * per_seq, ss = dir * (int64_t)tiles * 64;
-    float* e = (back ? p.sum_r : p.sum_e) + (b * p.nseg + first) * per_seq + in_seq;
-    const float* s = p.sum_s + (b * p.nseg + first) * (int64_t)tiles * 64 + tile * 64 + lane;
+    const int64_t unit = ((int64_t)b * p.nseg + (back ? p.nseg - 1 : 0)) * tiles + tile;
+    const int64_t ss = (back ? -1 : 1) * (int64_t)tiles * 64, se = ss * NS;
+    float* e = (back ? p.sum_r : p.sum_e) + (unit * NS + n) * 64;
+    const float* s = p.sum_s + unit * 64;
     const float* start = back ? p.dh_final : p.h0;
     float h = start && on ? start[at] : 0.f;
-    for (int k = 0; k < p.nseg; k += kAhead) {
-        float ev[kAhead], sv[kAhead];
+    auto run = [&](auto ahead) {
+        constexpr int kAhead = decltype(ahead)::value;
+        for (int k = 0; k < p.nseg; k += kAhead) {
+            float ev[kAhead], sv[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            // (forward alone, the last segment has no summary: none is used)
-            const int j = k + i < p.nseg - (GRAD ? 0 : 1) ? k + i : 0;
-            ev[i] = e[j * se];
-            sv[i] = s[j * ss];
-        }
+            for (int i = 0; i < kAhead; ++i) {
+                // (forward alone, the last segment has no summary: none is used)
+                const int j = k + i < p.nseg - (GRAD ? 0 : 1) ? k + i : 0;
+                ev[i] = e[j * se + lane];
+                sv[i] = s[j * ss + lane];
+            }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (k + i < p.nseg) {
-                e[(k + i) * se] = h;
-                h = fmaf(exp2_hw(sv[i] * a), h, ev[i]);
+            for (int i = 0; i < kAhead; ++i) {
+                if (k + i < p.nseg) {
+                    e[(k + i) * se + lane] = h;
+                    h = fmaf(exp2_hw(sv[i] * a), h, ev[i]);
+                }
             }
         }
-    }
+    };
+    if (p.nseg <= 4) run(std::integral_constant<int, 4>());
+    else run(std::integral_constant<int, 32>());
     if (back && p.dh0 && on) p.dh0[at] = h;
 }
 
