@@ -168,7 +168,10 @@ gdn_status validate(const gdn_ssm_shape* s) {
 // chip has 1024 vector units, which hold three such waves each.  Segments cost
 // the decays a second time, so there are none when the channels alone give
 // that many waves, and as few as do otherwise; of 16 tokens at least, where
-// what a segment costs besides its tokens is a fifth of it.
+// what a segment costs besides its tokens is a fifth of it.  Two more launches
+// pay from 64 tokens on (one sequence of 64, 16 states: 20 us either way), and
+// with more states from 32 (2 x 33 x 1000 with 64 states: 53 us in one pass, 46
+// in segments; 2 x 60: 83 and 47).
 struct SsmPlan {
     int seg_len, nseg;
     size_t off_s, bytes;
@@ -177,7 +180,7 @@ SsmPlan ssm_fwd_plan(const gdn_ssm_shape& s) {
     const int64_t tiles = (int64_t)s.G * ceil_div(s.D / s.G, 64), waves = s.B * tiles;
     SsmPlan pl{s.T, 1, 0, 0};
     const int64_t want = ceil_div(3 * 1024, waves);
-    if (want > 1 && s.T >= 64) {
+    if (want > 1 && s.T >= (gdn::ssm_states(s.N) > 16 ? 32 : 64)) {
         const int64_t len = ceil_div(ceil_div(s.T, want), gdn::kTok) * gdn::kTok;
         pl.seg_len = (int)(len < 16 ? 16 : len);
         pl.nseg = (int)ceil_div(s.T, pl.seg_len);

@@ -109,6 +109,20 @@ def test_padded_batch(dtype, T, lens, state):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,N", [(31, 64), (32, 64), (33, 33), (40, 17), (63, 24)])
+def test_short_segments(dtype, T, N):
+    """Around the shortest prompts that are cut into segments, padded."""
+    say(f"case: ssm short segments {dtype} T{T} N{N}")
+    a = inputs(4, T, 70, N, 2, dtype, T + N, True, True, [T, 16, 17, 0])
+    dead = kill(a)
+    y, h = run(a)
+    want, wh = ref.ssm(**ref.wide(a))
+    ref.close("y", y, want)
+    ref.close("h", h, wh)
+    assert (y.cpu()[dead] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_strided_rows(dtype):
     """x, dt, z, B and C as slices of wider rows at odd offsets: the same bits."""
     a = ref.dev(inputs(2, 140, 50, 16, 2, dtype, 8))
