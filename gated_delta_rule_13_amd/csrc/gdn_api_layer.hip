@@ -250,6 +250,8 @@ SsmGradPlan ssm_bwd_plan(const gdn_ssm_shape& s) {
     g.seg_len = 64;
     while (g.seg_len > 16 && (int64_t)s.B * tiles * ceil_div(s.T, g.seg_len) < 1024) g.seg_len /= 2;
     g.nseg = (int)ceil_div(s.T, g.seg_len);
+    // (one segment: nothing is kept for groups that it does not have)
+    if (g.nseg == 1) g.seg_len = (int)ceil_div(s.T, gdn::kTok) * gdn::kTok;
     const size_t units = (size_t)s.B * g.nseg * tiles, ns = gdn::ssm_states(s.N);
     g.e = 0;
     g.r = g.e + units * ns * 64 * 4;

@@ -136,6 +136,15 @@ def test_large_states(lib_nogpu):  # noqa: F811
     assert "aligned" in lib_nogpu.gdn_last_error().decode()
 
 
+def test_gradient_of_one_token_keeps_no_groups(lib_nogpu):  # noqa: F811
+    """Its workspace: a state, its gradient and dA for 64 lanes, dB and dC of
+    each tile of channels, and 3 numbers a lane."""
+    s = ssm_shape(B=128, T=1, D=4096, N=64, G=1)
+    lanes, tiles = 128 * 4096, 64
+    want = lanes * (3 * 64 + 3) * 4 + tiles * 128 * 2 * 64 * 4
+    assert lib_nogpu.gdn_ssm_bwd_workspace_bytes(ctypes.byref(s)) == want
+
+
 def test_gradient_of_the_gate_goes_with_the_gate(lib_nogpu):  # noqa: F811
     for entry in ("gdn_ssm_bwd", "gdn_norm_bwd"):
         assert call(lib_nogpu, entry, CALLS[entry][0](), z=None, x=ODD) == 1
