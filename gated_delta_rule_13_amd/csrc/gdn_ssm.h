@@ -204,7 +204,8 @@ __device__ __forceinline__ void pin(float (&v)[N]) {
 
 __device__ __forceinline__ float ssm_step_size(float raw, bool soft) { return soft ? softplus(raw) : raw; }
 
-// Tokens behind t1 take the step size 0: they leave the state as it is.
+// Tokens behind t1 take the step size 0 and x 0 (the last one's may be
+// infinite): they leave the state as it is.
 template <bool BF, int NS>
 __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmParams p) {
     __shared__ __align__(16) float bc[2][kTok][2][NS];
@@ -245,7 +246,7 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
                 const float raw = nd.v[i].get(0) + bias, soft = softplus(raw), open = silu(nz.v[i].get(0));
-                x[i] = nx.v[i].get(0);
+                x[i] = t + i < w.t1 ? nx.v[i].get(0) : 0.f;
                 s[i] = t + i < w.t1 ? (p.softplus ? soft : raw) : 0.f;
                 gate[i] = p.z ? open : 1.f;
             }
@@ -325,7 +326,7 @@ __global__ __launch_bounds__(64, NS <= 16 && !GRAD ? 3 : 1) void gdn_ssm_sum_ker
                 const bool in = t + i < w.t1;
                 const float raw = nd.v[i].get(0) + bias, soft = softplus(raw);
                 s[i] = in ? (p.softplus ? soft : raw) : 0.f;
-                u[i] = s[i] * nx.v[i].get(0);
+                u[i] = in ? s[i] * nx.v[i].get(0) : 0.f;
                 g[i] = 0.f;
                 if (GRAD) {
                     const float dy = ng.v[i].get(0), open = silu(nz.v[i].get(0));

@@ -122,6 +122,21 @@ def test_short_segments(dtype, T, N):
     assert (y.cpu()[dead] == 0).all()
 
 
+@pytest.mark.parametrize("T,n", [(9, 9), (20, 3), (300, 150), (300, 299)])
+def test_infinite_last_token(T, n):
+    """The infinity of a sequence's last token reaches the final state as one,
+    through the empty places of its group and the segments behind it."""
+    a = inputs(2, T, 20, 16, 1, F32, T, True, True, [n, n - 1])
+    a["x"][0, n - 1] = float("inf")
+    a["x"][1, n - 2] = float("-inf")
+    y, h = run(a)
+    s = torch.nn.functional.softplus(a["dt"].double() + a["dt_bias"].double())
+    for b, t in ((0, n - 1), (1, n - 2)):
+        want = torch.sign(a["x"][b, t, :, None] * a["Bm"][b, t, 0][None]) * float("inf")
+        assert (s[b, t] > 0).all() and torch.equal(h[b].cpu(), want.float())
+        assert torch.isfinite(y[b, :t]).all() and not y[b, t + 1:].any()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_strided_rows(dtype):
     """x, dt, z, B and C as slices of wider rows at odd offsets: the same bits."""
