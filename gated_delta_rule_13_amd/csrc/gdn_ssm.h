@@ -16,7 +16,7 @@
 // group: the wave stages them in LDS as fp32, kTok tokens ahead, and every lane
 // reads them at the same address (reading none of them changes nothing in the
 // time).  A lane for each state instead (16 lanes a channel, no segments below)
-// was built and took 231 us or more for what follows in 129, for the moves
+// was built and took 231 us or more for what follows in 130, for the moves
 // between lanes.
 //
 // Few channels on long sequences leave the chip empty, so the tokens are cut
@@ -28,9 +28,9 @@
 //                           another
 //   gdn_ssm_fwd_kernel      the outputs (all segments at once)
 // which costs the exponentials twice.  Measured at 4 x 4096 x 2048 with 16
-// states, bf16, gated: 97 + 8 + 129 us (24 segments), the last two thirds of
+// states, bf16, gated: 97 + 8 + 130 us (24 segments), the last two thirds of
 // what the vector units' issue rate would allow at 2.4 GHz, and at 1 x 32768 x
-// 1024: 97 + 17 + 129 us.
+// 1024: 97 + 16 + 130 us.
 #pragma once
 #include <type_traits>
 
