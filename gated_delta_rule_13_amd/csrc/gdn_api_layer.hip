@@ -72,6 +72,12 @@ gdn_status check_counts(int64_t B, int64_t T, int64_t D) {
     if ((long double)B * T * D > 1.0e15L) return set_error(GDN_ERR_BAD_SHAPE, "tensor too large");
     return GDN_OK;
 }
+// The convolution and the scan count a sequence's tokens in 32 bits, up to a
+// tile of 64 and two groups of 8 past its end.
+gdn_status check_tokens(int64_t T) {
+    if (T > 0x80000000ll - 128) return set_error(GDN_ERR_UNSUPPORTED, "T must be at most 2^31 - 128");
+    return GDN_OK;
+}
 
 // ---- short convolution ----
 gdn_status validate(const gdn_conv_shape* s) {
@@ -83,7 +89,8 @@ gdn_status validate(const gdn_conv_shape* s) {
     if (s->W < 2 || s->W > 4) return set_error(GDN_ERR_UNSUPPORTED, "W must be 2, 3 or 4");
     if (s->silu != 0 && s->silu != 1) return set_error(GDN_ERR_UNSUPPORTED, "silu must be 0 or 1");
     if (s->x_stride_b < 0 || s->x_stride_t < 0) return set_error(GDN_ERR_BAD_SHAPE, "strides must be >= 0");
-    const gdn_status st = check_counts(s->B, s->T, s->D);
+    gdn_status st = check_counts(s->B, s->T, s->D);
+    if (st == GDN_OK) st = check_tokens(s->T);
     if (st != GDN_OK) return st;
     if (s->D > (1 << 25)) return set_error(GDN_ERR_UNSUPPORTED, "D must be at most 2^25");
     return GDN_OK;
@@ -159,9 +166,8 @@ gdn_status validate(const gdn_ssm_shape* s) {
     if (s->T > 1)
         for (int64_t v : {s->x_stride_t, s->dt_stride_t, s->z_stride_t, s->b_stride_t, s->c_stride_t})
             if (v > kMaxRow) return set_error(GDN_ERR_UNSUPPORTED, "strides of tokens must be at most 2^24");
-    gdn_status st = check_counts(s->B, s->T, (int64_t)s->D * s->N);
-    if (st != GDN_OK) return st;
-    return GDN_OK;
+    const gdn_status st = check_counts(s->B, s->T, (int64_t)s->D * s->N);
+    return st != GDN_OK ? st : check_tokens(s->T);
 }
 
 // Segments of the forward pass.  One wave takes 64 channels of a segment; the

@@ -310,6 +310,7 @@ gdn_status gdn_recurrent_fwd_eta(const gdn_shape* s,
 /* Short causal convolution of each channel over W tokens. */
 typedef struct {
     int32_t B, T, D;          /* sequences, tokens, channels                   */
+                              /* (T up to 2^31 - 128, D up to 2^25)            */
     int32_t W;                /* taps: 2, 3 or 4                               */
     int32_t H;                /* heads of y and dy (D a multiple of H)         */
     int32_t dtype;            /* gdn_dtype of x, y, the states, their gradients */
@@ -356,7 +357,8 @@ typedef struct {
     int32_t B, T, D;          /* sequences, tokens, channels                   */
     int32_t N;                /* states per channel: 1 .. 64                   */
     int32_t G;                /* groups of B and C (D a multiple of G)         */
-                              /* (D and the strides of tokens: up to 2^24)     */
+                              /* (D and the strides of tokens: up to 2^24,     */
+                              /* T up to 2^31 - 128)                           */
     int32_t dtype;            /* gdn_dtype of x, dt, Bm, C, z, y and their gradients */
     int32_t dt_softplus;      /* 1: dt passes through softplus, 0: as it is    */
     int64_t x_stride_b, x_stride_t;     /* x  [B, T, D]                        */
