@@ -7,6 +7,7 @@
 #include <string>
 
 #include "gdn.h"
+#include "gdn_colsum.h"
 #include "gdn_conv.h"
 #include "gdn_error.h"
 #include "gdn_launch.h"
@@ -305,6 +306,13 @@ gdn_status validate(const gdn_norm_shape* s) {
         return set_error(GDN_ERR_UNSUPPORTED, "G must be below 2^24, and G d at most 2^27 for weights [G, d]");
     return GDN_OK;
 }
+// Whether the gradient's sums over w and b fit a launch.
+gdn_status norm_bwd_fits(const gdn_norm_shape& s) {
+    const int64_t cols = 2 * (s.w_per_group ? (int64_t)s.G * s.d : s.d);
+    if (!threads_ok(gdn::colsum_threads(cols)))
+        return set_error(GDN_ERR_UNSUPPORTED, "G d must be below 2^27 in the gradient for weights [G, d]");
+    return GDN_OK;
+}
 gdn::NormParams norm_params(const gdn_norm_shape& s, const void* x, const float* w, const float* b, const void* z) {
     gdn::NormParams p{};
     p.x = x;
@@ -537,7 +545,7 @@ gdn_status gdn_norm_fwd(const gdn_norm_shape* s, const void* x, const float* wei
 
 size_t gdn_norm_bwd_workspace_bytes(const gdn_norm_shape* s) {
     gdn::clear_error();
-    if (validate(s) != GDN_OK) return kInvalid;
+    if (validate(s) != GDN_OK || norm_bwd_fits(*s) != GDN_OK) return kInvalid;
     return up256((size_t)norm_bwd_blocks(*s, gdn::kNormResident) * 2 * s->G * s->d * 4);
 }
 
@@ -546,6 +554,7 @@ gdn_status gdn_norm_bwd(const gdn_norm_shape* s, const void* dy, const void* x, 
                         float* dweight, float* dbias, void* dz, void* workspace, size_t workspace_bytes, void* stream) {
     gdn::clear_error();
     gdn_status st = validate(s);
+    if (st == GDN_OK) st = norm_bwd_fits(*s);
     if (st != GDN_OK) return st;
     if (!dy || !x || !dx) return set_error(GDN_ERR_NULL_ARG, "dy, x and dx are required");
     if ((z != nullptr) != (dz != nullptr)) return set_error(GDN_ERR_NULL_ARG, "dz goes with z");

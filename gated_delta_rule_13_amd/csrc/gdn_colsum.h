@@ -44,6 +44,9 @@ static __global__ __launch_bounds__(64 * kColsumSlices) void gdn_colsum_kernel(C
     }
 }
 
+// Threads of a sum over `cols` columns (a launch counts them in 32 bits).
+constexpr int64_t colsum_threads(int64_t cols) { return (cols + 63) / 64 * 64 * kColsumSlices; }
+
 inline void launch_colsum(const float* part, int64_t rows, float* out0, int64_t n0, float* out1, int64_t n1,
                           hipStream_t st) {
     ColsumParams p{part, out0, out1, rows, n0, n1};

@@ -420,7 +420,8 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape* s, const void* dy, const void* x, co
 /* Normalisation of each head of each token, with an activation or a gate. */
 typedef struct {
     int32_t B, T, G, d;       /* sequences, tokens, heads (groups), head size 1 .. 4096 */
-                              /* (G below 2^24; weights [G, d]: G d up to 2^27) */
+                              /* (G below 2^24; weights [G, d]: G d up to 2^27,
+                                 in the gradient below it) */
     int32_t x_dtype;          /* gdn_dtype of x and dx                         */
     int32_t o_dtype;          /* gdn_dtype of y, dy, z and dz                  */
     int32_t center;           /* 1: subtract the mean, 0: root mean square only */

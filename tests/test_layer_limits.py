@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from tests.test_abi import lib, lib_nogpu  # noqa: F401
-from tests.test_layer_abi import BIG, CALLS, ODD, WORKSPACE, call
+from tests.test_layer_abi import BIG, CALLS, ODD, WORKSPACE, call, norm_shape
 
 MOST = 2 ** 31 - 128                # tokens: the kernels walk them, a tile ahead, in 32 bits
 
@@ -24,3 +24,18 @@ def test_tokens(lib_nogpu, entry, past):  # noqa: F811
         query = getattr(lib_nogpu, entry + "_workspace_bytes")
         assert query(ctypes.byref(shape(T=MOST, **one))) < BIG
         assert query(ctypes.byref(shape(T=MOST + past, **one))) == BIG
+
+
+def test_gradient_of_many_head_weights(lib_nogpu):  # noqa: F811
+    """The sums over w and b of 2^27 numbers each: one thread more than a
+    launch counts.  (The forward pass has no such sums.)"""
+    query = lib_nogpu.gdn_norm_bwd_workspace_bytes
+    for d, fits in ((128, False), (127, True)):
+        shape = norm_shape(G=2 ** 20, d=d, w_per_group=1)
+        assert (query(ctypes.byref(shape)) < BIG) == fits
+        assert call(lib_nogpu, "gdn_norm_bwd", shape, strides=(2 ** 34, 2 ** 27, 128), x=ODD) == 4
+        assert ("aligned" in lib_nogpu.gdn_last_error().decode()) == fits
+        assert call(lib_nogpu, "gdn_norm_fwd", shape, x=ODD) == 4
+        assert "aligned" in lib_nogpu.gdn_last_error().decode()
+    # (weights [d]: one sum for all heads)
+    assert query(ctypes.byref(norm_shape(G=2 ** 20, d=256))) < BIG
