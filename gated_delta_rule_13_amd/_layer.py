@@ -22,6 +22,7 @@ __all__ = ["gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step", "gdn_conv_bwd_worksp
            "gdn_ssm_bwd_workspace_bytes",
            "gdn_norm_fwd", "gdn_norm_bwd", "gdn_norm_bwd_workspace_bytes"]
 
+_INT32 = 2 ** 31 - 1
 _CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 
 
@@ -87,6 +88,8 @@ def _check(name, t, shape, dtype, device, tail=None):
 def _rank(name, t, n):
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+    if t.numel() > _INT32 and max(t.shape) > _INT32:      # (the shape structures would wrap)
+        raise ValueError(f"the dimensions of {name} must be below 2^31, got {tuple(t.shape)}")
 
 
 def _separate(name, out, **inputs):
