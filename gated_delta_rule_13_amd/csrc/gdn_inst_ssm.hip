@@ -27,7 +27,9 @@ template <int NS>
 void fwd(const SsmParams& p, hipStream_t st) {
     const int64_t tiles = (int64_t)p.G * p.tpg;
     if (p.nseg > 1) summaries<NS, false>(p, p.nseg - 1, st);
-    hipLaunchKernelGGL((gdn_ssm_fwd_kernel<kBF, NS>), dim3((unsigned)(p.B * p.nseg * tiles)), dim3(64), 0, st, p);
+    const dim3 grid((unsigned)(p.B * p.nseg * tiles));
+    if (p.N == NS) hipLaunchKernelGGL((gdn_ssm_fwd_kernel<kBF, NS, false>), grid, dim3(64), 0, st, p);
+    else hipLaunchKernelGGL((gdn_ssm_fwd_kernel<kBF, NS, true>), grid, dim3(64), 0, st, p);
 }
 
 template <int NS, int NB>

@@ -172,7 +172,8 @@ __device__ __forceinline__ void load_states(float (&v)[NS], const float* s, cons
         for (int n = 0; n < NS; ++n) v[n] = n0 + n < p.N ? s[row * p.N + n0 + n] : 0.f;
     }
 }
-// A log2(e) (0 behind the N states, which then stay 0)
+// A log2(e) (0 behind the N states, which then stay 0 while x and the step size
+// are finite)
 template <int NS>
 __device__ __forceinline__ void load_decay(float (&a)[NS], const SsmParams& p, int c, int n0 = 0) {
     load_states<NS>(a, p.A, p, c, n0);
@@ -204,9 +205,61 @@ __device__ __forceinline__ void pin(float (&v)[N]) {
 
 __device__ __forceinline__ float ssm_step_size(float raw, bool soft) { return soft ? softplus(raw) : raw; }
 
-// Tokens behind t1 take the step size 0 and x 0 (the last one's may be
-// infinite): they leave the state as it is.
+// The state that enters a segment.
+template <int NS>
+__device__ __forceinline__ void load_entering(float (&h)[NS], const SsmParams& p, const SsmPlace& w, int lane) {
+    if (p.nseg > 1) {
+        load_sum<NS>(h, p.sum_e, w.unit, lane);
+    } else if (p.h0) {
+        load_states<NS>(h, p.h0, p, (int64_t)w.b * p.D + w.c);
+    } else {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) h[n] = 0.f;
+    }
+}
+
+// The outputs of a segment token by token, over the N states alone.
 template <bool BF, int NS>
+__device__ __forceinline__ void ssm_fwd_tokens(float (&h)[NS], unsigned id, int lane) {
+    // (the kernel's only argument read again, so that nothing of this takes
+    // registers in the loop over groups)
+    typedef const __attribute__((address_space(4))) SsmParams* Arg;
+    Arg arg = (Arg)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(id), "+s"(arg));
+    const SsmParams p = *(const SsmParams*)arg;
+    const SsmPlace w = ssm_place(p, id, p.nseg, lane);
+    float a[NS];
+    load_entering<NS>(h, p, w, lane);
+    load_decay<NS>(a, p, w.c);
+    const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
+#pragma unroll 1
+    for (int t = w.t0; t < w.t1; ++t) {
+        const char* bm = row_at<BF>(p.Bm, w.b * p.bsb + t * p.bst + w.g * p.N);
+        const char* cm = row_at<BF>(p.C, w.b * p.csb + t * p.cst + w.g * p.N);
+        const float x = load_one<BF>(p.x, w.b * p.xsb + t * p.xst + w.c);
+        const float s = ssm_step_size(load_one<BF>(p.dt, w.b * p.dsb + t * p.dst + w.c) + bias, p.softplus), u = s * x;
+        float y = dskip * x;
+        int N = p.N;
+        asm volatile("" : "+s"(N));                  // (the comparisons stay here)
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            if (n < N) {
+                h[n] = fmaf(exp2_hw(s * a[n]), h[n], u * load_one<BF>(bm, n));
+                y = fmaf(h[n], load_one<BF>(cm, n), y);
+            }
+        }
+        if (p.z) y *= silu(load_one<BF>(p.z, w.b * p.zsb + t * p.zst + w.c));
+        if (w.on) store_one<BF>(p.y, ((int64_t)w.b * p.T + t) * p.D + w.c, y);
+    }
+}
+
+// Tokens behind t1 take the step size 0 and x 0 (the last one's may be
+// infinite): they leave the state as it is.  PAD: fewer than NS states.  The
+// places behind them stay 0 by themselves unless u is infinite (u times their 0
+// is NaN, and is in y): the last place shows it, and the segment is done again
+// without them.  (Leaving the places out in the loop, state by state, took 316
+// us for 270 at 4 x 2048 x 1024 with 48 states; clearing them there 297.)
+template <bool BF, int NS, bool PAD>
 __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmParams p) {
     __shared__ __align__(16) float bc[2][kTok][2][NS];
     const int lane = threadIdx.x;
@@ -218,14 +271,7 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
     const int64_t zb = p.z ? w.b * p.zsb + w.c0 : xb, zst = p.z ? p.zst : p.xst;
     const uint32_t off = (uint32_t)(w.c - w.c0) * (BF ? 2 : 4), out = w.on ? off : kOutside;
     float a[NS], h[NS];
-    if (p.nseg > 1) {
-        load_sum<NS>(h, p.sum_e, w.unit, lane);
-    } else if (p.h0) {
-        load_states<NS>(h, p.h0, p, (int64_t)w.b * p.D + w.c);
-    } else {
-#pragma unroll
-        for (int n = 0; n < NS; ++n) h[n] = 0.f;
-    }
+    load_entering<NS>(h, p, w, lane);
     const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
 
     if (w.t0 < w.t1) {
@@ -266,6 +312,7 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
                 pin(h);
             }
         }
+        if (PAD && __any(__builtin_isnan(h[NS - 1]))) ssm_fwd_tokens<BF, NS>(h, blockIdx.x, lane);
     }
     if (w.on) {
         for (int t = w.t0 > w.t1 ? w.t0 : w.t1; t < w.tz; ++t) store_one<BF>(p.y, yb + (int64_t)t * p.D, 0.f);
@@ -404,7 +451,8 @@ __global__ __launch_bounds__(kChainThreads) void gdn_ssm_chain_kernel(SsmParams 
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 if (k + i < p.nseg) {
-                    e[(k + i) * se + lane] = h;
+                    // (0 where there is no state: an infinite x leaves NaN in the summaries there)
+                    e[(k + i) * se + lane] = on ? h : 0.f;
                     h = fmaf(exp2_hw(sv[i] * a), h, ev[i]);
                 }
             }
@@ -786,6 +834,7 @@ __global__ __launch_bounds__(kStepThreads) void gdn_ssm_step_kernel(SsmStepParam
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         h[e] = fmaf(exp2_hw(s * (a[e] * kLog2e)), h[e], u * bm[e]);
+        if (n0 + e >= p.N) h[e] = 0.f;           // (an infinite u leaves NaN behind the states)
         y = fmaf(h[e], cm[e], y);
     }
 #pragma unroll

@@ -1,0 +1,72 @@
+"""Infinite numbers in the operators around the recurrence: an output is what
+the formula gives, wherever the infinity falls in a kernel's groups, tiles and
+padding.  Inputs are positive where the formula would otherwise subtract two
+infinities; what the formula leaves undefined is not compared."""
+import pytest
+import torch
+
+import gated_delta_rule_13_amd as gdn
+from tests import layer_ref as ref
+from tests.gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+INF = float("inf")
+
+
+def meets(name, got, want):
+    """got where the fp64 reference has a value: infinities alike, the finite
+    numbers as layer_ref.close takes them (the largest of the finite ones)."""
+    assert tuple(got.shape) == tuple(want.shape), (name, tuple(got.shape), tuple(want.shape))
+    g, w = got.detach().double().cpu(), want.detach().double().cpu()
+    wild = torch.isinf(w)
+    bad = wild & (g != w)
+    assert not bad.any(), f"{name}: {int(bad.sum())} of {int(wild.sum())} infinities are not, e.g. {g[bad][:3].tolist()}"
+    calm = torch.isfinite(w)
+    if calm.any():
+        ref.close(name, got.detach().cpu()[calm], w[calm])
+
+
+def inputs(T, D, N, dtype, seed, D_=True, z=True):
+    g = ref.gen(seed)
+    pos = lambda *s, **k: ref.rand(g, *s, **k).abs() + 0.01  # noqa: E731
+    return {"x": pos(1, T, D).to(dtype), "dt": ref.rand(g, 1, T, D, std=0.5, dtype=dtype),
+            "A": -torch.arange(1, N + 1).float() * torch.exp(ref.rand(g, D, N, std=0.2)),
+            "Bm": pos(1, T, 1, N).to(dtype), "C": pos(1, T, 1, N).to(dtype), "D": pos(D) if D_ else None,
+            "z": pos(1, T, D).to(dtype) if z else None, "dt_bias": ref.rand(g, D) - 3, "h0": pos(1, D, N)}
+
+
+ROWS = ("x", "dt", "Bm", "C", "z")
+
+
+def padded(a, T, names=ROWS):
+    """The sequence in a batch padded to T rows, NaN behind it."""
+    n = a["x"].shape[1]
+    out = dict(a, lens=torch.tensor([n], dtype=torch.int32))
+    for k in names:
+        if a.get(k) is not None:
+            out[k] = torch.full((1, T) + tuple(a[k].shape[2:]), float("nan"), dtype=a[k].dtype)
+            out[k][:, :n] = a[k]
+    return out
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [1, 3, 5, 7, 12, 17, 24, 33, 48, 4, 16, 64])
+@pytest.mark.parametrize("T", [1, 13, 200])
+@pytest.mark.parametrize("where", ["x", "dt"])
+def test_scan_states(dtype, N, T, where):
+    """Any number of states: those that fill up a kernel's size take no part."""
+    say(f"case: infinite {where} {dtype} T{T} N{N}")
+    a = inputs(T, 20, N, dtype, T + N)
+    a[where][0, T // 2, 3] = INF
+    want, wh = ref.ssm(**ref.wide(a))
+    assert torch.isinf(want).any() and torch.isfinite(want).any()
+    y, h = gdn.gdn_ssm_fwd(**ref.dev(a))
+    meets("y", y, want)
+    meets("h", h, wh)
+    if T == 1:
+        d = {k: v[:, 0] if k in ROWS else v for k, v in ref.dev(a).items()}
+        state = d.pop("h0")
+        meets("y", gdn.gdn_ssm_step(**d, h=state), want[:, 0])
+        meets("h", state, wh)
