@@ -37,7 +37,9 @@ void bwd(const SsmParams& p, float* dA, void* dBm, void* dC, float* dD, float* d
     constexpr int NSA = NS * NB;
     const int64_t tiles = (int64_t)p.G * p.tpg;
     summaries<NSA, true>(p, p.nseg, st);
-    hipLaunchKernelGGL((gdn_ssm_bwd_kernel<kBF, NS, NB>), dim3((unsigned)(p.B * p.nseg * tiles)), dim3(64 * NB), 0, st, p);
+    const dim3 grid((unsigned)(p.B * p.nseg * tiles));
+    if (p.N == NSA) hipLaunchKernelGGL((gdn_ssm_bwd_kernel<kBF, NS, NB, false>), grid, dim3(64 * NB), 0, st, p);
+    else hipLaunchKernelGGL((gdn_ssm_bwd_kernel<kBF, NS, NB, true>), grid, dim3(64 * NB), 0, st, p);
     SsmSumParams q{p, dBm, dC, dA, dD, dbias, NSA, blocks((int64_t)p.B * p.T * p.G * 2 * NSA, kSumThreads)};
     hipLaunchKernelGGL((gdn_ssm_grad_sum_kernel<kBF>), dim3(q.bc + (unsigned)(tiles * (NSA + 2))), dim3(kSumThreads), 0, st,
                        q);

@@ -218,15 +218,20 @@ __device__ __forceinline__ void load_entering(float (&h)[NS], const SsmParams& p
     }
 }
 
-// The outputs of a segment token by token, over the N states alone.
-template <bool BF, int NS>
-__device__ __forceinline__ void ssm_fwd_tokens(float (&h)[NS], unsigned id, int lane) {
-    // (the kernel's only argument read again, so that nothing of this takes
-    // registers in the loop over groups)
+// The argument of a kernel that has no other, read again, and the workgroup's
+// number as if it were new: so that what is done with them, in a case that is
+// rare, takes no registers from what comes before.
+__device__ __forceinline__ SsmParams argument_again(unsigned& id) {
     typedef const __attribute__((address_space(4))) SsmParams* Arg;
     Arg arg = (Arg)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(id), "+s"(arg));
-    const SsmParams p = *(const SsmParams*)arg;
+    return *(const SsmParams*)arg;
+}
+
+// The outputs of a segment token by token, over the N states alone.
+template <bool BF, int NS>
+__device__ __forceinline__ void ssm_fwd_tokens(float (&h)[NS], unsigned id, int lane) {
+    const SsmParams p = argument_again(id);
     const SsmPlace w = ssm_place(p, id, p.nseg, lane);
     float a[NS];
     load_entering<NS>(h, p, w, lane);
@@ -511,19 +516,24 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // sums over tiles and segments 11.  The vector units are busy nine tenths of
 // the time: about 26 issue slots for a (token, channel, state) with its share
 // of the rest, two fifths of them in the sums over channels.
-template <bool BF, int NS, int NB>
-__global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 ? 4 : 3) void gdn_ssm_bwd_kernel(SsmParams p) {
+//
+// CLEAR: the places behind the N states are 0, whatever the inputs.  They are 0
+// by themselves unless a step size, u or dyg is infinite; then they are NaN, and
+// so would be du, ds and y.  Returns whether the last of them was.  (p by value:
+// a reference costs 2.6 % in the order of instructions.)
+template <bool BF, int NS, int NB, bool CLEAR>
+__device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float (&bc_all)[NB][kTok][2][NS],
+                                                float (&el)[5][kTok][64], float (&start)[NB][NS][64],
+                                                float (&cross)[NB > 1 ? NB : 1][NB > 1 ? 3 * kTok : 1][64]) {
     constexpr int NSA = NS * NB;                     // states of the layout
     constexpr bool HOLD = NS <= 4;                   // the group's decays stay in registers too
-    __shared__ __align__(16) float bc_all[NB][kTok][2][NS];
-    __shared__ float el[5][kTok][64];
-    __shared__ float start[NB][NS][64];
     enum { kS, kX, kGy, kZs, kSg };                  // step size, x, dy silu(z), dy silu'(z), slope of softplus
-    __shared__ float cross[NB > 1 ? NB : 1][NB > 1 ? 3 * kTok : 1][64];
     const int lane = threadIdx.x & 63, blk = NB > 1 ? threadIdx.x >> 6 : 0;
     float(&bc)[kTok][2][NS] = bc_all[blk];
-    const SsmPlace w = ssm_place(p, blockIdx.x, p.nseg, lane);
+    const SsmPlace w = ssm_place(p, id, p.nseg, lane);
     const int n0 = blk * NS;
+    const int states = CLEAR ? __builtin_amdgcn_readfirstlane(p.N - n0) : NS;    // of the wave
+    bool wild = false;
     const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c;
     const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
     const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
@@ -550,6 +560,9 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 ? 4 : 3) void gdn_ssm_b
             for (int n = 0; n < NS; ++n)
                 h[n] = fmaf(exp2_hw(sk * a[n]), h[n], p.keep_h[(at * NSA + n0 + n) * 64 + lane]);
         }
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            if (CLEAR && n >= states) h[n] = 0.f;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kTok * 2 * NS / 64; ++i) {
@@ -601,10 +614,12 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 ? 4 : 3) void gdn_ssm_b
             for (int n = 0; n < NS; ++n) {
                 const float decay = exp2_hw(si * a[n]);
                 hs[i][n] = fmaf(decay, i > 0 ? hs[i > 0 ? i - 1 : 0][n] : h[n], u * bc[i][0][n]);
+                if (CLEAR && n >= states) hs[i][n] = 0.f;
                 if (HOLD) decays[i][HOLD ? n : 0] = decay;
             }
             pin(hs[i]);
         }
+        wild |= __builtin_isnan(hs[kTok - 1][NS - 1]);
         // the outputs of token i of the lane's channel
         auto finish = [&](int i, float y, float du, float ds) {
             if (t + i < w.t1) {
@@ -636,10 +651,12 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 ? 4 : 3) void gdn_ssm_b
                 for (int n = 0; n < NS; ++n) {
                     const float c = bc[i][1][n];
                     g[n] = fmaf(c, gy, g[n]);
+                    if (CLEAR && n >= states) g[n] = 0.f;
                     v[(i - i0) * NS + n] = swap32_add(g[n] * u, gy * hs[i][n]);
                     y = fmaf(hs[i][n], c, y);
                     du = fmaf(g[n], bc[i][0][n], du);
                     g[n] *= HOLD ? decays[i][HOLD ? n : 0] : exp2_hw(si * a[n]);
+                    if (CLEAR && n >= states) g[n] = 0.f;
                     const float q = g[n] * (i > 0 ? hs[i > 0 ? i - 1 : 0][n] : start[blk][n][lane]);
                     ds = fmaf(q, a[n], ds);
                     da[n] = fmaf(q, si, da[n]);
@@ -675,6 +692,7 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 ? 4 : 3) void gdn_ssm_b
             }
         }
     }
+    wild |= __builtin_isnan(g[NS - 1]);
     const unsigned tiles = (unsigned)(p.G * p.tpg);
     const int64_t at = ((int64_t)w.b * p.nseg + w.seg) * tiles + w.tile;
 #pragma unroll
@@ -702,6 +720,25 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 ? 4 : 3) void gdn_ssm_b
                 if (p.z) store_one<BF>(p.dz, o, 0.f);
             }
         }
+    }
+    return wild;
+}
+
+// PAD: fewer than NS NB states.  A segment with such numbers is done again
+// (clearing the places every time: 107.8 us for 103.3 at 2 x 1024 x 1024 with 24
+// states).  One wave with both forms needs the registers of three on a vector
+// unit (3 states: 44.8 us, in those of four 47.2).
+template <bool BF, int NS, int NB, bool PAD>
+__global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 && !(PAD && NB == 1) ? 4 : 3) void gdn_ssm_bwd_kernel(SsmParams p) {
+    __shared__ __align__(16) float bc[NB][kTok][2][NS];
+    __shared__ float el[5][kTok][64];
+    __shared__ float start[NB][NS][64];
+    __shared__ float cross[NB > 1 ? NB : 1][NB > 1 ? 3 * kTok : 1][64];
+    const bool wild = ssm_bwd_segment<BF, NS, NB, false>(p, blockIdx.x, bc, el, start, cross);
+    if (PAD && __syncthreads_or(wild)) {
+        unsigned id = blockIdx.x;
+        const SsmParams again = argument_again(id);
+        ssm_bwd_segment<BF, NS, NB, true>(again, id, bc, el, start, cross);
     }
 }
 

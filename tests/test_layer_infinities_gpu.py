@@ -29,10 +29,12 @@ def meets(name, got, want):
 
 
 def inputs(T, D, N, dtype, seed, D_=True, z=True):
+    """(Decay rates up to about 3: the decay over a segment of tokens stays a
+    number of fp32 above 0, whose product with an infinity is one.)"""
     g = ref.gen(seed)
     pos = lambda *s, **k: ref.rand(g, *s, **k).abs() + 0.01  # noqa: E731
     return {"x": pos(1, T, D).to(dtype), "dt": ref.rand(g, 1, T, D, std=0.5, dtype=dtype),
-            "A": -torch.arange(1, N + 1).float() * torch.exp(ref.rand(g, D, N, std=0.2)),
+            "A": -2 * torch.arange(1, N + 1).float() / N * torch.exp(ref.rand(g, D, N, std=0.2)),
             "Bm": pos(1, T, 1, N).to(dtype), "C": pos(1, T, 1, N).to(dtype), "D": pos(D) if D_ else None,
             "z": pos(1, T, D).to(dtype) if z else None, "dt_bias": ref.rand(g, D) - 3, "h0": pos(1, D, N)}
 
@@ -70,3 +72,42 @@ def test_scan_states(dtype, N, T, where):
         state = d.pop("h0")
         meets("y", gdn.gdn_ssm_step(**d, h=state), want[:, 0])
         meets("h", state, wh)
+
+
+def gradient(a, dy, dh, **kw):
+    got = gdn.gdn_ssm_bwd(dy.cuda(), **ref.dev(a), dh_final=dh.cuda(), **kw)
+    return {("B" if k == "dB" else k): v for k, v in got.items()}
+
+
+def check_gradient(a, dy, dh, T=None):
+    """Against autograd through the formula, the sequence alone or padded to T
+    rows."""
+    n = a["x"].shape[1]
+    names = [k for k in ("x", "dt", "A", "Bm", "C", "D", "z", "dt_bias", "h0") if a[k] is not None]
+    want = ref.gradients(ref.ssm, ref.wide(a), names, (dy, dh))
+    if T is not None:
+        rows = padded(dict(a, dy=dy), T, ROWS + ("dy",))
+        dy = rows.pop("dy")
+        a = rows
+    got = gradient(a, dy, dh)
+    for k in names:
+        v = got["B" if k == "Bm" else "d" + k]
+        if k in ROWS and T is not None:
+            assert not v[:, n:].any(), k
+            v = v[:, :n]
+        meets("d" + k, v, want[k])
+    return want
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [1, 3, 5, 7, 12, 24, 33, 48, 4, 16, 64])
+@pytest.mark.parametrize("where", ["x", "dy", "dt"])
+@pytest.mark.parametrize("T,t", [(24, 9), (88, 49)])
+def test_scan_gradient_states(dtype, N, where, T, t):
+    say(f"case: infinite {where}, gradient {dtype} N{N} T{T}")
+    a = inputs(T, 64, N, dtype, N)
+    g = ref.gen(N)
+    dy, dh = ref.rand(g, 1, T, 64).abs().to(dtype), ref.rand(g, 1, 64, N).abs()
+    (dy if where == "dy" else a[where])[0, t, 3] = INF
+    want = check_gradient(a, dy, dh)
+    assert any(torch.isinf(v).any() for v in want.values())
