@@ -218,6 +218,20 @@ __device__ __forceinline__ void load_entering(float (&h)[NS], const SsmParams& p
     }
 }
 
+template <int NS>
+__device__ __forceinline__ void store_final(const float (&h)[NS], const SsmParams& p, const SsmPlace& w) {
+    float* out = p.h_final + ((int64_t)w.b * p.D + w.c) * p.N;
+    if (p.wide_out) {
+#pragma unroll
+        for (int n = 0; n < NS; n += 4)
+            if (n < p.N) *reinterpret_cast<f32x4*>(out + n) = f32x4{h[n], h[n + 1], h[n + 2], h[n + 3]};
+    } else {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            if (n < p.N) out[n] = h[n];
+    }
+}
+
 // The argument of a kernel that has no other, read again, and the workgroup's
 // number as if it were new: so that what is done with them, in a case that is
 // rare, takes no registers from what comes before.
@@ -228,12 +242,13 @@ __device__ __forceinline__ SsmParams argument_again(unsigned& id) {
     return *(const SsmParams*)arg;
 }
 
-// The outputs of a segment token by token, over the N states alone.
+// The outputs and the final state of a segment token by token, over the N states
+// alone.
 template <bool BF, int NS>
-__device__ __forceinline__ void ssm_fwd_tokens(float (&h)[NS], unsigned id, int lane) {
+__device__ __forceinline__ void ssm_fwd_tokens(unsigned id, int lane) {
     const SsmParams p = argument_again(id);
     const SsmPlace w = ssm_place(p, id, p.nseg, lane);
-    float a[NS];
+    float a[NS], h[NS];
     load_entering<NS>(h, p, w, lane);
     load_decay<NS>(a, p, w.c);
     const float dskip = p.Dskip ? p.Dskip[w.c] : 0.f, bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
@@ -256,6 +271,7 @@ __device__ __forceinline__ void ssm_fwd_tokens(float (&h)[NS], unsigned id, int 
         if (p.z) y *= silu(load_one<BF>(p.z, w.b * p.zsb + t * p.zst + w.c));
         if (w.on) store_one<BF>(p.y, ((int64_t)w.b * p.T + t) * p.D + w.c, y);
     }
+    if (w.on && p.h_final && w.seg == p.nseg - 1) store_final<NS>(h, p, w);
 }
 
 // Tokens behind t1 take the step size 0 and x 0 (the last one's may be
@@ -317,23 +333,13 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
                 pin(h);
             }
         }
-        if (PAD && __any(__builtin_isnan(h[NS - 1]))) ssm_fwd_tokens<BF, NS>(h, blockIdx.x, lane);
     }
+    const bool again = PAD && __any(__builtin_isnan(h[NS - 1]));
     if (w.on) {
         for (int t = w.t0 > w.t1 ? w.t0 : w.t1; t < w.tz; ++t) store_one<BF>(p.y, yb + (int64_t)t * p.D, 0.f);
-        if (p.h_final && w.seg == p.nseg - 1) {
-            float* out_h = p.h_final + ((int64_t)w.b * p.D + w.c) * p.N;
-            if (p.wide_out) {
-#pragma unroll
-                for (int n = 0; n < NS; n += 4)
-                    if (n < p.N) *reinterpret_cast<f32x4*>(out_h + n) = f32x4{h[n], h[n + 1], h[n + 2], h[n + 3]};
-            } else {
-#pragma unroll
-                for (int n = 0; n < NS; ++n)
-                    if (n < p.N) out_h[n] = h[n];
-            }
-        }
+        if (!again && p.h_final && w.seg == p.nseg - 1) store_final<NS>(h, p, w);
     }
+    if (again) ssm_fwd_tokens<BF, NS>(blockIdx.x, lane);
 }
 
 // Summaries of the segments.  E = sum_t P_end / P_t u_t Bm_t, with P_t the
