@@ -203,6 +203,11 @@ __device__ __forceinline__ void pin(float (&v)[N]) {
     for (int n = 0; n < N; ++n) asm volatile("" : "+v"(v[n]) : : "memory");
 }
 
+// a + Dskip b.  Without a skip a itself: not 0 times what may be infinite.
+__device__ __forceinline__ float ssm_skip(const SsmParams& p, float dskip, float b, float a) {
+    return p.Dskip ? fmaf(dskip, b, a) : a;
+}
+
 __device__ __forceinline__ float ssm_step_size(float raw, bool soft) { return soft ? softplus(raw) : raw; }
 
 // The state that enters a segment.
@@ -258,7 +263,7 @@ __device__ __forceinline__ void ssm_fwd_tokens(unsigned id, int lane) {
         const char* cm = row_at<BF>(p.C, w.b * p.csb + t * p.cst + w.g * p.N);
         const float x = load_one<BF>(p.x, w.b * p.xsb + t * p.xst + w.c);
         const float s = ssm_step_size(load_one<BF>(p.dt, w.b * p.dsb + t * p.dst + w.c) + bias, p.softplus), u = s * x;
-        float y = dskip * x;
+        float y = ssm_skip(p, dskip, x, 0.f);
         int N = p.N;
         asm volatile("" : "+s"(N));                  // (the comparisons stay here)
 #pragma unroll
@@ -323,7 +328,7 @@ __global__ __launch_bounds__(64, NS <= 16 ? 3 : 1) void gdn_ssm_fwd_kernel(SsmPa
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
                 const float u = s[i] * x[i];
-                float y = dskip * x[i];
+                float y = ssm_skip(p, dskip, x[i], 0.f);
 #pragma unroll
                 for (int n = 0; n < NS; ++n) {
                     h[n] = fmaf(exp2_hw(s[i] * a[n]), h[n], u * bc[buf][i][0][n]);
@@ -636,9 +641,9 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
                 dd = fmaf(gy, x, dd);
                 if (w.on) {
                     const int64_t o = yb + (int64_t)(t + i) * p.D;
-                    store_one<BF>(p.dx, o, fmaf(dskip, gy, el[kS][i][lane] * du));
+                    store_one<BF>(p.dx, o, ssm_skip(p, dskip, gy, el[kS][i][lane] * du));
                     store_one<BF>(p.ddt, o, dr);
-                    if (p.z) store_one<BF>(p.dz, o, el[kZs][i][lane] * fmaf(dskip, x, y));
+                    if (p.z) store_one<BF>(p.dz, o, el[kZs][i][lane] * ssm_skip(p, dskip, x, y));
                 }
             }
         };
@@ -890,7 +895,7 @@ __global__ __launch_bounds__(kStepThreads) void gdn_ssm_step_kernel(SsmStepParam
         for (int e = 0; e < 4; ++e)
             if (n0 + e < p.N) q.h[hi + e] = h[e];
     }
-    if (n0 == 0) store_one<BF>(p.y, b * p.D + d, fmaf(p.Dskip ? p.Dskip[d] : 0.f, x, y) * gate);
+    if (n0 == 0) store_one<BF>(p.y, b * p.D + d, ssm_skip(p, p.Dskip ? p.Dskip[d] : 0.f, x, y) * gate);
 }
 
 }  // namespace gdn

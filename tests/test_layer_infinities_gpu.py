@@ -111,3 +111,29 @@ def test_scan_gradient_states(dtype, N, where, T, t):
     (dy if where == "dy" else a[where])[0, t, 3] = INF
     want = check_gradient(a, dy, dh)
     assert any(torch.isinf(v).any() for v in want.values())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [11, 90])
+def test_scan_without_skip(dtype, T):
+    """No skip term: not 0 times an infinite x."""
+    a = inputs(T, 24, 16, dtype, T, D_=False, z=False)
+    a["x"][0, 6, 5] = INF
+    want, _ = ref.ssm(**ref.wide(a))
+    y, _ = gdn.gdn_ssm_fwd(**ref.dev(a))
+    assert torch.isinf(want).any()
+    meets("y", y, want)
+    one = {k: v[:, 6] if k in ROWS else v for k, v in ref.dev({k: v for k, v in a.items() if v is not None}).items()}
+    state = one.pop("h0")
+    first, _ = ref.ssm(**{k: v[:, 6:7] if k in ROWS and v is not None else v for k, v in ref.wide(a).items()})
+    meets("y", gdn.gdn_ssm_step(**one, h=state), first[:, 0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("where", ["x", "dy"])
+def test_scan_gradient_without_skip(dtype, where):
+    a = inputs(16, 64, 16, dtype, 4, D_=False)
+    g = ref.gen(5)
+    dy, dh = ref.rand(g, 1, 16, 64).abs().to(dtype), ref.rand(g, 1, 64, 16).abs()
+    (dy if where == "dy" else a["x"])[0, 9, 3] = INF
+    check_gradient(a, dy, dh)
