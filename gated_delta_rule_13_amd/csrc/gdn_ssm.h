@@ -528,10 +528,11 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // the time: about 26 issue slots for a (token, channel, state) with its share
 // of the rest, two fifths of them in the sums over channels.
 //
-// CLEAR: the places behind the N states are 0, whatever the inputs.  They are 0
-// by themselves unless a step size, u or dyg is infinite; then they are NaN, and
-// so would be du, ds and y.  Returns whether the last of them was.  (p by value:
-// a reference costs 2.6 % in the order of instructions.)
+// CLEAR: the places behind the N states are 0, whatever the inputs, and so is dA
+// before a segment's last token.  They are so by themselves unless a step size,
+// u, dyg or state is infinite; then they are NaN, and so would be du, ds and y,
+// or dA.  Returns whether one of them was.  (p by value: a reference costs 2.6 %
+// in the order of instructions.)
 template <bool BF, int NS, int NB, bool CLEAR>
 __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float (&bc_all)[NB][kTok][2][NS],
                                                 float (&el)[5][kTok][64], float (&start)[NB][NS][64],
@@ -585,6 +586,13 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
                 v = ((e / NS) & 1) ? load_one<BF>(p.C, w.b * p.csb + tt * p.cst + w.g * p.N + n)
                                    : load_one<BF>(p.Bm, w.b * p.bsb + tt * p.bst + w.g * p.N + n);
             (&bc[0][0][0])[e] = v;
+        }
+        if (t + kTok > w.t1) {                       // (behind the last token: an infinite C times dyg 0 is NaN)
+#pragma unroll
+            for (int i = 0; i < kTok * 2 * NS / 64; ++i) {
+                const int e = lane + 64 * i;
+                if (t + e / (2 * NS) >= w.t1) (&bc[0][0][0])[e] = 0.f;
+            }
         }
         // What the tokens' channels need besides the states goes through LDS,
         // for the registers' sake, and so that each wave computes its share
@@ -658,6 +666,15 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
             for (int i = i0 + kSum - 1; i >= i0; --i) {
                 float y = 0.f, du = 0.f, ds = 0.f;
                 const float si = el[kS][i][lane], gy = el[kGy][i][lane], u = si * el[kX][i][lane];
+                // The places behind the last token came before it here.  They leave
+                // g as it is, but their q, of an infinite state, times 0 is NaN.
+                // (With eight states to a wave this branch costs 1.5 %, and the
+                // segment is done again instead: there 0.3, here 1.8.)
+                if ((NS <= 4 || CLEAR) && t + i == w.t1 - 1) {
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) da[n] = 0.f;
+                    pin(da);                         // (a branch, not a choice for every token)
+                }
 #pragma unroll
                 for (int n = 0; n < NS; ++n) {
                     const float c = bc[i][1][n];
@@ -704,6 +721,10 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
         }
     }
     wild |= __builtin_isnan(g[NS - 1]);
+    if (NS > 4) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) wild |= __builtin_isnan(da[n]);
+    }
     const unsigned tiles = (unsigned)(p.G * p.tpg);
     const int64_t at = ((int64_t)w.b * p.nseg + w.seg) * tiles + w.tile;
 #pragma unroll
@@ -735,7 +756,7 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
     return wild;
 }
 
-// PAD: fewer than NS NB states.  A segment with such numbers is done again
+// PAD: fewer than NS NB states.  A segment with such NaN is done again
 // (clearing the places every time: 107.8 us for 103.3 at 2 x 1024 x 1024 with 24
 // states).  One wave with both forms needs the registers of three on a vector
 // unit (3 states: 44.8 us, in those of four 47.2).
@@ -746,7 +767,7 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 && !(PAD && NB == 1) ? 
     __shared__ float start[NB][NS][64];
     __shared__ float cross[NB > 1 ? NB : 1][NB > 1 ? 3 * kTok : 1][64];
     const bool wild = ssm_bwd_segment<BF, NS, NB, false>(p, blockIdx.x, bc, el, start, cross);
-    if (PAD && __syncthreads_or(wild)) {
+    if ((PAD || NS > 4) && __syncthreads_or(wild)) {
         unsigned id = blockIdx.x;
         const SsmParams again = argument_again(id);
         ssm_bwd_segment<BF, NS, NB, true>(again, id, bc, el, start, cross);

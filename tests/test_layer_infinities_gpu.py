@@ -137,3 +137,18 @@ def test_scan_gradient_without_skip(dtype, where):
     dy, dh = ref.rand(g, 1, 16, 64).abs().to(dtype), ref.rand(g, 1, 64, 16).abs()
     (dy if where == "dy" else a["x"])[0, 9, 3] = INF
     check_gradient(a, dy, dh)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 15, 16, 17, 70])
+@pytest.mark.parametrize("where", ["x", "Bm", "C"])
+def test_scan_gradient_of_the_last_token(dtype, n, where):
+    """The infinity of a sequence's last token, wherever its length falls in a
+    group of tokens: as the sequence alone, with no rows behind it."""
+    say(f"case: infinite last {where}, gradient {dtype} n{n}")
+    a = inputs(n, 64, 16, dtype, n)
+    g = ref.gen(n)
+    dy, dh = ref.rand(g, 1, n, 64).abs().to(dtype), ref.rand(g, 1, 64, 16).abs()
+    a[where][0, n - 1, 0 if where != "x" else 3] = INF
+    check_gradient(a, dy, dh)
+    check_gradient(a, dy, dh, T=n + 13)
