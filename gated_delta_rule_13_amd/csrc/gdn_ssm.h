@@ -361,11 +361,12 @@ __global__ __launch_bounds__(64, NS <= 16 && !GRAD ? 3 : 1) void gdn_ssm_sum_ker
     const int64_t xb = w.b * p.xsb + w.c0, db = w.b * p.dsb + w.c0, y0 = (int64_t)w.b * p.T * p.D + w.c0;
     const void* zsrc = p.z ? p.z : p.x;
     const int64_t zb = p.z ? w.b * p.zsb + w.c0 : xb, zst = p.z ? p.zst : p.xst;
-    const uint32_t off = (uint32_t)(w.c - w.c0) * (BF ? 2 : 4);
+    // (lanes without a channel read 0, and leave states of 0)
+    const uint32_t off = w.on ? (uint32_t)(w.c - w.c0) * (BF ? 2 : 4) : kOutside;
     float a[NS], h[NS], pr[NS], r[NS], total = 0.f;
 #pragma unroll
     for (int n = 0; n < NS; ++n) h[n] = r[n] = 0.f, pr[n] = 1.f;
-    const float bias = p.dt_bias ? p.dt_bias[w.c] : 0.f;
+    const float bias = p.dt_bias && w.on ? p.dt_bias[w.c] : 0.f;
     if (w.t0 < w.t1) {
         StagedBC<BF, NS> nbc;
         Column<BF> nx, nd, nz, ng;
@@ -615,8 +616,9 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
             const float soft = softplus(raw), slope_soft = sigmoid(raw);
             float val, slope;
             silu_both(rz[j].get(0), val, slope);
-            el[kS][i][lane] = in ? (p.softplus ? soft : raw) : 0.f;
-            // (lanes without a channel add nothing to the sums over channels)
+            // (lanes without a channel add nothing to the sums over channels: their
+            // states are 0, and these)
+            el[kS][i][lane] = in && w.on ? (p.softplus ? soft : raw) : 0.f;
             el[kX][i][lane] = in && w.on ? rx[j].get(0) : 0.f;
             el[kGy][i][lane] = in && w.on ? (p.z ? dy * val : dy) : 0.f;
             el[kZs][i][lane] = in ? dy * slope : 0.f;

@@ -152,3 +152,17 @@ def test_scan_gradient_of_the_last_token(dtype, n, where):
     a[where][0, n - 1, 0 if where != "x" else 3] = INF
     check_gradient(a, dy, dh)
     check_gradient(a, dy, dh, T=n + 13)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [20, 70])
+@pytest.mark.parametrize("n", [8, 40])
+@pytest.mark.parametrize("where", ["x", "dy", "dt"])
+def test_scan_gradient_of_the_last_channel(dtype, D, n, where):
+    """Lanes without a channel add nothing to the sums over channels, also
+    where the channel beside them is infinite."""
+    a = inputs(n, D, 16, dtype, n)
+    g = ref.gen(n)
+    dy, dh = ref.rand(g, 1, n, D).abs().to(dtype), ref.rand(g, 1, D, 16).abs()
+    (dy if where == "dy" else a[where])[0, 5, D - 1] = INF
+    check_gradient(a, dy, dh)
