@@ -529,10 +529,11 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // the time: about 26 issue slots for a (token, channel, state) with its share
 // of the rest, two fifths of them in the sums over channels.
 //
-// CLEAR: the places behind the N states are 0, whatever the inputs, and so is dA
-// before a segment's last token.  They are so by themselves unless a step size,
-// u, dyg or state is infinite; then they are NaN, and so would be du, ds and y,
-// or dA.  Returns whether one of them was.  (p by value: a reference costs 2.6 %
+// CLEAR: the places behind the N states are 0, whatever the inputs, and so are
+// Bm and C behind a segment's last token, and dA before it.  The usual way does
+// without that where it would cost time in the loop; an infinite step size, u,
+// dyg, state or C then leaves NaN in the last place, in dA or in g.  Returns
+// whether it did.  (p by value: a reference costs 2.6 %
 // in the order of instructions.)
 template <bool BF, int NS, int NB, bool CLEAR>
 __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float (&bc_all)[NB][kTok][2][NS],
@@ -588,7 +589,7 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
                                    : load_one<BF>(p.Bm, w.b * p.bsb + tt * p.bst + w.g * p.N + n);
             (&bc[0][0][0])[e] = v;
         }
-        if (t + kTok > w.t1) {                       // (behind the last token: an infinite C times dyg 0 is NaN)
+        if ((NS <= 4 || CLEAR) && t + kTok > w.t1) { // (behind the last token: an infinite C times dyg 0 is NaN)
 #pragma unroll
             for (int i = 0; i < kTok * 2 * NS / 64; ++i) {
                 const int e = lane + 64 * i;
@@ -725,7 +726,7 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
     wild |= __builtin_isnan(g[NS - 1]);
     if (NS > 4) {
 #pragma unroll
-        for (int n = 0; n < NS; ++n) wild |= __builtin_isnan(da[n]);
+        for (int n = 0; n < NS; ++n) wild |= __builtin_isnan(da[n]) || __builtin_isnan(g[n]);
     }
     const unsigned tiles = (unsigned)(p.G * p.tpg);
     const int64_t at = ((int64_t)w.b * p.nseg + w.seg) * tiles + w.tile;
