@@ -254,9 +254,11 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_bwd_kernel(ConvBwdParam
                         silu_both(a, val, slope);
                         const float d = g[i].get(v) * (p.silu ? slope : 1.f);
                         dp[W - 1 + i][v] = live ? d : 0.f;
+                        // (a row of another tile, or a repeated one, may be infinite: 0 in its
+                        // place; a branch here takes the product into dbias' sum unrounded)
                         const float own = mine ? d : 0.f;
 #pragma unroll
-                        for (int j = 0; j < W; ++j) acc[j][v] = fmaf(own, win[i + j].get(v), acc[j][v]);
+                        for (int j = 0; j < W; ++j) acc[j][v] = fmaf(own, mine ? win[i + j].get(v) : 0.f, acc[j][v]);
                         acc[W][v] += own;
                         f[v] = 0.f;
 #pragma unroll

@@ -166,3 +166,28 @@ def test_scan_gradient_of_the_last_channel(dtype, D, n, where):
     dy, dh = ref.rand(g, 1, n, D).abs().to(dtype), ref.rand(g, 1, D, 16).abs()
     (dy if where == "dy" else a[where])[0, 5, D - 1] = INF
     check_gradient(a, dy, dh)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("T", [1, 4, 7, 20])
+def test_convolution_gradient(dtype, W, T):
+    """An infinite row at every place: rows of other tiles, and those that
+    stand behind a sequence's end, add nothing to the taps' gradients."""
+    g = ref.gen(T + W)
+    x, w, b = ref.rand(g, 1, T, 6, dtype=dtype), ref.rand(g, 6, W).abs() + 0.1, ref.rand(g, 6)
+    dy = ref.rand(g, 1, T, 6, dtype=dtype)
+    for t in range(T):
+        bad = x.clone()
+        bad[0, t, 2] = INF
+        a = {"x": bad, "weight": w, "bias": b}
+        want = ref.gradients(lambda **k: ref.conv(**k, act=None), ref.wide(a), list(a), (dy, None))
+        got = gdn.gdn_conv_bwd(dy.cuda(), **ref.dev(a), act=None)
+        long = torch.full((1, T + 6, 6), float("nan"), dtype=dtype)
+        more = torch.full((1, T + 6, 6), float("nan"), dtype=dtype)
+        long[:, :T], more[:, :T] = bad, dy
+        pad = gdn.gdn_conv_bwd(more.cuda(), long.cuda(), w.cuda(), b.cuda(), lens=torch.tensor([T], dtype=torch.int32).cuda(),
+                               act=None)
+        for k in want:
+            meets(f"d{k}, row {t}", got["d" + k], want[k])
+            meets(f"d{k}, row {t}, padded", pad["d" + k][:, :T] if k == "x" else pad["d" + k], want[k])
