@@ -174,13 +174,13 @@ def gdn_conv_fwd(x, weight, bias=None, state0=None, lens=None, heads=None, act="
         y = x.new_empty(_conv_out_shape(s, heads))
     else:
         _check("y", y, _conv_out_shape(s, heads), x.dtype, dev)
-        _separate("y", y, x=x, state0=state0)
+        _separate("y", y, x=x, weight=weight, bias=bias, state0=state0, lens=lens)
     if state_out is None:
         state_out = x.new_empty((s.B, s.W - 1, s.D))
     else:
         _check("state_out", state_out, (s.B, s.W - 1, s.D), x.dtype, dev)
         same = state0 is not None and state_out.data_ptr() == state0.data_ptr()
-        _separate("state_out", state_out, x=x, y=y, state0=None if same else state0)
+        _separate("state_out", state_out, x=x, weight=weight, bias=bias, state0=None if same else state0, lens=lens, y=y)
     check(load().gdn_conv_fwd(ctypes.byref(s), x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state0), _ptr(lens),
                               y.data_ptr(), state_out.data_ptr(), _stream(x)))
     return y, state_out
@@ -208,7 +208,7 @@ def gdn_conv_step(x, weight, bias, state, act="silu", y=None, stream=None):
         y = x.new_empty((B, D))
     else:
         _check("y", y, (B, D), io, dev)
-        _separate("y", y, x=x, state=state)
+        _separate("y", y, x=x, weight=weight, bias=bias, state=state)
     check(load().gdn_conv_step(ctypes.byref(s), x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(),
                                y.data_ptr(), _stream(x)))
     return y
@@ -309,13 +309,14 @@ def gdn_ssm_fwd(x, dt, A, Bm, C, D=None, z=None, dt_bias=None, h0=None, lens=Non
         y = x.new_empty((s.B, s.T, s.D))
     else:
         _check("y", y, (s.B, s.T, s.D), x.dtype, dev)
-        _separate("y", y, x=x, dt=dt, z=z, Bm=Bm, C=C)
+        _separate("y", y, x=x, dt=dt, A=A, Bm=Bm, C=C, D=D, z=z, dt_bias=dt_bias, h0=h0, lens=lens)
     if h_final is None:
         h_final = A.new_empty((s.B, s.D, s.N))
     else:
         _check("h_final", h_final, (s.B, s.D, s.N), torch.float32, dev)
         same = h0 is not None and h_final.data_ptr() == h0.data_ptr()
-        _separate("h_final", h_final, h0=None if same else h0, x=x, dt=dt, A=A, y=y)
+        _separate("h_final", h_final, x=x, dt=dt, A=A, Bm=Bm, C=C, D=D, z=z, dt_bias=dt_bias, h0=None if same else h0,
+                  lens=lens, y=y)
     nbytes = gdn_ssm_fwd_workspace_bytes(s)
     wp, ws = _workspace(nbytes, dev)
     check(load().gdn_ssm_fwd(ctypes.byref(s), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), C.data_ptr(),
@@ -361,7 +362,7 @@ def gdn_ssm_step(x, dt, A, Bm, C, D=None, z=None, dt_bias=None, h=None, dt_softp
         y = x.new_empty((B, Dc))
     else:
         _check("y", y, (B, Dc), io, dev)
-        _separate("y", y, x=x, dt=dt, z=z, Bm=Bm, C=C, h=h)
+        _separate("y", y, x=x, dt=dt, A=A, Bm=Bm, C=C, D=D, z=z, dt_bias=dt_bias, h=h)
     check(load().gdn_ssm_step(ctypes.byref(s), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), C.data_ptr(),
                               _ptr(D), _ptr(z), _ptr(dt_bias), h.data_ptr(), y.data_ptr(), _stream(x)))
     return y
@@ -448,7 +449,7 @@ def gdn_norm_fwd(x, weight=None, bias=None, z=None, act="silu", center=False, ep
         y = torch.empty(x.shape, dtype=o_dtype, device=dev)
     else:
         _check("y", y, x.shape, o_dtype, dev)
-        _separate("y", y, x=x, z=z)
+        _separate("y", y, x=x, weight=weight, bias=bias, z=z)
     check(load().gdn_norm_fwd(ctypes.byref(s), x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z), y.data_ptr(),
                               _stream(x)))
     return y

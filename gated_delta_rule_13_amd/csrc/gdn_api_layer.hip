@@ -63,6 +63,27 @@ bool rows2(const void* p, int dtype, std::initializer_list<int64_t> strides) {
         if (s % 2 != 0) return false;
     return true;
 }
+// The memory of an operand, from its first element to its last: `rows` rows of
+// `row` elements, `stride` apart.
+struct Extent {
+    const char* name;
+    const void* p;
+    uint64_t bytes;
+    Extent(const char* what, const void* at, int dtype, uint64_t rows, uint64_t row, uint64_t stride)
+        : name(what), p(at), bytes(((rows - 1) * stride + row) * (dtype == GDN_BF16 ? 2 : 4)) {}
+    Extent(const char* what, const void* at, int dtype, uint64_t n) : Extent(what, at, dtype, 1, n, 0) {}
+};
+// A token's state is updated where it lies: nothing else that the call reads or
+// writes may lie there.
+gdn_status check_apart(const Extent& out, std::initializer_list<Extent> others) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(out.p);
+    for (const Extent& o : others) {
+        const uint64_t b = reinterpret_cast<uintptr_t>(o.p);
+        if (o.p && a < b + o.bytes && b < a + out.bytes)
+            return set_error(GDN_ERR_UNSUPPORTED, std::string(out.name) + " may not overlap " + o.name);
+    }
+    return GDN_OK;
+}
 gdn_status check_workspace(const void* ws, size_t given, size_t need, const char* query) {
     if (need == 0) return GDN_OK;
     if (!ws || given < need) return set_error(GDN_ERR_WORKSPACE, std::string("workspace smaller than ") + query);
@@ -363,6 +384,14 @@ gdn_status gdn_conv_step(const gdn_conv_shape* s, const void* x, const float* we
     if (st != GDN_OK) return st;
     if (s->T != 1) return set_error(GDN_ERR_BAD_SHAPE, "T must be 1");
     if (!state) return set_error(GDN_ERR_NULL_ARG, "state is required");
+    if (x && weight && y) {
+        const int64_t D = s->D;
+        const Extent ex("x", x, s->dtype, s->B, D, s->x_stride_b), ew("weight", weight, GDN_F32, D * s->W),
+            eb("bias", bias, GDN_F32, D), es("state", state, s->dtype, s->B * (s->W - 1) * D), ey("y", y, s->dtype, s->B * D);
+        st = check_apart(es, {ex, ew, eb, ey});
+        if (st == GDN_OK) st = check_apart(ey, {ex, ew, eb});
+        if (st != GDN_OK) return st;
+    }
     return conv_forward(s, x, weight, bias, state, nullptr, y, state, stream);
 }
 
@@ -467,6 +496,14 @@ gdn_status gdn_ssm_step(const gdn_ssm_shape* s, const void* x, const void* dt, c
     q.wide_bc = s->N % 4 == 0 && rows4(Bm, s->dtype, {s->b_stride_b}) && rows4(C, s->dtype, {s->c_stride_b});
     // (the grid's second dimension counts sequences)
     if (s->B > 65535) return set_error(GDN_ERR_UNSUPPORTED, "B must be at most 65535");
+    const int64_t B = s->B, D = s->D, bc = (int64_t)s->G * s->N;
+    const Extent ex("x", x, s->dtype, B, D, s->x_stride_b), ed("dt", dt, s->dtype, B, D, s->dt_stride_b),
+        eA("A", A, GDN_F32, D * s->N), eB("Bm", Bm, s->dtype, B, bc, s->b_stride_b), eC("C", C, s->dtype, B, bc, s->c_stride_b),
+        eD("Dskip", Dskip, GDN_F32, D), ez("z", z, s->dtype, B, D, s->z_stride_b), eb("dt_bias", dt_bias, GDN_F32, D),
+        eh("h", h, GDN_F32, B * D * s->N), ey("y", y, s->dtype, B * D);
+    st = check_apart(eh, {ex, ed, eA, eB, eC, eD, ez, eb, ey});
+    if (st == GDN_OK) st = check_apart(ey, {ex, ed, eA, eB, eC, eD, ez, eb});
+    if (st != GDN_OK) return st;
     gdn::ssm_step_run(q, s->dtype == GDN_BF16, reinterpret_cast<hipStream_t>(stream));
     return gdn::launch_status();
 }

@@ -302,7 +302,8 @@ gdn_status gdn_recurrent_fwd_eta(const gdn_shape* s,
  *         output; the output and gradient rows there are written as zero;
  *         the final state is the one after the last token (the initial one
  *         for a length of 0).
- * Outputs may not overlap inputs or each other, except where stated.
+ * Outputs may not overlap inputs or each other, except where stated (checked
+ * by the entries for one token, whose state is updated in place).
  * Gradients of parameters and of broadcast rows are sums in fp32 in a fixed
  * order: the same call gives the same bits.
  */

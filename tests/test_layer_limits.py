@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from tests.test_abi import lib, lib_nogpu  # noqa: F401
-from tests.test_layer_abi import BIG, CALLS, ODD, WORKSPACE, call, norm_shape
+from tests.test_layer_abi import BIG, CALLS, ODD, WORKSPACE, call, conv_shape, norm_shape, ssm_shape
 
 MOST = 2 ** 31 - 128                # tokens: the kernels walk them, a tile ahead, in 32 bits
 
@@ -39,3 +39,35 @@ def test_gradient_of_many_head_weights(lib_nogpu):  # noqa: F811
         assert "aligned" in lib_nogpu.gdn_last_error().decode()
     # (weights [d]: one sum for all heads)
     assert query(ctypes.byref(norm_shape(G=2 ** 20, d=256))) < BIG
+
+
+def apart(names):
+    """Pointers 16 MiB from each other."""
+    return {n: (i + 1) << 24 for i, n in enumerate(names.split())}
+
+
+@pytest.mark.parametrize("entry", ["gdn_conv_step", "gdn_ssm_step"])
+def test_state_in_place_overlaps_nothing(lib_nogpu, entry):  # noqa: F811
+    """The state of a token's call, or its output, in the memory of another
+    operand: its end, or its beginning."""
+    if "conv" in entry:
+        shape, state = conv_shape(B=3, T=1, D=64, H=1, x_stride_b=100), "state"
+        size = {"x": (2 * 100 + 64) * 2, "weight": 64 * 4 * 4, "bias": 64 * 4, "state": 3 * 3 * 64 * 2, "y": 3 * 64 * 2}
+    else:
+        strides = {n + "_stride_b": 100 for n in "x dt z b c".split()}
+        shape, state = ssm_shape(B=3, T=1, D=64, N=16, G=2, **strides), "h"
+        row, bc = (2 * 100 + 64) * 2, (2 * 100 + 32) * 2
+        size = {"x": row, "dt": row, "A": 64 * 16 * 4, "Bm": bc, "C": bc, "Dskip": 64 * 4, "z": row, "dt_bias": 64 * 4,
+                "h": 3 * 64 * 16 * 4, "y": 3 * 64 * 2}
+    names = CALLS[entry][1]
+    assert set(size) == set(names.split())
+    for out in (state, "y"):
+        for other in size:
+            if other == out or (out == "y" and other == state):
+                continue
+            base = apart(names)
+            # (4 bytes into the other's end: aligned to either type)
+            for moved, to in ((out, base[other] + size[other] - 4), (other, base[out] + size[out] - 4)):
+                ptrs = {n: ctypes.c_void_p(v) for n, v in {**base, moved: to}.items()}
+                assert call(lib_nogpu, entry, shape, **ptrs) == 4, (out, other, moved)
+                assert "overlap" in lib_nogpu.gdn_last_error().decode(), (out, other, moved)
