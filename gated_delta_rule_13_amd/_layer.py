@@ -5,7 +5,9 @@ computation runs in the HIP kernels of ``libgdn.so``.
 
 Strided inputs may be views (slices of a projection's output, transposed
 heads): only their last dimension has to be contiguous, or where it is stated
-the last two.  Calls run on ``stream`` (the current stream of the tensors'
+the last two.  Outputs carry no autograd history, whatever their inputs
+require: a model joins a call and its ``_bwd`` in an autograd function of its
+own.  Calls run on ``stream`` (the current stream of the tensors'
 device by default), asynchronously.
 """
 from __future__ import annotations
@@ -377,7 +379,9 @@ def gdn_ssm_bwd(dy, x, dt, A, Bm, C, D=None, z=None, dt_bias=None, h0=None, lens
     """Gradient of gdn_ssm_fwd: dy [B,T,D] contiguous, dh_final [B,D,N] fp32
     or None.  Returns a dict: dx, ddt [B,T,D], dB, dC [B,T,G,N] in x's dtype, dA
     [D,N] fp32 and, with the inputs they belong to, dD, ddt_bias [D] fp32, dz
-    [B,T,D], dh0 [B,D,N] fp32."""
+    [B,T,D], dh0 [B,D,N] fp32.  The call takes a workspace of about 0.8 N bytes
+    for each token and channel (gdn_ssm_bwd_workspace_bytes), 6 times x in bf16
+    at 16 states, and gives it back when it is done."""
     if _elsewhere(x, stream):
         with _moved("gdn_ssm_bwd", x, stream):
             return gdn_ssm_bwd(dy, x, dt, A, Bm, C, D, z, dt_bias, h0, lens, dh_final, dt_softplus)

@@ -148,9 +148,12 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_fwd_kernel(ConvParams p
 // once and dx written once, which bounds it.  The sums over rows stay in
 // registers, are added over the workgroup's tiles in LDS, and written as one
 // row of partial sums for each workgroup.  Measured at 4 x 4096 x 2048 in bf16,
-// 4 taps: 52 us for 201 MB (3.9 TB/s) and 5 us for the sum of the partial rows.
-// About 31 vector instructions an element take as long as the memory, so the
-// waves matter: two channels to a thread (117 registers, four waves on a
+// 4 taps: 53 us for 201 MB and 5 us for the sum of the partial rows.  It moves
+// 267 MB (5.0 TB/s, the rate of a large copy): 21 are the rows before and behind
+// a tile, 41 cache lines that two workgroups share, whose L2s differ, where x's
+// rows begin within a line (155 MB read for 196, and 45 us for 49 in one
+// measurement, where they do not).  44 vector instructions an element keep the
+// vector units busy 78 % of the time, so the waves matter too: two channels to a thread (117 registers, four waves on a
 // vector unit) took 52 us where four (205 registers) took 59 and eight spilled;
 // branches on the activation and at the ends of tiles inside the row loop cost
 // 8 us more.

@@ -70,7 +70,8 @@ struct NormBwdParams;
 struct SsmParams;
 struct SsmStepParams;
 
-// short convolution: W in {2, 3, 4}; wide: 16-byte pieces of a row
+// short convolution: W in {2, 3, 4}; wide: 16-byte pieces of a row, in the
+// gradient pairs of channels (else number by number)
 using ConvLauncher = void (*)(const ConvParams&, hipStream_t);
 using ConvBwdLauncher = void (*)(const ConvBwdParams&, hipStream_t);
 ConvLauncher conv_launcher(bool bf16, int W, bool wide);
@@ -78,7 +79,8 @@ ConvBwdLauncher conv_bwd_launcher(bool bf16, int W, bool wide);
 int64_t conv_bwd_part_rows(int64_t row_tiles);
 void conv_bwd_sum(const float* part, int64_t rows, int D, int W, float* dweight, float* dbias, hipStream_t st);
 
-// head normalisation: wide: 16-byte pieces of a row (else number by number)
+// head normalisation: wide: four numbers of a row at a time (else number by
+// number)
 using NormLauncher = void (*)(const NormParams&, hipStream_t);
 using NormBwdLauncher = void (*)(const NormBwdParams&, int nblk, hipStream_t);
 void norm_launchers(bool x_bf16, bool o_bf16, int d, bool wide, NormLauncher* fwd, NormBwdLauncher* bwd,

@@ -5,8 +5,8 @@
 
 namespace gdn {
 
-// Vectors of V elements as they lie in memory (bf16: V in {1, 4, 8}; float:
-// V in {1, 4}), kept raw until they are used so that nothing waits for a
+// Vectors of V elements as they lie in memory (bf16: V in {1, 2, 4, 8}; float:
+// V in {1, 2, 4}), kept raw until they are used so that nothing waits for a
 // load that is only prefetched.
 template <bool BF, int V>
 struct Raw {

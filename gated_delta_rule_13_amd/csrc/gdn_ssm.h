@@ -522,11 +522,11 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // the group's states and decays into registers, then the gradient backwards.
 // The states are split over the workgroup's NB waves, NS each; what sums over
 // states (du, ds, y) is added through LDS.  Measured at 2 x 4096 x 2048 with 16
-// states, bf16, gated, all launches 347 us: summaries 97, chain 16, this
-// kernel 221 (four states to a wave, held decays; computed again 238; eight
+// states, bf16, gated, all launches 345 us: summaries 96, chain 16, this
+// kernel 220 (four states to a wave, held decays; computed again 238; eight
 // states to a wave took 299 when four took 256, all 16 in one wave 322), the
-// sums over tiles and segments 11.  The vector units are busy nine tenths of
-// the time: about 26 issue slots for a (token, channel, state) with its share
+// sums over tiles and segments 11.  The vector units are busy 82 % of the time:
+// about 26 issue slots for a (token, channel, state) with its share
 // of the rest, two fifths of them in the sums over channels.
 //
 // CLEAR: the places behind the N states are 0, whatever the inputs, and so are
