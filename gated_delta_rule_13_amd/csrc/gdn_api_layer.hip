@@ -199,7 +199,10 @@ gdn_status validate(const gdn_ssm_shape* s) {
 // what a segment costs besides its tokens is a fifth of it.  Two more launches
 // pay from 64 tokens on (one sequence of 64, 16 states: 20 us either way), and
 // with more states from 32 (2 x 33 x 1000 with 64 states: 53 us in one pass, 46
-// in segments; 2 x 60: 83 and 47).
+// in segments; 2 x 60: 83 and 47).  Measured at both sides of the number of
+// waves, with 16 states: 1024 waves (16 x 2048 x 4096) 790 us in segments, 833
+// in one pass; 2048 waves (32 x 1024 x 4096) 764 and 537, 2944 waves (46 x 1024
+// x 4096) 959 and 718: from about 1500 on one pass would be faster.
 struct SsmPlan {
     int seg_len, nseg;
     size_t off_s, bytes;
