@@ -38,7 +38,7 @@ void bwd(const SsmParams& p, float* dA, void* dBm, void* dC, float* dD, float* d
     const int64_t tiles = (int64_t)p.G * p.tpg;
     summaries<NSA, true>(p, p.nseg, st);
     const dim3 grid((unsigned)(p.B * p.nseg * tiles));
-    if (p.N == NSA) hipLaunchKernelGGL((gdn_ssm_bwd_kernel<kBF, NS, NB, false>), grid, dim3(64 * NB), 0, st, p);
+    if (p.N == NSA && p.Dg % 64 == 0) hipLaunchKernelGGL((gdn_ssm_bwd_kernel<kBF, NS, NB, false>), grid, dim3(64 * NB), 0, st, p);
     else hipLaunchKernelGGL((gdn_ssm_bwd_kernel<kBF, NS, NB, true>), grid, dim3(64 * NB), 0, st, p);
     SsmSumParams q{p, dBm, dC, dA, dD, dbias, NSA, blocks((int64_t)p.B * p.T * p.G * 2 * NSA, kSumThreads)};
     hipLaunchKernelGGL((gdn_ssm_grad_sum_kernel<kBF>), dim3(q.bc + (unsigned)(tiles * (NSA + 2))), dim3(kSumThreads), 0, st,

@@ -529,13 +529,14 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // about 26 issue slots for a (token, channel, state) with its share
 // of the rest, two fifths of them in the sums over channels.
 //
-// CLEAR: the places behind the N states are 0, whatever the inputs, and so are
-// Bm and C behind a segment's last token, and dA before it.  The usual way does
-// without that where it would cost time in the loop; an infinite step size, u,
-// dyg, state or C then leaves NaN in the last place, in dA or in g.  Returns
-// whether it did.  (p by value: a reference costs 2.6 %
+// CLEAR: the places behind the N states and lanes without a channel are 0,
+// whatever the inputs, and so are Bm and C behind a segment's last token, and dA
+// before it.  The usual way does without that where it would cost time in the
+// loop; an infinite step size, u, dyg, state, Bm or C then leaves NaN in dA of
+// those places, lanes and tokens, or in the last state.  Returns whether there is
+// any.  (p by value: a reference costs 2.6 %
 // in the order of instructions.)
-template <bool BF, int NS, int NB, bool CLEAR>
+template <bool BF, int NS, int NB, bool PAD, bool CLEAR>
 __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float (&bc_all)[NB][kTok][2][NS],
                                                 float (&el)[5][kTok][64], float (&start)[NB][NS][64],
                                                 float (&cross)[NB > 1 ? NB : 1][NB > 1 ? 3 * kTok : 1][64]) {
@@ -546,7 +547,7 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
     float(&bc)[kTok][2][NS] = bc_all[blk];
     const SsmPlace w = ssm_place(p, id, p.nseg, lane);
     const int n0 = blk * NS;
-    const int states = CLEAR ? __builtin_amdgcn_readfirstlane(p.N - n0) : NS;    // of the wave
+    const int states = CLEAR && w.on ? p.N - n0 : CLEAR ? 0 : NS;                // of the lane
     bool wild = false;
     const int64_t xb = w.b * p.xsb + w.c, db = w.b * p.dsb + w.c;
     const int64_t yb = (int64_t)w.b * p.T * p.D + w.c;
@@ -641,7 +642,10 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
             }
             pin(hs[i]);
         }
-        wild |= __builtin_isnan(hs[kTok - 1][NS - 1]);
+        if (PAD && k == groups - 1) {                // (the last state: the others' NaN comes into dA)
+#pragma unroll
+            for (int n = 0; n < NS; ++n) wild |= (n == NS - 1 || !w.on) && __builtin_isnan(hs[kTok - 1][n]);
+        }
         // the outputs of token i of the lane's channel
         auto finish = [&](int i, float y, float du, float ds) {
             if (t + i < w.t1) {
@@ -723,11 +727,8 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
             }
         }
     }
-    wild |= __builtin_isnan(g[NS - 1]);
-    if (NS > 4) {
 #pragma unroll
-        for (int n = 0; n < NS; ++n) wild |= __builtin_isnan(da[n]) || __builtin_isnan(g[n]);
-    }
+    for (int n = 0; n < NS; ++n) wild |= __builtin_isnan(da[n]);
     const unsigned tiles = (unsigned)(p.G * p.tpg);
     const int64_t at = ((int64_t)w.b * p.nseg + w.seg) * tiles + w.tile;
 #pragma unroll
@@ -759,9 +760,9 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
     return wild;
 }
 
-// PAD: fewer than NS NB states.  A segment with such NaN is done again
-// (clearing the places every time: 107.8 us for 103.3 at 2 x 1024 x 1024 with 24
-// states).  One wave with both forms needs the registers of three on a vector
+// PAD: fewer than NS NB states, or channels that fill no whole number of waves.
+// A segment with such NaN is done again (clearing the places every time: 107.8
+// us for 103.3 at 2 x 1024 x 1024 with 24 states).  One wave with both forms needs the registers of three on a vector
 // unit (3 states: 44.8 us, in those of four 47.2).
 template <bool BF, int NS, int NB, bool PAD>
 __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 && !(PAD && NB == 1) ? 4 : 3) void gdn_ssm_bwd_kernel(SsmParams p) {
@@ -769,11 +770,11 @@ __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 && !(PAD && NB == 1) ? 
     __shared__ float el[5][kTok][64];
     __shared__ float start[NB][NS][64];
     __shared__ float cross[NB > 1 ? NB : 1][NB > 1 ? 3 * kTok : 1][64];
-    const bool wild = ssm_bwd_segment<BF, NS, NB, false>(p, blockIdx.x, bc, el, start, cross);
+    const bool wild = ssm_bwd_segment<BF, NS, NB, PAD, false>(p, blockIdx.x, bc, el, start, cross);
     if ((PAD || NS > 4) && __syncthreads_or(wild)) {
         unsigned id = blockIdx.x;
         const SsmParams again = argument_again(id);
-        ssm_bwd_segment<BF, NS, NB, true>(again, id, bc, el, start, cross);
+        ssm_bwd_segment<BF, NS, NB, PAD, true>(again, id, bc, el, start, cross);
     }
 }
 

@@ -191,3 +191,19 @@ def test_convolution_gradient(dtype, W, T):
         for k in want:
             meets(f"d{k}, row {t}", got["d" + k], want[k])
             meets(f"d{k}, row {t}, padded", pad["d" + k][:, :T] if k == "x" else pad["d" + k], want[k])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [1, 20, 70])
+@pytest.mark.parametrize("N", [4, 7, 16, 32, 64])
+@pytest.mark.parametrize("T,t", [(8, 5), (40, 21)])
+@pytest.mark.parametrize("where", ["Bm", "C"])
+def test_scan_gradient_of_part_of_a_wave(dtype, D, N, T, t, where):
+    """Lanes without a channel add nothing to the sums over channels where B or
+    C, which all lanes take, is infinite."""
+    a = inputs(T, D, N, dtype, T)
+    g = ref.gen(N)
+    dy, dh = ref.rand(g, 1, T, D).abs().to(dtype), ref.rand(g, 1, D, N).abs()
+    a[where][0, t, 0, N // 2] = INF
+    check_gradient(a, dy, dh)
+    check_gradient(a, dy, dh, T=T + 13)
