@@ -525,7 +525,7 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // states, bf16, gated, all launches 345 us: summaries 96, chain 16, this
 // kernel 220 (four states to a wave, held decays; computed again 238; eight
 // states to a wave took 299 when four took 256, all 16 in one wave 322), the
-// sums over tiles and segments 11.  The vector units are busy 82 % of the time:
+// sums over tiles and segments 11.  The vector units are busy 93 % of the time:
 // about 26 issue slots for a (token, channel, state) with its share
 // of the rest, two fifths of them in the sums over channels.
 //
