@@ -153,10 +153,10 @@ __global__ __launch_bounds__(kConvThreads) void gdn_conv_fwd_kernel(ConvParams p
 // a tile, 41 cache lines that two workgroups share, whose L2s differ, where x's
 // rows begin within a line (155 MB read for 196, and 45 us for 49 in one
 // measurement, where they do not).  44 vector instructions an element keep the
-// vector units busy 78 % of the time, so the waves matter too: two channels to a thread (117 registers, four waves on a
-// vector unit) took 52 us where four (205 registers) took 59 and eight spilled;
-// branches on the activation and at the ends of tiles inside the row loop cost
-// 8 us more.
+// vector units busy 76 % of the time, so the waves matter too: two channels to a
+// thread (119 registers, four waves on a vector unit) took 52 us where four (205
+// registers) took 59 and eight spilled; branches on the activation and at the
+// ends of tiles inside the row loop cost 8 us more.
 struct ConvBwdParams {
     ConvParams f;
     const void* dy;

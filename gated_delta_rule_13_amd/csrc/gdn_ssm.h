@@ -534,8 +534,7 @@ __device__ __forceinline__ float row_sums(float (&v)[R], int lane) {
 // before it.  The usual way does without that where it would cost time in the
 // loop; an infinite step size, u, dyg, state, Bm or C then leaves NaN in dA of
 // those places, lanes and tokens, or in the last state.  Returns whether there is
-// any.  (p by value: a reference costs 2.6 %
-// in the order of instructions.)
+// any.  (p by value: a reference costs 2.6 % in the order of instructions.)
 template <bool BF, int NS, int NB, bool PAD, bool CLEAR>
 __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float (&bc_all)[NB][kTok][2][NS],
                                                 float (&el)[5][kTok][64], float (&start)[NB][NS][64],
@@ -762,8 +761,9 @@ __device__ __forceinline__ bool ssm_bwd_segment(SsmParams p, unsigned id, float 
 
 // PAD: fewer than NS NB states, or channels that fill no whole number of waves.
 // A segment with such NaN is done again (clearing the places every time: 107.8
-// us for 103.3 at 2 x 1024 x 1024 with 24 states).  One wave with both forms needs the registers of three on a vector
-// unit (3 states: 44.8 us, in those of four 47.2).
+// us for 103.3 at 2 x 1024 x 1024 with 24 states).  One wave with both forms
+// needs the registers of three on a vector unit (3 states: 44.8 us, in those of
+// four 47.2).
 template <bool BF, int NS, int NB, bool PAD>
 __global__ __launch_bounds__(64 * NB, NS <= 4 && NB != 2 && !(PAD && NB == 1) ? 4 : 3) void gdn_ssm_bwd_kernel(SsmParams p) {
     __shared__ __align__(16) float bc[NB][kTok][2][NS];
