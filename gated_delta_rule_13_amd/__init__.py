@@ -12,21 +12,24 @@ computes, for every (b, h) sequence and with S of shape [d_v, d_k],
 The operators around it in a layer are gdn_conv_* (the short causal
 convolution), gdn_ssm_* (the selective state space recurrence) and gdn_norm_*
 (the normalisation and gate of the heads), each for prompts, with its
-gradient, and the first two for single tokens.
+gradient, and the first two for single tokens.  gdn_lin_* is linear attention
+with a decay for each head (the delta rule's state without the erasing) for
+prompts, single tokens and gradients, and gdn_block_norm_* the norms after and
+before a block with its gate, its scale and the residual stream.
 """
 from __future__ import annotations
 
 import ctypes
 
-from ._lib import (EXPORTS, GDN_BF16, GDN_F32, GdnConvShape, GdnError, GdnNormShape, GdnShape, GdnSsmShape,
-                   check, load)
+from ._lib import (EXPORTS, GDN_BF16, GDN_F32, GdnBlockNormShape, GdnConvShape, GdnError, GdnLinShape, GdnNormShape,
+                   GdnShape, GdnSsmShape, check, load)
 
 __all__ = ["gdn_chunk_fwd", "gdn_chunk_fwd_eta", "gdn_chunk_fwd_precise", "gdn_chunk_fwd_stages",
            "gdn_chunk_fwd_seq", "gdn_chunk_fwd_seq_workspace_bytes", "gdn_chunk_fwd_seq_noalloc",
            "gdn_chunk_prep", "gdn_chunk_fwd_workspace_bytes",
            "gdn_recurrent_fwd", "gdn_recurrent_fwd_eta",
            "gdn_status_string", "gdn_last_error", "gdn_version", "GdnError", "GdnShape",
-           "GdnConvShape", "GdnSsmShape", "GdnNormShape", "EXPORTS"]
+           "GdnConvShape", "GdnSsmShape", "GdnNormShape", "GdnLinShape", "GdnBlockNormShape", "EXPORTS"]
 
 # the operators around the recurrence, from _layer.py at their first use (it
 # imports torch, which building and loading the library do without)
@@ -34,14 +37,22 @@ _LAYER = ("gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step", "gdn_conv_bwd_workspa
           "gdn_ssm_fwd", "gdn_ssm_bwd", "gdn_ssm_step", "gdn_ssm_fwd_workspace_bytes",
           "gdn_ssm_bwd_workspace_bytes",
           "gdn_norm_fwd", "gdn_norm_bwd", "gdn_norm_bwd_workspace_bytes")
-__all__ += _LAYER
+# linear attention and the norms around a block, likewise from _mix.py
+_MIX = ("gdn_lin_fwd", "gdn_lin_bwd", "gdn_lin_step", "gdn_lin_fwd_workspace_bytes", "gdn_lin_bwd_workspace_bytes",
+        "gdn_block_norm_fwd", "gdn_block_norm_bwd", "gdn_block_norm_bwd_workspace_bytes")
+__all__ += _LAYER + _MIX
 
 
 def __getattr__(name):
-    if name not in _LAYER:
+    if name in _LAYER:
+        from . import _layer as module
+        names = _LAYER
+    elif name in _MIX:
+        from . import _mix as module
+        names = _MIX
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import _layer
-    globals().update({n: getattr(_layer, n) for n in _LAYER})
+    globals().update({n: getattr(module, n) for n in names})
     return globals()[name]
 
 

@@ -29,6 +29,8 @@ EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_eta"
            "gdn_ssm_fwd_workspace_bytes", "gdn_ssm_fwd", "gdn_ssm_step",
            "gdn_ssm_bwd_workspace_bytes", "gdn_ssm_bwd",
            "gdn_norm_fwd", "gdn_norm_bwd_workspace_bytes", "gdn_norm_bwd",
+           "gdn_lin_fwd_workspace_bytes", "gdn_lin_fwd", "gdn_lin_step", "gdn_lin_bwd_workspace_bytes", "gdn_lin_bwd",
+           "gdn_block_norm_fwd", "gdn_block_norm_bwd_workspace_bytes", "gdn_block_norm_bwd",
            "gdn_status_string", "gdn_last_error", "gdn_version")
 
 
@@ -53,6 +55,19 @@ class GdnNormShape(ctypes.Structure):
                  ("B", "T", "G", "d", "x_dtype", "o_dtype", "center", "w_per_group", "silu")] +
                 [("eps", ctypes.c_float)] +
                 [(f"{name}_stride_{dim}", ctypes.c_int64) for name in ("x", "z") for dim in "btg"])
+
+
+class GdnLinShape(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int32) for name in
+                 ("B", "H", "T", "Hq", "Hk", "d_k", "d_v", "dtype", "o_dtype", "per_head")] +
+                [("scale", ctypes.c_float)] +
+                [(f"{name}_stride_{dim}", ctypes.c_int64) for name in ("q", "k", "v", "a") for dim in "bht"])
+
+
+class GdnBlockNormShape(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int32) for name in ("B", "T", "D", "dtype", "x_dtype", "post", "act")] +
+                [("eps", ctypes.c_float)] +
+                [(f"{name}_stride_{dim}", ctypes.c_int64) for name in ("o", "x", "g") for dim in "bt"])
 
 
 class GdnError(RuntimeError):
@@ -109,6 +124,18 @@ def load():
     lib.gdn_ssm_bwd.argtypes = [ss] + [vp] * 21 + [vp, size, vp]
     lib.gdn_norm_fwd.argtypes = [ns] + [vp] * 6
     lib.gdn_norm_bwd.argtypes = [ns] + [vp] * 6 + [ctypes.c_int64] * 3 + [vp] * 3 + [vp, size, vp]
+    ls, bs = ctypes.POINTER(GdnLinShape), ctypes.POINTER(GdnBlockNormShape)
+    lib.gdn_lin_fwd.argtypes = [ls] + [vp] * 8 + [vp, size, vp]
+    lib.gdn_lin_step.argtypes = [ls] + [vp] * 7
+    lib.gdn_lin_bwd.argtypes = [ls] + [vp] * 13 + [vp, size, vp]
+    lib.gdn_block_norm_fwd.argtypes = [bs] + [vp] * 9
+    lib.gdn_block_norm_bwd.argtypes = [bs] + [vp] * 14 + [vp, size, vp]
+    for entry in (lib.gdn_lin_fwd, lib.gdn_lin_step, lib.gdn_lin_bwd, lib.gdn_block_norm_fwd, lib.gdn_block_norm_bwd):
+        entry.restype = ctypes.c_int
+    for entry, sp in ((lib.gdn_lin_fwd_workspace_bytes, ls), (lib.gdn_lin_bwd_workspace_bytes, ls),
+                      (lib.gdn_block_norm_bwd_workspace_bytes, bs)):
+        entry.argtypes = [sp]
+        entry.restype = size
     for entry in (lib.gdn_conv_fwd, lib.gdn_conv_step, lib.gdn_conv_bwd, lib.gdn_ssm_fwd, lib.gdn_ssm_step,
                   lib.gdn_ssm_bwd, lib.gdn_norm_fwd, lib.gdn_norm_bwd):
         entry.restype = ctypes.c_int

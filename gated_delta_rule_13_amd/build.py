@@ -29,6 +29,8 @@ ARCH = "gfx950"
 # d_k 16 runs on the d_k 32 kernel, zero-padded
 FAST_PAIRS = ([(c, d) for c in (16, 32, 64) for d in (16, 32, 64, 96, 128)] +
               [(16, 256), (32, 256)])
+# sizes that linear attention's rows are rounded up to
+LIN_ROWS = (32, 64, 96, 128, 256)
 
 
 def hipcc() -> str:
@@ -57,6 +59,12 @@ def units() -> list[tuple[str, str, list[str]]]:
            ("gdn_inst_norm.o", "gdn_inst_norm.hip", []),
            ("gdn_inst_ssm_bf16.o", "gdn_inst_ssm.hip", ["-DGDN_SSM_BF16=1"]),
            ("gdn_inst_ssm_f32.o", "gdn_inst_ssm.hip", ["-DGDN_SSM_BF16=0"])]
+    out.append(("gdn_api_mix.o", "gdn_api_mix.hip", []))
+    for bf in (1, 0):
+        for nk in LIN_ROWS:
+            out.append((f"gdn_inst_lin_{bf}_{nk}.o", "gdn_inst_lin.hip", [f"-DGDN_LIN_BF16={bf}", f"-DGDN_LIN_NK={nk}"]))
+        for ob in (1, 0):
+            out.append((f"gdn_inst_block_{bf}_{ob}.o", "gdn_inst_block.hip", [f"-DGDN_BLOCK_XB={bf}", f"-DGDN_BLOCK_OB={ob}"]))
     for c, d in FAST_PAIRS:
         out.append((f"gdn_inst_fast_c{c}_d{d}.o", "gdn_inst_fast.hip", [f"-DGDN_C={c}", f"-DGDN_DK={d}"]))
     return out

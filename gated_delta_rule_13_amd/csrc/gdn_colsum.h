@@ -8,20 +8,23 @@ namespace gdn {
 
 // out[c] = sum over r of part[r][c], r ascending within each of 16 slices of
 // the rows and the slices in order: a fixed order.  Columns [0, n0) go to
-// out0, [n0, n0 + n1) to out1 (either may be null).
+// out0, the n1 behind them to out1 and the n2 behind those to out2 (each may be
+// null).
 struct ColsumParams {
     const float* part;
     float* out0;
     float* out1;
     int64_t rows;
     int64_t n0, n1;
+    float* out2;
+    int64_t n2;
 };
 constexpr int kColsumSlices = 16;
 
 static __global__ __launch_bounds__(64 * kColsumSlices) void gdn_colsum_kernel(ColsumParams p) {
     __shared__ float s[kColsumSlices][64];
     const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
-    const int64_t cols = p.n0 + p.n1;
+    const int64_t cols = p.n0 + p.n1 + p.n2;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     const int64_t per = (p.rows + kColsumSlices - 1) / kColsumSlices;
     const int64_t r1 = (slice + 1) * per < p.rows ? (slice + 1) * per : p.rows;
@@ -38,8 +41,10 @@ static __global__ __launch_bounds__(64 * kColsumSlices) void gdn_colsum_kernel(C
         for (int i = 0; i < kColsumSlices; ++i) t += s[i][lane];
         if (c < p.n0) {
             if (p.out0) p.out0[c] = t;
-        } else if (p.out1) {
-            p.out1[c - p.n0] = t;
+        } else if (c < p.n0 + p.n1) {
+            if (p.out1) p.out1[c - p.n0] = t;
+        } else if (p.out2) {
+            p.out2[c - p.n0 - p.n1] = t;
         }
     }
 }
@@ -48,9 +53,9 @@ static __global__ __launch_bounds__(64 * kColsumSlices) void gdn_colsum_kernel(C
 constexpr int64_t colsum_threads(int64_t cols) { return (cols + 63) / 64 * 64 * kColsumSlices; }
 
 inline void launch_colsum(const float* part, int64_t rows, float* out0, int64_t n0, float* out1, int64_t n1,
-                          hipStream_t st) {
-    ColsumParams p{part, out0, out1, rows, n0, n1};
-    hipLaunchKernelGGL(gdn_colsum_kernel, dim3((unsigned)((n0 + n1 + 63) / 64)), dim3(64 * kColsumSlices), 0, st, p);
+                          hipStream_t st, float* out2 = nullptr, int64_t n2 = 0) {
+    ColsumParams p{part, out0, out1, rows, n0, n1, out2, n2};
+    hipLaunchKernelGGL(gdn_colsum_kernel, dim3((unsigned)((n0 + n1 + n2 + 63) / 64)), dim3(64 * kColsumSlices), 0, st, p);
 }
 
 }  // namespace gdn

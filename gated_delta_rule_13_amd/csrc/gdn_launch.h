@@ -94,4 +94,36 @@ void ssm_bwd_run(const SsmParams& p, bool bf16, float* dA, void* dBm, void* dC, 
                  hipStream_t st);
 void ssm_step_run(const SsmStepParams& q, bool bf16, hipStream_t st);
 
+// linear attention: rows of nk numbers, rounded up to a built size (32, 64, 96,
+// 128, 256); set: the passes that one launch runs
+struct LinParams;
+struct LinStepParams;
+using LinLauncher = void (*)(const LinParams&, int64_t blocks, hipStream_t);
+using LinStepLauncher = void (*)(const LinStepParams&, int64_t bhs, hipStream_t);
+#define GDN_LIN_DECL(nk) \
+    LinLauncher lin_launcher_0_##nk(int set); \
+    LinLauncher lin_launcher_1_##nk(int set);
+GDN_LIN_DECL(32)
+GDN_LIN_DECL(64)
+GDN_LIN_DECL(96)
+GDN_LIN_DECL(128)
+GDN_LIN_DECL(256)
+#undef GDN_LIN_DECL
+// *rows: rows of the state to a workgroup
+LinStepLauncher lin_step_launcher_bf16(int dk, bool wide, int* rows);
+LinStepLauncher lin_step_launcher_f32(int dk, bool wide, int* rows);
+
+// norms around a block: rows: those that a workgroup holds at once
+struct BlockParams;
+struct BlockBwdParams;
+struct BlockLaunchers {
+    void (*fwd)(const BlockParams&, int64_t blocks, hipStream_t);
+    void (*bwd)(const BlockBwdParams&, int64_t blocks, hipStream_t);
+    int rows;
+};
+BlockLaunchers block_launchers_0_0(int D, bool wide);
+BlockLaunchers block_launchers_0_1(int D, bool wide);
+BlockLaunchers block_launchers_1_0(int D, bool wide);
+BlockLaunchers block_launchers_1_1(int D, bool wide);
+
 }  // namespace gdn

@@ -1,0 +1,799 @@
+// gdn_lin.h -- linear attention with a decay for each head on gfx950: chunked
+// passes over prompts, their gradient, and the step of a single token.
+//
+//     S_t = a_t S_{t-1} + v_t k_t^T,   o_t = s S_t q_t,   a_t = exp(log_alpha_t)
+//
+// Over a chunk of C tokens, with G_r the sum of log a from the chunk's first
+// token to r and S the state before it:
+//     o_r = s ( e^{G_r} S q_r + sum_{i <= r} e^{G_r - G_i} (q_r . k_i) v_i )
+//     S  <- e^{G_C} S + sum_i e^{G_C - G_i} v_i k_i^T
+// With D_t the gradient of S_t (D_t = a_{t+1} D_{t+1} + s do_t q_t^T) the
+// gradients are dq_t = s S_t^T do_t, dk_t = D_t^T v_t, dv_t = D_t k_t, which are
+// the same pass with other operands: dq that of (do, v, k) on S transposed, and
+// backwards in time dk that of (v, do, q) and dv that of (k, q, do).  So one
+// kernel serves all four: rows `a` meet rows `b` (over NK numbers), which
+// contribute rows `c`.
+//
+// The decay's gradient a_t <D_t, S_{t-1}> is a sum over pairs of tokens, one
+// that reads at or after t and one that writes before t.  Pairs inside t's chunk:
+// their products M_ri, summed over rows and columns; pairs with one token
+// outside: q_r . dq_r and k_i . dk_i without their chunk's part; pairs with both
+// outside: <D, S> over the chunk, from the chunks' sums.  Nothing is a
+// difference of long sums, which strong decays would not survive.
+//
+// Products on the matrix units: bf16 rows as they lie, and what is computed (the
+// state, decayed values, products of rows times their decay) in two or three bf16
+// numbers that add up to it (errors of 2^-17 or 2^-24); fp32 rows on the fp32
+// units.
+#pragma once
+#include "gdn_layer.h"
+
+namespace gdn {
+
+struct LinTensor {
+    const void* p;
+    int64_t sb, sh, st;     // elements between sequences, heads, tokens
+    int rep;                // heads of values to one of its heads
+    int wide;               // rows of 16-byte pieces
+};
+
+// One pass: rows a, b of nk numbers, c (and x) of nv.
+struct LinRole {
+    LinTensor a, b, c;
+    LinTensor x;            // gradient of the decay: q beside dq, k beside dk
+    int nk, nv, tiles;
+    const float* first;     // state to start from, or null
+    const float* carry;     // states that segments start from [B H, nseg, d_v, d_k]
+    float* last;            // state at the end, or null
+    const float* end_grad;  // gradient of the last state (for <D, S> at the end), or null
+    void* out;              // [B, H, T, nv]
+    int out_bf16, out_wide;
+    float* sum_w;           // [tiles, B H, T]: pairs inside the chunk
+    float* sum_x;           // [tiles, B H, T]: pairs with one token outside
+    float* chunk_x;         // [tiles, B H, chunks]: their sums over a chunk
+    float* end_share;       // [tiles, B H]
+};
+
+struct LinParams {
+    LinRole r[3];
+    const float* log_alpha; // or null
+    int64_t lsb, lsh, lst;
+    const int32_t* lens;    // or null
+    float* seg_sum;         // [B H, nseg, d_v, d_k]: what each segment adds
+    float* seg_decay;       // [B H, nseg]: log2 of its decay
+    float* seg_sum_d;       // the same of D
+    int64_t units;          // B H nseg
+    int B, H, T, dk, dv, nseg, seg_len;
+    float scale;
+};
+
+enum LinMode { kLinFwd, kLinDq, kLinDk, kLinDv, kLinSum, kLinSumD };
+
+constexpr int kLinThreads = 256;
+constexpr int kLinTile = 32;        // columns of c to a workgroup
+// Tokens to a chunk: as many as let two chunks' rows and two states lie in LDS.
+constexpr int lin_chunk(bool bf16, int nk) { return bf16 && nk <= 128 ? 64 : 32; }
+// A decay below 2^-kLinFloor counts as 0 (fp32 has none that is smaller).
+constexpr float kLinFloor = 256.f;
+
+typedef __attribute__((ext_vector_type(8))) float f32x8;
+typedef __attribute__((address_space(3))) char lds_char;
+template <typename V>
+__device__ __forceinline__ V lds_get(const lds_char* p) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) V*>(p);
+}
+template <typename V>
+__device__ __forceinline__ void lds_put(lds_char* p, V v) {
+    *reinterpret_cast<__attribute__((address_space(3))) V*>(p) = v;
+}
+
+// Operands of a matrix product over 32 numbers: lane 16 g + n has row (or
+// column) n and numbers 8 g .. 8 g + 7.
+template <bool BF>
+struct LinFrag;
+template <>
+struct LinFrag<true> {
+    bf16x8 v;
+    __device__ __forceinline__ float get(int i) const { return (float)v[i]; }
+};
+template <>
+struct LinFrag<false> {
+    f32x8 v;
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+};
+__device__ __forceinline__ f32x4 lin_mma(const LinFrag<true>& a, const LinFrag<true>& b, f32x4 c) { return mfma_bf16(a.v, b.v, c); }
+// (the fp32 unit takes four numbers at a time: one of each lane's eight)
+__device__ __forceinline__ f32x4 lin_mma(const LinFrag<false>& a, const LinFrag<false>& b, f32x4 c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c = mfma_f32(a.v[i], b.v[i], c);
+    return c;
+}
+// A computed operand: N bf16 numbers that add up to it, or fp32.
+template <bool BF, int N>
+struct LinSplit;
+template <int N>
+struct LinSplit<true, N> {
+    LinFrag<true> part[N];
+    __device__ __forceinline__ void set(int i, float x) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const __bf16 h = (__bf16)x;
+            part[k].v[i] = h;
+            x -= (float)h;
+        }
+    }
+};
+template <int N>
+struct LinSplit<false, N> {
+    LinFrag<false> part[1];
+    __device__ __forceinline__ void set(int i, float x) { part[0].v[i] = x; }
+};
+template <bool BF, int N>
+__device__ __forceinline__ f32x4 lin_mma(const LinFrag<BF>& a, const LinSplit<BF, N>& b, f32x4 c) {
+#pragma unroll
+    for (int k = 0; k < (BF ? N : 1); ++k) c = lin_mma(a, b.part[k], c);
+    return c;
+}
+
+// Rows of ROWB bytes in LDS, without padding between them; piece p (16 bytes)
+// of row r lies at p ^ turn(r), so that the same piece of 16 rows, which a
+// matrix operand is read from, covers all banks.
+template <int ROWB>
+__device__ __forceinline__ int lin_turn(int r) {
+    if constexpr (ROWB % 256 == 0) return r & 15;
+    else if constexpr (ROWB % 128 == 0) return (r >> 1) & 7;
+    else return (r >> 2) & 3;
+}
+template <int ROWB>
+__device__ __forceinline__ int lin_piece(int r, int p) { return r * ROWB + ((p ^ lin_turn<ROWB>(r)) << 4); }
+
+// Rows row0 + n, numbers 32 ks + 8 g ..
+template <bool BF, int ROWB>
+__device__ __forceinline__ LinFrag<BF> lin_rows(const lds_char* t, int row0, int ks, int n, int g) {
+    LinFrag<BF> f;
+    if constexpr (BF) {
+        f.v = lds_get<bf16x8>(t + lin_piece<ROWB>(row0 + n, 4 * ks + g));
+    } else {
+        const f32x4 a = lds_get<f32x4>(t + lin_piece<ROWB>(row0 + n, 8 * ks + 2 * g));
+        const f32x4 b = lds_get<f32x4>(t + lin_piece<ROWB>(row0 + n, 8 * ks + 2 * g + 1));
+        f.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    return f;
+}
+// Column col0 + n of tokens 32 m + 4 g + j and 32 m + 16 + 4 g + j: the order
+// in which a product's result holds the rows of two tiles.
+template <bool BF, int ROWB>
+__device__ __forceinline__ LinFrag<BF> lin_cols(const lds_char* t, int m, int col0, int n, int g) {
+    LinFrag<BF> f;
+    if constexpr (BF) {
+        // (the transposing read: lane n of a group addresses four columns of
+        // token n / 4 and receives four tokens of column n)
+        const int r = 32 * m + 4 * g + (n >> 2), p = (col0 >> 3) + ((n & 3) >> 1), half = (n & 1) * 8;
+        typedef __attribute__((ext_vector_type(4))) short s4;
+        typedef __attribute__((address_space(3))) s4 lds_s4;
+        const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(t + lin_piece<ROWB>(r, p) + half));
+        const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(t + lin_piece<ROWB>(r + 16, p) + half));
+        f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+        const int c = col0 + n;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = 32 * m + 4 * g + (j & 3) + (j >> 2) * 16;
+            f.v[j] = lds_get<float>(t + lin_piece<ROWB>(r, c >> 2) + (c & 3) * 4);
+        }
+    }
+    return f;
+}
+
+// `rows` rows of `cols` numbers into a tile of C rows of ROWB bytes; the rest of
+// the tile is 0.
+template <bool BF, int ROWB, int C>
+__device__ __forceinline__ void lin_stage(lds_char* tile, const char* src, int64_t stride, int rows, int cols, int wide) {
+    constexpr int kEl = BF ? 8 : 4, kPieces = ROWB / 16, kBytes = BF ? 2 : 4;
+    for (int i = threadIdx.x; i < C * kPieces; i += kLinThreads) {
+        const int r = i / kPieces, q = i % kPieces, c = q * kEl;
+        u32x4 v = {0, 0, 0, 0};
+        if (r < rows && c < cols) {
+            const char* at = src + ((int64_t)r * stride + c) * kBytes;
+            if (wide && c + kEl <= cols) {
+                v = *reinterpret_cast<const u32x4*>(at);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kEl; ++e) {
+                    if (c + e >= cols) break;
+                    if constexpr (BF) {
+                        const uint32_t x = reinterpret_cast<const unsigned short*>(at)[e];
+                        v[e / 2] |= x << (16 * (e & 1));
+                    } else {
+                        v[e] = reinterpret_cast<const uint32_t*>(at)[e];
+                    }
+                }
+            }
+        }
+        lds_put(tile + lin_piece<ROWB>(r, q), v);
+    }
+}
+
+template <bool BF, int NK, int C, int MODE>
+struct LinPlan {
+    static constexpr bool kOut = MODE < kLinSum, kGrad = MODE == kLinDq || MODE == kLinDk;
+    static constexpr int kEl = BF ? 2 : 4;
+    static constexpr int kRowA = NK * kEl, kRowC = kLinTile * kEl;
+    static constexpr int kA = 0;
+    static constexpr int kB = kA + (kOut ? C * kRowA : 0);
+    static constexpr int kC = kB + C * kRowA;
+    static constexpr int kX = kC + C * kRowC;
+    static constexpr int kVec = kX + (kGrad ? C * kRowC : 0);       // Gh, Gl, out factor, state factor
+    static constexpr int kSums = kVec + 4 * C * 4;                  // rows, columns of each row tile, x of each column tile
+    static constexpr int kState = (kSums + (kGrad ? (1 + C / 16 + 2) * C * 4 : 0) + 255) / 256 * 256;
+    static constexpr int kStateBytes = kLinTile * NK * 4;           // bf16 pairs, or fp32
+    static constexpr int kBytes = kState + (kOut ? 2 * kStateBytes : 0);
+};
+
+// Sum over lanes 16 g + n of all g, in each.
+__device__ __forceinline__ float lin_sum_groups(float v) {
+    v = swap16_add(v, v);
+    return swap32_add(v, v);
+}
+
+template <bool BF, int NK, int C, int MODE>
+__device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, int64_t unit, int tile, char* shared) {
+    typedef LinPlan<BF, NK, C, MODE> L;
+    constexpr bool kRev = MODE == kLinDk || MODE == kLinDv || MODE == kLinSumD;
+    constexpr bool kTurned = MODE == kLinDq || MODE == kLinDk;      // the state transposed
+    constexpr int RT = C / 16;                      // row tiles
+    constexpr int CT = RT == 4 ? 2 : 1;             // column tiles of a wave
+    constexpr int KS = NK / 32, KT = NK / 32;       // steps over nk; state tiles of a wave
+    constexpr int EB = L::kEl;
+    lds_char* lds = (lds_char*)shared;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int64_t bh = unit / p.nseg;
+    const int seg = (int)(unit % p.nseg);
+    const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+    const int t0 = seg * p.seg_len, t1 = p.T - t0 > p.seg_len ? t0 + p.seg_len : p.T;
+    int tl = seq_len(p.lens, b, p.T);
+    tl = tl < t0 ? t0 : (tl > t1 ? t1 : tl);
+    const int chunks = (tl - t0 + C - 1) / C;
+    const int col0 = tile * kLinTile, cols = R.nv - col0 < kLinTile ? R.nv - col0 : kLinTile;
+    auto head = [&](const LinTensor& x, int c) __attribute__((always_inline)) {
+        return reinterpret_cast<const char*>(x.p) + (b * x.sb + (h / x.rep) * x.sh + c) * EB;
+    };
+    const char* pa = L::kOut ? head(R.a, 0) : nullptr;
+    const char* pb = head(R.b, 0);
+    const char* pc = head(R.c, col0);
+    const char* px = L::kGrad && R.x.p ? head(R.x, col0) : nullptr;
+    const float* la = p.log_alpha ? p.log_alpha + b * p.lsb + h * p.lsh : nullptr;
+    const float pscale = kRev ? p.scale : 1.f, oscale = kRev ? 1.f : p.scale;
+
+    // The state, rows nk and columns nv: this wave's tiles are KT rows of tiles
+    // from kt0 and one column of tiles.
+    const int nvt = wave & 1, kt0 = (wave >> 1) * KT;
+    const int64_t plane = (int64_t)p.dk * p.dv;
+    const int64_t sn = kTurned ? 1 : p.dk, sk = kTurned ? p.dk : 1;
+    const int scol = col0 + nvt * 16 + n;
+    f32x4 S[KT];
+    {
+        const float* from = nullptr;
+        if constexpr (L::kOut) from = R.carry ? R.carry + unit * plane : R.first ? R.first + bh * plane : nullptr;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = (kt0 + t) * 16 + 4 * g + j;
+                S[t][j] = from && k < R.nk && scol < R.nv ? from[k * sk + scol * sn] : 0.f;
+            }
+    }
+    auto publish = [&](int buf) __attribute__((always_inline)) {
+        lds_char* at = lds + L::kState + buf * L::kStateBytes;
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+            const int row = nvt * 16 + n;
+            if constexpr (BF) {
+                const bf16x4 hi = __builtin_convertvector(S[t], bf16x4);
+                const bf16x4 lo = __builtin_convertvector(S[t] - __builtin_convertvector(hi, f32x4), bf16x4);
+                const int off = lin_piece<L::kRowA>(row, 2 * (kt0 + t) + (g >> 1)) + (g & 1) * 8;
+                lds_put(at + off, hi);
+                lds_put(at + kLinTile * L::kRowA + off, lo);
+            } else {
+                lds_put(at + lin_piece<L::kRowA>(row, 4 * (kt0 + t) + g), S[t]);
+            }
+        }
+    };
+    if constexpr (L::kOut) publish(0);
+    float total = 0.f;      // log2 of the decay so far
+    const int rt = RT == 4 ? wave : wave >> 1, ct0 = RT == 4 ? 0 : wave & 1;
+
+    // what the last chunk left for the decay's gradient
+    auto emit = [&](int ch) __attribute__((always_inline)) {
+        if constexpr (L::kGrad) {
+            if (!R.sum_x || wave != 1) return;
+            lds_char* sums = lds + L::kSums;
+            const int t = t0 + ch * C + lane;
+            float w = 0.f, x = 0.f;
+            if (lane < C) {
+                x = lds_get<float>(sums + ((1 + RT) * C + lane) * 4);
+                if constexpr (RT == 2) x += lds_get<float>(sums + ((2 + RT) * C + lane) * 4);
+                if constexpr (MODE == kLinDq) {
+                    w = lds_get<float>(sums + lane * 4);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) w -= lds_get<float>(sums + ((1 + i) * C + lane) * 4);
+                }
+                const int64_t at = (tile * (int64_t)p.B * p.H + bh) * p.T + t;
+                if (t < tl) {
+                    R.sum_x[at] = x;
+                    if constexpr (MODE == kLinDq) R.sum_w[at] = w;
+                } else {
+                    x = 0.f;
+                }
+            }
+            x = lanes_sum<64>(x);
+            if (lane == 0) {
+                const int64_t per = (p.T + C - 1) / C;
+                R.chunk_x[(tile * (int64_t)p.B * p.H + bh) * per + t0 / C + ch] = x;
+            }
+        }
+    };
+
+    for (int it = 0; it < chunks; ++it) {
+        const int ch = kRev ? chunks - 1 - it : it, tc = t0 + ch * C, rows = tl - tc < C ? tl - tc : C;
+        __syncthreads();
+        if (it > 0) emit(kRev ? ch + 1 : ch - 1);
+        if constexpr (L::kOut) lin_stage<BF, L::kRowA, C>(lds + L::kA, pa + tc * R.a.st * EB, R.a.st, rows, R.nk, R.a.wide);
+        lin_stage<BF, L::kRowA, C>(lds + L::kB, pb + tc * R.b.st * EB, R.b.st, rows, R.nk, R.b.wide);
+        lin_stage<BF, L::kRowC, C>(lds + L::kC, pc + tc * R.c.st * EB, R.c.st, rows, cols, R.c.wide);
+        if constexpr (L::kGrad) {
+            if (px) lin_stage<BF, L::kRowC, C>(lds + L::kX, px + tc * R.x.st * EB, R.x.st, rows, cols, R.x.wide);
+        }
+        if (wave == 0) {
+            float l = la && lane < rows ? la[(tc + lane) * p.lst] * kLog2e : 0.f;
+            l = l < -kLinFloor ? -kLinFloor : l;    // (NaN stays)
+            double G = l;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const double o = __shfl_up(G, d);
+                if (lane >= d) G += o;
+            }
+            const double end = __shfl(G, C - 1);
+            if (lane < C) {
+                lds_char* v = lds + L::kVec + lane * 4;
+                const float gh = (float)G;
+                const float from = exp2_hw(gh), to = exp2_hw((float)(end - G));
+                lds_put(v, gh);
+                lds_put(v + C * 4, (float)(G - gh));
+                lds_put(v + 2 * C * 4, kRev ? to : from);
+                lds_put(v + 3 * C * 4, kRev ? from * p.scale : to);
+            }
+        }
+        __syncthreads();
+        const lds_char* vec = lds + L::kVec;
+        const float gend = lds_get<float>(vec + (C - 1) * 4);
+        total += gend;
+        if constexpr (L::kOut) {
+            const lds_char* st = lds + L::kState + (it & 1) * L::kStateBytes;
+            LinFrag<BF> fa[KS];
+            f32x4 acc[CT];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) fa[ks] = lin_rows<BF, L::kRowA>(lds + L::kA, rt * 16, ks, n, g);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                acc[c] = zero4();
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    acc[c] = lin_mma(lin_rows<BF, L::kRowA>(st, (ct0 + c) * 16, ks, n, g), fa[ks], acc[c]);
+                    if constexpr (BF)
+                        acc[c] = lin_mma(lin_rows<BF, L::kRowA>(st + kLinTile * L::kRowA, (ct0 + c) * 16, ks, n, g), fa[ks], acc[c]);
+                }
+            }
+            const int row = rt * 16 + n;
+            const float gh = lds_get<float>(vec + row * 4), gl = lds_get<float>(vec + (C + row) * 4);
+            const float of = lds_get<float>(vec + (2 * C + row) * 4);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[c] *= of;
+            float sums_x = 0.f, sums_w = 0.f;
+            if constexpr (L::kGrad) {
+                if (R.sum_x) {
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int col = (ct0 + c) * 16 + 4 * g + j;
+                            const lds_char* at = lds + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
+                            float x;
+                            if constexpr (BF) x = (float)lds_get<__bf16>(at);
+                            else x = lds_get<float>(at);
+                            sums_x = fmaf(acc[c][j], x, sums_x);
+                        }
+                    sums_x = lin_sum_groups(sums_x) * oscale;
+                    if (g == 0) lds_put(lds + L::kSums + ((1 + RT + ct0) * C + row) * 4, sums_x);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < C / 32; ++m) {
+                // (tiles of 32 tokens that hold any at or before the rows, or
+                // behind them)
+                if (kRev ? 2 * m + 1 < rt : 2 * m > rt) {
+                    if constexpr (MODE == kLinDq) {
+                        if (R.sum_x && ct0 == 0)
+                            for (int i = lane; i < 32; i += 64) lds_put(lds + L::kSums + ((1 + rt) * C + 32 * m + i) * 4, 0.f);
+                    }
+                    continue;
+                }
+                LinSplit<BF, 2> pp;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int i0 = 32 * m + 16 * half, col = i0 + 4 * g;
+                    const bool some = kRev ? 2 * m + half >= rt : 2 * m + half <= rt;
+                    f32x4 pr = zero4();
+                    if (some) {
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) pr = lin_mma(lin_rows<BF, L::kRowA>(lds + L::kB, i0, ks, n, g), fa[ks], pr);
+                        const f32x4 ih = lds_get<f32x4>(vec + col * 4), il = lds_get<f32x4>(vec + (C + col) * 4);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float d = (gh - ih[j]) + (gl - il[j]);
+                            const bool in = kRev ? col + j >= row : col + j <= row;
+                            pr[j] = in ? pr[j] * (exp2_hw(kRev ? -d : d) * pscale) : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) pp.set(4 * half + j, pr[j]);
+                    if constexpr (MODE == kLinDq) {
+                        if (R.sum_x) {
+                            f32x4 other = zero4();
+                            if (some) {
+                                const LinFrag<BF> fx = lin_rows<BF, L::kRowC>(lds + L::kX, rt * 16, 0, n, g);
+                                other = lin_mma(lin_rows<BF, L::kRowC>(lds + L::kC, i0, 0, n, g), fx, other);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float mm = some && col + j < row ? other[j] * pr[j] * oscale : 0.f;
+                                sums_w += mm;
+                                const float down = lanes_sum<16>(mm);
+                                if (n == 0 && ct0 == 0) lds_put(lds + L::kSums + ((1 + rt) * C + col + j) * 4, down);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    acc[c] = lin_mma(lin_cols<BF, L::kRowC>(lds + L::kC, m, (ct0 + c) * 16, n, g), pp, acc[c]);
+            }
+            if constexpr (MODE == kLinDq) {
+                if (R.sum_x) {
+                    sums_w = lin_sum_groups(sums_w);
+                    if (g == 0 && ct0 == 0) lds_put(lds + L::kSums + row * 4, sums_w);
+                }
+            }
+            // (rows behind the sequence's end inside its last chunk are 0)
+            const int t = tc + row;
+            if (t < t1) {
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    const int col = col0 + (ct0 + c) * 16 + 4 * g;
+                    const f32x4 o = t < tl ? acc[c] * oscale : zero4();
+                    const int64_t at = (bh * p.T + t) * R.nv + col;
+                    if (R.out_wide) {
+                        if (col < R.nv) {
+                            if (R.out_bf16) *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(R.out) + at) = __builtin_convertvector(o, bf16x4);
+                            else *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(R.out) + at) = o;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (col + j < R.nv) {
+                                if (R.out_bf16) reinterpret_cast<__bf16*>(R.out)[at + j] = (__bf16)o[j];
+                                else reinterpret_cast<float*>(R.out)[at + j] = o[j];
+                            }
+                    }
+                }
+            }
+        }
+        // the state behind the chunk
+        const float whole = exp2_hw(gend);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S[t] *= whole;
+#pragma unroll
+        for (int m = 0; m < C / 32; ++m) {
+            const LinFrag<BF> raw = lin_cols<BF, L::kRowC>(lds + L::kC, m, nvt * 16, n, g);
+            const f32x4 u0 = lds_get<f32x4>(vec + (3 * C + 32 * m + 4 * g) * 4);
+            const f32x4 u1 = lds_get<f32x4>(vec + (3 * C + 32 * m + 16 + 4 * g) * 4);
+            LinSplit<BF, 3> fc;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                fc.set(j, raw.get(j) * u0[j]);
+                fc.set(j + 4, raw.get(j + 4) * u1[j]);
+            }
+#pragma unroll
+            for (int t = 0; t < KT; ++t) S[t] = lin_mma(lin_cols<BF, L::kRowA>(lds + L::kB, m, (kt0 + t) * 16, n, g), fc, S[t]);
+        }
+        if constexpr (L::kOut) publish((it + 1) & 1);
+    }
+    if constexpr (L::kGrad) {
+        __syncthreads();
+        if (chunks > 0) emit(kRev ? 0 : chunks - 1);
+    }
+    if constexpr (L::kOut) {
+        // rows behind the last chunk
+        const int64_t z0 = t0 + (int64_t)chunks * C;
+        const int span = cols;
+        for (int64_t i = z0 * span + threadIdx.x; i < (int64_t)t1 * span; i += kLinThreads) {
+            const int64_t at = (bh * p.T + i / span) * R.nv + col0 + i % span;
+            if (R.out_bf16) reinterpret_cast<__bf16*>(R.out)[at] = (__bf16)0.f;
+            else reinterpret_cast<float*>(R.out)[at] = 0.f;
+        }
+    }
+    float* to = nullptr;
+    if constexpr (MODE == kLinSum) to = p.seg_sum + unit * plane;
+    if constexpr (MODE == kLinSumD) to = p.seg_sum_d + unit * plane;
+    if constexpr (L::kOut) {
+        if (R.last && seg == (kRev ? 0 : p.nseg - 1)) to = R.last + bh * plane;
+    }
+    float share = 0.f;
+    const bool ends = MODE == kLinDq && R.end_share && seg == p.nseg - 1;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = (kt0 + t) * 16 + 4 * g + j;
+            if (k < R.nk && scol < R.nv) {
+                if (to) to[k * sk + scol * sn] = S[t][j];
+                if (ends) share = fmaf(S[t][j], R.end_grad[bh * plane + k * sk + scol * sn], share);
+            }
+        }
+    if constexpr (MODE == kLinSum || MODE == kLinSumD) {
+        if (MODE == kLinSum && tile == 0 && threadIdx.x == 0) p.seg_decay[unit] = total;
+    }
+    if constexpr (MODE == kLinDq) {
+        if (ends) {
+            __syncthreads();
+            share = lanes_sum<64>(share);
+            if (lane == 0) lds_put(lds + L::kSums + wave * 4, share);
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                float s = 0.f;
+                for (int i = 0; i < kLinThreads / 64; ++i) s += lds_get<float>(lds + L::kSums + i * 4);
+                R.end_share[tile * (int64_t)p.B * p.H + bh] = s;
+            }
+        }
+    }
+}
+
+// Workgroups: the tiles of a unit (a head of a sequence, or a segment of one)
+// beside each other on one XCD, whose L2 then holds the rows that they share;
+// neighbouring units too, whose heads may share queries and keys.
+enum LinSet { kLinSetFwd, kLinSetQk, kLinSetV, kLinSetAll, kLinSetSum, kLinSetSums };
+constexpr int kXcds = 8;
+
+template <bool BF, int NK, int SET>
+struct LinBytes {
+    static constexpr int C = lin_chunk(BF, NK);
+    static constexpr int kGrad = LinPlan<BF, NK, C, kLinDq>::kBytes;
+    static constexpr int kFwd = LinPlan<BF, NK, C, kLinFwd>::kBytes;
+    static constexpr int kSum = LinPlan<BF, NK, C, kLinSum>::kBytes;
+    static constexpr int value = SET == kLinSetFwd || SET == kLinSetV ? kFwd : SET == kLinSetSum || SET == kLinSetSums ? kSum : kGrad;
+};
+
+template <bool BF, int NK, int SET>
+__global__ __launch_bounds__(kLinThreads) void gdn_lin_kernel(LinParams p) {
+    __shared__ __align__(256) char lin_lds[LinBytes<BF, NK, SET>::value];
+    constexpr int C = lin_chunk(BF, NK);
+    constexpr int kRoles = SET == kLinSetAll ? 3 : SET == kLinSetQk || SET == kLinSetSums ? 2 : 1;
+    int tiles = 0;
+#pragma unroll
+    for (int i = 0; i < kRoles; ++i) tiles += p.r[i].tiles;
+    const int64_t per = (p.units + kXcds - 1) / kXcds;
+    const int64_t at = blockIdx.x / kXcds;
+    const int64_t unit = (blockIdx.x % kXcds) * per + at / tiles;
+    int tile = (int)(at % tiles);
+    if (at / tiles >= per || unit >= p.units) return;
+    if constexpr (SET == kLinSetFwd) {
+        lin_pass<BF, NK, C, kLinFwd>(p, p.r[0], unit, tile, lin_lds);
+    } else if constexpr (SET == kLinSetV) {
+        lin_pass<BF, NK, C, kLinDv>(p, p.r[0], unit, tile, lin_lds);
+    } else if constexpr (SET == kLinSetSum) {
+        lin_pass<BF, NK, C, kLinSum>(p, p.r[0], unit, tile, lin_lds);
+    } else {
+        if (tile < p.r[0].tiles) {
+            if constexpr (SET == kLinSetSums) lin_pass<BF, NK, C, kLinSum>(p, p.r[0], unit, tile, lin_lds);
+            else lin_pass<BF, NK, C, kLinDq>(p, p.r[0], unit, tile, lin_lds);
+            return;
+        }
+        tile -= p.r[0].tiles;
+        if (tile < p.r[1].tiles) {
+            if constexpr (SET == kLinSetSums) lin_pass<BF, NK, C, kLinSumD>(p, p.r[1], unit, tile, lin_lds);
+            else lin_pass<BF, NK, C, kLinDk>(p, p.r[1], unit, tile, lin_lds);
+            return;
+        }
+        if constexpr (SET == kLinSetAll) lin_pass<BF, NK, C, kLinDv>(p, p.r[2], unit, tile - p.r[1].tiles, lin_lds);
+    }
+}
+
+// The states that segments start from, in the place of what each adds: X_{j+1}
+// = a_j X_j + E_j from the first segment on, or backwards in time.
+struct LinChainParams {
+    float* sum;             // [B H, nseg, plane]
+    const float* decay;     // [B H, nseg]
+    const float* first;     // [B H, plane] or null
+    int64_t plane;
+    int nseg, rev;
+};
+static __global__ __launch_bounds__(256) void gdn_lin_chain_kernel(LinChainParams p, LinChainParams q) {
+    const LinChainParams& c = blockIdx.z ? q : p;
+    const int64_t i = blockIdx.x * 256ll + threadIdx.x, bh = blockIdx.y;
+    if (i >= c.plane) return;
+    float x = c.first ? c.first[bh * c.plane + i] : 0.f;
+    for (int s = 0; s < c.nseg; ++s) {
+        const int64_t j = bh * c.nseg + (c.rev ? c.nseg - 1 - s : s);
+        const float e = c.sum[j * c.plane + i];
+        c.sum[j * c.plane + i] = x;
+        x = fmaf(exp2_hw(c.decay[j]), x, e);
+    }
+}
+
+// The decay's gradient from the passes' sums: a wave to a chunk.
+struct LinDecayParams {
+    const float* sum_w;     // [tiles, B H, T]
+    const float* sum_x;
+    const float* sum_y;
+    const float* chunk_x;   // [tiles, B H, chunks]
+    const float* chunk_y;
+    const float* end_share; // [tiles, B H] or null
+    const float* log_alpha;
+    int64_t lsb, lsh, lst;
+    const int32_t* lens;
+    float* out;             // [B, H, T]
+    int64_t bhs;
+    int H, T, C, tiles;
+};
+static __global__ __launch_bounds__(256) void gdn_lin_decay_kernel(LinDecayParams p) {
+    const int per = (p.T + p.C - 1) / p.C;
+    const int groups = (per + 3) / 4;
+    const int64_t bh = blockIdx.x / groups;
+    const int ch = (int)(blockIdx.x % groups) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (ch >= per) return;
+    const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+    const int len = seq_len(p.lens, b, p.T), chunks = (len + p.C - 1) / p.C;
+    const int t = ch * p.C + lane;
+    double w = 0, x = 0, y = 0, F = 0;
+    if (ch < chunks) {
+        for (int i = 0; i < p.tiles; ++i) {
+            const int64_t row = i * p.bhs + bh;
+            if (lane < p.C && t < len) {
+                w += p.sum_w[row * p.T + t];
+                x += p.sum_x[row * p.T + t];
+                y += p.sum_y[row * p.T + t];
+            }
+            // <D, S> behind this chunk
+            for (int c = ch + 1 + lane; c < chunks; c += 64) F += (double)p.chunk_x[row * per + c] - p.chunk_y[row * per + c];
+            if (lane == 0 && p.end_share) F += p.end_share[row];
+            if (lane == 0) F -= p.chunk_y[row * per + ch];
+        }
+    }
+    double before = y;      // sums of y up to a token, of w + x from it on
+    double behind = w + x;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const double u = __shfl_up(before, d), v = __shfl_down(behind, d);
+        F += __shfl_xor(F, d);
+        if (lane >= d) before += u;
+        if (lane + d < 64) behind += v;
+    }
+    if (lane < p.C && t < p.T) {
+        const float la = p.log_alpha[b * p.lsb + h * p.lsh + t * p.lst];
+        float r = (float)(behind + (before - y) + F);
+        // (behind a decay of 0 nothing is left to have a gradient)
+        if (t >= len || la < -150.f / kLog2e) r = 0.f;
+        p.out[bh * p.T + t] = r;
+    }
+}
+
+// Sums over sequences and tokens of one head's [B, H, T] numbers, in a fixed
+// order.
+static __global__ __launch_bounds__(1024) void gdn_lin_head_sum_kernel(const float* in, float* out, int B, int H, int T) {
+    __shared__ double part[16];
+    const int h = blockIdx.x;
+    double s = 0;
+    for (int b = 0; b < B; ++b)
+        for (int t = threadIdx.x; t < T; t += 1024) s += in[((int64_t)b * H + h) * T + t];
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double r = 0;
+        for (int i = 0; i < 16; ++i) r += part[i];
+        out[h] = (float)r;
+    }
+}
+
+// Sums over the heads that share a head of queries or keys: [B, H, T, d] fp32
+// to [B, H / rep, T, d].
+struct LinGroupParams {
+    const float* in;
+    void* out;
+    int64_t row;            // T d
+    int64_t n;              // B (H / rep) T d
+    int rep;
+};
+template <bool BF>
+static __global__ __launch_bounds__(256) void gdn_lin_group_sum_kernel(LinGroupParams p) {
+    const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+    if (i >= p.n) return;
+    const int64_t head = i / p.row, e = i - head * p.row;
+    float s = 0.f;
+    for (int r = 0; r < p.rep; ++r) s += p.in[(head * p.rep + r) * p.row + e];
+    store_one<BF>(p.out, i, s);
+}
+
+// One token of every sequence.  A group of L lanes holds a row of the state (d_k
+// numbers, V to a piece), kLinStepRows rows in turn: k and q are loaded once for
+// them.
+struct LinStepParams {
+    LinTensor q, k, v;
+    const float* log_alpha;
+    int64_t lsb, lsh;
+    float* S;
+    void* out;
+    int H, dk, dv, blocks, out_bf16;
+    float scale;
+};
+constexpr int kLinStepThreads = 128;
+constexpr int kLinStepRows = 4;
+template <bool BF, int L, int J, int V>
+__global__ __launch_bounds__(kLinStepThreads) void gdn_lin_step_kernel(LinStepParams p) {
+    constexpr int kGroups = kLinStepThreads / L;
+    const int m = threadIdx.x % L, grp = threadIdx.x / L;
+    const int64_t bh = blockIdx.x / p.blocks;
+    const int row0 = (int)(blockIdx.x % p.blocks) * kGroups * kLinStepRows + grp;
+    const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+    const int64_t q0 = b * p.q.sb + (h / p.q.rep) * p.q.sh, k0 = b * p.k.sb + (h / p.k.rep) * p.k.sh;
+    const int64_t v0 = b * p.v.sb + h * p.v.sh;
+    Raw<false, V> S[kLinStepRows][J];
+    Raw<BF, V> kr[J], qr[J];
+#pragma unroll
+    for (int r = 0; r < kLinStepRows; ++r) {
+        const int row = row0 + r * kGroups;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int c = (j * L + m) * V;
+            S[r][j].zero();
+            if (row < p.dv && c < p.dk) S[r][j].load(p.S, (bh * p.dv + row) * p.dk + c);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = (j * L + m) * V;
+        kr[j].zero();
+        qr[j].zero();
+        if (c < p.dk) {
+            kr[j].load(p.k.p, k0 + c);
+            qr[j].load(p.q.p, q0 + c);
+        }
+    }
+    const float a = p.log_alpha ? exp2_hw(p.log_alpha[b * p.lsb + h * p.lsh] * kLog2e) : 1.f;
+#pragma unroll
+    for (int r = 0; r < kLinStepRows; ++r) {
+        const int row = row0 + r * kGroups;
+        const float v = row < p.dv ? load_one<BF>(p.v.p, v0 + row) : 0.f;
+        float o = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int c = (j * L + m) * V;
+            float f[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                f[e] = fmaf(v, kr[j].get(e), a * S[r][j].get(e));
+                o = fmaf(f[e], qr[j].get(e), o);
+            }
+            if (row < p.dv && c < p.dk) store_vec<false, V>(p.S, (bh * p.dv + row) * p.dk + c, f);
+        }
+        o = lanes_sum<L>(o) * p.scale;
+        if (row < p.dv && m == 0) {
+            if (p.out_bf16) reinterpret_cast<__bf16*>(p.out)[bh * p.dv + row] = (__bf16)o;
+            else reinterpret_cast<float*>(p.out)[bh * p.dv + row] = o;
+        }
+    }
+}
+
+}  // namespace gdn

@@ -465,6 +465,119 @@ gdn_status gdn_norm_bwd(const gdn_norm_shape* s, const void* dy, const void* x,
                         float* dweight, float* dbias, void* dz,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the delta rule's state without
+ * its erasing.  The conventions of the operators above hold (strides, lens,
+ * padded rows, sums in a fixed order).
+ *     S_t = a_t S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t,   a_t = exp(log_alpha_t)
+ * log_alpha <= 0 decays; minus infinity starts anew at its token (documents
+ * packed into one row); values above 0 grow.  A value below -256 ln 2 counts
+ * as minus infinity.
+ */
+typedef struct {
+    int32_t B, H, T;          /* sequences, heads of values, tokens            */
+                              /* (T up to 2^31 - 128)                          */
+    int32_t Hq, Hk;           /* heads of queries and of keys, each a divisor of H:
+                                 head h reads heads h / (H / Hq), h / (H / Hk) */
+    int32_t d_k, d_v;         /* 1 .. 256                                      */
+    int32_t dtype;            /* gdn_dtype of q, k, v, dO and their gradients  */
+    int32_t o_dtype;          /* gdn_dtype of O                                */
+    int32_t per_head;         /* log_alpha: 0 [B, H, T], 1 [H]                 */
+    float scale;
+    int64_t q_stride_b, q_stride_h, q_stride_t;   /* q [B, Hq, T, d_k]         */
+    int64_t k_stride_b, k_stride_h, k_stride_t;   /* k [B, Hk, T, d_k]         */
+    int64_t v_stride_b, v_stride_h, v_stride_t;   /* v [B, H, T, d_v]          */
+    int64_t a_stride_b, a_stride_h, a_stride_t;   /* log_alpha (not read for [H],
+                                                     which is contiguous)      */
+} gdn_lin_shape;
+
+/*
+ *   log_alpha  float, strided, or NULL (no decay)
+ *   S0         [B, H, d_v, d_k] float or NULL (zero)
+ *   O          [B, H, T, d_v] o_dtype, contiguous
+ *   S_final    [B, H, d_v, d_k] float or NULL; may be S0 (in place)
+ * Chunks of 64 tokens (32 for fp32, and above d_k 128) on the matrix units; bf16
+ * products of what is computed take two or three bf16 numbers that add up to
+ * it, so that results are those of fp32 arithmetic to about 1e-5 of a tensor's
+ * largest number; any finite numbers whose products fit fp32.
+ * An infinite or NaN input reaches the outputs of its sequence and head (where
+ * heads share queries or keys, of those heads).  Few heads on long sequences:
+ * the tokens are cut into segments that run at once, from what each adds to the
+ * state.  workspace: gdn_lin_fwd_workspace_bytes(s) bytes (0 without segments;
+ * (size_t)-1 for an invalid shape).
+ */
+size_t gdn_lin_fwd_workspace_bytes(const gdn_lin_shape* s);
+gdn_status gdn_lin_fwd(const gdn_lin_shape* s, const void* q, const void* k, const void* v,
+                       const float* log_alpha, const float* S0, const int32_t* lens,
+                       void* O, float* S_final,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every sequence (T must be 1): gdn_lin_fwd with the state S
+ * [B, H, d_v, d_k] updated in place; O [B, H, d_v].  Token strides are not read. */
+gdn_status gdn_lin_step(const gdn_lin_shape* s, const void* q, const void* k, const void* v,
+                        const float* log_alpha, float* S, void* O, void* stream);
+
+/*
+ * Gradient of gdn_lin_fwd (o_dtype is not read).  dO [B, H, T, d_v] dtype
+ * contiguous; dS_final [B, H, d_v, d_k] float or NULL (zero).  Written, all
+ * contiguous: dq [B, Hq, T, d_k], dk [B, Hk, T, d_k] (sums over the heads that
+ * share one), dv [B, H, T, d_v] in dtype; dlog_alpha float shaped as log_alpha
+ * ([B, H, T] or [H]; NULL without log_alpha, or where it is not wanted; 0 where
+ * the decay itself is 0); dS0 float or NULL.  The states are computed again.
+ * workspace: gdn_lin_bwd_workspace_bytes(s) bytes.
+ */
+size_t gdn_lin_bwd_workspace_bytes(const gdn_lin_shape* s);
+gdn_status gdn_lin_bwd(const gdn_lin_shape* s, const void* dO, const void* q, const void* k, const void* v,
+                       const float* log_alpha, const float* S0, const float* dS_final, const int32_t* lens,
+                       void* dq, void* dk, void* dv, float* dlog_alpha, float* dS0,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norms after and before a block, with the block's gate, the scale of its
+ * part and the residual stream between them. */
+typedef struct {
+    int32_t B, T, D;          /* sequences, tokens, channels (D up to 16384)   */
+    int32_t dtype;            /* gdn_dtype of o, gate, y and their gradients   */
+    int32_t x_dtype;          /* gdn_dtype of x, x_out and their gradients     */
+    int32_t post;             /* 1: o is normalised, 0: taken as it is         */
+    int32_t act;              /* of the gate: 0 none, 1 sigmoid, 2 SiLU        */
+    float eps;                /* > 0                                           */
+    int64_t o_stride_b, o_stride_t;   /* o    [B, T, D]                        */
+    int64_t x_stride_b, x_stride_t;   /* x    [B, T, D]                        */
+    int64_t g_stride_b, g_stride_t;   /* gate [B, T, D]                        */
+} gdn_block_norm_shape;
+
+/*
+ *     n = o / sqrt(mean(o^2) + eps) w_post     (post 0: n = o)
+ *     x_out = x + scale act(gate) n
+ *     y = x_out / sqrt(mean(x_out^2) + eps) w_pre
+ * over the D channels of a token: o is what a block computed, x the residual
+ * stream, y what the next block reads (of x_out before it is rounded to x_dtype).
+ *   gate      dtype or NULL (act(gate) = 1);  w_post, scale, w_pre  [D] float or
+ *             NULL (1)
+ *   x_out     [B, T, D] x_dtype, contiguous; may be x where x is contiguous (in
+ *             place)
+ *   y         [B, T, D] dtype, contiguous, or NULL (not wanted)
+ */
+gdn_status gdn_block_norm_fwd(const gdn_block_norm_shape* s, const void* o, const void* x, const void* gate,
+                              const float* w_post, const float* scale, const float* w_pre,
+                              void* x_out, void* y, void* stream);
+
+/*
+ * Gradient of gdn_block_norm_fwd from what it was given and x_out (strided as x
+ * in the shape; statistics are taken from it as it is stored).  dx_out [B, T, D]
+ * x_dtype, dy [B, T, D] dtype, contiguous, either may be NULL (zero), not both.
+ * Written, contiguous: dx x_dtype, dO (the gradient of o) and dgate (NULL
+ * without a gate) dtype; dw_post, dscale, dw_pre [D] float, each with the input
+ * that it belongs to or NULL.  workspace: gdn_block_norm_bwd_workspace_bytes(s)
+ * bytes.
+ */
+size_t gdn_block_norm_bwd_workspace_bytes(const gdn_block_norm_shape* s);
+gdn_status gdn_block_norm_bwd(const gdn_block_norm_shape* s, const void* dx_out, const void* dy,
+                              const void* x_out, const void* o, const void* gate,
+                              const float* w_post, const float* scale, const float* w_pre,
+                              void* dx, void* dO, void* dgate, float* dw_post, float* dscale, float* dw_pre,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* gdn_status_string(gdn_status st);
 
