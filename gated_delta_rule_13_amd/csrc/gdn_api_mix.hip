@@ -106,7 +106,7 @@ gdn_status lin_fits(const gdn_lin_shape& s, bool grad) {
     return ok ? GDN_OK : set_error(GDN_ERR_UNSUPPORTED, "more workgroups than a launch holds");
 }
 
-LinTensor lin_tensor(const void* p, int dtype, int64_t sb, int64_t sh, int64_t st, int rep) {
+LinTensor lin_tensor(const void* p, int dtype, int d, int64_t sb, int64_t sh, int64_t st, int rep) {
     LinTensor t{};
     t.p = p;
     t.sb = sb;
@@ -114,6 +114,9 @@ LinTensor lin_tensor(const void* p, int dtype, int64_t sb, int64_t sh, int64_t s
     t.st = st;
     t.rep = rep;
     t.wide = rows16(p, dtype, {sb, sh, st});
+    // (a chunk's rows within 32 bits of its first)
+    const int bytes = dtype == GDN_BF16 ? 2 : 4;
+    t.direct = t.wide && d * bytes % 16 == 0 && st < (1ll << 31) / (64 * bytes);
     return t;
 }
 LinParams lin_params(const gdn_lin_shape& s, const LinPlanSizes& pl, const float* log_alpha, const int32_t* lens, char* ws) {
@@ -242,9 +245,9 @@ gdn_status gdn_lin_fwd(const gdn_lin_shape* s, const void* q, const void* k, con
     st = check_workspace(workspace, workspace_bytes, pl.bytes, "gdn_lin_fwd_workspace_bytes");
     if (st != GDN_OK) return st;
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    const LinTensor tq = lin_tensor(q, s->dtype, s->q_stride_b, s->q_stride_h, s->q_stride_t, s->H / s->Hq),
-                    tk = lin_tensor(k, s->dtype, s->k_stride_b, s->k_stride_h, s->k_stride_t, s->H / s->Hk),
-                    tv = lin_tensor(v, s->dtype, s->v_stride_b, s->v_stride_h, s->v_stride_t, 1);
+    const LinTensor tq = lin_tensor(q, s->dtype, s->d_k, s->q_stride_b, s->q_stride_h, s->q_stride_t, s->H / s->Hq),
+                    tk = lin_tensor(k, s->dtype, s->d_k, s->k_stride_b, s->k_stride_h, s->k_stride_t, s->H / s->Hk),
+                    tv = lin_tensor(v, s->dtype, s->d_v, s->v_stride_b, s->v_stride_h, s->v_stride_t, 1);
     LinParams p = lin_params(*s, pl, log_alpha, lens, static_cast<char*>(workspace));
     if (pl.nseg > 1) lin_segments(p, *s, tq, tk, tv, nullptr, S0, nullptr, hs);
     p.r[0] = lin_role(tq, tk, tv, s->d_k, s->d_v, O, s->o_dtype == GDN_BF16);
@@ -277,9 +280,9 @@ gdn_status gdn_lin_step(const gdn_lin_shape* s, const void* q, const void* k, co
     if (st == GDN_OK) st = check_apart(eO, {eq, ek, ev, ea});
     if (st != GDN_OK) return st;
     LinStepParams p{};
-    p.q = lin_tensor(q, s->dtype, s->q_stride_b, s->q_stride_h, 0, s->H / s->Hq);
-    p.k = lin_tensor(k, s->dtype, s->k_stride_b, s->k_stride_h, 0, s->H / s->Hk);
-    p.v = lin_tensor(v, s->dtype, s->v_stride_b, s->v_stride_h, 0, 1);
+    p.q = lin_tensor(q, s->dtype, s->d_k, s->q_stride_b, s->q_stride_h, 0, s->H / s->Hq);
+    p.k = lin_tensor(k, s->dtype, s->d_k, s->k_stride_b, s->k_stride_h, 0, s->H / s->Hk);
+    p.v = lin_tensor(v, s->dtype, s->d_v, s->v_stride_b, s->v_stride_h, 0, 1);
     p.log_alpha = log_alpha;
     p.lsb = s->per_head ? 0 : s->a_stride_b;
     p.lsh = s->per_head ? 1 : s->a_stride_h;
@@ -325,10 +328,10 @@ gdn_status gdn_lin_bwd(const gdn_lin_shape* s, const void* dO, const void* q, co
     if (st != GDN_OK) return st;
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    const LinTensor tq = lin_tensor(q, s->dtype, s->q_stride_b, s->q_stride_h, s->q_stride_t, s->H / s->Hq),
-                    tk = lin_tensor(k, s->dtype, s->k_stride_b, s->k_stride_h, s->k_stride_t, s->H / s->Hk),
-                    tv = lin_tensor(v, s->dtype, s->v_stride_b, s->v_stride_h, s->v_stride_t, 1),
-                    td = lin_tensor(dO, s->dtype, (int64_t)s->H * s->T * s->d_v, (int64_t)s->T * s->d_v, s->d_v, 1);
+    const LinTensor tq = lin_tensor(q, s->dtype, s->d_k, s->q_stride_b, s->q_stride_h, s->q_stride_t, s->H / s->Hq),
+                    tk = lin_tensor(k, s->dtype, s->d_k, s->k_stride_b, s->k_stride_h, s->k_stride_t, s->H / s->Hk),
+                    tv = lin_tensor(v, s->dtype, s->d_v, s->v_stride_b, s->v_stride_h, s->v_stride_t, 1),
+                    td = lin_tensor(dO, s->dtype, s->d_v, (int64_t)s->H * s->T * s->d_v, (int64_t)s->T * s->d_v, s->d_v, 1);
     LinParams p = lin_params(*s, pl, log_alpha, lens, ws);
     if (pl.nseg > 1) lin_segments(p, *s, tq, tk, tv, &td, S0, dS_final, hs);
     const float* carry = pl.nseg > 1 ? p.seg_sum : nullptr;

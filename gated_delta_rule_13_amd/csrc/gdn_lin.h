@@ -35,6 +35,7 @@ struct LinTensor {
     int64_t sb, sh, st;     // elements between sequences, heads, tokens
     int rep;                // heads of values to one of its heads
     int wide;               // rows of 16-byte pieces
+    int direct;             // and whole ones, near enough to go straight to LDS
 };
 
 // One pass: rows a, b of nk numbers, c (and x) of nv.
@@ -214,20 +215,95 @@ __device__ __forceinline__ void lin_stage(lds_char* tile, const char* src, int64
     }
 }
 
+// Rows straight from memory into LDS: lane l of a wave writes 16 bytes (or 4) at
+// `to` + 16 l.  The compiler knows nothing of these loads: lin_wait counts them.
+// (M0, which holds the place, is no register that it keeps anything in.)
+__device__ __forceinline__ void lin_direct16(uint32_t to, uint32_t off, const char* base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void lin_direct4(uint32_t to, const char* from) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
+}
+// All waves: at most N of this wave's memory operations left under way (they end
+// in order), its LDS writes done.
+template <int N>
+__device__ __forceinline__ void lin_wait() {
+    static_assert(N < 64, "");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+// Where this lane's pieces of a tile of C rows lie in memory (bytes from its
+// first row) and whether they are inside the row.
+template <bool BF, int ROWB, int C>
+struct LinDirect {
+    // (kSure: those that every wave makes)
+    static constexpr int kPieces = ROWB / 16, kSure = C * kPieces / kLinThreads, kLoads = (C * kPieces + kLinThreads - 1) / kLinThreads;
+    uint32_t off[kLoads];
+    uint32_t in;
+    __device__ __forceinline__ void set(int64_t stride, int cols, int wave, int lane) {
+        in = 0;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const int i = (k * (kLinThreads / 64) + wave) * 64 + lane, r = i / kPieces;
+            const int q = (i % kPieces) ^ lin_turn<ROWB>(r);
+            off[k] = (uint32_t)((int64_t)r * stride * (BF ? 2 : 4)) + q * 16;
+            if (i < C * kPieces && q * (BF ? 8 : 4) < cols) in |= 1u << k;
+        }
+    }
+    __device__ __forceinline__ void load(uint32_t tile, const char* rows, int wave) const {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            if (in & (1u << k)) lin_direct16(tile + (k * (kLinThreads / 64) + wave) * 1024, off[k], rows);
+    }
+};
+
+// Inclusive sums over the first C lanes in 64 bits.
+template <int N>
+__device__ __forceinline__ double lin_row_shr(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, 0x110 + N, 0xf, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), 0x110 + N, 0xf, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lin_lane(double x, int l) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, l), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lin_scan(double x, int lane) {
+    x += lin_row_shr<1>(x);
+    x += lin_row_shr<2>(x);
+    x += lin_row_shr<4>(x);
+    x += lin_row_shr<8>(x);
+    const double a = lin_lane(x, 15), b = a + lin_lane(x, 31), c = b + lin_lane(x, 47);
+    const int row = lane >> 4;
+    return x + (row == 0 ? 0. : row == 1 ? a : row == 2 ? b : c);
+}
+
+// LDS of a pass.  kStages chunks of rows: the one at work and those under way.
 template <bool BF, int NK, int C, int MODE>
 struct LinPlan {
     static constexpr bool kOut = MODE < kLinSum, kGrad = MODE == kLinDq || MODE == kLinDk;
     static constexpr int kEl = BF ? 2 : 4;
     static constexpr int kRowA = NK * kEl, kRowC = kLinTile * kEl;
+    // the state as an operand: bf16 numbers that add up to it (three where the
+    // decay's gradient is summed over many chunks), or fp32
+    static constexpr int kParts = BF ? (kGrad ? 3 : 2) : 1;
+    static constexpr int kStateBytes = kParts * kLinTile * kRowA;
     static constexpr int kA = 0;
     static constexpr int kB = kA + (kOut ? C * kRowA : 0);
     static constexpr int kC = kB + C * kRowA;
     static constexpr int kX = kC + C * kRowC;
-    static constexpr int kVec = kX + (kGrad ? C * kRowC : 0);       // Gh, Gl, out factor, state factor
-    static constexpr int kSums = kVec + 4 * C * 4;                  // rows, columns of each row tile, x of each column tile
-    static constexpr int kState = (kSums + (kGrad ? (1 + C / 16 + 2) * C * 4 : 0) + 255) / 256 * 256;
-    static constexpr int kStateBytes = kLinTile * NK * 4;           // bf16 pairs, or fp32
-    static constexpr int kBytes = kState + (kOut ? 2 * kStateBytes : 0);
+    static constexpr int kStageBytes = kX + (kGrad ? C * kRowC : 0);
+    static constexpr int kVec = 0;                                  // of two chunks: Gh, Gl, out factor, state factor
+    static constexpr int kLog = kVec + 2 * 4 * C * 4;               // log_alpha of four chunks
+    static constexpr int kSums = kLog + 4 * 64 * 4;                 // of two: rows, columns of each row tile, x of each column tile
+    static constexpr int kSumBytes = kGrad ? (1 + C / 16 + 2) * C * 4 : 0;
+    static constexpr int kState = (kSums + 2 * kSumBytes + 255) / 256 * 256;
+    static constexpr int kStage = kState + (kOut ? 2 * kStateBytes : 0);
+    static constexpr int kRoom = 160 * 1024 - kStage;
+    static constexpr int kStages = kRoom >= 3 * kStageBytes ? 3 : kRoom >= 2 * kStageBytes ? 2 : 1;
+    static constexpr int kBytes = kStage + kStages * kStageBytes;
+    static_assert(kBytes <= 160 * 1024, "");
 };
 
 // Sum over lanes 16 g + n of all g, in each.
@@ -262,7 +338,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     const char* pa = L::kOut ? head(R.a, 0) : nullptr;
     const char* pb = head(R.b, 0);
     const char* pc = head(R.c, col0);
-    const char* px = L::kGrad && R.x.p ? head(R.x, col0) : nullptr;
+    const char* px = L::kGrad ? head(R.x, col0) : nullptr;
     const float* la = p.log_alpha ? p.log_alpha + b * p.lsb + h * p.lsh : nullptr;
     const float pscale = kRev ? p.scale : 1.f, oscale = kRev ? 1.f : p.scale;
 
@@ -290,11 +366,14 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         for (int t = 0; t < KT; ++t) {
             const int row = nvt * 16 + n;
             if constexpr (BF) {
-                const bf16x4 hi = __builtin_convertvector(S[t], bf16x4);
-                const bf16x4 lo = __builtin_convertvector(S[t] - __builtin_convertvector(hi, f32x4), bf16x4);
                 const int off = lin_piece<L::kRowA>(row, 2 * (kt0 + t) + (g >> 1)) + (g & 1) * 8;
-                lds_put(at + off, hi);
-                lds_put(at + kLinTile * L::kRowA + off, lo);
+                f32x4 x = S[t];
+#pragma unroll
+                for (int k = 0; k < L::kParts; ++k) {
+                    const bf16x4 part = __builtin_convertvector(x, bf16x4);
+                    lds_put(at + k * kLinTile * L::kRowA + off, part);
+                    if (k + 1 < L::kParts) x -= __builtin_convertvector(part, f32x4);
+                }
             } else {
                 lds_put(at + lin_piece<L::kRowA>(row, 4 * (kt0 + t) + g), S[t]);
             }
@@ -305,10 +384,10 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     const int rt = RT == 4 ? wave : wave >> 1, ct0 = RT == 4 ? 0 : wave & 1;
 
     // what the last chunk left for the decay's gradient
-    auto emit = [&](int ch) __attribute__((always_inline)) {
+    auto emit = [&](int ch, int buf) __attribute__((always_inline)) {
         if constexpr (L::kGrad) {
             if (!R.sum_x || wave != 1) return;
-            lds_char* sums = lds + L::kSums;
+            lds_char* sums = lds + L::kSums + buf * L::kSumBytes;
             const int t = t0 + ch * C + lane;
             float w = 0.f, x = 0.f;
             if (lane < C) {
@@ -335,38 +414,103 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         }
     };
 
-    for (int it = 0; it < chunks; ++it) {
-        const int ch = kRev ? chunks - 1 - it : it, tc = t0 + ch * C, rows = tl - tc < C ? tl - tc : C;
-        __syncthreads();
-        if (it > 0) emit(kRev ? ch + 1 : ch - 1);
-        if constexpr (L::kOut) lin_stage<BF, L::kRowA, C>(lds + L::kA, pa + tc * R.a.st * EB, R.a.st, rows, R.nk, R.a.wide);
-        lin_stage<BF, L::kRowA, C>(lds + L::kB, pb + tc * R.b.st * EB, R.b.st, rows, R.nk, R.b.wide);
-        lin_stage<BF, L::kRowC, C>(lds + L::kC, pc + tc * R.c.st * EB, R.c.st, rows, cols, R.c.wide);
-        if constexpr (L::kGrad) {
-            if (px) lin_stage<BF, L::kRowC, C>(lds + L::kX, px + tc * R.x.st * EB, R.x.st, rows, cols, R.x.wide);
+    // Rows of chunk number `it` into its stage, and its log_alpha, a chunk
+    // earlier; `full`: straight to LDS, which keeps kLoads loads under way.
+    constexpr int kStages = L::kStages, kAhead = kStages - 1;
+    constexpr int kLoads = (L::kOut ? 2 : 1) * LinDirect<BF, L::kRowA, C>::kSure + (L::kGrad ? 2 : 1) * LinDirect<BF, L::kRowC, C>::kSure;
+    const bool direct = kAhead > 0 && R.b.direct && R.c.direct && (!L::kOut || R.a.direct) && (!L::kGrad || R.x.direct) && cols % (16 / EB) == 0;
+    LinDirect<BF, L::kRowA, C> da, db;
+    LinDirect<BF, L::kRowC, C> dc, dx;
+    if (direct) {
+        if constexpr (L::kOut) da.set(R.a.st, R.nk, wave, lane);
+        db.set(R.b.st, R.nk, wave, lane);
+        dc.set(R.c.st, cols, wave, lane);
+        if constexpr (L::kGrad) dx.set(R.x.st, cols, wave, lane);
+        // (pieces behind a row's end are not written again)
+        if (R.nk < NK || cols < kLinTile) {
+            for (int i = threadIdx.x; i < kStages * L::kStageBytes / 16; i += kLinThreads)
+                lds_put(lds + L::kStage + i * 16, u32x4{0, 0, 0, 0});
+            __syncthreads();
         }
-        if (wave == 0) {
-            float l = la && lane < rows ? la[(tc + lane) * p.lst] * kLog2e : 0.f;
-            l = l < -kLinFloor ? -kLinFloor : l;    // (NaN stays)
-            double G = l;
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+    auto number = [&](int it) __attribute__((always_inline)) { return kRev ? chunks - 1 - it : it; };
+    auto is_full = [&](int it) __attribute__((always_inline)) { return direct && it < chunks && t0 + (number(it) + 1) * C <= tl; };
+    constexpr int kVecWave = kRev ? 3 : 0;      // (the wave with the fewest products)
+    auto load_log = [&](int it) __attribute__((always_inline)) {
+        if (wave == kVecWave && la && it < chunks) {
+            const int t = t0 + number(it) * C + lane;
+            if (lane < C && t < tl) lin_direct4(lds0 + L::kLog + (it & 3) * 256, reinterpret_cast<const char*>(la + t * p.lst));
+        }
+    };
+    auto load = [&](int it) __attribute__((always_inline)) {
+        if (it >= chunks) return;
+        const int tc = t0 + number(it) * C, rows = tl - tc < C ? tl - tc : C;
+        const int stage = L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes;
+        const char *ra = L::kOut ? pa + tc * R.a.st * EB : nullptr, *rb = pb + tc * R.b.st * EB, *rc = pc + tc * R.c.st * EB;
+        const char* rx = L::kGrad ? px + tc * R.x.st * EB : nullptr;
+        if (direct && rows == C) {
+            if constexpr (L::kOut) da.load(lds0 + stage + L::kA, ra, wave);
+            db.load(lds0 + stage + L::kB, rb, wave);
+            dc.load(lds0 + stage + L::kC, rc, wave);
+            if constexpr (L::kGrad) dx.load(lds0 + stage + L::kX, rx, wave);
+        } else {
+            if constexpr (L::kOut) lin_stage<BF, L::kRowA, C>(lds + stage + L::kA, ra, R.a.st, rows, R.nk, R.a.wide);
+            lin_stage<BF, L::kRowA, C>(lds + stage + L::kB, rb, R.b.st, rows, R.nk, R.b.wide);
+            lin_stage<BF, L::kRowC, C>(lds + stage + L::kC, rc, R.c.st, rows, cols, R.c.wide);
+            if constexpr (L::kGrad) lin_stage<BF, L::kRowC, C>(lds + stage + L::kX, rx, R.x.st, rows, cols, R.x.wide);
+        }
+    };
+    // the decays of chunk number `it`
+    auto vectors = [&](int it) __attribute__((always_inline)) {
+        if (wave != kVecWave || it >= chunks) return;
+        const int rows = tl - (t0 + number(it) * C);
+        float l = la && lane < rows && lane < C ? lds_get<float>(lds + L::kLog + (it & 3) * 256 + lane * 4) * kLog2e : 0.f;
+        l = l < -kLinFloor ? -kLinFloor : l;    // (NaN stays)
+        const double G = lin_scan(l, lane), end = lin_lane(G, C - 1);
+        if (lane < C) {
+            lds_char* v = lds + L::kVec + (it & 1) * 4 * C * 4 + lane * 4;
+            const float gh = (float)G;
+            const float from = exp2_hw(gh), to = exp2_hw((float)(end - G));
+            lds_put(v, gh);
+            lds_put(v + C * 4, (float)(G - gh));
+            lds_put(v + 2 * C * 4, kRev ? to : from);
+            lds_put(v + 3 * C * 4, kRev ? from * p.scale : to);
+        }
+    };
+    // Stores of a chunk's rows that are sure to come from every wave.
+    const bool whole_rows = L::kOut && R.out_wide && cols == kLinTile;
+    load_log(0);
+    load_log(1);
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const double o = __shfl_up(G, d);
-                if (lane >= d) G += o;
-            }
-            const double end = __shfl(G, C - 1);
-            if (lane < C) {
-                lds_char* v = lds + L::kVec + lane * 4;
-                const float gh = (float)G;
-                const float from = exp2_hw(gh), to = exp2_hw((float)(end - G));
-                lds_put(v, gh);
-                lds_put(v + C * 4, (float)(G - gh));
-                lds_put(v + 2 * C * 4, kRev ? to : from);
-                lds_put(v + 3 * C * 4, kRev ? from * p.scale : to);
-            }
+    for (int i = 0; i < kAhead; ++i) {
+        load(i);
+        if (i + 1 < kAhead || kAhead == 1) load_log(i + 2);
+    }
+    lin_wait<0>();
+    vectors(0);
+    for (int it = 0; it < chunks; ++it) {
+        const int ch = number(it), tc = t0 + ch * C;
+        // what chunk `it` needs has come; what was asked for since may be under
+        // way, and the stores of the chunk before
+        if constexpr (kAhead == 0) {
+            lin_wait<0>();
+            load(it);
+            load_log(it + 1);
+            lin_wait<0>();
+        } else {
+            const bool ahead = kAhead == 1 || is_full(it + kAhead - 1);
+            if (!ahead || it == 0) lin_wait<0>();
+            else if (whole_rows && is_full(it - 1)) lin_wait<(kAhead - 1) * kLoads + CT>();
+            else lin_wait<(kAhead - 1) * kLoads>();
+            load_log(it + kAhead + 1);
+            load(it + kAhead);
         }
-        __syncthreads();
-        const lds_char* vec = lds + L::kVec;
+        if (it > 0) emit(number(it - 1), (it - 1) & 1);
+        vectors(it + 1);
+        const lds_char* rows_at = lds + L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes;
+        const lds_char* vec = lds + L::kVec + (it & 1) * 4 * C * 4;
+        lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
         const float gend = lds_get<float>(vec + (C - 1) * 4);
         total += gend;
         if constexpr (L::kOut) {
@@ -374,15 +518,16 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             LinFrag<BF> fa[KS];
             f32x4 acc[CT];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) fa[ks] = lin_rows<BF, L::kRowA>(lds + L::kA, rt * 16, ks, n, g);
+            for (int ks = 0; ks < KS; ++ks) fa[ks] = lin_rows<BF, L::kRowA>(rows_at + L::kA, rt * 16, ks, n, g);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 acc[c] = zero4();
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     acc[c] = lin_mma(lin_rows<BF, L::kRowA>(st, (ct0 + c) * 16, ks, n, g), fa[ks], acc[c]);
-                    if constexpr (BF)
-                        acc[c] = lin_mma(lin_rows<BF, L::kRowA>(st + kLinTile * L::kRowA, (ct0 + c) * 16, ks, n, g), fa[ks], acc[c]);
+#pragma unroll
+                    for (int k = 1; k < L::kParts; ++k)
+                        acc[c] = lin_mma(lin_rows<BF, L::kRowA>(st + k * kLinTile * L::kRowA, (ct0 + c) * 16, ks, n, g), fa[ks], acc[c]);
                 }
             }
             const int row = rt * 16 + n;
@@ -398,14 +543,14 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int col = (ct0 + c) * 16 + 4 * g + j;
-                            const lds_char* at = lds + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
+                            const lds_char* at = rows_at + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
                             float x;
                             if constexpr (BF) x = (float)lds_get<__bf16>(at);
                             else x = lds_get<float>(at);
                             sums_x = fmaf(acc[c][j], x, sums_x);
                         }
                     sums_x = lin_sum_groups(sums_x) * oscale;
-                    if (g == 0) lds_put(lds + L::kSums + ((1 + RT + ct0) * C + row) * 4, sums_x);
+                    if (g == 0) lds_put(sums + ((1 + RT + ct0) * C + row) * 4, sums_x);
                 }
             }
 #pragma unroll
@@ -415,7 +560,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 if (kRev ? 2 * m + 1 < rt : 2 * m > rt) {
                     if constexpr (MODE == kLinDq) {
                         if (R.sum_x && ct0 == 0)
-                            for (int i = lane; i < 32; i += 64) lds_put(lds + L::kSums + ((1 + rt) * C + 32 * m + i) * 4, 0.f);
+                            for (int i = lane; i < 32; i += 64) lds_put(sums + ((1 + rt) * C + 32 * m + i) * 4, 0.f);
                     }
                     continue;
                 }
@@ -427,7 +572,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                     f32x4 pr = zero4();
                     if (some) {
 #pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) pr = lin_mma(lin_rows<BF, L::kRowA>(lds + L::kB, i0, ks, n, g), fa[ks], pr);
+                        for (int ks = 0; ks < KS; ++ks) pr = lin_mma(lin_rows<BF, L::kRowA>(rows_at + L::kB, i0, ks, n, g), fa[ks], pr);
                         const f32x4 ih = lds_get<f32x4>(vec + col * 4), il = lds_get<f32x4>(vec + (C + col) * 4);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -442,27 +587,27 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                         if (R.sum_x) {
                             f32x4 other = zero4();
                             if (some) {
-                                const LinFrag<BF> fx = lin_rows<BF, L::kRowC>(lds + L::kX, rt * 16, 0, n, g);
-                                other = lin_mma(lin_rows<BF, L::kRowC>(lds + L::kC, i0, 0, n, g), fx, other);
+                                const LinFrag<BF> fx = lin_rows<BF, L::kRowC>(rows_at + L::kX, rt * 16, 0, n, g);
+                                other = lin_mma(lin_rows<BF, L::kRowC>(rows_at + L::kC, i0, 0, n, g), fx, other);
                             }
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const float mm = some && col + j < row ? other[j] * pr[j] * oscale : 0.f;
                                 sums_w += mm;
                                 const float down = lanes_sum<16>(mm);
-                                if (n == 0 && ct0 == 0) lds_put(lds + L::kSums + ((1 + rt) * C + col + j) * 4, down);
+                                if (n == 0 && ct0 == 0) lds_put(sums + ((1 + rt) * C + col + j) * 4, down);
                             }
                         }
                     }
                 }
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
-                    acc[c] = lin_mma(lin_cols<BF, L::kRowC>(lds + L::kC, m, (ct0 + c) * 16, n, g), pp, acc[c]);
+                    acc[c] = lin_mma(lin_cols<BF, L::kRowC>(rows_at + L::kC, m, (ct0 + c) * 16, n, g), pp, acc[c]);
             }
             if constexpr (MODE == kLinDq) {
                 if (R.sum_x) {
                     sums_w = lin_sum_groups(sums_w);
-                    if (g == 0 && ct0 == 0) lds_put(lds + L::kSums + row * 4, sums_w);
+                    if (g == 0 && ct0 == 0) lds_put(sums + row * 4, sums_w);
                 }
             }
             // (rows behind the sequence's end inside its last chunk are 0)
@@ -495,7 +640,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         for (int t = 0; t < KT; ++t) S[t] *= whole;
 #pragma unroll
         for (int m = 0; m < C / 32; ++m) {
-            const LinFrag<BF> raw = lin_cols<BF, L::kRowC>(lds + L::kC, m, nvt * 16, n, g);
+            const LinFrag<BF> raw = lin_cols<BF, L::kRowC>(rows_at + L::kC, m, nvt * 16, n, g);
             const f32x4 u0 = lds_get<f32x4>(vec + (3 * C + 32 * m + 4 * g) * 4);
             const f32x4 u1 = lds_get<f32x4>(vec + (3 * C + 32 * m + 16 + 4 * g) * 4);
             LinSplit<BF, 3> fc;
@@ -505,13 +650,13 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 fc.set(j + 4, raw.get(j + 4) * u1[j]);
             }
 #pragma unroll
-            for (int t = 0; t < KT; ++t) S[t] = lin_mma(lin_cols<BF, L::kRowA>(lds + L::kB, m, (kt0 + t) * 16, n, g), fc, S[t]);
+            for (int t = 0; t < KT; ++t) S[t] = lin_mma(lin_cols<BF, L::kRowA>(rows_at + L::kB, m, (kt0 + t) * 16, n, g), fc, S[t]);
         }
         if constexpr (L::kOut) publish((it + 1) & 1);
     }
     if constexpr (L::kGrad) {
         __syncthreads();
-        if (chunks > 0) emit(kRev ? 0 : chunks - 1);
+        if (chunks > 0) emit(number(chunks - 1), (chunks - 1) & 1);
     }
     if constexpr (L::kOut) {
         // rows behind the last chunk
@@ -565,13 +710,20 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 enum LinSet { kLinSetFwd, kLinSetQk, kLinSetV, kLinSetAll, kLinSetSum, kLinSetSums };
 constexpr int kXcds = 8;
 
+constexpr int lin_most(int a, int b) { return a > b ? a : b; }
+// LDS of a launch: the most that one of its passes takes.
 template <bool BF, int NK, int SET>
 struct LinBytes {
     static constexpr int C = lin_chunk(BF, NK);
     static constexpr int kGrad = LinPlan<BF, NK, C, kLinDq>::kBytes;
-    static constexpr int kFwd = LinPlan<BF, NK, C, kLinFwd>::kBytes;
+    static constexpr int kRows = LinPlan<BF, NK, C, kLinFwd>::kBytes;
     static constexpr int kSum = LinPlan<BF, NK, C, kLinSum>::kBytes;
-    static constexpr int value = SET == kLinSetFwd || SET == kLinSetV ? kFwd : SET == kLinSetSum || SET == kLinSetSums ? kSum : kGrad;
+    static constexpr int value = SET == kLinSetFwd || SET == kLinSetV     ? kRows
+                                 : SET == kLinSetSum || SET == kLinSetSums ? kSum
+                                 : SET == kLinSetQk                        ? kGrad
+                                                                           : lin_most(kGrad, kRows);
+    static_assert(kGrad == LinPlan<BF, NK, C, kLinDk>::kBytes && kRows == LinPlan<BF, NK, C, kLinDv>::kBytes, "");
+    static_assert(kSum == LinPlan<BF, NK, C, kLinSumD>::kBytes, "");
 };
 
 template <bool BF, int NK, int SET>

@@ -108,6 +108,23 @@ def test_segments(dtype, T, decay):
     check_gradient(a, dO, dS, gdn.gdn_lin_bwd(dO.cuda(), **ref.dev(a), dS_final=dS.cuda(), scale=SCALE))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv,lens", [(32, 32, None), (64, 64, [400, 321]), (96, 96, [399, 256]), (128, 128, None), (256, 256, [385, 400]),
+                                        (128, 64, [193, 400]), (64, 256, None), (256, 96, None), (104, 40, None), (16, 128, None)])
+def test_many_chunks(dtype, dk, dv, lens):
+    """More chunks than LDS holds at once, in every built size of rows."""
+    say(f"case: lin chunks {dtype} {dk}x{dv}")
+    T = 400
+    a = inputs(2, 2, 2, 2, T, dk, dv, dtype, dk + dv, "token", True, lens)
+    w = ref.wide(a)
+    O, S = gdn.gdn_lin_fwd(**ref.dev(a), scale=SCALE)
+    (wo, ws), (bo, bs) = mix.lin(**w, scale=SCALE), mix.lin_bound(w, scale=SCALE)
+    mix.within("O", O, wo, bo)
+    mix.within("S", S, ws, bs)
+    dO, dS = ref.rand(ref.gen(1), 2, 2, T, dv, dtype=dtype), ref.rand(ref.gen(2), 2, 2, dv, dk)
+    check_gradient(a, dO, dS, gdn.gdn_lin_bwd(dO.cuda(), **ref.dev(a), dS_final=dS.cuda(), scale=SCALE))
+
+
 @pytest.mark.parametrize("strong", [1.0, 8.0, 60.0])
 def test_strong_decays(strong):
     """Chunks whose decay spans up to e^-3000: no factor leaves its range, and
