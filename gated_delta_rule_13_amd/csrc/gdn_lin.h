@@ -70,7 +70,10 @@ struct LinParams {
 
 enum LinMode { kLinFwd, kLinDq, kLinDk, kLinDv, kLinSum, kLinSumD };
 
-constexpr int kLinThreads = 256;
+// Four waves form the outputs of a chunk, four others move rows and keep the
+// state: both read the same chunk's rows and the state before it, and run beside
+// each other, two waves to a SIMD.
+constexpr int kLinThreads = 512, kLinMovers = 256;
 constexpr int kLinTile = 32;        // columns of c to a workgroup
 // Tokens to a chunk: as many as let two chunks' rows and two states lie in LDS.
 constexpr int lin_chunk(bool bf16, int nk) { return bf16 && nk <= 128 ? 64 : 32; }
@@ -95,12 +98,12 @@ struct LinFrag;
 template <>
 struct LinFrag<true> {
     bf16x8 v;
-    __device__ __forceinline__ float get(int i) const { return (float)v[i]; }
+    __device__ __forceinline__ f32x8 wide() const { return __builtin_convertvector(v, f32x8); }
 };
 template <>
 struct LinFrag<false> {
     f32x8 v;
-    __device__ __forceinline__ float get(int i) const { return v[i]; }
+    __device__ __forceinline__ f32x8 wide() const { return v; }
 };
 __device__ __forceinline__ f32x4 lin_mma(const LinFrag<true>& a, const LinFrag<true>& b, f32x4 c) { return mfma_bf16(a.v, b.v, c); }
 // (the fp32 unit takes four numbers at a time: one of each lane's eight)
@@ -115,19 +118,18 @@ struct LinSplit;
 template <int N>
 struct LinSplit<true, N> {
     LinFrag<true> part[N];
-    __device__ __forceinline__ void set(int i, float x) {
+    __device__ __forceinline__ void set(f32x8 x) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const __bf16 h = (__bf16)x;
-            part[k].v[i] = h;
-            x -= (float)h;
+            part[k].v = __builtin_convertvector(x, bf16x8);
+            if (k + 1 < N) x -= __builtin_convertvector(part[k].v, f32x8);
         }
     }
 };
 template <int N>
 struct LinSplit<false, N> {
     LinFrag<false> part[1];
-    __device__ __forceinline__ void set(int i, float x) { part[0].v[i] = x; }
+    __device__ __forceinline__ void set(f32x8 x) { part[0].v = x; }
 };
 template <bool BF, int N>
 __device__ __forceinline__ f32x4 lin_mma(const LinFrag<BF>& a, const LinSplit<BF, N>& b, f32x4 c) {
@@ -191,7 +193,7 @@ __device__ __forceinline__ LinFrag<BF> lin_cols(const lds_char* t, int m, int co
 template <bool BF, int ROWB, int C>
 __device__ __forceinline__ void lin_stage(lds_char* tile, const char* src, int64_t stride, int rows, int cols, int wide) {
     constexpr int kEl = BF ? 8 : 4, kPieces = ROWB / 16, kBytes = BF ? 2 : 4;
-    for (int i = threadIdx.x; i < C * kPieces; i += kLinThreads) {
+    for (int i = threadIdx.x % kLinMovers; i < C * kPieces; i += kLinMovers) {
         const int r = i / kPieces, q = i % kPieces, c = q * kEl;
         u32x4 v = {0, 0, 0, 0};
         if (r < rows && c < cols) {
@@ -215,7 +217,7 @@ __device__ __forceinline__ void lin_stage(lds_char* tile, const char* src, int64
     }
 }
 
-// Rows straight from memory into LDS: lane l of a wave writes 16 bytes (or 4) at
+// Rows straight from memory into LDS, which the movers do: lane l of a wave writes 16 bytes (or 4) at
 // `to` + 16 l.  The compiler knows nothing of these loads: lin_wait counts them.
 // (M0, which holds the place, is no register that it keeps anything in.)
 __device__ __forceinline__ void lin_direct16(uint32_t to, uint32_t off, const char* base) {
@@ -231,19 +233,21 @@ __device__ __forceinline__ void lin_wait() {
     static_assert(N < 64, "");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
+// The same for waves that wait for no loads.
+__device__ __forceinline__ void lin_wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 // Where this lane's pieces of a tile of C rows lie in memory (bytes from its
 // first row) and whether they are inside the row.
 template <bool BF, int ROWB, int C>
 struct LinDirect {
     // (kSure: those that every wave makes)
-    static constexpr int kPieces = ROWB / 16, kSure = C * kPieces / kLinThreads, kLoads = (C * kPieces + kLinThreads - 1) / kLinThreads;
+    static constexpr int kPieces = ROWB / 16, kSure = C * kPieces / kLinMovers, kLoads = (C * kPieces + kLinMovers - 1) / kLinMovers;
     uint32_t off[kLoads];
     uint32_t in;
     __device__ __forceinline__ void set(int64_t stride, int cols, int wave, int lane) {
         in = 0;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
-            const int i = (k * (kLinThreads / 64) + wave) * 64 + lane, r = i / kPieces;
+            const int i = (k * (kLinMovers / 64) + wave) * 64 + lane, r = i / kPieces;
             const int q = (i % kPieces) ^ lin_turn<ROWB>(r);
             off[k] = (uint32_t)((int64_t)r * stride * (BF ? 2 : 4)) + q * 16;
             if (i < C * kPieces && q * (BF ? 8 : 4) < cols) in |= 1u << k;
@@ -252,7 +256,7 @@ struct LinDirect {
     __device__ __forceinline__ void load(uint32_t tile, const char* rows, int wave) const {
 #pragma unroll
         for (int k = 0; k < kLoads; ++k)
-            if (in & (1u << k)) lin_direct16(tile + (k * (kLinThreads / 64) + wave) * 1024, off[k], rows);
+            if (in & (1u << k)) lin_direct16(tile + (k * (kLinMovers / 64) + wave) * 1024, off[k], rows);
     }
 };
 
@@ -288,6 +292,7 @@ struct LinPlan {
     // the state as an operand: bf16 numbers that add up to it (three where the
     // decay's gradient is summed over many chunks), or fp32
     static constexpr int kParts = BF ? (kGrad ? 3 : 2) : 1;
+    static constexpr int kValueParts = 3;                           // decayed values, whose sums the state is
     static constexpr int kStateBytes = kParts * kLinTile * kRowA;
     static constexpr int kA = 0;
     static constexpr int kB = kA + (kOut ? C * kRowA : 0);
@@ -322,7 +327,8 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     constexpr int KS = NK / 32, KT = NK / 32;       // steps over nk; state tiles of a wave
     constexpr int EB = L::kEl;
     lds_char* lds = (lds_char*)shared;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3;
+    const bool mover = wave8 >= 4;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int64_t bh = unit / p.nseg;
     const int seg = (int)(unit % p.nseg);
@@ -332,63 +338,220 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     tl = tl < t0 ? t0 : (tl > t1 ? t1 : tl);
     const int chunks = (tl - t0 + C - 1) / C;
     const int col0 = tile * kLinTile, cols = R.nv - col0 < kLinTile ? R.nv - col0 : kLinTile;
-    auto head = [&](const LinTensor& x, int c) __attribute__((always_inline)) {
-        return reinterpret_cast<const char*>(x.p) + (b * x.sb + (h / x.rep) * x.sh + c) * EB;
-    };
-    const char* pa = L::kOut ? head(R.a, 0) : nullptr;
-    const char* pb = head(R.b, 0);
-    const char* pc = head(R.c, col0);
-    const char* px = L::kGrad ? head(R.x, col0) : nullptr;
-    const float* la = p.log_alpha ? p.log_alpha + b * p.lsb + h * p.lsh : nullptr;
-    const float pscale = kRev ? p.scale : 1.f, oscale = kRev ? 1.f : p.scale;
-
-    // The state, rows nk and columns nv: this wave's tiles are KT rows of tiles
-    // from kt0 and one column of tiles.
-    const int nvt = wave & 1, kt0 = (wave >> 1) * KT;
+    constexpr int kStages = L::kStages, kAhead = kStages - 1;
+    auto number = [&](int it) __attribute__((always_inline)) { return kRev ? chunks - 1 - it : it; };
     const int64_t plane = (int64_t)p.dk * p.dv;
-    const int64_t sn = kTurned ? 1 : p.dk, sk = kTurned ? p.dk : 1;
-    const int scol = col0 + nvt * 16 + n;
-    f32x4 S[KT];
-    {
-        const float* from = nullptr;
-        if constexpr (L::kOut) from = R.carry ? R.carry + unit * plane : R.first ? R.first + bh * plane : nullptr;
+    const int64_t part = tile * (int64_t)p.B * p.H + bh;            // (rows of the partial sums)
+
+    if (mover) {
+        auto head = [&](const LinTensor& x, int c) __attribute__((always_inline)) {
+            return reinterpret_cast<const char*>(x.p) + (b * x.sb + (h / x.rep) * x.sh + c) * EB;
+        };
+        const char* pa = L::kOut ? head(R.a, 0) : nullptr;
+        const char* pb = head(R.b, 0);
+        const char* pc = head(R.c, col0);
+        const char* px = L::kGrad ? head(R.x, col0) : nullptr;
+        const float* la = p.log_alpha ? p.log_alpha + b * p.lsb + h * p.lsh : nullptr;
+
+        // The state, rows nk and columns nv: this wave's tiles are KT rows of
+        // tiles from kt0 and one column of tiles.
+        const int nvt = wave & 1, kt0 = (wave >> 1) * KT;
+        const int64_t sn = kTurned ? 1 : p.dk, sk = kTurned ? p.dk : 1;
+        const int scol = col0 + nvt * 16 + n;
+        f32x4 S[KT];
+        {
+            const float* from = nullptr;
+            if constexpr (L::kOut) from = R.carry ? R.carry + unit * plane : R.first ? R.first + bh * plane : nullptr;
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = (kt0 + t) * 16 + 4 * g + j;
+                    S[t][j] = from && k < R.nk && scol < R.nv ? from[k * sk + scol * sn] : 0.f;
+                }
+        }
+        auto publish = [&](int buf) __attribute__((always_inline)) {
+            lds_char* at = lds + L::kState + buf * L::kStateBytes;
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                const int row = nvt * 16 + n;
+                if constexpr (BF) {
+                    const int off = lin_piece<L::kRowA>(row, 2 * (kt0 + t) + (g >> 1)) + (g & 1) * 8;
+                    f32x4 x = S[t];
+#pragma unroll
+                    for (int k = 0; k < L::kParts; ++k) {
+                        const bf16x4 part4 = __builtin_convertvector(x, bf16x4);
+                        lds_put(at + k * kLinTile * L::kRowA + off, part4);
+                        if (k + 1 < L::kParts) x -= __builtin_convertvector(part4, f32x4);
+                    }
+                } else {
+                    lds_put(at + lin_piece<L::kRowA>(row, 4 * (kt0 + t) + g), S[t]);
+                }
+            }
+        };
+        // Rows of chunk number `it` into its stage, and its log_alpha, a chunk
+        // earlier.  A whole chunk goes straight to LDS and keeps kLoads loads of
+        // each wave under way.
+        constexpr int kLoads = (L::kOut ? 2 : 1) * LinDirect<BF, L::kRowA, C>::kSure + (L::kGrad ? 2 : 1) * LinDirect<BF, L::kRowC, C>::kSure;
+        const bool direct = kAhead > 0 && R.b.direct && R.c.direct && (!L::kOut || R.a.direct) && (!L::kGrad || R.x.direct) && cols % (16 / EB) == 0;
+        LinDirect<BF, L::kRowA, C> da, db;
+        LinDirect<BF, L::kRowC, C> dc, dx;
+        if (direct) {
+            if constexpr (L::kOut) da.set(R.a.st, R.nk, wave, lane);
+            db.set(R.b.st, R.nk, wave, lane);
+            dc.set(R.c.st, cols, wave, lane);
+            if constexpr (L::kGrad) dx.set(R.x.st, cols, wave, lane);
+        }
+        const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+        auto is_full = [&](int it) __attribute__((always_inline)) { return direct && it < chunks && t0 + (number(it) + 1) * C <= tl; };
+        auto load_log = [&](int it) __attribute__((always_inline)) {
+            if (wave == 0 && la && it < chunks) {
+                const int t = t0 + number(it) * C + lane;
+                if (lane < C && t < tl) lin_direct4(lds0 + L::kLog + (it & 3) * 256, reinterpret_cast<const char*>(la + t * p.lst));
+            }
+        };
+        auto load = [&](int it) __attribute__((always_inline)) {
+            if (it >= chunks) return;
+            const int tc = t0 + number(it) * C, rows = tl - tc < C ? tl - tc : C;
+            const int stage = L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes;
+            const char *ra = L::kOut ? pa + tc * R.a.st * EB : nullptr, *rb = pb + tc * R.b.st * EB, *rc = pc + tc * R.c.st * EB;
+            const char* rx = L::kGrad ? px + tc * R.x.st * EB : nullptr;
+            if (direct && rows == C) {
+                if constexpr (L::kOut) da.load(lds0 + stage + L::kA, ra, wave);
+                db.load(lds0 + stage + L::kB, rb, wave);
+                dc.load(lds0 + stage + L::kC, rc, wave);
+                if constexpr (L::kGrad) dx.load(lds0 + stage + L::kX, rx, wave);
+            } else {
+                if constexpr (L::kOut) lin_stage<BF, L::kRowA, C>(lds + stage + L::kA, ra, R.a.st, rows, R.nk, R.a.wide);
+                lin_stage<BF, L::kRowA, C>(lds + stage + L::kB, rb, R.b.st, rows, R.nk, R.b.wide);
+                lin_stage<BF, L::kRowC, C>(lds + stage + L::kC, rc, R.c.st, rows, cols, R.c.wide);
+                if constexpr (L::kGrad) lin_stage<BF, L::kRowC, C>(lds + stage + L::kX, rx, R.x.st, rows, cols, R.x.wide);
+            }
+        };
+        // the decays of chunk number `it`
+        auto vectors = [&](int it) __attribute__((always_inline)) {
+            if (wave != 0 || it >= chunks) return;
+            const int rows = tl - (t0 + number(it) * C);
+            float l = la && lane < rows && lane < C ? lds_get<float>(lds + L::kLog + (it & 3) * 256 + lane * 4) * kLog2e : 0.f;
+            l = l < -kLinFloor ? -kLinFloor : l;    // (NaN stays)
+            const double G = lin_scan(l, lane), end = lin_lane(G, C - 1);
+            if (lane < C) {
+                lds_char* v = lds + L::kVec + (it & 1) * 4 * C * 4 + lane * 4;
+                const float gh = (float)G;
+                const float from = exp2_hw(gh), to = exp2_hw((float)(end - G));
+                lds_put(v, gh);
+                lds_put(v + C * 4, (float)(G - gh));
+                lds_put(v + 2 * C * 4, kRev ? to : from);
+                lds_put(v + 3 * C * 4, kRev ? from * p.scale : to);
+            }
+        };
+        // (pieces behind a row's end are not written again)
+        if (direct && (R.nk < NK || cols < kLinTile)) {
+            for (int i = threadIdx.x % kLinMovers; i < kStages * L::kStageBytes / 16; i += kLinMovers)
+                lds_put(lds + L::kStage + i * 16, u32x4{0, 0, 0, 0});
+        }
+        if constexpr (L::kOut) publish(0);
+        lin_wait<0>();
+        load_log(0);
+        load_log(1);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            load(i);
+            if (i + 1 < kAhead || kAhead == 1) load_log(i + 2);
+        }
+        lin_wait<0>();
+        vectors(0);
+        float total = 0.f;      // log2 of the decay so far
+        for (int it = 0; it < chunks; ++it) {
+            // what chunk `it` needs has come; what was asked for since may be
+            // under way
+            if constexpr (kAhead == 0) {
+                lin_wait<0>();
+                load(it);
+                load_log(it + 1);
+                lin_wait<0>();
+            } else {
+                if (kAhead > 1 && is_full(it + kAhead - 1)) lin_wait<(kAhead - 1) * kLoads>();
+                else lin_wait<0>();
+                load_log(it + kAhead + 1);
+                load(it + kAhead);
+            }
+            vectors(it + 1);
+            const lds_char* rows_at = lds + L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes;
+            const lds_char* vec = lds + L::kVec + (it & 1) * 4 * C * 4;
+            const float gend = lds_get<float>(vec + (C - 1) * 4);
+            total += gend;
+            const float whole = exp2_hw(gend);
+#pragma unroll
+            for (int t = 0; t < KT; ++t) S[t] *= whole;
+#pragma unroll
+            for (int m = 0; m < C / 32; ++m) {
+                const f32x4 u0 = lds_get<f32x4>(vec + (3 * C + 32 * m + 4 * g) * 4);
+                const f32x4 u1 = lds_get<f32x4>(vec + (3 * C + 32 * m + 16 + 4 * g) * 4);
+                LinSplit<BF, L::kValueParts> fc;
+                fc.set(lin_cols<BF, L::kRowC>(rows_at + L::kC, m, nvt * 16, n, g).wide() *
+                       __builtin_shufflevector(u0, u1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+                    S[t] = lin_mma(lin_cols<BF, L::kRowA>(rows_at + L::kB, m, (kt0 + t) * 16, n, g), fc, S[t]);
+            }
+            if constexpr (L::kOut) publish((it + 1) & 1);
+        }
+        // the state at the end
+        float* to = nullptr;
+        if constexpr (MODE == kLinSum) to = p.seg_sum + unit * plane;
+        if constexpr (MODE == kLinSumD) to = p.seg_sum_d + unit * plane;
+        if constexpr (L::kOut) {
+            if (R.last && seg == (kRev ? 0 : p.nseg - 1)) to = R.last + bh * plane;
+        }
+        float share = 0.f;
+        const bool ends = MODE == kLinDq && R.end_share && seg == p.nseg - 1;
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int k = (kt0 + t) * 16 + 4 * g + j;
-                S[t][j] = from && k < R.nk && scol < R.nv ? from[k * sk + scol * sn] : 0.f;
-            }
-    }
-    auto publish = [&](int buf) __attribute__((always_inline)) {
-        lds_char* at = lds + L::kState + buf * L::kStateBytes;
-#pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            const int row = nvt * 16 + n;
-            if constexpr (BF) {
-                const int off = lin_piece<L::kRowA>(row, 2 * (kt0 + t) + (g >> 1)) + (g & 1) * 8;
-                f32x4 x = S[t];
-#pragma unroll
-                for (int k = 0; k < L::kParts; ++k) {
-                    const bf16x4 part = __builtin_convertvector(x, bf16x4);
-                    lds_put(at + k * kLinTile * L::kRowA + off, part);
-                    if (k + 1 < L::kParts) x -= __builtin_convertvector(part, f32x4);
+                if (k < R.nk && scol < R.nv) {
+                    if (to) to[k * sk + scol * sn] = S[t][j];
+                    if (ends) share = fmaf(S[t][j], R.end_grad[bh * plane + k * sk + scol * sn], share);
                 }
-            } else {
-                lds_put(at + lin_piece<L::kRowA>(row, 4 * (kt0 + t) + g), S[t]);
+            }
+        if (MODE == kLinSum && tile == 0 && wave == 0 && lane == 0) p.seg_decay[unit] = total;
+        if constexpr (MODE == kLinDq) {
+            share = lanes_sum<64>(share);
+            if (lane == 0) lds_put(lds + L::kLog + wave * 4, share);
+        }
+        if constexpr (L::kGrad) {
+            __syncthreads();
+            if (ends && wave == 0 && lane == 0) {
+                float s = 0.f;
+                for (int i = 0; i < 4; ++i) s += lds_get<float>(lds + L::kLog + i * 4);
+                R.end_share[part] = s;
             }
         }
-    };
-    if constexpr (L::kOut) publish(0);
-    float total = 0.f;      // log2 of the decay so far
-    const int rt = RT == 4 ? wave : wave >> 1, ct0 = RT == 4 ? 0 : wave & 1;
+        return;
+    }
 
-    // what the last chunk left for the decay's gradient
-    auto emit = [&](int ch, int buf) __attribute__((always_inline)) {
+    // ---- the waves that form the outputs ----
+    if constexpr (!L::kOut) {
+        // (as many barriers as the movers pass)
+        lin_wait_lds();
+        lin_wait_lds();
+        for (int it = 0; it < chunks; ++it) {
+            lin_wait_lds();
+            if constexpr (kAhead == 0) lin_wait_lds();
+        }
+        return;
+    }
+    const float pscale = kRev ? p.scale : 1.f, oscale = kRev ? 1.f : p.scale;
+    const int rt = RT == 4 ? wave : wave >> 1, ct0 = RT == 4 ? 0 : wave & 1;
+    const int row = rt * 16 + n;
+    // what a chunk left for the decay's gradient
+    auto emit = [&](int it) __attribute__((always_inline)) {
         if constexpr (L::kGrad) {
-            if (!R.sum_x || wave != 1) return;
-            lds_char* sums = lds + L::kSums + buf * L::kSumBytes;
-            const int t = t0 + ch * C + lane;
+            if (!R.sum_x || wave != (kRev ? 3 : 0)) return;         // (the wave with the fewest products)
+            const lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
+            const int ch = number(it), t = t0 + ch * C + lane;
             float w = 0.f, x = 0.f;
             if (lane < C) {
                 x = lds_get<float>(sums + ((1 + RT) * C + lane) * 4);
@@ -398,309 +561,147 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 #pragma unroll
                     for (int i = 0; i < RT; ++i) w -= lds_get<float>(sums + ((1 + i) * C + lane) * 4);
                 }
-                const int64_t at = (tile * (int64_t)p.B * p.H + bh) * p.T + t;
                 if (t < tl) {
-                    R.sum_x[at] = x;
-                    if constexpr (MODE == kLinDq) R.sum_w[at] = w;
+                    R.sum_x[part * p.T + t] = x;
+                    if constexpr (MODE == kLinDq) R.sum_w[part * p.T + t] = w;
                 } else {
                     x = 0.f;
                 }
             }
             x = lanes_sum<64>(x);
-            if (lane == 0) {
-                const int64_t per = (p.T + C - 1) / C;
-                R.chunk_x[(tile * (int64_t)p.B * p.H + bh) * per + t0 / C + ch] = x;
-            }
+            if (lane == 0) R.chunk_x[part * ((p.T + C - 1) / C) + t0 / C + ch] = x;
         }
     };
-
-    // Rows of chunk number `it` into its stage, and its log_alpha, a chunk
-    // earlier; `full`: straight to LDS, which keeps kLoads loads under way.
-    constexpr int kStages = L::kStages, kAhead = kStages - 1;
-    constexpr int kLoads = (L::kOut ? 2 : 1) * LinDirect<BF, L::kRowA, C>::kSure + (L::kGrad ? 2 : 1) * LinDirect<BF, L::kRowC, C>::kSure;
-    const bool direct = kAhead > 0 && R.b.direct && R.c.direct && (!L::kOut || R.a.direct) && (!L::kGrad || R.x.direct) && cols % (16 / EB) == 0;
-    LinDirect<BF, L::kRowA, C> da, db;
-    LinDirect<BF, L::kRowC, C> dc, dx;
-    if (direct) {
-        if constexpr (L::kOut) da.set(R.a.st, R.nk, wave, lane);
-        db.set(R.b.st, R.nk, wave, lane);
-        dc.set(R.c.st, cols, wave, lane);
-        if constexpr (L::kGrad) dx.set(R.x.st, cols, wave, lane);
-        // (pieces behind a row's end are not written again)
-        if (R.nk < NK || cols < kLinTile) {
-            for (int i = threadIdx.x; i < kStages * L::kStageBytes / 16; i += kLinThreads)
-                lds_put(lds + L::kStage + i * 16, u32x4{0, 0, 0, 0});
-            __syncthreads();
-        }
-    }
-    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-    auto number = [&](int it) __attribute__((always_inline)) { return kRev ? chunks - 1 - it : it; };
-    auto is_full = [&](int it) __attribute__((always_inline)) { return direct && it < chunks && t0 + (number(it) + 1) * C <= tl; };
-    constexpr int kVecWave = kRev ? 3 : 0;      // (the wave with the fewest products)
-    auto load_log = [&](int it) __attribute__((always_inline)) {
-        if (wave == kVecWave && la && it < chunks) {
-            const int t = t0 + number(it) * C + lane;
-            if (lane < C && t < tl) lin_direct4(lds0 + L::kLog + (it & 3) * 256, reinterpret_cast<const char*>(la + t * p.lst));
-        }
-    };
-    auto load = [&](int it) __attribute__((always_inline)) {
-        if (it >= chunks) return;
-        const int tc = t0 + number(it) * C, rows = tl - tc < C ? tl - tc : C;
-        const int stage = L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes;
-        const char *ra = L::kOut ? pa + tc * R.a.st * EB : nullptr, *rb = pb + tc * R.b.st * EB, *rc = pc + tc * R.c.st * EB;
-        const char* rx = L::kGrad ? px + tc * R.x.st * EB : nullptr;
-        if (direct && rows == C) {
-            if constexpr (L::kOut) da.load(lds0 + stage + L::kA, ra, wave);
-            db.load(lds0 + stage + L::kB, rb, wave);
-            dc.load(lds0 + stage + L::kC, rc, wave);
-            if constexpr (L::kGrad) dx.load(lds0 + stage + L::kX, rx, wave);
-        } else {
-            if constexpr (L::kOut) lin_stage<BF, L::kRowA, C>(lds + stage + L::kA, ra, R.a.st, rows, R.nk, R.a.wide);
-            lin_stage<BF, L::kRowA, C>(lds + stage + L::kB, rb, R.b.st, rows, R.nk, R.b.wide);
-            lin_stage<BF, L::kRowC, C>(lds + stage + L::kC, rc, R.c.st, rows, cols, R.c.wide);
-            if constexpr (L::kGrad) lin_stage<BF, L::kRowC, C>(lds + stage + L::kX, rx, R.x.st, rows, cols, R.x.wide);
-        }
-    };
-    // the decays of chunk number `it`
-    auto vectors = [&](int it) __attribute__((always_inline)) {
-        if (wave != kVecWave || it >= chunks) return;
-        const int rows = tl - (t0 + number(it) * C);
-        float l = la && lane < rows && lane < C ? lds_get<float>(lds + L::kLog + (it & 3) * 256 + lane * 4) * kLog2e : 0.f;
-        l = l < -kLinFloor ? -kLinFloor : l;    // (NaN stays)
-        const double G = lin_scan(l, lane), end = lin_lane(G, C - 1);
-        if (lane < C) {
-            lds_char* v = lds + L::kVec + (it & 1) * 4 * C * 4 + lane * 4;
-            const float gh = (float)G;
-            const float from = exp2_hw(gh), to = exp2_hw((float)(end - G));
-            lds_put(v, gh);
-            lds_put(v + C * 4, (float)(G - gh));
-            lds_put(v + 2 * C * 4, kRev ? to : from);
-            lds_put(v + 3 * C * 4, kRev ? from * p.scale : to);
-        }
-    };
-    // Stores of a chunk's rows that are sure to come from every wave.
-    const bool whole_rows = L::kOut && R.out_wide && cols == kLinTile;
-    load_log(0);
-    load_log(1);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-        load(i);
-        if (i + 1 < kAhead || kAhead == 1) load_log(i + 2);
-    }
-    lin_wait<0>();
-    vectors(0);
+    lin_wait_lds();
+    lin_wait_lds();
     for (int it = 0; it < chunks; ++it) {
-        const int ch = number(it), tc = t0 + ch * C;
-        // what chunk `it` needs has come; what was asked for since may be under
-        // way, and the stores of the chunk before
-        if constexpr (kAhead == 0) {
-            lin_wait<0>();
-            load(it);
-            load_log(it + 1);
-            lin_wait<0>();
-        } else {
-            const bool ahead = kAhead == 1 || is_full(it + kAhead - 1);
-            if (!ahead || it == 0) lin_wait<0>();
-            else if (whole_rows && is_full(it - 1)) lin_wait<(kAhead - 1) * kLoads + CT>();
-            else lin_wait<(kAhead - 1) * kLoads>();
-            load_log(it + kAhead + 1);
-            load(it + kAhead);
-        }
-        if (it > 0) emit(number(it - 1), (it - 1) & 1);
-        vectors(it + 1);
+        const int tc = t0 + number(it) * C;
+        lin_wait_lds();
+        if constexpr (kAhead == 0) lin_wait_lds();
         const lds_char* rows_at = lds + L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes;
         const lds_char* vec = lds + L::kVec + (it & 1) * 4 * C * 4;
+        const lds_char* st = lds + L::kState + (it & 1) * L::kStateBytes;
         lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
-        const float gend = lds_get<float>(vec + (C - 1) * 4);
-        total += gend;
-        if constexpr (L::kOut) {
-            const lds_char* st = lds + L::kState + (it & 1) * L::kStateBytes;
-            LinFrag<BF> fa[KS];
-            f32x4 acc[CT];
+        LinFrag<BF> fa[KS];
+        f32x4 acc[CT];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) fa[ks] = lin_rows<BF, L::kRowA>(rows_at + L::kA, rt * 16, ks, n, g);
+        for (int ks = 0; ks < KS; ++ks) fa[ks] = lin_rows<BF, L::kRowA>(rows_at + L::kA, rt * 16, ks, n, g);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                acc[c] = zero4();
+        for (int c = 0; c < CT; ++c) acc[c] = zero4();
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    acc[c] = lin_mma(lin_rows<BF, L::kRowA>(st, (ct0 + c) * 16, ks, n, g), fa[ks], acc[c]);
+        for (int k = 0; k < L::kParts; ++k)
 #pragma unroll
-                    for (int k = 1; k < L::kParts; ++k)
-                        acc[c] = lin_mma(lin_rows<BF, L::kRowA>(st + k * kLinTile * L::kRowA, (ct0 + c) * 16, ks, n, g), fa[ks], acc[c]);
-                }
-            }
-            const int row = rt * 16 + n;
-            const float gh = lds_get<float>(vec + row * 4), gl = lds_get<float>(vec + (C + row) * 4);
-            const float of = lds_get<float>(vec + (2 * C + row) * 4);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) acc[c] *= of;
-            float sums_x = 0.f, sums_w = 0.f;
-            if constexpr (L::kGrad) {
-                if (R.sum_x) {
-#pragma unroll
-                    for (int c = 0; c < CT; ++c)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int col = (ct0 + c) * 16 + 4 * g + j;
-                            const lds_char* at = rows_at + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
-                            float x;
-                            if constexpr (BF) x = (float)lds_get<__bf16>(at);
-                            else x = lds_get<float>(at);
-                            sums_x = fmaf(acc[c][j], x, sums_x);
-                        }
-                    sums_x = lin_sum_groups(sums_x) * oscale;
-                    if (g == 0) lds_put(sums + ((1 + RT + ct0) * C + row) * 4, sums_x);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < C / 32; ++m) {
-                // (tiles of 32 tokens that hold any at or before the rows, or
-                // behind them)
-                if (kRev ? 2 * m + 1 < rt : 2 * m > rt) {
-                    if constexpr (MODE == kLinDq) {
-                        if (R.sum_x && ct0 == 0)
-                            for (int i = lane; i < 32; i += 64) lds_put(sums + ((1 + rt) * C + 32 * m + i) * 4, 0.f);
-                    }
-                    continue;
-                }
-                LinSplit<BF, 2> pp;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int i0 = 32 * m + 16 * half, col = i0 + 4 * g;
-                    const bool some = kRev ? 2 * m + half >= rt : 2 * m + half <= rt;
-                    f32x4 pr = zero4();
-                    if (some) {
-#pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) pr = lin_mma(lin_rows<BF, L::kRowA>(rows_at + L::kB, i0, ks, n, g), fa[ks], pr);
-                        const f32x4 ih = lds_get<f32x4>(vec + col * 4), il = lds_get<f32x4>(vec + (C + col) * 4);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float d = (gh - ih[j]) + (gl - il[j]);
-                            const bool in = kRev ? col + j >= row : col + j <= row;
-                            pr[j] = in ? pr[j] * (exp2_hw(kRev ? -d : d) * pscale) : 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) pp.set(4 * half + j, pr[j]);
-                    if constexpr (MODE == kLinDq) {
-                        if (R.sum_x) {
-                            f32x4 other = zero4();
-                            if (some) {
-                                const LinFrag<BF> fx = lin_rows<BF, L::kRowC>(rows_at + L::kX, rt * 16, 0, n, g);
-                                other = lin_mma(lin_rows<BF, L::kRowC>(rows_at + L::kC, i0, 0, n, g), fx, other);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float mm = some && col + j < row ? other[j] * pr[j] * oscale : 0.f;
-                                sums_w += mm;
-                                const float down = lanes_sum<16>(mm);
-                                if (n == 0 && ct0 == 0) lds_put(sums + ((1 + rt) * C + col + j) * 4, down);
-                            }
-                        }
-                    }
-                }
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
-                    acc[c] = lin_mma(lin_cols<BF, L::kRowC>(rows_at + L::kC, m, (ct0 + c) * 16, n, g), pp, acc[c]);
-            }
-            if constexpr (MODE == kLinDq) {
-                if (R.sum_x) {
-                    sums_w = lin_sum_groups(sums_w);
-                    if (g == 0 && ct0 == 0) lds_put(sums + row * 4, sums_w);
-                }
-            }
-            // (rows behind the sequence's end inside its last chunk are 0)
-            const int t = tc + row;
-            if (t < t1) {
+                    acc[c] = lin_mma(lin_rows<BF, L::kRowA>(st + k * kLinTile * L::kRowA, (ct0 + c) * 16, ks, n, g), fa[ks], acc[c]);
+        const float gh = lds_get<float>(vec + row * 4), gl = lds_get<float>(vec + (C + row) * 4);
+        const float of = lds_get<float>(vec + (2 * C + row) * 4);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[c] *= of;
+        float sums_x = 0.f, sums_w = 0.f;
+        if constexpr (L::kGrad) {
+            if (it > 0) emit(it - 1);
+            if (R.sum_x) {
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
-                    const int col = col0 + (ct0 + c) * 16 + 4 * g;
-                    const f32x4 o = t < tl ? acc[c] * oscale : zero4();
-                    const int64_t at = (bh * p.T + t) * R.nv + col;
-                    if (R.out_wide) {
-                        if (col < R.nv) {
-                            if (R.out_bf16) *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(R.out) + at) = __builtin_convertvector(o, bf16x4);
-                            else *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(R.out) + at) = o;
-                        }
-                    } else {
+                    const int col = (ct0 + c) * 16 + 4 * g;
+                    const lds_char* at = rows_at + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
+                    f32x4 x;
+                    if constexpr (BF) x = __builtin_convertvector(lds_get<bf16x4>(at), f32x4);
+                    else x = lds_get<f32x4>(at);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (col + j < R.nv) {
-                                if (R.out_bf16) reinterpret_cast<__bf16*>(R.out)[at + j] = (__bf16)o[j];
-                                else reinterpret_cast<float*>(R.out)[at + j] = o[j];
-                            }
+                    for (int j = 0; j < 4; ++j) sums_x = fmaf(acc[c][j], x[j], sums_x);
+                }
+                sums_x = lin_sum_groups(sums_x) * oscale;
+                if (g == 0) lds_put(sums + ((1 + RT + ct0) * C + row) * 4, sums_x);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < C / 32; ++m) {
+            // (pairs of tiles that hold any token at or before the rows, or
+            // at or behind them)
+            if (kRev ? 2 * m + 1 < rt : 2 * m > rt) {
+                if constexpr (MODE == kLinDq) {
+                    if (R.sum_x && ct0 == 0 && lane < 32) lds_put(sums + ((1 + rt) * C + 32 * m + lane) * 4, 0.f);
+                }
+                continue;
+            }
+            f32x4 pr[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i0 = 32 * m + 16 * half, col = i0 + 4 * g;
+                pr[half] = zero4();
+                // (a tile on the other side of the rows is masked whole)
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) pr[half] = lin_mma(lin_rows<BF, L::kRowA>(rows_at + L::kB, i0, ks, n, g), fa[ks], pr[half]);
+                const f32x4 ih = lds_get<f32x4>(vec + col * 4), il = lds_get<f32x4>(vec + (C + col) * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float d = (gh - ih[j]) + (gl - il[j]);
+                    const bool in = kRev ? col + j >= row : col + j <= row;
+                    pr[half][j] = in ? pr[half][j] * (exp2_hw(kRev ? -d : d) * pscale) : 0.f;
+                }
+                if constexpr (MODE == kLinDq) {
+                    if (R.sum_x) {
+                        const f32x4 other = lin_mma(lin_rows<BF, L::kRowC>(rows_at + L::kC, i0, 0, n, g),
+                                                    lin_rows<BF, L::kRowC>(rows_at + L::kX, rt * 16, 0, n, g), zero4());
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float mm = col + j < row ? other[j] * pr[half][j] * oscale : 0.f;
+                            sums_w += mm;
+                            const float down = lanes_sum<16>(mm);
+                            if (n == 0 && ct0 == 0) lds_put(sums + ((1 + rt) * C + col + j) * 4, down);
+                        }
                     }
                 }
             }
+            LinSplit<BF, 2> pp;
+            pp.set(__builtin_shufflevector(pr[0], pr[1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                acc[c] = lin_mma(lin_cols<BF, L::kRowC>(rows_at + L::kC, m, (ct0 + c) * 16, n, g), pp, acc[c]);
         }
-        // the state behind the chunk
-        const float whole = exp2_hw(gend);
-#pragma unroll
-        for (int t = 0; t < KT; ++t) S[t] *= whole;
-#pragma unroll
-        for (int m = 0; m < C / 32; ++m) {
-            const LinFrag<BF> raw = lin_cols<BF, L::kRowC>(rows_at + L::kC, m, nvt * 16, n, g);
-            const f32x4 u0 = lds_get<f32x4>(vec + (3 * C + 32 * m + 4 * g) * 4);
-            const f32x4 u1 = lds_get<f32x4>(vec + (3 * C + 32 * m + 16 + 4 * g) * 4);
-            LinSplit<BF, 3> fc;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                fc.set(j, raw.get(j) * u0[j]);
-                fc.set(j + 4, raw.get(j + 4) * u1[j]);
+        if constexpr (MODE == kLinDq) {
+            if (R.sum_x) {
+                sums_w = lin_sum_groups(sums_w);
+                if (g == 0 && ct0 == 0) lds_put(sums + row * 4, sums_w);
             }
-#pragma unroll
-            for (int t = 0; t < KT; ++t) S[t] = lin_mma(lin_cols<BF, L::kRowA>(rows_at + L::kB, m, (kt0 + t) * 16, n, g), fc, S[t]);
         }
-        if constexpr (L::kOut) publish((it + 1) & 1);
+        // (rows behind the sequence's end inside its last chunk are 0)
+        const int t = tc + row;
+        if (t < t1) {
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const int col = col0 + (ct0 + c) * 16 + 4 * g;
+                const f32x4 o = t < tl ? acc[c] * oscale : zero4();
+                const int64_t at = (bh * p.T + t) * R.nv + col;
+                if (R.out_wide) {
+                    if (col < R.nv) {
+                        if (R.out_bf16) *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(R.out) + at) = __builtin_convertvector(o, bf16x4);
+                        else *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(R.out) + at) = o;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (col + j < R.nv) {
+                            if (R.out_bf16) reinterpret_cast<__bf16*>(R.out)[at + j] = (__bf16)o[j];
+                            else reinterpret_cast<float*>(R.out)[at + j] = o[j];
+                        }
+                }
+            }
+        }
     }
     if constexpr (L::kGrad) {
         __syncthreads();
-        if (chunks > 0) emit(number(chunks - 1), (chunks - 1) & 1);
+        if (chunks > 0) emit(chunks - 1);
     }
-    if constexpr (L::kOut) {
-        // rows behind the last chunk
-        const int64_t z0 = t0 + (int64_t)chunks * C;
-        const int span = cols;
-        for (int64_t i = z0 * span + threadIdx.x; i < (int64_t)t1 * span; i += kLinThreads) {
-            const int64_t at = (bh * p.T + i / span) * R.nv + col0 + i % span;
-            if (R.out_bf16) reinterpret_cast<__bf16*>(R.out)[at] = (__bf16)0.f;
-            else reinterpret_cast<float*>(R.out)[at] = 0.f;
-        }
-    }
-    float* to = nullptr;
-    if constexpr (MODE == kLinSum) to = p.seg_sum + unit * plane;
-    if constexpr (MODE == kLinSumD) to = p.seg_sum_d + unit * plane;
-    if constexpr (L::kOut) {
-        if (R.last && seg == (kRev ? 0 : p.nseg - 1)) to = R.last + bh * plane;
-    }
-    float share = 0.f;
-    const bool ends = MODE == kLinDq && R.end_share && seg == p.nseg - 1;
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = (kt0 + t) * 16 + 4 * g + j;
-            if (k < R.nk && scol < R.nv) {
-                if (to) to[k * sk + scol * sn] = S[t][j];
-                if (ends) share = fmaf(S[t][j], R.end_grad[bh * plane + k * sk + scol * sn], share);
-            }
-        }
-    if constexpr (MODE == kLinSum || MODE == kLinSumD) {
-        if (MODE == kLinSum && tile == 0 && threadIdx.x == 0) p.seg_decay[unit] = total;
-    }
-    if constexpr (MODE == kLinDq) {
-        if (ends) {
-            __syncthreads();
-            share = lanes_sum<64>(share);
-            if (lane == 0) lds_put(lds + L::kSums + wave * 4, share);
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                float s = 0.f;
-                for (int i = 0; i < kLinThreads / 64; ++i) s += lds_get<float>(lds + L::kSums + i * 4);
-                R.end_share[tile * (int64_t)p.B * p.H + bh] = s;
-            }
-        }
+    // rows behind the last chunk
+    const int64_t z0 = t0 + (int64_t)chunks * C;
+    for (int64_t i = z0 * cols + (int)threadIdx.x; i < (int64_t)t1 * cols; i += kLinThreads - kLinMovers) {
+        const int64_t at = (bh * p.T + i / cols) * R.nv + col0 + i % cols;
+        if (R.out_bf16) reinterpret_cast<__bf16*>(R.out)[at] = (__bf16)0.f;
+        else reinterpret_cast<float*>(R.out)[at] = 0.f;
     }
 }
 
