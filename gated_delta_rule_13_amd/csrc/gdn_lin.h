@@ -26,6 +26,8 @@
 // numbers that add up to it (errors of 2^-17 or 2^-24); fp32 rows on the fp32
 // units.
 #pragma once
+#include <type_traits>
+
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -70,10 +72,9 @@ struct LinParams {
 
 enum LinMode { kLinFwd, kLinDq, kLinDk, kLinDv, kLinSum, kLinSumD };
 
-// Four waves form the outputs of a chunk, four others move rows and keep the
-// state: both read the same chunk's rows and the state before it, and run beside
-// each other, two waves to a SIMD.
-constexpr int kLinThreads = 512, kLinMovers = 256;
+// Four waves form the outputs of a chunk, four keep the state and four move rows:
+// all work on the same chunk at once, one wave of each kind to a SIMD.
+constexpr int kLinRole = 256, kLinThreads = 3 * kLinRole;
 constexpr int kLinTile = 32;        // columns of c to a workgroup
 // Tokens to a chunk: as many as let two chunks' rows and two states lie in LDS.
 constexpr int lin_chunk(bool bf16, int nk) { return bf16 && nk <= 128 ? 64 : 32; }
@@ -90,6 +91,8 @@ template <typename V>
 __device__ __forceinline__ void lds_put(lds_char* p, V v) {
     *reinterpret_cast<__attribute__((address_space(3))) V*>(p) = v;
 }
+
+__device__ __forceinline__ lds_char* lds_at32(uint32_t a) { return (lds_char*)(uintptr_t)a; }
 
 // Operands of a matrix product over 32 numbers: lane 16 g + n has row (or
 // column) n and numbers 8 g .. 8 g + 7.
@@ -112,6 +115,25 @@ __device__ __forceinline__ f32x4 lin_mma(const LinFrag<false>& a, const LinFrag<
     for (int i = 0; i < 8; ++i) c = mfma_f32(a.v[i], b.v[i], c);
     return c;
 }
+// Two numbers in bf16, and what they are short of: the dot product with (-1, 0)
+// or (0, -1) takes one half from the number that it was rounded from, exactly,
+// in one instruction.  (The empty asm keeps the compiler from converting each
+// number again where it is widened.)
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+__device__ __forceinline__ uint32_t lin_pack(float a, float b) {
+    uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+    asm("" : "+v"(w));
+    return w;
+}
+__device__ __forceinline__ void lin_rest(uint32_t w, float& a, float& b) {
+    // (held in registers: as a literal, -1.0 stands for the upper half here)
+    uint32_t first = 0xbf80u, second = 0xbf800000u;
+    asm("" : "+s"(first), "+s"(second));
+    const bf16x2 h = __builtin_bit_cast(bf16x2, w);
+    a = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2, first), a, false);
+    b = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2, second), b, false);
+}
 // A computed operand: N bf16 numbers that add up to it, or fp32.
 template <bool BF, int N>
 struct LinSplit;
@@ -119,11 +141,18 @@ template <int N>
 struct LinSplit<true, N> {
     LinFrag<true> part[N];
     __device__ __forceinline__ void set(f32x8 x) {
+        u32x4 w[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            part[k].v = __builtin_convertvector(x, bf16x8);
-            if (k + 1 < N) x -= __builtin_convertvector(part[k].v, f32x8);
+        for (int i = 0; i < 4; ++i) {
+            float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                w[k][i] = lin_pack(a, b);
+                if (k + 1 < N) lin_rest(w[k][i], a, b);
+            }
         }
+#pragma unroll
+        for (int k = 0; k < N; ++k) part[k].v = __builtin_bit_cast(bf16x8, w[k]);
     }
 };
 template <int N>
@@ -150,50 +179,84 @@ __device__ __forceinline__ int lin_turn(int r) {
 template <int ROWB>
 __device__ __forceinline__ int lin_piece(int r, int p) { return r * ROWB + ((p ^ lin_turn<ROWB>(r)) << 4); }
 
-// Rows row0 + n, numbers 32 ks + 8 g ..
-template <bool BF, int ROWB>
-__device__ __forceinline__ LinFrag<BF> lin_rows(const lds_char* t, int row0, int ks, int n, int g) {
-    LinFrag<BF> f;
-    if constexpr (BF) {
-        f.v = lds_get<bf16x8>(t + lin_piece<ROWB>(row0 + n, 4 * ks + g));
-    } else {
-        const f32x4 a = lds_get<f32x4>(t + lin_piece<ROWB>(row0 + n, 8 * ks + 2 * g));
-        const f32x4 b = lds_get<f32x4>(t + lin_piece<ROWB>(row0 + n, 8 * ks + 2 * g + 1));
-        f.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-    return f;
-}
-// Column col0 + n of tokens 32 m + 4 g + j and 32 m + 16 + 4 g + j: the order
-// in which a product's result holds the rows of two tiles.
-template <bool BF, int ROWB>
-__device__ __forceinline__ LinFrag<BF> lin_cols(const lds_char* t, int m, int col0, int n, int g) {
-    LinFrag<BF> f;
-    if constexpr (BF) {
-        // (the transposing read: lane n of a group addresses four columns of
-        // token n / 4 and receives four tokens of column n)
-        const int r = 32 * m + 4 * g + (n >> 2), p = (col0 >> 3) + ((n & 3) >> 1), half = (n & 1) * 8;
-        typedef __attribute__((ext_vector_type(4))) short s4;
-        typedef __attribute__((address_space(3))) s4 lds_s4;
-        const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(t + lin_piece<ROWB>(r, p) + half));
-        const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(t + lin_piece<ROWB>(r + 16, p) + half));
-        f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
-    } else {
-        const int c = col0 + n;
+// Where a lane reads operands from a tile, computed once: rows row0 + n (row0 a
+// multiple of 16, which turns nothing), numbers 32 ks + 8 g ..
+template <bool BF, int ROWB, int KS>
+struct LinRows {
+    static constexpr int kPer = BF ? 1 : 2;
+    uint32_t o[KS * kPer];
+    __device__ __forceinline__ LinRows(int n, int g) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int r = 32 * m + 4 * g + (j & 3) + (j >> 2) * 16;
-            f.v[j] = lds_get<float>(t + lin_piece<ROWB>(r, c >> 2) + (c & 3) * 4);
+        for (int i = 0; i < KS * kPer; ++i) o[i] = lin_piece<ROWB>(n, BF ? 4 * i + g : 8 * (i / 2) + 2 * g + i % 2);
+    }
+    __device__ __forceinline__ LinRows(const LinRows& from, uint32_t base) {
+#pragma unroll
+        for (int i = 0; i < KS * kPer; ++i) {
+            o[i] = from.o[i] + base;
+            asm("" : "+v"(o[i]));       // (one register each, what is added to it goes into the reads)
         }
     }
-    return f;
-}
+    __device__ __forceinline__ LinFrag<BF> get(int tile, int row0, int ks) const {
+        LinFrag<BF> f;
+        if constexpr (BF) {
+            f.v = lds_get<bf16x8>(lds_at32(o[ks]) + tile + row0 * ROWB);
+        } else {
+            const f32x4 a = lds_get<f32x4>(lds_at32(o[2 * ks]) + tile + row0 * ROWB), b = lds_get<f32x4>(lds_at32(o[2 * ks + 1]) + tile + row0 * ROWB);
+            f.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+        return f;
+    }
+};
+// Columns col0 + 16 i + n of tokens 32 m + 4 g + j and 32 m + 16 + 4 g + j: the
+// order in which a product's result holds the rows of two tiles.
+template <bool BF, int ROWB, int TILES>
+struct LinCols {
+    static constexpr int kPer = BF ? 1 : 4;
+    uint32_t o[TILES * kPer];
+    __device__ __forceinline__ LinCols(int col0, int n, int g) {
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+            const int c = col0 + 16 * i;
+            if constexpr (BF) {
+                // (the transposing read: lane n of a group addresses four columns
+                // of token n / 4 and receives four tokens of column n)
+                o[i] = lin_piece<ROWB>(4 * g + (n >> 2), (c >> 3) + ((n & 3) >> 1)) + (n & 1) * 8;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i * 4 + j] = lin_piece<ROWB>(4 * g + j, (c + n) >> 2) + (n & 3) * 4;
+            }
+        }
+    }
+    __device__ __forceinline__ LinCols(const LinCols& from, uint32_t base) {
+#pragma unroll
+        for (int i = 0; i < TILES * kPer; ++i) {
+            o[i] = from.o[i] + base;
+            asm("" : "+v"(o[i]));
+        }
+    }
+    __device__ __forceinline__ LinFrag<BF> get(int tile, int m, int i) const {
+        LinFrag<BF> f;
+        if constexpr (BF) {
+            typedef __attribute__((ext_vector_type(4))) short s4;
+            typedef __attribute__((address_space(3))) s4 lds_s4;
+            const lds_char* at = lds_at32(o[i]) + tile + 32 * m * ROWB;
+            const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
+            const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(at + 16 * ROWB));
+            f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f.v[j] = lds_get<float>(lds_at32(o[i * 4 + (j & 3)]) + tile + (32 * m + 16 * (j >> 2)) * ROWB);
+        }
+        return f;
+    }
+};
 
 // `rows` rows of `cols` numbers into a tile of C rows of ROWB bytes; the rest of
 // the tile is 0.
 template <bool BF, int ROWB, int C>
 __device__ __forceinline__ void lin_stage(lds_char* tile, const char* src, int64_t stride, int rows, int cols, int wide) {
     constexpr int kEl = BF ? 8 : 4, kPieces = ROWB / 16, kBytes = BF ? 2 : 4;
-    for (int i = threadIdx.x % kLinMovers; i < C * kPieces; i += kLinMovers) {
+    for (int i = threadIdx.x % kLinRole; i < C * kPieces; i += kLinRole) {
         const int r = i / kPieces, q = i % kPieces, c = q * kEl;
         u32x4 v = {0, 0, 0, 0};
         if (r < rows && c < cols) {
@@ -240,23 +303,25 @@ __device__ __forceinline__ void lin_wait_lds() { asm volatile("s_waitcnt lgkmcnt
 template <bool BF, int ROWB, int C>
 struct LinDirect {
     // (kSure: those that every wave makes)
-    static constexpr int kPieces = ROWB / 16, kSure = C * kPieces / kLinMovers, kLoads = (C * kPieces + kLinMovers - 1) / kLinMovers;
+    static constexpr int kPieces = ROWB / 16, kSure = C * kPieces / kLinRole, kLoads = (C * kPieces + kLinRole - 1) / kLinRole;
     uint32_t off[kLoads];
-    uint32_t in;
+    uint32_t in;            // bit k: the piece of load k lies inside the row
     __device__ __forceinline__ void set(int64_t stride, int cols, int wave, int lane) {
         in = 0;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
-            const int i = (k * (kLinMovers / 64) + wave) * 64 + lane, r = i / kPieces;
+            const int i = (k * (kLinRole / 64) + wave) * 64 + lane, r = i / kPieces;
             const int q = (i % kPieces) ^ lin_turn<ROWB>(r);
             off[k] = (uint32_t)((int64_t)r * stride * (BF ? 2 : 4)) + q * 16;
             if (i < C * kPieces && q * (BF ? 8 : 4) < cols) in |= 1u << k;
         }
     }
+    // ALL: every piece of every load lies inside
+    template <bool ALL>
     __device__ __forceinline__ void load(uint32_t tile, const char* rows, int wave) const {
 #pragma unroll
         for (int k = 0; k < kLoads; ++k)
-            if (in & (1u << k)) lin_direct16(tile + (k * (kLinMovers / 64) + wave) * 1024, off[k], rows);
+            if ((ALL && kSure == kLoads) || (in & (1u << k))) lin_direct16(tile + (k * (kLinRole / 64) + wave) * 1024, off[k], rows);
     }
 };
 
@@ -299,8 +364,9 @@ struct LinPlan {
     static constexpr int kC = kB + C * kRowA;
     static constexpr int kX = kC + C * kRowC;
     static constexpr int kStageBytes = kX + (kGrad ? C * kRowC : 0);
-    static constexpr int kVec = 0;                                  // of two chunks: Gh, Gl, out factor, state factor
-    static constexpr int kLog = kVec + 2 * 4 * C * 4;               // log_alpha of four chunks
+    static constexpr int kVec = 0;                                  // of two chunks: see LinDecays
+    static constexpr int kVecBytes = (6 * C + 4) * 4;
+    static constexpr int kLog = kVec + 2 * kVecBytes;               // log_alpha of four chunks
     static constexpr int kSums = kLog + 4 * 64 * 4;                 // of two: rows, columns of each row tile, x of each column tile
     static constexpr int kSumBytes = kGrad ? (1 + C / 16 + 2) * C * 4 : 0;
     static constexpr int kState = (kSums + 2 * kSumBytes + 255) / 256 * 256;
@@ -317,6 +383,13 @@ __device__ __forceinline__ float lin_sum_groups(float v) {
     return swap32_add(v, v);
 }
 
+// The decays of a chunk in LDS, C numbers each.  Where the chunk spans little, a
+// decay between two tokens is the product of kOut of one and kIn of the other
+// (from the middle of the span, 2^-48 to 2^48); else the exponential of the
+// difference of G, which is kept in two numbers.
+enum LinDecays { kLinOut, kLinIn, kLinGh, kLinGl, kLinFirst, kLinState, kLinWhole };
+constexpr float kLinSpan = 48.f;
+
 template <bool BF, int NK, int C, int MODE>
 __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, int64_t unit, int tile, char* shared) {
     typedef LinPlan<BF, NK, C, MODE> L;
@@ -327,8 +400,8 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     constexpr int KS = NK / 32, KT = NK / 32;       // steps over nk; state tiles of a wave
     constexpr int EB = L::kEl;
     lds_char* lds = (lds_char*)shared;
-    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3;
-    const bool mover = wave8 >= 4;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+    const int wave12 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave12 & 3;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int64_t bh = unit / p.nseg;
     const int seg = (int)(unit % p.nseg);
@@ -340,24 +413,179 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     const int col0 = tile * kLinTile, cols = R.nv - col0 < kLinTile ? R.nv - col0 : kLinTile;
     constexpr int kStages = L::kStages, kAhead = kStages - 1;
     auto number = [&](int it) __attribute__((always_inline)) { return kRev ? chunks - 1 - it : it; };
+    auto stage_of = [&](int it) __attribute__((always_inline)) { return lds0 + L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes; };
     const int64_t plane = (int64_t)p.dk * p.dv;
     const int64_t part = tile * (int64_t)p.B * p.H + bh;            // (rows of the partial sums)
 
-    if (mover) {
+    if (wave12 >= 8) {
+        // ---- the waves that move rows ----
         auto head = [&](const LinTensor& x, int c) __attribute__((always_inline)) {
             return reinterpret_cast<const char*>(x.p) + (b * x.sb + (h / x.rep) * x.sh + c) * EB;
         };
-        const char* pa = L::kOut ? head(R.a, 0) : nullptr;
-        const char* pb = head(R.b, 0);
-        const char* pc = head(R.c, col0);
-        const char* px = L::kGrad ? head(R.x, col0) : nullptr;
         const float* la = p.log_alpha ? p.log_alpha + b * p.lsb + h * p.lsh : nullptr;
+        // Rows of chunk number `it` into its stage, and its log_alpha, a chunk
+        // earlier.  A whole chunk goes straight to LDS and keeps kLoads loads of
+        // each wave under way.
+        constexpr int kLoads = (L::kOut ? 2 : 1) * LinDirect<BF, L::kRowA, C>::kSure + (L::kGrad ? 2 : 1) * LinDirect<BF, L::kRowC, C>::kSure;
+        const bool direct = kAhead > 0 && R.b.direct && R.c.direct && (!L::kOut || R.a.direct) && (!L::kGrad || R.x.direct) && cols % (16 / EB) == 0;
+        const bool all = R.nk == NK && cols == kLinTile;
+        LinDirect<BF, L::kRowA, C> da, db;
+        LinDirect<BF, L::kRowC, C> dc, dx;
+        if (direct) {
+            if constexpr (L::kOut) da.set(R.a.st, R.nk, wave, lane);
+            db.set(R.b.st, R.nk, wave, lane);
+            dc.set(R.c.st, cols, wave, lane);
+            if constexpr (L::kGrad) dx.set(R.x.st, cols, wave, lane);
+            // (pieces behind a row's end are not written again)
+            if (!all) {
+                for (int i = threadIdx.x % kLinRole; i < kStages * L::kStageBytes / 16; i += kLinRole)
+                    lds_put(lds + L::kStage + i * 16, u32x4{0, 0, 0, 0});
+            }
+        }
+        auto is_full = [&](int it) __attribute__((always_inline)) { return direct && it < chunks && t0 + (number(it) + 1) * C <= tl; };
+        auto load_log = [&](int it) __attribute__((always_inline)) {
+            if (wave == 0 && la && it < chunks) {
+                const int t = t0 + number(it) * C + lane;
+                if (lane < C && t < tl) lin_direct4(lds0 + L::kLog + (it & 3) * 256, reinterpret_cast<const char*>(la + t * p.lst));
+            }
+        };
+        // (called for one chunk after the other)
+        const char *ra = L::kOut ? head(R.a, 0) : nullptr, *rb = head(R.b, 0), *rc = head(R.c, col0), *rx = L::kGrad ? head(R.x, col0) : nullptr;
+        const int64_t first = t0 + (int64_t)number(0) * C, turn = kRev ? -C : C;
+        if constexpr (L::kOut) ra += first * R.a.st * EB;
+        rb += first * R.b.st * EB;
+        rc += first * R.c.st * EB;
+        if constexpr (L::kGrad) rx += first * R.x.st * EB;
+        const int64_t sa = turn * R.a.st * EB, sb = turn * R.b.st * EB, sc = turn * R.c.st * EB, sx = turn * R.x.st * EB;
+        auto load_all = [&](uint32_t at, auto whole) __attribute__((always_inline)) {
+            constexpr bool ALL = decltype(whole)::value;
+            if constexpr (L::kOut) da.template load<ALL>(at + L::kA, ra, wave);
+            db.template load<ALL>(at + L::kB, rb, wave);
+            dc.template load<ALL>(at + L::kC, rc, wave);
+            if constexpr (L::kGrad) dx.template load<ALL>(at + L::kX, rx, wave);
+        };
+        auto load = [&](int it) __attribute__((always_inline)) {
+            if (it >= chunks) return;
+            const int tc = t0 + number(it) * C, rows = tl - tc < C ? tl - tc : C;
+            const uint32_t stage = stage_of(it);
+            if (direct && rows == C) {
+                if (all) load_all(stage, std::true_type{});
+                else load_all(stage, std::false_type{});
+            } else {
+                lds_char* to = lds_at32(stage);
+                if constexpr (L::kOut) lin_stage<BF, L::kRowA, C>(to + L::kA, ra, R.a.st, rows, R.nk, R.a.wide);
+                lin_stage<BF, L::kRowA, C>(to + L::kB, rb, R.b.st, rows, R.nk, R.b.wide);
+                lin_stage<BF, L::kRowC, C>(to + L::kC, rc, R.c.st, rows, cols, R.c.wide);
+                if constexpr (L::kGrad) lin_stage<BF, L::kRowC, C>(to + L::kX, rx, R.x.st, rows, cols, R.x.wide);
+            }
+            if constexpr (L::kOut) ra += sa;
+            rb += sb;
+            rc += sc;
+            if constexpr (L::kGrad) rx += sx;
+        };
+        // the decays of chunk number `it`
+        auto decays = [&](int it) __attribute__((always_inline)) {
+            if (wave != 0 || it >= chunks) return;
+            const int rows = tl - (t0 + number(it) * C);
+            float l = la && lane < rows && lane < C ? lds_get<float>(lds + L::kLog + (it & 3) * 256 + lane * 4) * kLog2e : 0.f;
+            l = l < -kLinFloor ? -kLinFloor : l;    // (NaN stays)
+            const double G = lin_scan(l, lane), end = lin_lane(G, C - 1), mid = 0.5 * end;
+            const float gh = (float)G, away = (float)(G - mid), gend = (float)end, gmid = (float)mid;
+            // (a NaN is far, too)
+            const bool far = __builtin_amdgcn_ballot_w64(!(__builtin_fabsf(away) <= kLinSpan)) != 0;
+            const float from = exp2_hw(gh), to = exp2_hw((float)(end - G));
+            lds_char* v = lds + L::kVec + (it & 1) * L::kVecBytes;
+            if (lane < C) {
+                lds_put(v + (kLinOut * C + lane) * 4, far ? 1.f : exp2_hw(kRev ? -away : away));
+                lds_put(v + (kLinIn * C + lane) * 4, far ? 1.f : exp2_hw(kRev ? away : -away) * (kRev ? p.scale : 1.f));
+                lds_put(v + (kLinGh * C + lane) * 4, gh);
+                lds_put(v + (kLinGl * C + lane) * 4, (float)(G - gh));
+                lds_put(v + (kLinFirst * C + lane) * 4, far ? (kRev ? to : from) : exp2_hw(gmid));
+                lds_put(v + (kLinState * C + lane) * 4, kRev ? from * p.scale : to);
+            }
+            if (lane == 0) {
+                lds_put(v + kLinWhole * C * 4, gend);
+                lds_put(v + kLinWhole * C * 4 + 4, far ? 1.f : 0.f);
+            }
+        };
+        // what a chunk left for the decay's gradient
+        auto emit = [&](int it) __attribute__((always_inline)) {
+            if constexpr (L::kGrad) {
+                if (!R.sum_x || wave != 1) return;
+                const lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
+                const int ch = number(it), t = t0 + ch * C + lane;
+                float w = 0.f, x = 0.f;
+                if (lane < C) {
+                    x = lds_get<float>(sums + ((1 + RT) * C + lane) * 4);
+                    if constexpr (RT == 2) x += lds_get<float>(sums + ((2 + RT) * C + lane) * 4);
+                    if constexpr (MODE == kLinDq) {
+                        w = lds_get<float>(sums + lane * 4);
+#pragma unroll
+                        for (int i = 0; i < RT; ++i) w -= lds_get<float>(sums + ((1 + i) * C + lane) * 4);
+                    }
+                    if (t < tl) {
+                        R.sum_x[part * p.T + t] = x;
+                        if constexpr (MODE == kLinDq) R.sum_w[part * p.T + t] = w;
+                    } else {
+                        x = 0.f;
+                    }
+                }
+                x = lanes_sum<64>(x);
+                if (lane == 0) R.chunk_x[part * ((p.T + C - 1) / C) + t0 / C + ch] = x;
+            }
+        };
+        lin_wait<0>();
+        load_log(0);
+        load_log(1);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            load(i);
+            if (i + 1 < kAhead || kAhead == 1) load_log(i + 2);
+        }
+        lin_wait<0>();
+        decays(0);
+        for (int it = 0; it < chunks; ++it) {
+            // what chunk `it` needs has come; what was asked for since may be
+            // under way
+            if constexpr (kAhead == 0) {
+                lin_wait<0>();
+                load(it);
+                load_log(it + 1);
+                lin_wait<0>();
+            } else {
+                if (kAhead > 1 && is_full(it + kAhead - 1)) lin_wait<(kAhead - 1) * kLoads>();
+                else lin_wait<0>();
+                load_log(it + kAhead + 1);
+                load(it + kAhead);
+            }
+            decays(it + 1);
+            if (it > 0) emit(it - 1);
+        }
+        if constexpr (L::kGrad) {
+            __syncthreads();
+            if (chunks > 0) emit(chunks - 1);
+        }
+        if constexpr (L::kOut) {
+            // rows behind the last chunk
+            const int64_t z0 = t0 + (int64_t)chunks * C;
+            for (int64_t i = z0 * cols + (int)(threadIdx.x % kLinRole); i < (int64_t)t1 * cols; i += kLinRole) {
+                const int64_t at = (bh * p.T + i / cols) * R.nv + col0 + i % cols;
+                if (R.out_bf16) reinterpret_cast<__bf16*>(R.out)[at] = (__bf16)0.f;
+                else reinterpret_cast<float*>(R.out)[at] = 0.f;
+            }
+        }
+        return;
+    }
 
-        // The state, rows nk and columns nv: this wave's tiles are KT rows of
-        // tiles from kt0 and one column of tiles.
+    if (wave12 >= 4) {
+        // ---- the waves that keep the state ----
+        // Rows nk and columns nv: this wave's tiles are KT rows of tiles from kt0
+        // and one column of tiles.
         const int nvt = wave & 1, kt0 = (wave >> 1) * KT;
         const int64_t sn = kTurned ? 1 : p.dk, sk = kTurned ? p.dk : 1;
         const int scol = col0 + nvt * 16 + n;
+        const LinCols<BF, L::kRowA, KT> at_b(kt0 * 16, n, g);
+        const LinCols<BF, L::kRowC, 1> at_c(nvt * 16, n, g);
         f32x4 S[KT];
         {
             const float* from = nullptr;
@@ -380,120 +608,58 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                     f32x4 x = S[t];
 #pragma unroll
                     for (int k = 0; k < L::kParts; ++k) {
-                        const bf16x4 part4 = __builtin_convertvector(x, bf16x4);
-                        lds_put(at + k * kLinTile * L::kRowA + off, part4);
-                        if (k + 1 < L::kParts) x -= __builtin_convertvector(part4, f32x4);
+                        const u32x2 w = {lin_pack(x[0], x[1]), lin_pack(x[2], x[3])};
+                        lds_put(at + k * kLinTile * L::kRowA + off, w);
+                        if (k + 1 < L::kParts) {
+                            float y[4] = {x[0], x[1], x[2], x[3]};
+                            lin_rest(w[0], y[0], y[1]);
+                            lin_rest(w[1], y[2], y[3]);
+                            x = f32x4{y[0], y[1], y[2], y[3]};
+                        }
                     }
                 } else {
                     lds_put(at + lin_piece<L::kRowA>(row, 4 * (kt0 + t) + g), S[t]);
                 }
             }
         };
-        // Rows of chunk number `it` into its stage, and its log_alpha, a chunk
-        // earlier.  A whole chunk goes straight to LDS and keeps kLoads loads of
-        // each wave under way.
-        constexpr int kLoads = (L::kOut ? 2 : 1) * LinDirect<BF, L::kRowA, C>::kSure + (L::kGrad ? 2 : 1) * LinDirect<BF, L::kRowC, C>::kSure;
-        const bool direct = kAhead > 0 && R.b.direct && R.c.direct && (!L::kOut || R.a.direct) && (!L::kGrad || R.x.direct) && cols % (16 / EB) == 0;
-        LinDirect<BF, L::kRowA, C> da, db;
-        LinDirect<BF, L::kRowC, C> dc, dx;
-        if (direct) {
-            if constexpr (L::kOut) da.set(R.a.st, R.nk, wave, lane);
-            db.set(R.b.st, R.nk, wave, lane);
-            dc.set(R.c.st, cols, wave, lane);
-            if constexpr (L::kGrad) dx.set(R.x.st, cols, wave, lane);
-        }
-        const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-        auto is_full = [&](int it) __attribute__((always_inline)) { return direct && it < chunks && t0 + (number(it) + 1) * C <= tl; };
-        auto load_log = [&](int it) __attribute__((always_inline)) {
-            if (wave == 0 && la && it < chunks) {
-                const int t = t0 + number(it) * C + lane;
-                if (lane < C && t < tl) lin_direct4(lds0 + L::kLog + (it & 3) * 256, reinterpret_cast<const char*>(la + t * p.lst));
-            }
-        };
-        auto load = [&](int it) __attribute__((always_inline)) {
-            if (it >= chunks) return;
-            const int tc = t0 + number(it) * C, rows = tl - tc < C ? tl - tc : C;
-            const int stage = L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes;
-            const char *ra = L::kOut ? pa + tc * R.a.st * EB : nullptr, *rb = pb + tc * R.b.st * EB, *rc = pc + tc * R.c.st * EB;
-            const char* rx = L::kGrad ? px + tc * R.x.st * EB : nullptr;
-            if (direct && rows == C) {
-                if constexpr (L::kOut) da.load(lds0 + stage + L::kA, ra, wave);
-                db.load(lds0 + stage + L::kB, rb, wave);
-                dc.load(lds0 + stage + L::kC, rc, wave);
-                if constexpr (L::kGrad) dx.load(lds0 + stage + L::kX, rx, wave);
-            } else {
-                if constexpr (L::kOut) lin_stage<BF, L::kRowA, C>(lds + stage + L::kA, ra, R.a.st, rows, R.nk, R.a.wide);
-                lin_stage<BF, L::kRowA, C>(lds + stage + L::kB, rb, R.b.st, rows, R.nk, R.b.wide);
-                lin_stage<BF, L::kRowC, C>(lds + stage + L::kC, rc, R.c.st, rows, cols, R.c.wide);
-                if constexpr (L::kGrad) lin_stage<BF, L::kRowC, C>(lds + stage + L::kX, rx, R.x.st, rows, cols, R.x.wide);
-            }
-        };
-        // the decays of chunk number `it`
-        auto vectors = [&](int it) __attribute__((always_inline)) {
-            if (wave != 0 || it >= chunks) return;
-            const int rows = tl - (t0 + number(it) * C);
-            float l = la && lane < rows && lane < C ? lds_get<float>(lds + L::kLog + (it & 3) * 256 + lane * 4) * kLog2e : 0.f;
-            l = l < -kLinFloor ? -kLinFloor : l;    // (NaN stays)
-            const double G = lin_scan(l, lane), end = lin_lane(G, C - 1);
-            if (lane < C) {
-                lds_char* v = lds + L::kVec + (it & 1) * 4 * C * 4 + lane * 4;
-                const float gh = (float)G;
-                const float from = exp2_hw(gh), to = exp2_hw((float)(end - G));
-                lds_put(v, gh);
-                lds_put(v + C * 4, (float)(G - gh));
-                lds_put(v + 2 * C * 4, kRev ? to : from);
-                lds_put(v + 3 * C * 4, kRev ? from * p.scale : to);
-            }
-        };
-        // (pieces behind a row's end are not written again)
-        if (direct && (R.nk < NK || cols < kLinTile)) {
-            for (int i = threadIdx.x % kLinMovers; i < kStages * L::kStageBytes / 16; i += kLinMovers)
-                lds_put(lds + L::kStage + i * 16, u32x4{0, 0, 0, 0});
-        }
         if constexpr (L::kOut) publish(0);
-        lin_wait<0>();
-        load_log(0);
-        load_log(1);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            load(i);
-            if (i + 1 < kAhead || kAhead == 1) load_log(i + 2);
-        }
-        lin_wait<0>();
-        vectors(0);
+        lin_wait_lds();
+        lin_wait_lds();
         float total = 0.f;      // log2 of the decay so far
         for (int it = 0; it < chunks; ++it) {
-            // what chunk `it` needs has come; what was asked for since may be
-            // under way
-            if constexpr (kAhead == 0) {
-                lin_wait<0>();
-                load(it);
-                load_log(it + 1);
-                lin_wait<0>();
-            } else {
-                if (kAhead > 1 && is_full(it + kAhead - 1)) lin_wait<(kAhead - 1) * kLoads>();
-                else lin_wait<0>();
-                load_log(it + kAhead + 1);
-                load(it + kAhead);
+            lin_wait_lds();
+            if constexpr (kAhead == 0) lin_wait_lds();
+            const lds_char* vec = lds + L::kVec + (it & 1) * L::kVecBytes;
+            const uint32_t stage = stage_of(it);
+            const LinCols<BF, L::kRowA, KT> rb(at_b, stage);
+            const LinCols<BF, L::kRowC, 1> rc(at_c, stage);
+            LinFrag<BF> vals[C / 32], keys[C / 32][KT];
+            f32x8 u[C / 32];
+            const float gend = lds_get<float>(vec + kLinWhole * C * 4);
+#pragma unroll
+            for (int m = 0; m < C / 32; ++m) {
+                vals[m] = rc.get(L::kC, m, 0);
+                u[m] = __builtin_shufflevector(lds_get<f32x4>(vec + (kLinState * C + 32 * m + 4 * g) * 4),
+                                               lds_get<f32x4>(vec + (kLinState * C + 32 * m + 16 + 4 * g) * 4), 0, 1, 2, 3, 4, 5, 6, 7);
             }
-            vectors(it + 1);
-            const lds_char* rows_at = lds + L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes;
-            const lds_char* vec = lds + L::kVec + (it & 1) * 4 * C * 4;
-            const float gend = lds_get<float>(vec + (C - 1) * 4);
+#pragma unroll
+            for (int m = 0; m < C / 32; ++m)
+#pragma unroll
+                for (int t = 0; t < KT; ++t) keys[m][t] = rb.get(L::kB, m, t);
+            // (all reads on their way before anything waits for one)
+            __builtin_amdgcn_sched_barrier(0);
             total += gend;
             const float whole = exp2_hw(gend);
 #pragma unroll
             for (int t = 0; t < KT; ++t) S[t] *= whole;
 #pragma unroll
             for (int m = 0; m < C / 32; ++m) {
-                const f32x4 u0 = lds_get<f32x4>(vec + (3 * C + 32 * m + 4 * g) * 4);
-                const f32x4 u1 = lds_get<f32x4>(vec + (3 * C + 32 * m + 16 + 4 * g) * 4);
                 LinSplit<BF, L::kValueParts> fc;
-                fc.set(lin_cols<BF, L::kRowC>(rows_at + L::kC, m, nvt * 16, n, g).wide() *
-                       __builtin_shufflevector(u0, u1, 0, 1, 2, 3, 4, 5, 6, 7));
+                fc.set(vals[m].wide() * u[m]);
 #pragma unroll
-                for (int t = 0; t < KT; ++t)
-                    S[t] = lin_mma(lin_cols<BF, L::kRowA>(rows_at + L::kB, m, (kt0 + t) * 16, n, g), fc, S[t]);
+                for (int k = 0; k < (BF ? L::kValueParts : 1); ++k)
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) S[t] = lin_mma(keys[m][t], fc.part[k], S[t]);
             }
             if constexpr (L::kOut) publish((it + 1) & 1);
         }
@@ -534,133 +700,147 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 
     // ---- the waves that form the outputs ----
     if constexpr (!L::kOut) {
-        // (as many barriers as the movers pass)
-        lin_wait_lds();
-        lin_wait_lds();
-        for (int it = 0; it < chunks; ++it) {
-            lin_wait_lds();
-            if constexpr (kAhead == 0) lin_wait_lds();
-        }
+        // (as many barriers as the others pass)
+        for (int it = 0; it < 2 + chunks * (kAhead == 0 ? 2 : 1); ++it) lin_wait_lds();
         return;
     }
-    const float pscale = kRev ? p.scale : 1.f, oscale = kRev ? 1.f : p.scale;
+    const float oscale = kRev ? 1.f : p.scale;
     const int rt = RT == 4 ? wave : wave >> 1, ct0 = RT == 4 ? 0 : wave & 1;
     const int row = rt * 16 + n;
-    // what a chunk left for the decay's gradient
-    auto emit = [&](int it) __attribute__((always_inline)) {
-        if constexpr (L::kGrad) {
-            if (!R.sum_x || wave != (kRev ? 3 : 0)) return;         // (the wave with the fewest products)
-            const lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
-            const int ch = number(it), t = t0 + ch * C + lane;
-            float w = 0.f, x = 0.f;
-            if (lane < C) {
-                x = lds_get<float>(sums + ((1 + RT) * C + lane) * 4);
-                if constexpr (RT == 2) x += lds_get<float>(sums + ((2 + RT) * C + lane) * 4);
-                if constexpr (MODE == kLinDq) {
-                    w = lds_get<float>(sums + lane * 4);
-#pragma unroll
-                    for (int i = 0; i < RT; ++i) w -= lds_get<float>(sums + ((1 + i) * C + lane) * 4);
-                }
-                if (t < tl) {
-                    R.sum_x[part * p.T + t] = x;
-                    if constexpr (MODE == kLinDq) R.sum_w[part * p.T + t] = w;
-                } else {
-                    x = 0.f;
-                }
-            }
-            x = lanes_sum<64>(x);
-            if (lane == 0) R.chunk_x[part * ((p.T + C - 1) / C) + t0 / C + ch] = x;
-        }
-    };
+    // (steps whose reads go out together)
+    constexpr int KB = KS == 1 ? 1 : (L::kParts == 3 || (!BF && NK > 128)) ? 2 : KS < 4 ? KS : 4;
+    const LinRows<BF, L::kRowA, KS> at_a(n, g);
+    const LinRows<BF, L::kRowC, 1> at_x(n, g);
+    const LinCols<BF, L::kRowC, CT> at_c(ct0 * 16, n, g);
     lin_wait_lds();
     lin_wait_lds();
     for (int it = 0; it < chunks; ++it) {
         const int tc = t0 + number(it) * C;
         lin_wait_lds();
         if constexpr (kAhead == 0) lin_wait_lds();
-        const lds_char* rows_at = lds + L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes;
-        const lds_char* vec = lds + L::kVec + (it & 1) * 4 * C * 4;
-        const lds_char* st = lds + L::kState + (it & 1) * L::kStateBytes;
+        const lds_char* vec = lds + L::kVec + (it & 1) * L::kVecBytes;
         lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
-        LinFrag<BF> fa[KS];
+        const uint32_t stage = stage_of(it);
+        const LinRows<BF, L::kRowA, KS> ra(at_a, stage), rs(at_a, lds0 + L::kState + (it & 1) * L::kStateBytes);
+        const LinCols<BF, L::kRowC, CT> rc(at_c, stage);
+        // Reads go out together, as many as registers hold (KB steps), before
+        // the products that wait for them.
+        LinFrag<BF> fa[KS], fs[L::kParts][CT][KB];
         f32x4 acc[CT];
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) fa[ks] = lin_rows<BF, L::kRowA>(rows_at + L::kA, rt * 16, ks, n, g);
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[c] = zero4();
 #pragma unroll
-        for (int k = 0; k < L::kParts; ++k)
+        for (int k0 = 0; k0 < KS; k0 += KB) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+            for (int ks = 0; ks < KB; ++ks) {
+                if (k0 + ks >= KS) break;
+                fa[k0 + ks] = ra.get(L::kA, rt * 16, k0 + ks);
 #pragma unroll
-                for (int c = 0; c < CT; ++c)
-                    acc[c] = lin_mma(lin_rows<BF, L::kRowA>(st + k * kLinTile * L::kRowA, (ct0 + c) * 16, ks, n, g), fa[ks], acc[c]);
-        const float gh = lds_get<float>(vec + row * 4), gl = lds_get<float>(vec + (C + row) * 4);
-        const float of = lds_get<float>(vec + (2 * C + row) * 4);
+                for (int k = 0; k < L::kParts; ++k)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) acc[c] *= of;
+                    for (int c = 0; c < CT; ++c) fs[k][c][ks] = rs.get(k * kLinTile * L::kRowA, (ct0 + c) * 16, k0 + ks);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int ks = 0; ks < KB; ++ks) {
+                if (k0 + ks >= KS) break;
+#pragma unroll
+                for (int k = 0; k < L::kParts; ++k)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fs[k][c][ks], fa[k0 + ks], acc[c]);
+            }
+        }
+        // products of the rows with every row of the chunk (tiles on the other
+        // side of the diagonal are masked whole), and what their decays need
+        f32x4 pr[C / 16];
+#pragma unroll
+        for (int i = 0; i < C / 16; ++i) pr[i] = zero4();
+#pragma unroll
+        for (int i0 = 0; i0 < C / 16; i0 += 2) {
+#pragma unroll
+            for (int k0 = 0; k0 < KS; k0 += KB) {
+                LinFrag<BF> fb[2][KB];
+#pragma unroll
+                for (int ks = 0; ks < KB; ++ks) {
+                    if (k0 + ks >= KS) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) fb[i][ks] = ra.get(L::kB, (i0 + i) * 16, k0 + ks);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int ks = 0; ks < KB; ++ks) {
+                    if (k0 + ks >= KS) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) pr[i0 + i] = lin_mma(fb[i][ks], fa[k0 + ks], pr[i0 + i]);
+                }
+            }
+        }
+        LinFrag<BF> fc[C / 32][CT];
+#pragma unroll
+        for (int m = 0; m < C / 32; ++m)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) fc[m][c] = rc.get(L::kC, m, c);
+        const float out = lds_get<float>(vec + (kLinOut * C + row) * 4), before = lds_get<float>(vec + (kLinFirst * C + row) * 4);
+        const bool far = __builtin_amdgcn_readfirstlane(lds_get<int>(vec + kLinWhole * C * 4 + 4)) != 0;
+        f32x4 in[C / 16];
+#pragma unroll
+        for (int i = 0; i < C / 16; ++i) in[i] = lds_get<f32x4>(vec + (kLinIn * C + 16 * i + 4 * g) * 4);
+        if (far) {
+            const float gh = lds_get<float>(vec + (kLinGh * C + row) * 4), gl = lds_get<float>(vec + (kLinGl * C + row) * 4);
+#pragma unroll
+            for (int i = 0; i < C / 16; ++i) {
+                const f32x4 ih = lds_get<f32x4>(vec + (kLinGh * C + 16 * i + 4 * g) * 4), il = lds_get<f32x4>(vec + (kLinGl * C + 16 * i + 4 * g) * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float d = (gh - ih[j]) + (gl - il[j]);
+                    in[i][j] = exp2_hw(kRev ? -d : d) * (kRev ? p.scale : 1.f);
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[c] *= before;
         float sums_x = 0.f, sums_w = 0.f;
         if constexpr (L::kGrad) {
-            if (it > 0) emit(it - 1);
             if (R.sum_x) {
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
                     const int col = (ct0 + c) * 16 + 4 * g;
-                    const lds_char* at = rows_at + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
+                    const lds_char* at = lds_at32(stage) + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
                     f32x4 x;
                     if constexpr (BF) x = __builtin_convertvector(lds_get<bf16x4>(at), f32x4);
                     else x = lds_get<f32x4>(at);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sums_x = fmaf(acc[c][j], x[j], sums_x);
                 }
-                sums_x = lin_sum_groups(sums_x) * oscale;
+                sums_x = lin_sum_groups(sums_x) * (out * oscale);
                 if (g == 0) lds_put(sums + ((1 + RT + ct0) * C + row) * 4, sums_x);
             }
         }
 #pragma unroll
-        for (int m = 0; m < C / 32; ++m) {
-            // (pairs of tiles that hold any token at or before the rows, or
-            // at or behind them)
-            if (kRev ? 2 * m + 1 < rt : 2 * m > rt) {
-                if constexpr (MODE == kLinDq) {
-                    if (R.sum_x && ct0 == 0 && lane < 32) lds_put(sums + ((1 + rt) * C + 32 * m + lane) * 4, 0.f);
-                }
-                continue;
-            }
-            f32x4 pr[2];
+        for (int i = 0; i < C / 16; ++i) {
+            const int col = 16 * i + 4 * g;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i0 = 32 * m + 16 * half, col = i0 + 4 * g;
-                pr[half] = zero4();
-                // (a tile on the other side of the rows is masked whole)
+            for (int j = 0; j < 4; ++j) pr[i][j] = (kRev ? col + j >= row : col + j <= row) ? pr[i][j] * in[i][j] : 0.f;
+            if constexpr (MODE == kLinDq) {
+                if (R.sum_x) {
+                    const LinRows<BF, L::kRowC, 1> rx(at_x, stage);
+                    const f32x4 other = lin_mma(rx.get(L::kC, 16 * i, 0), rx.get(L::kX, rt * 16, 0), zero4());
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) pr[half] = lin_mma(lin_rows<BF, L::kRowA>(rows_at + L::kB, i0, ks, n, g), fa[ks], pr[half]);
-                const f32x4 ih = lds_get<f32x4>(vec + col * 4), il = lds_get<f32x4>(vec + (C + col) * 4);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float d = (gh - ih[j]) + (gl - il[j]);
-                    const bool in = kRev ? col + j >= row : col + j <= row;
-                    pr[half][j] = in ? pr[half][j] * (exp2_hw(kRev ? -d : d) * pscale) : 0.f;
-                }
-                if constexpr (MODE == kLinDq) {
-                    if (R.sum_x) {
-                        const f32x4 other = lin_mma(lin_rows<BF, L::kRowC>(rows_at + L::kC, i0, 0, n, g),
-                                                    lin_rows<BF, L::kRowC>(rows_at + L::kX, rt * 16, 0, n, g), zero4());
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float mm = col + j < row ? other[j] * pr[half][j] * oscale : 0.f;
-                            sums_w += mm;
-                            const float down = lanes_sum<16>(mm);
-                            if (n == 0 && ct0 == 0) lds_put(sums + ((1 + rt) * C + col + j) * 4, down);
-                        }
+                    for (int j = 0; j < 4; ++j) {
+                        const float mm = col + j < row ? other[j] * pr[i][j] * (out * oscale) : 0.f;
+                        sums_w += mm;
+                        const float down = lanes_sum<16>(mm);
+                        if (n == 0 && ct0 == 0) lds_put(sums + ((1 + rt) * C + col + j) * 4, down);
                     }
                 }
             }
-            LinSplit<BF, 2> pp;
-            pp.set(__builtin_shufflevector(pr[0], pr[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        }
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
-                acc[c] = lin_mma(lin_cols<BF, L::kRowC>(rows_at + L::kC, m, (ct0 + c) * 16, n, g), pp, acc[c]);
+        for (int m = 0; m < C / 32; ++m) {
+            LinSplit<BF, 2> pp;
+            pp.set(__builtin_shufflevector(pr[2 * m], pr[2 * m + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fc[m][c], pp, acc[c]);
         }
         if constexpr (MODE == kLinDq) {
             if (R.sum_x) {
@@ -674,7 +854,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 const int col = col0 + (ct0 + c) * 16 + 4 * g;
-                const f32x4 o = t < tl ? acc[c] * oscale : zero4();
+                const f32x4 o = t < tl ? acc[c] * (out * oscale) : zero4();
                 const int64_t at = (bh * p.T + t) * R.nv + col;
                 if (R.out_wide) {
                     if (col < R.nv) {
@@ -692,17 +872,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             }
         }
     }
-    if constexpr (L::kGrad) {
-        __syncthreads();
-        if (chunks > 0) emit(chunks - 1);
-    }
-    // rows behind the last chunk
-    const int64_t z0 = t0 + (int64_t)chunks * C;
-    for (int64_t i = z0 * cols + (int)threadIdx.x; i < (int64_t)t1 * cols; i += kLinThreads - kLinMovers) {
-        const int64_t at = (bh * p.T + i / cols) * R.nv + col0 + i % cols;
-        if (R.out_bf16) reinterpret_cast<__bf16*>(R.out)[at] = (__bf16)0.f;
-        else reinterpret_cast<float*>(R.out)[at] = 0.f;
-    }
+    if constexpr (L::kGrad) __syncthreads();
 }
 
 // Workgroups: the tiles of a unit (a head of a sequence, or a segment of one)
