@@ -55,7 +55,7 @@ int64_t lin_blocks(int64_t units, int tiles) { return ceil_div(units, kXcds) * k
 struct LinPlanSizes {
     int nseg, seg_len;
     int64_t units;
-    size_t sum, sum_d, decay, w, x, y, cx, cy, share, dla, dq, dk, bytes;
+    size_t sum, sum_d, decay, w, x, v, y, cx, cy, share, dla, dq, dk, bytes;
 };
 LinPlanSizes lin_plan(const gdn_lin_shape& s, bool grad) {
     LinPlanSizes pl{};
@@ -80,6 +80,7 @@ LinPlanSizes lin_plan(const gdn_lin_shape& s, bool grad) {
         pl.sum_d = take(pl.nseg > 1, pl.units * plane);
         pl.w = take(true, tiles * tokens);
         pl.x = take(true, tiles * tokens);
+        pl.v = take(true, tiles * tokens);
         pl.y = take(true, tiles * tokens);
         pl.cx = take(true, tiles * bh * ceil_div(s.T, C));
         pl.cy = take(true, tiles * bh * ceil_div(s.T, C));
@@ -352,6 +353,7 @@ gdn_status gdn_lin_bwd(const gdn_lin_shape* s, const void* dO, const void* q, co
     rk.x = tk;
     rk.first = dS_final;
     rk.carry = carry_d;
+    rk.sum_w = sum(pl.v);
     rk.sum_x = sum(pl.y);
     rk.chunk_x = sum(pl.cy);
     LinRole rv = lin_role(tk, tq, td, s->d_k, s->d_v, dv, bf);
@@ -382,6 +384,7 @@ gdn_status gdn_lin_bwd(const gdn_lin_shape* s, const void* dO, const void* q, co
         LinDecayParams d{};
         d.sum_w = rq.sum_w;
         d.sum_x = rq.sum_x;
+        d.sum_v = rk.sum_w;
         d.sum_y = rk.sum_x;
         d.chunk_x = rq.chunk_x;
         d.chunk_y = rk.chunk_x;

@@ -51,8 +51,8 @@ struct LinRole {
     const float* end_grad;  // gradient of the last state (for <D, S> at the end), or null
     void* out;              // [B, H, T, nv]
     int out_bf16, out_wide;
-    float* sum_w;           // [tiles, B H, T]: pairs inside the chunk
-    float* sum_x;           // [tiles, B H, T]: pairs with one token outside
+    float* sum_w;           // [tiles, B H, T]: a row's pairs inside its chunk
+    float* sum_x;           // [tiles, B H, T]: its pairs with tokens outside
     float* chunk_x;         // [tiles, B H, chunks]: their sums over a chunk
     float* end_share;       // [tiles, B H]
 };
@@ -168,13 +168,14 @@ __device__ __forceinline__ f32x4 lin_mma(const LinFrag<BF>& a, const LinSplit<BF
 }
 
 // Rows of ROWB bytes in LDS, without padding between them; piece p (16 bytes)
-// of row r lies at p ^ turn(r), so that the same piece of 16 rows, which a
-// matrix operand is read from, covers all banks.
+// of row r lies at p ^ turn(r), so that what is read together covers all banks:
+// the same piece of 16 rows, and a pair of pieces of 8 rows (the transposing
+// read).  turn(r) counts rows that begin at the same bank, in steps of two first.
 template <int ROWB>
 __device__ __forceinline__ int lin_turn(int r) {
-    if constexpr (ROWB % 256 == 0) return r & 15;
-    else if constexpr (ROWB % 128 == 0) return (r >> 1) & 7;
-    else return (r >> 2) & 3;
+    if constexpr (ROWB % 256 == 0) return ((r & 7) << 1) | ((r >> 3) & 1);
+    else if constexpr (ROWB % 128 == 0) return (((r >> 1) & 3) << 1) | ((r >> 3) & 1);
+    else return ((r >> 2) & 1) << 1 | ((r >> 3) & 1);
 }
 template <int ROWB>
 __device__ __forceinline__ int lin_piece(int r, int p) { return r * ROWB + ((p ^ lin_turn<ROWB>(r)) << 4); }
@@ -367,8 +368,8 @@ struct LinPlan {
     static constexpr int kVec = 0;                                  // of two chunks: see LinDecays
     static constexpr int kVecBytes = (6 * C + 4) * 4;
     static constexpr int kLog = kVec + 2 * kVecBytes;               // log_alpha of four chunks
-    static constexpr int kSums = kLog + 4 * 64 * 4;                 // of two: rows, columns of each row tile, x of each column tile
-    static constexpr int kSumBytes = kGrad ? (1 + C / 16 + 2) * C * 4 : 0;
+    static constexpr int kSums = kLog + 4 * 64 * 4;                 // of two: pairs inside, pairs outside by column tile
+    static constexpr int kSumBytes = kGrad ? 3 * C * 4 : 0;
     static constexpr int kState = (kSums + 2 * kSumBytes + 255) / 256 * 256;
     static constexpr int kStage = kState + (kOut ? 2 * kStateBytes : 0);
     static constexpr int kRoom = 160 * 1024 - kStage;
@@ -419,6 +420,8 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 
     if (wave12 >= 8) {
         // ---- the waves that move rows ----
+        // (few instructions that all others wait for)
+        __builtin_amdgcn_s_setprio(3);
         auto head = [&](const LinTensor& x, int c) __attribute__((always_inline)) {
             return reinterpret_cast<const char*>(x.p) + (b * x.sb + (h / x.rep) * x.sh + c) * EB;
         };
@@ -514,18 +517,13 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 if (!R.sum_x || wave != 1) return;
                 const lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
                 const int ch = number(it), t = t0 + ch * C + lane;
-                float w = 0.f, x = 0.f;
+                float x = 0.f;
                 if (lane < C) {
-                    x = lds_get<float>(sums + ((1 + RT) * C + lane) * 4);
-                    if constexpr (RT == 2) x += lds_get<float>(sums + ((2 + RT) * C + lane) * 4);
-                    if constexpr (MODE == kLinDq) {
-                        w = lds_get<float>(sums + lane * 4);
-#pragma unroll
-                        for (int i = 0; i < RT; ++i) w -= lds_get<float>(sums + ((1 + i) * C + lane) * 4);
-                    }
+                    x = lds_get<float>(sums + (C + lane) * 4);
+                    if constexpr (RT == 2) x += lds_get<float>(sums + (2 * C + lane) * 4);
                     if (t < tl) {
                         R.sum_x[part * p.T + t] = x;
-                        if constexpr (MODE == kLinDq) R.sum_w[part * p.T + t] = w;
+                        R.sum_w[part * p.T + t] = lds_get<float>(sums + lane * 4);
                     } else {
                         x = 0.f;
                     }
@@ -555,10 +553,12 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             } else {
                 if (kAhead > 1 && is_full(it + kAhead - 1)) lin_wait<(kAhead - 1) * kLoads>();
                 else lin_wait<0>();
+                // (rows that are one chunk ahead come first, two ahead can wait)
                 load_log(it + kAhead + 1);
+                if constexpr (kAhead > 1) decays(it + 1);
                 load(it + kAhead);
             }
-            decays(it + 1);
+            if constexpr (kAhead <= 1) decays(it + 1);
             if (it > 0) emit(it - 1);
         }
         if constexpr (L::kGrad) {
@@ -750,13 +750,14 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                     for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fs[k][c][ks], fa[k0 + ks], acc[c]);
             }
         }
-        // products of the rows with every row of the chunk (tiles on the other
-        // side of the diagonal are masked whole), and what their decays need
+        // products of the rows with the pairs of tiles that hold any row on their
+        // side of the diagonal, and what their decays need
         f32x4 pr[C / 16];
 #pragma unroll
         for (int i = 0; i < C / 16; ++i) pr[i] = zero4();
 #pragma unroll
         for (int i0 = 0; i0 < C / 16; i0 += 2) {
+            if (kRev ? i0 + 1 < rt : i0 > rt) continue;
 #pragma unroll
             for (int k0 = 0; k0 < KS; k0 += KB) {
                 LinFrag<BF> fb[2][KB];
@@ -780,6 +781,13 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         for (int m = 0; m < C / 32; ++m)
 #pragma unroll
             for (int c = 0; c < CT; ++c) fc[m][c] = rc.get(L::kC, m, c);
+        LinFrag<BF> fx[L::kGrad ? C / 16 : 1], fx_row;
+        if constexpr (L::kGrad) {
+            const LinRows<BF, L::kRowC, 1> rx(at_x, stage);
+            fx_row = rx.get(L::kX, rt * 16, 0);
+#pragma unroll
+            for (int i = 0; i < C / 16; ++i) fx[i] = rx.get(L::kC, 16 * i, 0);
+        }
         const float out = lds_get<float>(vec + (kLinOut * C + row) * 4), before = lds_get<float>(vec + (kLinFirst * C + row) * 4);
         const bool far = __builtin_amdgcn_readfirstlane(lds_get<int>(vec + kLinWhole * C * 4 + 4)) != 0;
         f32x4 in[C / 16];
@@ -813,7 +821,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                     for (int j = 0; j < 4; ++j) sums_x = fmaf(acc[c][j], x[j], sums_x);
                 }
                 sums_x = lin_sum_groups(sums_x) * (out * oscale);
-                if (g == 0) lds_put(sums + ((1 + RT + ct0) * C + row) * 4, sums_x);
+                if (g == 0) lds_put(sums + ((1 + ct0) * C + row) * 4, sums_x);
             }
         }
 #pragma unroll
@@ -821,17 +829,11 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             const int col = 16 * i + 4 * g;
 #pragma unroll
             for (int j = 0; j < 4; ++j) pr[i][j] = (kRev ? col + j >= row : col + j <= row) ? pr[i][j] * in[i][j] : 0.f;
-            if constexpr (MODE == kLinDq) {
+            if constexpr (L::kGrad) {
                 if (R.sum_x) {
-                    const LinRows<BF, L::kRowC, 1> rx(at_x, stage);
-                    const f32x4 other = lin_mma(rx.get(L::kC, 16 * i, 0), rx.get(L::kX, rt * 16, 0), zero4());
+                    const f32x4 other = lin_mma(fx[i], fx_row, zero4());
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float mm = col + j < row ? other[j] * pr[i][j] * (out * oscale) : 0.f;
-                        sums_w += mm;
-                        const float down = lanes_sum<16>(mm);
-                        if (n == 0 && ct0 == 0) lds_put(sums + ((1 + rt) * C + col + j) * 4, down);
-                    }
+                    for (int j = 0; j < 4; ++j) sums_w += (kRev ? col + j > row : col + j < row) ? other[j] * pr[i][j] : 0.f;
                 }
             }
         }
@@ -842,9 +844,9 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 #pragma unroll
             for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fc[m][c], pp, acc[c]);
         }
-        if constexpr (MODE == kLinDq) {
+        if constexpr (L::kGrad) {
             if (R.sum_x) {
-                sums_w = lin_sum_groups(sums_w);
+                sums_w = lin_sum_groups(sums_w) * (out * oscale);
                 if (g == 0 && ct0 == 0) lds_put(sums + row * 4, sums_w);
             }
         }
@@ -956,8 +958,9 @@ static __global__ __launch_bounds__(256) void gdn_lin_chain_kernel(LinChainParam
 
 // The decay's gradient from the passes' sums: a wave to a chunk.
 struct LinDecayParams {
-    const float* sum_w;     // [tiles, B H, T]
+    const float* sum_w;     // [tiles, B H, T]: of the pass of dq
     const float* sum_x;
+    const float* sum_v;     // of the pass of dk
     const float* sum_y;
     const float* chunk_x;   // [tiles, B H, chunks]
     const float* chunk_y;
@@ -983,7 +986,7 @@ static __global__ __launch_bounds__(256) void gdn_lin_decay_kernel(LinDecayParam
         for (int i = 0; i < p.tiles; ++i) {
             const int64_t row = i * p.bhs + bh;
             if (lane < p.C && t < len) {
-                w += p.sum_w[row * p.T + t];
+                w += (double)p.sum_w[row * p.T + t] - p.sum_v[row * p.T + t];
                 x += p.sum_x[row * p.T + t];
                 y += p.sum_y[row * p.T + t];
             }
