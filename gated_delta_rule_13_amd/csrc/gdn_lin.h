@@ -70,7 +70,8 @@ struct LinParams {
     float scale;
 };
 
-enum LinMode { kLinFwd, kLinDq, kLinDk, kLinDv, kLinSum, kLinSumD };
+// (kLinFine: the forward pass to fp32)
+enum LinMode { kLinFwd, kLinFine, kLinDq, kLinDk, kLinDv, kLinSum, kLinSumD };
 
 // Four waves form the outputs of a chunk, four keep the state and four move rows:
 // all work on the same chunk at once, one wave of each kind to a SIMD.
@@ -355,10 +356,16 @@ struct LinPlan {
     static constexpr bool kOut = MODE < kLinSum, kGrad = MODE == kLinDq || MODE == kLinDk;
     static constexpr int kEl = BF ? 2 : 4;
     static constexpr int kRowA = NK * kEl, kRowC = kLinTile * kEl;
-    // the state as an operand: bf16 numbers that add up to it (three where the
-    // decay's gradient is summed over many chunks), or fp32
-    static constexpr int kParts = BF ? (kGrad ? 3 : 2) : 1;
-    static constexpr int kValueParts = 3;                           // decayed values, whose sums the state is
+    // What is computed becomes an operand of bf16 rows in parts that add up to it:
+    // decayed values three (their sums are the state, which stays fp32); the
+    // state and the products of rows one where the output is bf16 (a rounding
+    // like the output's own: prompts come out 2.2e-3 off in the mean, and 1.7e-3
+    // with two parts, 17 us slower at 4 x 4096 x 16 x 128), two where it is
+    // fp32; the state three where the decay's gradient is summed over many
+    // chunks.
+    static constexpr int kParts = !BF ? 1 : kGrad ? 3 : MODE == kLinFine ? 2 : 1;
+    static constexpr int kRowParts = MODE == kLinFine ? 2 : 1;
+    static constexpr int kValueParts = 3;
     static constexpr int kStateBytes = kParts * kLinTile * kRowA;
     static constexpr int kA = 0;
     static constexpr int kB = kA + (kOut ? C * kRowA : 0);
@@ -608,6 +615,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                     f32x4 x = S[t];
 #pragma unroll
                     for (int k = 0; k < L::kParts; ++k) {
+                        if (k > 0 && L::kGrad && !R.sum_x) break;
                         const u32x2 w = {lin_pack(x[0], x[1]), lin_pack(x[2], x[3])};
                         lds_put(at + k * kLinTile * L::kRowA + off, w);
                         if (k + 1 < L::kParts) {
@@ -708,7 +716,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     const int rt = RT == 4 ? wave : wave >> 1, ct0 = RT == 4 ? 0 : wave & 1;
     const int row = rt * 16 + n;
     // (steps whose reads go out together)
-    constexpr int KB = KS == 1 ? 1 : (L::kParts == 3 || (!BF && NK > 128)) ? 2 : KS < 4 ? KS : 4;
+    constexpr int KB = KS < 4 ? KS : BF || NK <= 128 ? 4 : 2;
     const LinRows<BF, L::kRowA, KS> at_a(n, g);
     const LinRows<BF, L::kRowC, 1> at_x(n, g);
     const LinCols<BF, L::kRowC, CT> at_c(ct0 * 16, n, g);
@@ -725,30 +733,41 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         const LinCols<BF, L::kRowC, CT> rc(at_c, stage);
         // Reads go out together, as many as registers hold (KB steps), before
         // the products that wait for them.
-        LinFrag<BF> fa[KS], fs[L::kParts][CT][KB];
+        LinFrag<BF> fa[KS];
         f32x4 acc[CT];
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[c] = zero4();
+        auto state_product = [&](auto first_, auto last_) __attribute__((always_inline)) {
+            constexpr int k1 = decltype(first_)::value, k2 = decltype(last_)::value;
 #pragma unroll
-        for (int k0 = 0; k0 < KS; k0 += KB) {
+            for (int k0 = 0; k0 < KS; k0 += KB) {
+                LinFrag<BF> fs[k2 - k1][CT][KB];
 #pragma unroll
-            for (int ks = 0; ks < KB; ++ks) {
-                if (k0 + ks >= KS) break;
-                fa[k0 + ks] = ra.get(L::kA, rt * 16, k0 + ks);
+                for (int ks = 0; ks < KB; ++ks) {
+                    if (k0 + ks >= KS) break;
+                    if constexpr (k1 == 0) fa[k0 + ks] = ra.get(L::kA, rt * 16, k0 + ks);
 #pragma unroll
-                for (int k = 0; k < L::kParts; ++k)
+                    for (int k = k1; k < k2; ++k)
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) fs[k][c][ks] = rs.get(k * kLinTile * L::kRowA, (ct0 + c) * 16, k0 + ks);
+                        for (int c = 0; c < CT; ++c) fs[k - k1][c][ks] = rs.get(k * kLinTile * L::kRowA, (ct0 + c) * 16, k0 + ks);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int ks = 0; ks < KB; ++ks) {
+                    if (k0 + ks >= KS) break;
+#pragma unroll
+                    for (int k = k1; k < k2; ++k)
+#pragma unroll
+                        for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fs[k - k1][c][ks], fa[k0 + ks], acc[c]);
+                }
             }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int ks = 0; ks < KB; ++ks) {
-                if (k0 + ks >= KS) break;
-#pragma unroll
-                for (int k = 0; k < L::kParts; ++k)
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fs[k][c][ks], fa[k0 + ks], acc[c]);
-            }
+        };
+        const bool sums_wanted = L::kGrad && R.sum_x;
+        if constexpr (L::kGrad && L::kParts > 1) {
+            state_product(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
+            if (sums_wanted) state_product(std::integral_constant<int, 1>{}, std::integral_constant<int, L::kParts>{});
+        } else {
+            state_product(std::integral_constant<int, 0>{}, std::integral_constant<int, L::kParts>{});
         }
         // products of the rows with the pairs of tiles that hold any row on their
         // side of the diagonal, and what their decays need
@@ -781,13 +800,6 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         for (int m = 0; m < C / 32; ++m)
 #pragma unroll
             for (int c = 0; c < CT; ++c) fc[m][c] = rc.get(L::kC, m, c);
-        LinFrag<BF> fx[L::kGrad ? C / 16 : 1], fx_row;
-        if constexpr (L::kGrad) {
-            const LinRows<BF, L::kRowC, 1> rx(at_x, stage);
-            fx_row = rx.get(L::kX, rt * 16, 0);
-#pragma unroll
-            for (int i = 0; i < C / 16; ++i) fx[i] = rx.get(L::kC, 16 * i, 0);
-        }
         const float out = lds_get<float>(vec + (kLinOut * C + row) * 4), before = lds_get<float>(vec + (kLinFirst * C + row) * 4);
         const bool far = __builtin_amdgcn_readfirstlane(lds_get<int>(vec + kLinWhole * C * 4 + 4)) != 0;
         f32x4 in[C / 16];
@@ -807,48 +819,52 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         }
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[c] *= before;
-        float sums_x = 0.f, sums_w = 0.f;
-        if constexpr (L::kGrad) {
-            if (R.sum_x) {
-#pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    const int col = (ct0 + c) * 16 + 4 * g;
-                    const lds_char* at = lds_at32(stage) + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
-                    f32x4 x;
-                    if constexpr (BF) x = __builtin_convertvector(lds_get<bf16x4>(at), f32x4);
-                    else x = lds_get<f32x4>(at);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) sums_x = fmaf(acc[c][j], x[j], sums_x);
-                }
-                sums_x = lin_sum_groups(sums_x) * (out * oscale);
-                if (g == 0) lds_put(sums + ((1 + ct0) * C + row) * 4, sums_x);
-            }
-        }
+        const float scale = out * oscale;
 #pragma unroll
         for (int i = 0; i < C / 16; ++i) {
             const int col = 16 * i + 4 * g;
 #pragma unroll
             for (int j = 0; j < 4; ++j) pr[i][j] = (kRev ? col + j >= row : col + j <= row) ? pr[i][j] * in[i][j] : 0.f;
-            if constexpr (L::kGrad) {
-                if (R.sum_x) {
-                    const f32x4 other = lin_mma(fx[i], fx_row, zero4());
+        }
+        if constexpr (L::kGrad) {
+            if (sums_wanted) {
+                const LinRows<BF, L::kRowC, 1> rx(at_x, stage);
+                const LinFrag<BF> mine = rx.get(L::kX, rt * 16, 0);
+                f32x4 other[C / 16], x[CT];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) sums_w += (kRev ? col + j > row : col + j < row) ? other[j] * pr[i][j] : 0.f;
+                for (int i = 0; i < C / 16; ++i) other[i] = lin_mma(rx.get(L::kC, 16 * i, 0), mine, zero4());
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    const int col = (ct0 + c) * 16 + 4 * g;
+                    const lds_char* at = lds_at32(stage) + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
+                    if constexpr (BF) x[c] = __builtin_convertvector(lds_get<bf16x4>(at), f32x4);
+                    else x[c] = lds_get<f32x4>(at);
+                }
+                float outside = 0.f, inside = 0.f;
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) outside = fmaf(acc[c][j], x[c][j], outside);
+#pragma unroll
+                for (int i = 0; i < C / 16; ++i) {
+                    const int col = 16 * i + 4 * g;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) inside = fmaf(other[i][j], col + j == row ? 0.f : pr[i][j], inside);
+                }
+                outside = lin_sum_groups(outside) * scale;
+                inside = lin_sum_groups(inside) * scale;
+                if (g == 0) {
+                    lds_put(sums + ((1 + ct0) * C + row) * 4, outside);
+                    if (ct0 == 0) lds_put(sums + row * 4, inside);
                 }
             }
         }
 #pragma unroll
         for (int m = 0; m < C / 32; ++m) {
-            LinSplit<BF, 2> pp;
+            LinSplit<BF, L::kRowParts> pp;
             pp.set(__builtin_shufflevector(pr[2 * m], pr[2 * m + 1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
             for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fc[m][c], pp, acc[c]);
-        }
-        if constexpr (L::kGrad) {
-            if (R.sum_x) {
-                sums_w = lin_sum_groups(sums_w) * (out * oscale);
-                if (g == 0 && ct0 == 0) lds_put(sums + row * 4, sums_w);
-            }
         }
         // (rows behind the sequence's end inside its last chunk are 0)
         const int t = tc + row;
@@ -856,7 +872,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 const int col = col0 + (ct0 + c) * 16 + 4 * g;
-                const f32x4 o = t < tl ? acc[c] * (out * oscale) : zero4();
+                const f32x4 o = t < tl ? acc[c] * scale : zero4();
                 const int64_t at = (bh * p.T + t) * R.nv + col;
                 if (R.out_wide) {
                     if (col < R.nv) {
@@ -880,7 +896,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 // Workgroups: the tiles of a unit (a head of a sequence, or a segment of one)
 // beside each other on one XCD, whose L2 then holds the rows that they share;
 // neighbouring units too, whose heads may share queries and keys.
-enum LinSet { kLinSetFwd, kLinSetQk, kLinSetV, kLinSetAll, kLinSetSum, kLinSetSums };
+enum LinSet { kLinSetFwd, kLinSetFine, kLinSetQk, kLinSetV, kLinSetAll, kLinSetSum, kLinSetSums };
 constexpr int kXcds = 8;
 
 constexpr int lin_most(int a, int b) { return a > b ? a : b; }
@@ -892,6 +908,7 @@ struct LinBytes {
     static constexpr int kRows = LinPlan<BF, NK, C, kLinFwd>::kBytes;
     static constexpr int kSum = LinPlan<BF, NK, C, kLinSum>::kBytes;
     static constexpr int value = SET == kLinSetFwd || SET == kLinSetV     ? kRows
+                                 : SET == kLinSetFine                      ? LinPlan<BF, NK, C, kLinFine>::kBytes
                                  : SET == kLinSetSum || SET == kLinSetSums ? kSum
                                  : SET == kLinSetQk                        ? kGrad
                                                                            : lin_most(kGrad, kRows);
@@ -914,6 +931,8 @@ __global__ __launch_bounds__(kLinThreads) void gdn_lin_kernel(LinParams p) {
     if (at / tiles >= per || unit >= p.units) return;
     if constexpr (SET == kLinSetFwd) {
         lin_pass<BF, NK, C, kLinFwd>(p, p.r[0], unit, tile, lin_lds);
+    } else if constexpr (SET == kLinSetFine) {
+        lin_pass<BF, NK, C, kLinFine>(p, p.r[0], unit, tile, lin_lds);
     } else if constexpr (SET == kLinSetV) {
         lin_pass<BF, NK, C, kLinDv>(p, p.r[0], unit, tile, lin_lds);
     } else if constexpr (SET == kLinSetSum) {

@@ -11,6 +11,11 @@ values, which the reference gives on absolute inputs (everything but the signs i
 products and sums).  The decay's gradient is in addition a sum over later tokens
 of rounded parts q . dq and k . dk, whose errors are independent: 2^-16 times the
 root of their number times the largest of them.
+
+Where an output is bf16, the state and the products of rows (not the decayed
+values, nor what fp32 outputs and the decay's gradient are made of) are rounded to
+one bf16 number: every term of the sum, which holds one of the two, is off by half
+a step more, 2^-8 of it.
 """
 from __future__ import annotations
 
@@ -47,11 +52,13 @@ def lin_bound(a, **k):
 
 def within(name, got, want, bound):
     """Every number within half a step of its type of the exact one, plus
-    LIN_TOL times `bound` there."""
+    LIN_TOL times `bound` there (bf16: and half a step of the terms)."""
     assert tuple(got.shape) == tuple(want.shape), (name, tuple(got.shape), tuple(want.shape))
     g, w = got.detach().double().cpu(), want.detach().double()
     assert torch.isfinite(g).all(), f"{name}: numbers that are not finite"
-    off = (g - w).abs() - torch.finfo(got.dtype).eps / 2 * w.abs() - LIN_TOL * bound.detach() * (1 + torch.finfo(got.dtype).eps)
+    half = torch.finfo(got.dtype).eps / 2
+    each = LIN_TOL + (half if got.dtype is torch.bfloat16 else 0)
+    off = (g - w).abs() - half * w.abs() - each * bound.detach() * (1 + 2 * half)
     worst = float(off.max())
     assert worst <= 1e-30, f"{name}: off by {worst:.3e} more than allowed (largest number {float(w.abs().max()):.3e})"
 
