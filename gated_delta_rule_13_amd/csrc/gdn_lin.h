@@ -720,6 +720,48 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     const LinRows<BF, L::kRowA, KS> at_a(n, g);
     const LinRows<BF, L::kRowC, 1> at_x(n, g);
     const LinCols<BF, L::kRowC, CT> at_c(ct0 * 16, n, g);
+    // A chunk's rows are stored during the next chunk, while that waits for its
+    // reads.
+    struct Rows {
+        f32x4 c[CT];
+    } done;
+    float done_scale = 0.f;
+    int done_at = 0;
+    char* const out_base = reinterpret_cast<char*>(R.out) + (bh * p.T * R.nv + col0) * (R.out_bf16 ? 2 : 4);
+    auto store = [&]() __attribute__((always_inline)) {
+        if (done_at >= t1) return;
+        // (rows behind the sequence's end inside its last chunk are 0)
+        const bool live = done_at < tl;
+        const int64_t first = (int64_t)done_at * R.nv;
+        if (BF && CT == 2 && R.out_wide && R.out_bf16 && cols == kLinTile && R.nv % 8 == 0) {
+            // 16 bytes a lane: lanes of even g take their neighbour's columns of
+            // the first tile, those of odd g theirs of the second
+            const f32x4 a = live ? done.c[0] * done_scale : zero4(), b = live ? done.c[CT - 1] * done_scale : zero4();
+            const auto lo = __builtin_amdgcn_permlane16_swap(lin_pack(a[0], a[1]), lin_pack(b[0], b[1]), false, false);
+            const auto hi = __builtin_amdgcn_permlane16_swap(lin_pack(a[2], a[3]), lin_pack(b[2], b[3]), false, false);
+            *reinterpret_cast<u32x4*>(out_base + (first + (g & 1) * 16 + (g >> 1) * 8) * 2) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+            return;
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            const int col = (ct0 + c) * 16 + 4 * g;
+            const f32x4 o = live ? done.c[c] * done_scale : zero4();
+            const int64_t at = first + col;
+            if (R.out_wide) {
+                if (col < cols) {
+                    if (R.out_bf16) *reinterpret_cast<bf16x4*>(out_base + at * 2) = __builtin_convertvector(o, bf16x4);
+                    else *reinterpret_cast<f32x4*>(out_base + at * 4) = o;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (col + j < cols) {
+                        if (R.out_bf16) *reinterpret_cast<__bf16*>(out_base + (at + j) * 2) = (__bf16)o[j];
+                        else *reinterpret_cast<float*>(out_base + (at + j) * 4) = o[j];
+                    }
+            }
+        }
+    };
     lin_wait_lds();
     lin_wait_lds();
     for (int it = 0; it < chunks; ++it) {
@@ -734,7 +776,8 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         // Reads go out together, as many as registers hold (KB steps), before
         // the products that wait for them.
         LinFrag<BF> fa[KS];
-        f32x4 acc[CT];
+        Rows now;
+        f32x4(&acc)[CT] = now.c;
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[c] = zero4();
         auto state_product = [&](auto first_, auto last_) __attribute__((always_inline)) {
@@ -752,6 +795,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                         for (int c = 0; c < CT; ++c) fs[k - k1][c][ks] = rs.get(k * kLinTile * L::kRowA, (ct0 + c) * 16, k0 + ks);
                 }
                 __builtin_amdgcn_sched_barrier(0);
+                if (k1 == 0 && k0 == 0 && it > 0) store();
 #pragma unroll
                 for (int ks = 0; ks < KB; ++ks) {
                     if (k0 + ks >= KS) break;
@@ -866,30 +910,11 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 #pragma unroll
             for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fc[m][c], pp, acc[c]);
         }
-        // (rows behind the sequence's end inside its last chunk are 0)
-        const int t = tc + row;
-        if (t < t1) {
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                const int col = col0 + (ct0 + c) * 16 + 4 * g;
-                const f32x4 o = t < tl ? acc[c] * scale : zero4();
-                const int64_t at = (bh * p.T + t) * R.nv + col;
-                if (R.out_wide) {
-                    if (col < R.nv) {
-                        if (R.out_bf16) *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(R.out) + at) = __builtin_convertvector(o, bf16x4);
-                        else *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(R.out) + at) = o;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (col + j < R.nv) {
-                            if (R.out_bf16) reinterpret_cast<__bf16*>(R.out)[at + j] = (__bf16)o[j];
-                            else reinterpret_cast<float*>(R.out)[at + j] = o[j];
-                        }
-                }
-            }
-        }
+        done = now;
+        done_scale = scale;
+        done_at = tc + row;
     }
+    if (chunks > 0) store();
     if constexpr (L::kGrad) __syncthreads();
 }
 
