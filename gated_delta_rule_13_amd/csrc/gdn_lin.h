@@ -298,6 +298,12 @@ __device__ __forceinline__ void lin_wait() {
     static_assert(N < 64, "");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
+// This wave's loads alone.
+template <int N>
+__device__ __forceinline__ void lin_arrived() {
+    static_assert(N < 64, "");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 // The same for waves that wait for no loads.
 __device__ __forceinline__ void lin_wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 // Where this lane's pieces of a tile of C rows lie in memory (bytes from its
@@ -422,6 +428,10 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     constexpr int kStages = L::kStages, kAhead = kStages - 1;
     auto number = [&](int it) __attribute__((always_inline)) { return kRev ? chunks - 1 - it : it; };
     auto stage_of = [&](int it) __attribute__((always_inline)) { return lds0 + L::kStage + (kStages == 1 ? 0 : it % kStages) * L::kStageBytes; };
+    // Whole chunks go straight to LDS; where their rows do not fill the tile, its
+    // rest is 0 from the start.
+    const bool direct = kAhead > 0 && R.b.direct && R.c.direct && (!L::kOut || R.a.direct) && (!L::kGrad || R.x.direct) && cols % (16 / EB) == 0;
+    const bool all = R.nk == NK && cols == kLinTile, fill = direct && !all;
     const int64_t plane = (int64_t)p.dk * p.dv;
     const int64_t part = tile * (int64_t)p.B * p.H + bh;            // (rows of the partial sums)
 
@@ -437,8 +447,6 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         // earlier.  A whole chunk goes straight to LDS and keeps kLoads loads of
         // each wave under way.
         constexpr int kLoads = (L::kOut ? 2 : 1) * LinDirect<BF, L::kRowA, C>::kSure + (L::kGrad ? 2 : 1) * LinDirect<BF, L::kRowC, C>::kSure;
-        const bool direct = kAhead > 0 && R.b.direct && R.c.direct && (!L::kOut || R.a.direct) && (!L::kGrad || R.x.direct) && cols % (16 / EB) == 0;
-        const bool all = R.nk == NK && cols == kLinTile;
         LinDirect<BF, L::kRowA, C> da, db;
         LinDirect<BF, L::kRowC, C> dc, dx;
         if (direct) {
@@ -446,8 +454,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             db.set(R.b.st, R.nk, wave, lane);
             dc.set(R.c.st, cols, wave, lane);
             if constexpr (L::kGrad) dx.set(R.x.st, cols, wave, lane);
-            // (pieces behind a row's end are not written again)
-            if (!all) {
+            if (fill) {
                 for (int i = threadIdx.x % kLinRole; i < kStages * L::kStageBytes / 16; i += kLinRole)
                     lds_put(lds + L::kStage + i * 16, u32x4{0, 0, 0, 0});
             }
@@ -539,7 +546,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 if (lane == 0) R.chunk_x[part * ((p.T + C - 1) / C) + t0 / C + ch] = x;
             }
         };
-        lin_wait<0>();
+        if (fill) lin_wait<0>();
         load_log(0);
         load_log(1);
 #pragma unroll
@@ -547,7 +554,9 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             load(i);
             if (i + 1 < kAhead || kAhead == 1) load_log(i + 2);
         }
-        lin_wait<0>();
+        // (log_alpha of the first chunk, which came first)
+        if (kAhead > 0 && is_full(0) && is_full(kAhead - 1)) lin_arrived<kAhead * kLoads>();
+        else lin_arrived<0>();
         decays(0);
         for (int it = 0; it < chunks; ++it) {
             // what chunk `it` needs has come; what was asked for since may be
@@ -631,8 +640,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             }
         };
         if constexpr (L::kOut) publish(0);
-        lin_wait_lds();
-        lin_wait_lds();
+        if (fill) lin_wait_lds();
         float total = 0.f;      // log2 of the decay so far
         for (int it = 0; it < chunks; ++it) {
             lin_wait_lds();
@@ -709,7 +717,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     // ---- the waves that form the outputs ----
     if constexpr (!L::kOut) {
         // (as many barriers as the others pass)
-        for (int it = 0; it < 2 + chunks * (kAhead == 0 ? 2 : 1); ++it) lin_wait_lds();
+        for (int it = 0; it < (fill ? 1 : 0) + chunks * (kAhead == 0 ? 2 : 1); ++it) lin_wait_lds();
         return;
     }
     const float oscale = kRev ? 1.f : p.scale;
@@ -762,8 +770,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             }
         }
     };
-    lin_wait_lds();
-    lin_wait_lds();
+    if (fill) lin_wait_lds();
     for (int it = 0; it < chunks; ++it) {
         const int tc = t0 + number(it) * C;
         lin_wait_lds();
