@@ -188,14 +188,14 @@ BlockLaunchers block_launchers(const gdn_block_norm_shape& s, bool wide) {
     if (xb) return ob ? block_launchers_1_1(s.D, wide) : block_launchers_1_0(s.D, wide);
     return ob ? block_launchers_0_1(s.D, wide) : block_launchers_0_0(s.D, wide);
 }
-// Workgroups that stay for all rows: of 256 lanes four to a compute unit, of
-// 1024 one.
-int64_t block_groups(const gdn_block_norm_shape& s, int rows, int64_t most) {
-    const int64_t need = ceil_div((int64_t)s.B * s.T, rows);
+// Workgroups, which stay for all rows: 1024 of 256 lanes forward (512 to 2048
+// measure alike, 256 50 % slower at 4 x 4096 x 2048), 512 backward, each of which
+// leaves a row of sums for the weights (152 us at that size; 1024 take 164, 256
+// 179); fewer of more lanes.
+int64_t block_groups(const gdn_block_norm_shape& s, bool grad) {
+    const int lanes = block_lanes(s.D), threads = lanes < 256 ? 256 : lanes;
+    const int64_t need = ceil_div((int64_t)s.B * s.T, threads / lanes), most = (grad ? 512 : 1024) * 256 / threads;
     return need < most ? need : most;
-}
-int64_t block_bwd_groups(const gdn_block_norm_shape& s) {
-    return block_groups(s, s.D <= 1024 ? 4 : 1, s.D <= 4096 ? 1024 : 256);
 }
 BlockParams block_params(const gdn_block_norm_shape& s, const void* o, const void* x, const void* g, const float* w_post,
                          const float* scale, const float* w_pre) {
@@ -427,14 +427,14 @@ gdn_status gdn_block_norm_fwd(const gdn_block_norm_shape* s, const void* o, cons
     const bool wide = rows4(o, s->dtype, {s->D, s->o_stride_b, s->o_stride_t}) && rows4(x, s->x_dtype, {s->x_stride_b, s->x_stride_t}) &&
                       rows4(gate, s->dtype, {s->g_stride_b, s->g_stride_t}) && rows4(x_out, s->x_dtype, {}) && rows4(y, s->dtype, {});
     const BlockLaunchers run = block_launchers(*s, wide);
-    run.fwd(p, block_groups(*s, run.rows, s->D <= 4096 ? 1024 : 256), reinterpret_cast<hipStream_t>(stream));
+    run.fwd(p, block_groups(*s, false), reinterpret_cast<hipStream_t>(stream));
     return launch_status();
 }
 
 size_t gdn_block_norm_bwd_workspace_bytes(const gdn_block_norm_shape* s) {
     clear_error();
     if (validate(s) != GDN_OK) return kInvalid;
-    return up256((size_t)block_bwd_groups(*s) * 3 * s->D * 4);
+    return up256((size_t)block_groups(*s, true) * 3 * s->D * 4);
 }
 
 gdn_status gdn_block_norm_bwd(const gdn_block_norm_shape* s, const void* dx_out, const void* dy, const void* x_out, const void* o,
@@ -469,7 +469,7 @@ gdn_status gdn_block_norm_bwd(const gdn_block_norm_shape* s, const void* dx_out,
                       rows4(gate, s->dtype, {s->g_stride_b, s->g_stride_t}) && rows4(dx_out, s->x_dtype, {}) && rows4(dy, s->dtype, {}) &&
                       rows4(dx, s->x_dtype, {}) && rows4(dO, s->dtype, {}) && rows4(dgate, s->dtype, {});
     const BlockLaunchers run = block_launchers(*s, wide);
-    const int64_t blocks = block_bwd_groups(*s);
+    const int64_t blocks = block_groups(*s, true);
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     run.bwd(q, blocks, hs);
     if (dw_post || dscale || dw_pre) launch_colsum(q.part, blocks, dw_post, s->D, dscale, s->D, hs, dw_pre, s->D);

@@ -43,6 +43,8 @@ struct BlockBwdParams {
 };
 
 constexpr int kBlockMaxD = 16384;
+// Lanes to a row.
+constexpr int block_lanes(int D) { return D <= 1024 ? 64 : D <= 4096 ? 256 : D <= 8192 ? 512 : 1024; }
 template <int L>
 constexpr int block_threads() { return L > 256 ? L : 256; }
 
@@ -192,10 +194,21 @@ __global__ __launch_bounds__(block_threads<L>()) void gdn_block_bwd_kernel(Block
     const int j = threadIdx.x % L, grp = __builtin_amdgcn_readfirstlane(threadIdx.x / L);
     const int64_t step = (int64_t)gridDim.x * kGroups;
     const float inv = 1.f / (float)p.D;
+    // (many numbers a lane in a large workgroup leave no registers for the
+    // weights, which come from the caches again for each row, and then none for
+    // the next row)
+    constexpr bool kLean = (L == 512 && K * V > 12) || L > 512, kAhead = !kLean;
     float wp[K][V], sc[K][V], wn[K][V], ap[K][V], as[K][V], an[K][V];
-    block_columns<L, K, V>(wp, p.w_post, p.D, j);
-    block_columns<L, K, V>(sc, p.scale, p.D, j);
-    block_columns<L, K, V>(wn, p.w_pre, p.D, j);
+    if constexpr (!kLean) {
+        block_columns<L, K, V>(wp, p.w_post, p.D, j);
+        block_columns<L, K, V>(sc, p.scale, p.D, j);
+        block_columns<L, K, V>(wn, p.w_pre, p.D, j);
+    }
+    auto column = [&](const float* src, const float (&w)[K][V], int k, int e) __attribute__((always_inline)) {
+        if constexpr (!kLean) return w[k][e];
+        const int c = (k * L + j) * V;
+        return src && c < p.D ? src[c + e] : 1.f;
+    };
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -217,15 +230,16 @@ __global__ __launch_bounds__(block_threads<L>()) void gdn_block_bwd_kernel(Block
             }
         }
     };
-    if (row < p.rows) load(row);
+    if (kAhead && row < p.rows) load(row);
     for (; row < p.rows; row += step) {
+        if constexpr (!kAhead) load(row);
         cur = next;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             dxc[k] = dxn[k];
             dyc[k] = dyn[k];
         }
-        if (row + step < p.rows) load(row + step);
+        if (kAhead && row + step < p.rows) load(row + step);
         float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -234,7 +248,7 @@ __global__ __launch_bounds__(block_threads<L>()) void gdn_block_bwd_kernel(Block
                 const float o = cur.o[k].get(e), x = cur.x[k].get(e);
                 s[0] = fmaf(o, o, s[0]);
                 s[1] = fmaf(x, x, s[1]);
-                s[2] = fmaf(dyc[k].get(e) * wn[k][e], x, s[2]);
+                s[2] = fmaf(dyc[k].get(e) * column(p.w_pre, wn, k, e), x, s[2]);
             }
         sum3(s);
         const float r = p.post ? 1.f / sqrtf(s[0] * inv + p.eps) : 1.f;
@@ -253,17 +267,17 @@ __global__ __launch_bounds__(block_threads<L>()) void gdn_block_bwd_kernel(Block
                 dx[e] = dxc[k].get(e);
                 if (q.dy) {
                     const float xh = cur.x[k].get(e) * rn;
-                    dx[e] = fmaf(rn, fmaf(-xh, mean, dy * wn[k][e]), dx[e]);
+                    dx[e] = fmaf(rn, fmaf(-xh, mean, dy * column(p.w_pre, wn, k, e)), dx[e]);
                     an[k][e] = fmaf(dy, xh, an[k][e]);
                 }
-                const float oh = cur.o[k].get(e) * r, n = oh * wp[k][e];
+                const float oh = cur.o[k].get(e) * r, wpk = column(p.w_post, wp, k, e), n = oh * wpk;
                 as[k][e] = fmaf(dx[e] * a, n, as[k][e]);
-                const float dxs = dx[e] * sc[k][e];
+                const float dxs = dx[e] * column(p.scale, sc, k, e);
                 dg[e] = dxs * n * slope;
                 d[k][e] = dxs * a;
                 if (p.post) {
                     ap[k][e] = fmaf(d[k][e], oh, ap[k][e]);
-                    d[k][e] *= wp[k][e];
+                    d[k][e] *= wpk;
                     t[0] = fmaf(c < p.D ? d[k][e] : 0.f, oh, t[0]);
                 }
             }

@@ -18,7 +18,6 @@ void bwd(const BlockBwdParams& q, int64_t blocks, hipStream_t st) {
 template <int L>
 BlockLaunchers pick(int numbers, bool wide) {
     BlockLaunchers r{};
-    r.rows = block_threads<L>() / L;
     if (wide) {
         switch ((numbers + 3) / 4) {
             case 1: r.fwd = fwd<L, 1, 4>; r.bwd = bwd<L, 1, 4>; break;
@@ -41,10 +40,15 @@ BlockLaunchers pick(int numbers, bool wide) {
 #define GDN_BLOCK_NAME2(xb, ob) block_launchers_##xb##_##ob
 #define GDN_BLOCK_NAME(xb, ob) GDN_BLOCK_NAME2(xb, ob)
 BlockLaunchers GDN_BLOCK_NAME(GDN_BLOCK_XB, GDN_BLOCK_OB)(int D, bool wide) {
-    // the fewest lanes that hold a row with at most sixteen numbers each
-    if (D <= 1024) return pick<64>((D + 63) / 64, wide);
-    if (D <= 4096) return pick<256>((D + 255) / 256, wide);
-    return pick<1024>((D + 1023) / 1024, wide);
+    // the fewest lanes that hold a row with at most sixteen numbers each (a
+    // thousand lanes leave the gradient too few registers: 4096 rows of 8192, bf16
+    // on an fp32 stream, take 529 us, and with 512 lanes 257; forward 68 and 78)
+    switch (block_lanes(D)) {
+        case 64: return pick<64>((D + 63) / 64, wide);
+        case 256: return pick<256>((D + 255) / 256, wide);
+        case 512: return pick<512>((D + 511) / 512, wide);
+        default: return pick<1024>((D + 1023) / 1024, wide);
+    }
 }
 
 }  // namespace gdn

@@ -113,13 +113,12 @@ GDN_LIN_DECL(256)
 LinStepLauncher lin_step_launcher_bf16(int dk, bool wide, int* rows);
 LinStepLauncher lin_step_launcher_f32(int dk, bool wide, int* rows);
 
-// norms around a block: rows: those that a workgroup holds at once
+// norms around a block
 struct BlockParams;
 struct BlockBwdParams;
 struct BlockLaunchers {
     void (*fwd)(const BlockParams&, int64_t blocks, hipStream_t);
     void (*bwd)(const BlockBwdParams&, int64_t blocks, hipStream_t);
-    int rows;
 };
 BlockLaunchers block_launchers_0_0(int D, bool wide);
 BlockLaunchers block_launchers_0_1(int D, bool wide);
