@@ -170,13 +170,16 @@ __device__ __forceinline__ f32x4 lin_mma(const LinFrag<BF>& a, const LinSplit<BF
 
 // Rows of ROWB bytes in LDS, without padding between them; piece p (16 bytes)
 // of row r lies at p ^ turn(r), so that what is read together covers all banks:
-// the same piece of 16 rows, and a pair of pieces of 8 rows (the transposing
-// read).  turn(r) counts rows that begin at the same bank, in steps of two first.
+// pieces p and p ^ 2 of 8 rows (an operand's read serves 8 lanes of each half of a
+// wave at a time), and pieces p and p ^ 1 of 8 rows (the transposing read).  So
+// the turns of 8 rows that begin at the same bank have bits 0 and 1 alike, 0 or 3,
+// and those of the next 8 have them unlike.  (With turns 0, 2, 4, .. a third of
+// all LDS cycles were conflicts.)
 template <int ROWB>
 __device__ __forceinline__ int lin_turn(int r) {
-    if constexpr (ROWB % 256 == 0) return ((r & 7) << 1) | ((r >> 3) & 1);
-    else if constexpr (ROWB % 128 == 0) return (((r >> 1) & 3) << 1) | ((r >> 3) & 1);
-    else return ((r >> 2) & 1) << 1 | ((r >> 3) & 1);
+    if constexpr (ROWB % 256 == 0) return ((r & 1) * 3 | (r & 6) << 1) ^ ((r >> 3) & 1);
+    else if constexpr (ROWB % 128 == 0) return (((r >> 1) & 1) * 3 | (r & 4)) ^ ((r >> 3) & 1);
+    else return ((r >> 2) & 1) * 3 ^ ((r >> 3) & 1);
 }
 template <int ROWB>
 __device__ __forceinline__ int lin_piece(int r, int p) { return r * ROWB + ((p ^ lin_turn<ROWB>(r)) << 4); }
