@@ -169,17 +169,18 @@ __device__ __forceinline__ f32x4 lin_mma(const LinFrag<BF>& a, const LinSplit<BF
 }
 
 // Rows of ROWB bytes in LDS, without padding between them; piece p (16 bytes)
-// of row r lies at p ^ turn(r), so that what is read together covers all banks:
-// pieces p and p ^ 2 of 8 rows (an operand's read serves 8 lanes of each half of a
-// wave at a time), and pieces p and p ^ 1 of 8 rows (the transposing read).  So
-// the turns of 8 rows that begin at the same bank have bits 0 and 1 alike, 0 or 3,
-// and those of the next 8 have them unlike.  (With turns 0, 2, 4, .. a third of
-// all LDS cycles were conflicts.)
+// of row r lies at p ^ turn(r), so that what is read together covers all banks.
+// As measured, an operand's read (16 bytes a lane) serves 16 lanes at a time
+// from 64 banks: rows 0 .. 3 and 12 .. 15 of piece p with rows 4 .. 11 of piece
+// p ^ 1 (fp32: p ^ 2), and the reverse; the transposing read serves 8 rows of a
+// pair of pieces.  So among rows that begin at the same bank the pairs (turn / 2)
+// of rows 0 .. 7 differ, and those of 8 .. 15, and of two rows of one pair, which
+// the first kind of read serves together, the pieces.
 template <int ROWB>
 __device__ __forceinline__ int lin_turn(int r) {
-    if constexpr (ROWB % 256 == 0) return ((r & 1) * 3 | (r & 6) << 1) ^ ((r >> 3) & 1);
-    else if constexpr (ROWB % 128 == 0) return (((r >> 1) & 1) * 3 | (r & 4)) ^ ((r >> 3) & 1);
-    else return ((r >> 2) & 1) * 3 ^ ((r >> 3) & 1);
+    constexpr int SH = ROWB % 256 == 0 ? 0 : ROWB % 128 == 0 ? 1 : 2;
+    const int h = (r >> 3) & 1;
+    return (((r & 7) ^ (h << 2)) >> SH) << 1 | h;
 }
 template <int ROWB>
 __device__ __forceinline__ int lin_piece(int r, int p) { return r * ROWB + ((p ^ lin_turn<ROWB>(r)) << 4); }
