@@ -620,27 +620,41 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         }
         auto publish = [&](int buf) __attribute__((always_inline)) {
             lds_char* at = lds + L::kState + buf * L::kStateBytes;
+            const int row = nvt * 16 + n;
+            if constexpr (BF) {
+                f32x4 x[KT];
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                const int row = nvt * 16 + n;
-                if constexpr (BF) {
-                    const int off = lin_piece<L::kRowA>(row, 2 * (kt0 + t) + (g >> 1)) + (g & 1) * 8;
-                    f32x4 x = S[t];
+                for (int t = 0; t < KT; ++t) x[t] = S[t];
 #pragma unroll
-                    for (int k = 0; k < L::kParts; ++k) {
-                        if (k > 0 && L::kGrad && !R.sum_x) break;
-                        const u32x2 w = {lin_pack(x[0], x[1]), lin_pack(x[2], x[3])};
-                        lds_put(at + k * kLinTile * L::kRowA + off, w);
+                for (int k = 0; k < L::kParts; ++k) {
+                    if (k > 0 && L::kGrad && !R.sum_x) break;
+                    u32x2 w[KT];
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        w[t] = u32x2{lin_pack(x[t][0], x[t][1]), lin_pack(x[t][2], x[t][3])};
                         if (k + 1 < L::kParts) {
-                            float y[4] = {x[0], x[1], x[2], x[3]};
-                            lin_rest(w[0], y[0], y[1]);
-                            lin_rest(w[1], y[2], y[3]);
-                            x = f32x4{y[0], y[1], y[2], y[3]};
+                            float y[4] = {x[t][0], x[t][1], x[t][2], x[t][3]};
+                            lin_rest(w[t][0], y[0], y[1]);
+                            lin_rest(w[t][1], y[2], y[3]);
+                            x[t] = f32x4{y[0], y[1], y[2], y[3]};
                         }
                     }
-                } else {
-                    lds_put(at + lin_piece<L::kRowA>(row, 4 * (kt0 + t) + g), S[t]);
+                    lds_char* to = at + k * kLinTile * L::kRowA;
+                    // Two tiles at once, 16 bytes a lane: lanes of even g take
+                    // their neighbour's numbers of the first, those of odd g
+                    // theirs of the second.
+#pragma unroll
+                    for (int t = 0; t + 1 < KT; t += 2) {
+                        const auto lo = __builtin_amdgcn_permlane16_swap(w[t][0], w[t + 1][0], false, false);
+                        const auto hi = __builtin_amdgcn_permlane16_swap(w[t][1], w[t + 1][1], false, false);
+                        lds_put(to + lin_piece<L::kRowA>(row, 2 * (kt0 + t + (g & 1)) + (g >> 1)), u32x4{lo[0], hi[0], lo[1], hi[1]});
+                    }
+                    if constexpr (KT % 2 == 1)
+                        lds_put(to + lin_piece<L::kRowA>(row, 2 * (kt0 + KT - 1) + (g >> 1)) + (g & 1) * 8, w[KT - 1]);
                 }
+            } else {
+#pragma unroll
+                for (int t = 0; t < KT; ++t) lds_put(at + lin_piece<L::kRowA>(row, 4 * (kt0 + t) + g), S[t]);
             }
         };
         if constexpr (L::kOut) publish(0);
