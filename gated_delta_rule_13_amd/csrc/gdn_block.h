@@ -9,7 +9,8 @@
 //     dX = dx' + r' (dy w_pre - x^ mean(dy w_pre x^))         (is dx)
 //     ds = sum dX act(g) n,   dg = dX s n act'(g),   dn = dX s act(g)
 //     do = r (dn w_post - o^ mean(dn w_post o^)),   dw_post = sum dn o^,   dw_pre = sum dy x^
-// One pass over memory bounds both: L lanes hold a row in registers, K pieces of
+// One pass over memory bounds both: 4 x 4096 x 2048 (x fp32, o bf16, gated) take
+// 92 us for 470 MB (5.1 TB/s), the gradient 150 for 738 (4.9).  L lanes hold a row in registers, K pieces of
 // V numbers to a lane, the next row's loads in flight, and their columns of the
 // weights for all the rows that they take.
 #pragma once

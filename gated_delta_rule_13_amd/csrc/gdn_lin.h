@@ -23,8 +23,19 @@
 //
 // Products on the matrix units: bf16 rows as they lie, and what is computed (the
 // state, decayed values, products of rows times their decay) in two or three bf16
-// numbers that add up to it (errors of 2^-17 or 2^-24); fp32 rows on the fp32
-// units.
+// numbers that add up to it (errors of 2^-17 or 2^-24), or in one where the
+// output is rounded to bf16 itself; fp32 rows on the fp32 units.
+//
+// A workgroup has 32 columns of c and all of a head's tokens (or a segment's):
+// the tiles of a head read the same rows a and b, from one XCD's L2, and the more
+// columns a tile had, the fewer workgroups there were for 256 compute units.
+// What bounds the passes is the chain of a chunk (reads from LDS, products,
+// rounding, barrier: about 2600 clocks), with the matrix units busy a quarter of
+// the time: 4 x 16 x 4096 of 128/128 in bf16 take 86 us (274 MB, 57 us at a
+// copy's rate), 1 x 8 x 32768 144 (of them 57 for the segments' sums and 8 for
+// their chain), 32 x 16 x 256 of 64/64 27 (84 MB, 18), the gradient of
+// 4 x 16 x 4096 324 (472 MB, 98); 3 x 6 x 1021 of 72/40 in fp32 39, in three
+// launches that each wait for few rows.
 #pragma once
 #include <type_traits>
 
@@ -286,8 +297,8 @@ __device__ __forceinline__ void lin_stage(lds_char* tile, const char* src, int64
     }
 }
 
-// Rows straight from memory into LDS, which the movers do: lane l of a wave writes 16 bytes (or 4) at
-// `to` + 16 l.  The compiler knows nothing of these loads: lin_wait counts them.
+// Rows straight from memory into LDS, which the movers do: lane l of a wave
+// writes 16 bytes (or 4) at `to` + 16 l (or 4 l).  The compiler knows nothing of these loads: lin_wait counts them.
 // (M0, which holds the place, is no register that it keeps anything in.)
 __device__ __forceinline__ void lin_direct16(uint32_t to, uint32_t off, const char* base) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
@@ -369,7 +380,7 @@ struct LinPlan {
     // What is computed becomes an operand of bf16 rows in parts that add up to it:
     // decayed values three (their sums are the state, which stays fp32); the
     // state and the products of rows one where the output is bf16 (a rounding
-    // like the output's own: prompts come out 2.2e-3 off in the mean, and 1.7e-3
+    // like the output's own: prompts come out 2.3e-3 off in the mean, and 1.7e-3
     // with two parts, 17 us slower at 4 x 4096 x 16 x 128), two where it is
     // fp32; the state three where the decay's gradient is summed over many
     // chunks.
@@ -1121,7 +1132,9 @@ static __global__ __launch_bounds__(256) void gdn_lin_group_sum_kernel(LinGroupP
     store_one<BF>(p.out, i, s);
 }
 
-// One token of every sequence.  A group of L lanes holds a row of the state (d_k
+// One token of every sequence, one pass over the state, which bounds it: 64 x 16
+// states of 128 x 128 take 20 us, 135 MB, part of which the last level of cache
+// holds from the call before.  A group of L lanes holds a row of the state (d_k
 // numbers, V to a piece), kLinStepRows rows in turn: k and q are loaded once for
 // them.
 struct LinStepParams {
