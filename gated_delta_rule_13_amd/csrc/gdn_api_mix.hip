@@ -53,7 +53,7 @@ int64_t lin_blocks(int64_t units, int tiles) { return ceil_div(units, kXcds) * k
 // Segments: where the heads and tiles leave compute units idle, the tokens are
 // cut so that they have about two workgroups each, of 256 tokens at least.  They
 // cost a pass over the rows for their sums, and win by the units that work:
-// 1 x 8 x 32768 of 128/128 take 144 us, the same tokens as 64 heads 86 without.
+// 1 x 8 x 32768 of 128/128 take 140 us, the same tokens as 64 heads 86 without.
 // (Aiming at 256 or 1024 workgroups measures alike.)
 struct LinPlanSizes {
     int nseg, seg_len;

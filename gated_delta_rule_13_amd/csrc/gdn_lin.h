@@ -32,7 +32,7 @@
 // What bounds the passes is the chain of a chunk (reads from LDS, products,
 // rounding, barrier: about 2600 clocks), with the matrix units busy a quarter of
 // the time: 4 x 16 x 4096 of 128/128 in bf16 take 86 us (274 MB, 57 us at a
-// copy's rate), 1 x 8 x 32768 144 (of them 57 for the segments' sums and 8 for
+// copy's rate), 1 x 8 x 32768 140 (of them 57 for the segments' sums and 8 for
 // their chain), 32 x 16 x 256 of 64/64 27 (84 MB, 18), the gradient of
 // 4 x 16 x 4096 324 (472 MB, 98); 3 x 6 x 1021 of 72/40 in fp32 39, in three
 // launches that each wait for few rows.
@@ -184,14 +184,15 @@ __device__ __forceinline__ f32x4 lin_mma(const LinFrag<BF>& a, const LinSplit<BF
 // As measured, an operand's read (16 bytes a lane) serves 16 lanes at a time
 // from 64 banks: rows 0 .. 3 and 12 .. 15 of piece p with rows 4 .. 11 of piece
 // p ^ 1 (fp32: p ^ 2), and the reverse; the transposing read serves 8 rows of a
-// pair of pieces.  So among rows that begin at the same bank the pairs (turn / 2)
-// of rows 0 .. 7 differ, and those of 8 .. 15, and of two rows of one pair, which
-// the first kind of read serves together, the pieces.
+// pair of pieces; a write serves one piece of 8 rows, on 32 banks.  So among rows
+// that begin at the same bank the pairs (turn / 2) of rows 0 .. 7 differ, and
+// those of 8 .. 15; two rows of one pair, which the first kind of read serves
+// together, have its two pieces; and four rows of the 8 (where rows fill the
+// banks) have the first, four the second.
 template <int ROWB>
 __device__ __forceinline__ int lin_turn(int r) {
     constexpr int SH = ROWB % 256 == 0 ? 0 : ROWB % 128 == 0 ? 1 : 2;
-    const int h = (r >> 3) & 1;
-    return (((r & 7) ^ (h << 2)) >> SH) << 1 | h;
+    return (((r & 7) ^ ((r >> 1) & 4)) >> SH) << 1 | ((r >> 2) & 1);
 }
 template <int ROWB>
 __device__ __forceinline__ int lin_piece(int r, int p) { return r * ROWB + ((p ^ lin_turn<ROWB>(r)) << 4); }
