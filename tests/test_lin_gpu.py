@@ -1,11 +1,13 @@
 """Linear attention with a decay for each head on the GPU, against the 64-bit
 reference."""
+import ctypes
 import math
 
 import pytest
 import torch
 
 import gated_delta_rule_13_amd as gdn
+from gated_delta_rule_13_amd import _lib, _mix
 from tests import layer_ref as ref
 from tests import mix_ref as mix
 from tests.gpu_helpers import say
@@ -259,3 +261,24 @@ def test_gradient_against_differences(name):
     # (q, k, v and S0 enter linearly; log_alpha's third derivative is at most the
     # tokens it acts over, cubed, times the direction's cube)
     assert abs(slope - want) < 2.0 ** -16 * size / step + (2e-2 * abs(want) + 0.05 if name == "log_alpha" else 1e-4 * abs(want)), (slope, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("decay,T", [("token", 200), ("head", 200), ("token", 700)])
+def test_gradient_without_the_decays(dtype, decay, T):
+    """The C entry without dlog_alpha and dS0: what is left is held to the same
+    bounds (in one pass, and in segments)."""
+    say(f"case: lin bwd without dlog_alpha {dtype} {decay} T{T}")
+    a = inputs(2, 2, 1, 2, T, 40, 64, dtype, T, decay, True, [T, T - 61])
+    dO, dS = ref.rand(ref.gen(1), 2, 2, T, 64, dtype=dtype), ref.rand(ref.gen(2), 2, 2, 64, 40)
+    d, do, ds = ref.dev(a), dO.cuda(), dS.cuda()
+    full = gdn.gdn_lin_bwd(do, **d, dS_final=ds, scale=SCALE)
+    some = {n: torch.full_like(full[n], math.nan) for n in ("dq", "dk", "dv")}
+    s = _mix._lin_shape(d["q"], d["k"], d["v"], d["log_alpha"], SCALE, dtype)
+    nbytes = gdn.gdn_lin_bwd_workspace_bytes(s)
+    ws = torch.full((nbytes,), 0xff, dtype=torch.uint8, device="cuda")
+    _lib.check(_lib.load().gdn_lin_bwd(
+        ctypes.byref(s), do.data_ptr(), d["q"].data_ptr(), d["k"].data_ptr(), d["v"].data_ptr(), d["log_alpha"].data_ptr(),
+        d["S0"].data_ptr(), ds.data_ptr(), d["lens"].data_ptr(), some["dq"].data_ptr(), some["dk"].data_ptr(),
+        some["dv"].data_ptr(), None, None, ws.data_ptr(), nbytes, torch.cuda.current_stream().cuda_stream))
+    check_gradient(a, dO, dS, {**full, **some})
