@@ -257,7 +257,7 @@ gdn_status gdn_lin_fwd(const gdn_lin_shape* s, const void* q, const void* k, con
     p.r[0].first = S0;
     p.r[0].carry = pl.nseg > 1 ? p.seg_sum : nullptr;
     p.r[0].last = S_final;
-    lin_launcher(s->dtype, lin_rows(s->d_k), s->o_dtype == GDN_BF16 ? kLinSetFwd : kLinSetFine)(p, lin_blocks(p.units, p.r[0].tiles), hs);
+    lin_launcher(s->dtype, lin_rows(s->d_k), kLinSetFwd)(p, lin_blocks(p.units, p.r[0].tiles), hs);
     return launch_status();
 }
 

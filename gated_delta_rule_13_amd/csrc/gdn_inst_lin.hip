@@ -20,7 +20,6 @@ void run(const LinParams& p, int64_t blocks, hipStream_t st) {
 LinLauncher GDN_LIN_NAME(GDN_LIN_BF16, GDN_LIN_NK)(int set) {
     switch (set) {
         case kLinSetFwd: return run<kLinSetFwd>;
-        case kLinSetFine: return run<kLinSetFine>;
         case kLinSetQk: return run<kLinSetQk>;
         case kLinSetV: return run<kLinSetV>;
         case kLinSetAll: return run<kLinSetAll>;

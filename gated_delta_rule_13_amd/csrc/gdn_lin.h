@@ -23,8 +23,8 @@
 //
 // Products on the matrix units: bf16 rows as they lie, and what is computed (the
 // state, decayed values, products of rows times their decay) in two or three bf16
-// numbers that add up to it (errors of 2^-17 or 2^-24), or in one where the
-// output is rounded to bf16 itself; fp32 rows on the fp32 units.
+// numbers that add up to it (errors of 2^-17 or 2^-24), so that a bf16 output is
+// rounded once, where it is stored; fp32 rows on the fp32 units.
 //
 // A workgroup has 32 columns of c and all of a head's tokens (or a segment's):
 // the tiles of a head read the same rows a and b, from one XCD's L2, and the more
@@ -81,8 +81,7 @@ struct LinParams {
     float scale;
 };
 
-// (kLinFine: the forward pass to fp32)
-enum LinMode { kLinFwd, kLinFine, kLinDq, kLinDk, kLinDv, kLinSum, kLinSumD };
+enum LinMode { kLinFwd, kLinDq, kLinDk, kLinDv, kLinSum, kLinSumD };
 
 // Four waves form the outputs of a chunk, four keep the state and four move rows:
 // all work on the same chunk at once, one wave of each kind to a SIMD.
@@ -380,13 +379,13 @@ struct LinPlan {
     static constexpr int kRowA = NK * kEl, kRowC = kLinTile * kEl;
     // What is computed becomes an operand of bf16 rows in parts that add up to it:
     // decayed values three (their sums are the state, which stays fp32); the
-    // state and the products of rows one where the output is bf16 (a rounding
-    // like the output's own: prompts come out 2.3e-3 off in the mean, and 1.7e-3
-    // with two parts, 17 us slower at 4 x 4096 x 16 x 128), two where it is
-    // fp32; the state three where the decay's gradient is summed over many
+    // state and the products of rows two, whose errors of 2^-17 a bf16 output's
+    // own rounding hides (with one, 17 us less at 4 x 4096 x 16 x 128, every term
+    // would be off by a rounding like the output's: 2.3e-3 in the mean for
+    // 1.7e-3); the state three where the decay's gradient is summed over many
     // chunks.
-    static constexpr int kParts = !BF ? 1 : kGrad ? 3 : MODE == kLinFine ? 2 : 1;
-    static constexpr int kRowParts = MODE == kLinFine ? 2 : 1;
+    static constexpr int kParts = !BF ? 1 : kGrad ? 3 : 2;
+    static constexpr int kRowParts = 2;
     static constexpr int kValueParts = 3;
     static constexpr int kStateBytes = kParts * kLinTile * kRowA;
     static constexpr int kA = 0;
@@ -639,7 +638,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 for (int t = 0; t < KT; ++t) x[t] = S[t];
 #pragma unroll
                 for (int k = 0; k < L::kParts; ++k) {
-                    if (k > 0 && L::kGrad && !R.sum_x) break;
+                    if (k > 1 && L::kGrad && !R.sum_x) break;
                     u32x2 w[KT];
 #pragma unroll
                     for (int t = 0; t < KT; ++t) {
@@ -845,8 +844,8 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         };
         const bool sums_wanted = L::kGrad && R.sum_x;
         if constexpr (L::kGrad && L::kParts > 1) {
-            state_product(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
-            if (sums_wanted) state_product(std::integral_constant<int, 1>{}, std::integral_constant<int, L::kParts>{});
+            state_product(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
+            if (sums_wanted) state_product(std::integral_constant<int, 2>{}, std::integral_constant<int, L::kParts>{});
         } else {
             state_product(std::integral_constant<int, 0>{}, std::integral_constant<int, L::kParts>{});
         }
@@ -958,7 +957,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 // Workgroups: the tiles of a unit (a head of a sequence, or a segment of one)
 // beside each other on one XCD, whose L2 then holds the rows that they share;
 // neighbouring units too, whose heads may share queries and keys.
-enum LinSet { kLinSetFwd, kLinSetFine, kLinSetQk, kLinSetV, kLinSetAll, kLinSetSum, kLinSetSums };
+enum LinSet { kLinSetFwd, kLinSetQk, kLinSetV, kLinSetAll, kLinSetSum, kLinSetSums };
 constexpr int kXcds = 8;
 
 constexpr int lin_most(int a, int b) { return a > b ? a : b; }
@@ -970,7 +969,6 @@ struct LinBytes {
     static constexpr int kRows = LinPlan<BF, NK, C, kLinFwd>::kBytes;
     static constexpr int kSum = LinPlan<BF, NK, C, kLinSum>::kBytes;
     static constexpr int value = SET == kLinSetFwd || SET == kLinSetV     ? kRows
-                                 : SET == kLinSetFine                      ? LinPlan<BF, NK, C, kLinFine>::kBytes
                                  : SET == kLinSetSum || SET == kLinSetSums ? kSum
                                  : SET == kLinSetQk                        ? kGrad
                                                                            : lin_most(kGrad, kRows);
@@ -993,8 +991,6 @@ __global__ __launch_bounds__(kLinThreads) void gdn_lin_kernel(LinParams p) {
     if (at / tiles >= per || unit >= p.units) return;
     if constexpr (SET == kLinSetFwd) {
         lin_pass<BF, NK, C, kLinFwd>(p, p.r[0], unit, tile, lin_lds);
-    } else if constexpr (SET == kLinSetFine) {
-        lin_pass<BF, NK, C, kLinFine>(p, p.r[0], unit, tile, lin_lds);
     } else if constexpr (SET == kLinSetV) {
         lin_pass<BF, NK, C, kLinDv>(p, p.r[0], unit, tile, lin_lds);
     } else if constexpr (SET == kLinSetSum) {

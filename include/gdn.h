@@ -498,9 +498,8 @@ typedef struct {
  *   S_final    [B, H, d_v, d_k] float or NULL; may be S0 (in place)
  * Chunks of 64 tokens (32 for fp32, and above d_k 128) on the matrix units; bf16
  * products of what is computed take two or three bf16 numbers that add up to
- * it, so that fp32 results are those of fp32 arithmetic to about 1e-5 of a
- * tensor's largest number, or one where the output is bf16 (each a rounding like
- * the output's own).  Any finite numbers whose products and sums of them over a
+ * it, so that results are those of fp32 arithmetic to about 1e-5 of a tensor's
+ * largest number, rounded once where they are bf16.  Any finite numbers whose products and sums of them over a
  * chunk fit fp32, with 2^48 to spare on both sides in chunks that decay by as
  * much as 2^-96.
  * An infinite or NaN input reaches the outputs of its sequence and head (where
