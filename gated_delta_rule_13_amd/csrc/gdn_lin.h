@@ -178,6 +178,30 @@ __device__ __forceinline__ f32x4 lin_mma(const LinFrag<BF>& a, const LinSplit<BF
     return c;
 }
 
+// Whether numbers are all finite: 0 times them is 0 (bf16: on the matrix units,
+// which have time for it).
+template <bool BF, int M, int N>
+__device__ __forceinline__ bool lin_finite(const LinFrag<BF> (&f)[M][N]) {
+    float z = 0.f;
+    if constexpr (BF) {
+        const LinFrag<true> none{};
+        f32x4 d = zero4();
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int c = 0; c < N; ++c) d = lin_mma(f[m][c], none, d);
+        z = (d[0] + d[1]) + (d[2] + d[3]);
+    } else {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z = fmaf(f[m][c].v[j], 0.f, z);
+    }
+    return __builtin_amdgcn_ballot_w64(!(z == 0.f)) == 0;
+}
+
 // Rows of ROWB bytes in LDS, without padding between them; piece p (16 bytes)
 // of row r lies at p ^ turn(r), so that what is read together covers all banks.
 // As measured, an operand's read (16 bytes a lane) serves 16 lanes at a time
@@ -880,6 +904,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         for (int m = 0; m < C / 32; ++m)
 #pragma unroll
             for (int c = 0; c < CT; ++c) fc[m][c] = rc.get(L::kC, m, c);
+        const bool finite = lin_finite(fc);
         const float out = lds_get<float>(vec + (kLinOut * C + row) * 4), before = lds_get<float>(vec + (kLinFirst * C + row) * 4);
         const bool far = __builtin_amdgcn_readfirstlane(lds_get<int>(vec + kLinWhole * C * 4 + 4)) != 0;
         f32x4 in[C / 16];
@@ -939,12 +964,39 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 }
             }
         }
+        // What a row may not see it has times 0, which is not 0 of an infinite or
+        // NaN number: a chunk that holds one is added up token by token, each to
+        // the rows that see it.
+        if (finite) {
 #pragma unroll
-        for (int m = 0; m < C / 32; ++m) {
-            LinSplit<BF, L::kRowParts> pp;
-            pp.set(__builtin_shufflevector(pr[2 * m], pr[2 * m + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+            for (int m = 0; m < C / 32; ++m) {
+                LinSplit<BF, L::kRowParts> pp;
+                pp.set(__builtin_shufflevector(pr[2 * m], pr[2 * m + 1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-            for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fc[m][c], pp, acc[c]);
+                for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fc[m][c], pp, acc[c]);
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < C / 32; ++m)
+#pragma unroll 1
+                for (int i = 0; i < 32; ++i) {
+                    LinFrag<BF> one[CT] = {};
+                    f32x8 x = {};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (i != 16 * (j >> 2) + 4 * g + (j & 3)) continue;
+                        x[j] = pr[2 * m + (j >> 2)][j & 3];
+#pragma unroll
+                        for (int c = 0; c < CT; ++c) one[c].v[j] = fc[m][c].v[j];
+                    }
+                    LinSplit<BF, L::kRowParts> pp;
+                    pp.set(x);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        const f32x4 o = lin_mma(one[c], pp, zero4());
+                        if (kRev ? 32 * m + i >= row : 32 * m + i <= row) acc[c] += o;
+                    }
+                }
         }
         done = now;
         done_scale = scale;

@@ -502,8 +502,10 @@ typedef struct {
  * largest number, rounded once where they are bf16.  Any finite numbers whose products and sums of them over a
  * chunk fit fp32, with 2^48 to spare on both sides in chunks that decay by as
  * much as 2^-96.
- * An infinite or NaN input reaches the outputs of its sequence and head (where
- * heads share queries or keys, of those heads).  Few heads on long sequences:
+ * An infinite or NaN input reaches what the formulas make from it, as infinity
+ * or NaN: outputs of its sequence and head (where heads share queries or keys, of
+ * those heads) from its token on, an infinite q that token's alone.  A decay of 0
+ * does not end it (0 times infinity is NaN).  Few heads on long sequences:
  * the tokens are cut into segments that run at once, from what each adds to the
  * state.  workspace: gdn_lin_fwd_workspace_bytes(s) bytes (0 without segments;
  * (size_t)-1 for an invalid shape).
