@@ -51,20 +51,21 @@ LinLauncher lin_launcher(int dtype, int nk, int set) {
 int64_t lin_blocks(int64_t units, int tiles) { return ceil_div(units, kXcds) * kXcds * tiles; }
 
 // Segments: where the heads and tiles leave compute units idle, the tokens are
-// cut so that they have about two workgroups each, of 256 tokens at least.  They
+// cut, into 256 each at least, so that they have about two workgroups each, or in
+// the gradient those of its smallest launch (the tiles of dq) one each.  They
 // cost a pass over the rows for their sums, and win by the units that work:
 // 1 x 8 x 32768 of 128/128 take 140 us, the same tokens as 64 heads 86 without.
 // (Aiming at 256 or 1024 workgroups measures alike.)
 struct LinPlanSizes {
     int nseg, seg_len;
     int64_t units;
-    size_t sum, sum_d, decay, w, x, v, y, cx, cy, share, dla, dq, dk, bytes;
+    size_t sum, sum_d, decay, w, x, v, y, f, hold, dla, dq, dk, bytes;
 };
 LinPlanSizes lin_plan(const gdn_lin_shape& s, bool grad) {
     LinPlanSizes pl{};
     const int64_t bh = (int64_t)s.B * s.H;
     const int64_t groups = bh * (lin_tiles(s.d_v) + (grad ? 2 * lin_tiles(s.d_k) : 0));
-    int64_t nseg = groups >= 256 ? 1 : ceil_div(512, groups);
+    int64_t nseg = groups >= 256 ? 1 : grad ? 256 / (bh * lin_tiles(s.d_k)) : ceil_div(512, groups);
     if (nseg > ceil_div(s.T, 256)) nseg = ceil_div(s.T, 256);
     pl.seg_len = (int)(ceil_div(ceil_div(s.T, nseg), 64) * 64);
     pl.nseg = (int)ceil_div(s.T, pl.seg_len);
@@ -85,9 +86,8 @@ LinPlanSizes lin_plan(const gdn_lin_shape& s, bool grad) {
         pl.x = take(true, tiles * tokens);
         pl.v = take(true, tiles * tokens);
         pl.y = take(true, tiles * tokens);
-        pl.cx = take(true, tiles * bh * ceil_div(s.T, C));
-        pl.cy = take(true, tiles * bh * ceil_div(s.T, C));
-        pl.share = take(true, tiles * bh);
+        pl.f = take(true, tiles * bh * ceil_div(s.T, C));
+        pl.hold = take(true, tiles * bh * ceil_div(s.T, C) * lin_rows(s.d_v) * kLinTile);
         pl.dla = take(s.per_head, tokens);
         pl.dq = take(s.Hq < s.H, tokens * s.d_k);
         pl.dk = take(s.Hk < s.H, tokens * s.d_k);
@@ -348,29 +348,41 @@ gdn_status gdn_lin_bwd(const gdn_lin_shape* s, const void* dO, const void* q, co
     rq.carry = carry;
     rq.sum_w = sum(pl.w);
     rq.sum_x = sum(pl.x);
-    rq.chunk_x = sum(pl.cx);
-    rq.end_grad = dS_final;
-    rq.end_share = dS_final ? sum(pl.share) : nullptr;
+    rq.sum_f = sum(pl.f);
+    rq.hold = sum(pl.hold);
     LinRole rk = lin_role(tv, td, tq, s->d_v, s->d_k, gk ? ws + pl.dk : dk, bf && !gk);
     rk.x = tk;
     rk.first = dS_final;
     rk.carry = carry_d;
     rk.sum_w = sum(pl.v);
     rk.sum_x = sum(pl.y);
-    rk.chunk_x = sum(pl.cy);
+    rk.hold = sum(pl.hold);
     LinRole rv = lin_role(tk, tq, td, s->d_k, s->d_v, dv, bf);
     rv.first = dS_final;
     rv.carry = carry_d;
     rv.last = dS0;
-    p.r[0] = rq;
-    p.r[1] = rk;
-    if (lin_rows(s->d_k) == lin_rows(s->d_v)) {
-        p.r[2] = rv;
-        lin_launcher(s->dtype, lin_rows(s->d_k), kLinSetAll)(p, lin_blocks(p.units, rq.tiles + rk.tiles + rv.tiles), hs);
+    const int rows_k = lin_rows(s->d_k), rows_v = lin_rows(s->d_v);
+    auto pass = [&](LinSet set, int rows, std::initializer_list<LinRole> roles) {
+        int tiles = 0, n = 0;
+        for (const LinRole& r : roles) {
+            p.r[n++] = r;
+            tiles += r.tiles;
+        }
+        lin_launcher(s->dtype, rows, set)(p, lin_blocks(p.units, tiles), hs);
+    };
+    if (dlog_alpha) {
+        if (rows_k == rows_v) {
+            pass(kLinSetKvSums, rows_v, {rk, rv});
+        } else {
+            pass(kLinSetKSums, rows_v, {rk});
+            pass(kLinSetV, rows_k, {rv});
+        }
+        pass(kLinSetQSums, rows_v, {rq});
+    } else if (rows_k == rows_v) {
+        pass(kLinSetAll, rows_v, {rq, rk, rv});
     } else {
-        lin_launcher(s->dtype, lin_rows(s->d_v), kLinSetQk)(p, lin_blocks(p.units, rq.tiles + rk.tiles), hs);
-        p.r[0] = rv;
-        lin_launcher(s->dtype, lin_rows(s->d_k), kLinSetV)(p, lin_blocks(p.units, rv.tiles), hs);
+        pass(kLinSetQk, rows_v, {rq, rk});
+        pass(kLinSetV, rows_k, {rv});
     }
     auto groups = [&](bool want, size_t from, void* to, int heads) {
         if (!want) return;
@@ -388,9 +400,7 @@ gdn_status gdn_lin_bwd(const gdn_lin_shape* s, const void* dO, const void* q, co
         d.sum_x = rq.sum_x;
         d.sum_v = rk.sum_w;
         d.sum_y = rk.sum_x;
-        d.chunk_x = rq.chunk_x;
-        d.chunk_y = rk.chunk_x;
-        d.end_share = rq.end_share;
+        d.sum_f = rq.sum_f;
         d.log_alpha = log_alpha;
         d.lsb = p.lsb;
         d.lsh = p.lsh;

@@ -23,6 +23,9 @@ LinLauncher GDN_LIN_NAME(GDN_LIN_BF16, GDN_LIN_NK)(int set) {
         case kLinSetQk: return run<kLinSetQk>;
         case kLinSetV: return run<kLinSetV>;
         case kLinSetAll: return run<kLinSetAll>;
+        case kLinSetKSums: return run<kLinSetKSums>;
+        case kLinSetKvSums: return run<kLinSetKvSums>;
+        case kLinSetQSums: return run<kLinSetQSums>;
         case kLinSetSum: return run<kLinSetSum>;
         default: return run<kLinSetSums>;
     }

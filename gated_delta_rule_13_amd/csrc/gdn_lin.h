@@ -18,8 +18,11 @@
 // that reads at or after t and one that writes before t.  Pairs inside t's chunk:
 // their products M_ri, summed over rows and columns; pairs with one token
 // outside: q_r . dq_r and k_i . dk_i without their chunk's part; pairs with both
-// outside: <D, S> over the chunk, from the chunks' sums.  Nothing is a
-// difference of long sums, which strong decays would not survive.
+// outside: e^{G_C} <D, S> of the states on the chunk's two sides.  The pass of dk
+// leaves D behind each chunk for that of dq, which runs after it: 32 KB to and fro
+// for a chunk and 32 columns at 128 (written as differences of sums over all
+// later tokens, as q . dq - k . dk would allow, an early token's gradient holds
+// the rounding of every later one's, also where a document lies between them).
 //
 // Products on the matrix units: bf16 rows as they lie, and what is computed (the
 // state, decayed values, products of rows times their decay) in two or three bf16
@@ -59,13 +62,14 @@ struct LinRole {
     const float* first;     // state to start from, or null
     const float* carry;     // states that segments start from [B H, nseg, d_v, d_k]
     float* last;            // state at the end, or null
-    const float* end_grad;  // gradient of the last state (for <D, S> at the end), or null
     void* out;              // [B, H, T, nv]
     int out_bf16, out_wide;
+    // gradient of the decay
     float* sum_w;           // [tiles, B H, T]: a row's pairs inside its chunk
     float* sum_x;           // [tiles, B H, T]: its pairs with tokens outside
-    float* chunk_x;         // [tiles, B H, chunks]: their sums over a chunk
-    float* end_share;       // [tiles, B H]
+    float* sum_f;           // [tiles, B H, chunks]: pairs around a chunk (dq)
+    float* hold;            // [B H, chunks, tiles, NK * 32]: D behind each chunk, as
+                            // the waves that keep it have it (dk writes, dq reads)
 };
 
 struct LinParams {
@@ -81,7 +85,8 @@ struct LinParams {
     float scale;
 };
 
-enum LinMode { kLinFwd, kLinDq, kLinDk, kLinDv, kLinSum, kLinSumD };
+// (kLinDqSums, kLinDkSums: with the sums for the decay's gradient)
+enum LinMode { kLinFwd, kLinDq, kLinDk, kLinDv, kLinDqSums, kLinDkSums, kLinSum, kLinSumD };
 
 // Four waves form the outputs of a chunk, four keep the state and four move rows:
 // all work on the same chunk at once, one wave of each kind to a SIMD.
@@ -398,7 +403,7 @@ __device__ __forceinline__ double lin_scan(double x, int lane) {
 // LDS of a pass.  kStages chunks of rows: the one at work and those under way.
 template <bool BF, int NK, int C, int MODE>
 struct LinPlan {
-    static constexpr bool kOut = MODE < kLinSum, kGrad = MODE == kLinDq || MODE == kLinDk;
+    static constexpr bool kOut = MODE < kLinSum, kGrad = MODE == kLinDqSums || MODE == kLinDkSums;
     static constexpr int kEl = BF ? 2 : 4;
     static constexpr int kRowA = NK * kEl, kRowC = kLinTile * kEl;
     // What is computed becomes an operand of bf16 rows in parts that add up to it:
@@ -406,9 +411,8 @@ struct LinPlan {
     // state and the products of rows two, whose errors of 2^-17 a bf16 output's
     // own rounding hides (with one, 17 us less at 4 x 4096 x 16 x 128, every term
     // would be off by a rounding like the output's: 2.3e-3 in the mean for
-    // 1.7e-3); the state three where the decay's gradient is summed over many
-    // chunks.
-    static constexpr int kParts = !BF ? 1 : kGrad ? 3 : 2;
+    // 1.7e-3).
+    static constexpr int kParts = BF ? 2 : 1;
     static constexpr int kRowParts = 2;
     static constexpr int kValueParts = 3;
     static constexpr int kStateBytes = kParts * kLinTile * kRowA;
@@ -420,8 +424,8 @@ struct LinPlan {
     static constexpr int kVec = 0;                                  // of two chunks: see LinDecays
     static constexpr int kVecBytes = (6 * C + 4) * 4;
     static constexpr int kLog = kVec + 2 * kVecBytes;               // log_alpha of four chunks
-    static constexpr int kSums = kLog + 4 * 64 * 4;                 // of two: pairs inside, pairs outside by column tile
-    static constexpr int kSumBytes = kGrad ? 3 * C * 4 : 0;
+    static constexpr int kSums = kLog + 4 * 64 * 4;                 // of two: pairs inside, outside by column tile, around
+    static constexpr int kSumBytes = kGrad ? (3 * C + 4) * 4 : 0;
     static constexpr int kState = (kSums + 2 * kSumBytes + 255) / 256 * 256;
     static constexpr int kStage = kState + (kOut ? 2 * kStateBytes : 0);
     static constexpr int kRoom = 160 * 1024 - kStage;
@@ -446,8 +450,8 @@ constexpr float kLinSpan = 48.f;
 template <bool BF, int NK, int C, int MODE>
 __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, int64_t unit, int tile, char* shared) {
     typedef LinPlan<BF, NK, C, MODE> L;
-    constexpr bool kRev = MODE == kLinDk || MODE == kLinDv || MODE == kLinSumD;
-    constexpr bool kTurned = MODE == kLinDq || MODE == kLinDk;      // the state transposed
+    constexpr bool kRev = MODE == kLinDk || MODE == kLinDkSums || MODE == kLinDv || MODE == kLinSumD;
+    constexpr bool kTurned = MODE == kLinDq || MODE == kLinDk || L::kGrad;      // the state transposed
     constexpr int RT = C / 16;                      // row tiles
     constexpr int CT = RT == 4 ? 2 : 1;             // column tiles of a wave
     constexpr int KS = NK / 32, KT = NK / 32;       // steps over nk; state tiles of a wave
@@ -567,22 +571,19 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         // what a chunk left for the decay's gradient
         auto emit = [&](int it) __attribute__((always_inline)) {
             if constexpr (L::kGrad) {
-                if (!R.sum_x || wave != 1) return;
+                if (wave != 1) return;
                 const lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
                 const int ch = number(it), t = t0 + ch * C + lane;
-                float x = 0.f;
-                if (lane < C) {
-                    x = lds_get<float>(sums + (C + lane) * 4);
+                if (lane < C && t < tl) {
+                    float x = lds_get<float>(sums + (C + lane) * 4);
                     if constexpr (RT == 2) x += lds_get<float>(sums + (2 * C + lane) * 4);
-                    if (t < tl) {
-                        R.sum_x[part * p.T + t] = x;
-                        R.sum_w[part * p.T + t] = lds_get<float>(sums + lane * 4);
-                    } else {
-                        x = 0.f;
-                    }
+                    R.sum_x[part * p.T + t] = x;
+                    R.sum_w[part * p.T + t] = lds_get<float>(sums + lane * 4);
                 }
-                x = lanes_sum<64>(x);
-                if (lane == 0) R.chunk_x[part * ((p.T + C - 1) / C) + t0 / C + ch] = x;
+                if (MODE == kLinDqSums && lane == 0) {
+                    const f32x4 f = lds_get<f32x4>(sums + 3 * C * 4);
+                    R.sum_f[part * ((p.T + C - 1) / C) + t0 / C + ch] = (f[0] + f[1]) + (f[2] + f[3]);
+                }
             }
         };
         if (fill) lin_wait<0>();
@@ -662,7 +663,6 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 for (int t = 0; t < KT; ++t) x[t] = S[t];
 #pragma unroll
                 for (int k = 0; k < L::kParts; ++k) {
-                    if (k > 1 && L::kGrad && !R.sum_x) break;
                     u32x2 w[KT];
 #pragma unroll
                     for (int t = 0; t < KT; ++t) {
@@ -693,6 +693,38 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             }
         };
         if constexpr (L::kOut) publish(0);
+        // What the states on a chunk's two sides share: the pass of dk leaves D
+        // behind chunk number `it`, that of dq reads it (a chunk ahead where
+        // registers hold it) and multiplies by S before it.
+        constexpr bool kEarly = KT <= 4;
+        float* const hold = L::kGrad ? R.hold + ((bh * ((p.T + C - 1) / C) + t0 / C) * R.tiles + tile) * (NK * kLinTile) + (wave * 64 + lane) * 4 : nullptr;
+        f32x4 behind[KT];
+        float around = 0.f;
+        auto load_behind = [&](int it) __attribute__((always_inline)) {
+            if (it >= chunks) return;
+            const float* at = hold + (int64_t)number(it) * R.tiles * (NK * kLinTile);
+#pragma unroll
+            for (int t = 0; t < KT; ++t) behind[t] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(at + t * 1024));
+        };
+        auto sides = [&](int it) __attribute__((always_inline)) {
+            if (it >= chunks) return;
+            if constexpr (MODE == kLinDkSums) {
+                float* at = hold + (int64_t)number(it) * R.tiles * (NK * kLinTile);
+#pragma unroll
+                for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4*>(at + t * 1024) = S[t];
+            }
+            if constexpr (MODE == kLinDqSums) {
+                if constexpr (!kEarly) load_behind(it);
+                around = 0.f;
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) around = fmaf(S[t][j], behind[t][j], around);
+                if constexpr (kEarly) load_behind(it + 1);
+            }
+        };
+        if constexpr (MODE == kLinDqSums && kEarly) load_behind(0);
+        sides(0);
         if (fill) lin_wait_lds();
         float total = 0.f;      // log2 of the decay so far
         for (int it = 0; it < chunks; ++it) {
@@ -731,6 +763,11 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                     for (int t = 0; t < KT; ++t) S[t] = lin_mma(keys[m][t], fc.part[k], S[t]);
             }
             if constexpr (L::kOut) publish((it + 1) & 1);
+            if constexpr (MODE == kLinDqSums) {
+                const float f = lanes_sum<64>(around) * whole;
+                if (lane == 0) lds_put(lds + L::kSums + (it & 1) * L::kSumBytes + (3 * C + wave) * 4, f);
+            }
+            sides(it + 1);
         }
         // the state at the end
         float* to = nullptr;
@@ -739,31 +776,15 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         if constexpr (L::kOut) {
             if (R.last && seg == (kRev ? 0 : p.nseg - 1)) to = R.last + bh * plane;
         }
-        float share = 0.f;
-        const bool ends = MODE == kLinDq && R.end_share && seg == p.nseg - 1;
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int k = (kt0 + t) * 16 + 4 * g + j;
-                if (k < R.nk && scol < R.nv) {
-                    if (to) to[k * sk + scol * sn] = S[t][j];
-                    if (ends) share = fmaf(S[t][j], R.end_grad[bh * plane + k * sk + scol * sn], share);
-                }
+                if (to && k < R.nk && scol < R.nv) to[k * sk + scol * sn] = S[t][j];
             }
         if (MODE == kLinSum && tile == 0 && wave == 0 && lane == 0) p.seg_decay[unit] = total;
-        if constexpr (MODE == kLinDq) {
-            share = lanes_sum<64>(share);
-            if (lane == 0) lds_put(lds + L::kLog + wave * 4, share);
-        }
-        if constexpr (L::kGrad) {
-            __syncthreads();
-            if (ends && wave == 0 && lane == 0) {
-                float s = 0.f;
-                for (int i = 0; i < 4; ++i) s += lds_get<float>(lds + L::kLog + i * 4);
-                R.end_share[part] = s;
-            }
-        }
+        if constexpr (L::kGrad) __syncthreads();
         return;
     }
 
@@ -840,38 +861,28 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         f32x4(&acc)[CT] = now.c;
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[c] = zero4();
-        auto state_product = [&](auto first_, auto last_) __attribute__((always_inline)) {
-            constexpr int k1 = decltype(first_)::value, k2 = decltype(last_)::value;
 #pragma unroll
-            for (int k0 = 0; k0 < KS; k0 += KB) {
-                LinFrag<BF> fs[k2 - k1][CT][KB];
+        for (int k0 = 0; k0 < KS; k0 += KB) {
+            LinFrag<BF> fs[L::kParts][CT][KB];
 #pragma unroll
-                for (int ks = 0; ks < KB; ++ks) {
-                    if (k0 + ks >= KS) break;
-                    if constexpr (k1 == 0) fa[k0 + ks] = ra.get(L::kA, rt * 16, k0 + ks);
+            for (int ks = 0; ks < KB; ++ks) {
+                if (k0 + ks >= KS) break;
+                fa[k0 + ks] = ra.get(L::kA, rt * 16, k0 + ks);
 #pragma unroll
-                    for (int k = k1; k < k2; ++k)
+                for (int k = 0; k < L::kParts; ++k)
 #pragma unroll
-                        for (int c = 0; c < CT; ++c) fs[k - k1][c][ks] = rs.get(k * kLinTile * L::kRowA, (ct0 + c) * 16, k0 + ks);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                if (k1 == 0 && k0 == 0 && it > 0) store();
-#pragma unroll
-                for (int ks = 0; ks < KB; ++ks) {
-                    if (k0 + ks >= KS) break;
-#pragma unroll
-                    for (int k = k1; k < k2; ++k)
-#pragma unroll
-                        for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fs[k - k1][c][ks], fa[k0 + ks], acc[c]);
-                }
+                    for (int c = 0; c < CT; ++c) fs[k][c][ks] = rs.get(k * kLinTile * L::kRowA, (ct0 + c) * 16, k0 + ks);
             }
-        };
-        const bool sums_wanted = L::kGrad && R.sum_x;
-        if constexpr (L::kGrad && L::kParts > 1) {
-            state_product(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
-            if (sums_wanted) state_product(std::integral_constant<int, 2>{}, std::integral_constant<int, L::kParts>{});
-        } else {
-            state_product(std::integral_constant<int, 0>{}, std::integral_constant<int, L::kParts>{});
+            __builtin_amdgcn_sched_barrier(0);
+            if (k0 == 0 && it > 0) store();
+#pragma unroll
+            for (int ks = 0; ks < KB; ++ks) {
+                if (k0 + ks >= KS) break;
+#pragma unroll
+                for (int k = 0; k < L::kParts; ++k)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fs[k][c][ks], fa[k0 + ks], acc[c]);
+            }
         }
         // products of the rows with the pairs of tiles that hold any row on their
         // side of the diagonal, and what their decays need
@@ -932,36 +943,34 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             for (int j = 0; j < 4; ++j) pr[i][j] = (kRev ? col + j >= row : col + j <= row) ? pr[i][j] * in[i][j] : 0.f;
         }
         if constexpr (L::kGrad) {
-            if (sums_wanted) {
-                const LinRows<BF, L::kRowC, 1> rx(at_x, stage);
-                const LinFrag<BF> mine = rx.get(L::kX, rt * 16, 0);
-                f32x4 other[C / 16], x[CT];
+            const LinRows<BF, L::kRowC, 1> rx(at_x, stage);
+            const LinFrag<BF> mine = rx.get(L::kX, rt * 16, 0);
+            f32x4 other[C / 16], x[CT];
 #pragma unroll
-                for (int i = 0; i < C / 16; ++i) other[i] = lin_mma(rx.get(L::kC, 16 * i, 0), mine, zero4());
+            for (int i = 0; i < C / 16; ++i) other[i] = lin_mma(rx.get(L::kC, 16 * i, 0), mine, zero4());
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    const int col = (ct0 + c) * 16 + 4 * g;
-                    const lds_char* at = lds_at32(stage) + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
-                    if constexpr (BF) x[c] = __builtin_convertvector(lds_get<bf16x4>(at), f32x4);
-                    else x[c] = lds_get<f32x4>(at);
-                }
-                float outside = 0.f, inside = 0.f;
+            for (int c = 0; c < CT; ++c) {
+                const int col = (ct0 + c) * 16 + 4 * g;
+                const lds_char* at = lds_at32(stage) + L::kX + lin_piece<L::kRowC>(row, col * EB / 16) + col * EB % 16;
+                if constexpr (BF) x[c] = __builtin_convertvector(lds_get<bf16x4>(at), f32x4);
+                else x[c] = lds_get<f32x4>(at);
+            }
+            float outside = 0.f, inside = 0.f;
 #pragma unroll
-                for (int c = 0; c < CT; ++c)
+            for (int c = 0; c < CT; ++c)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) outside = fmaf(acc[c][j], x[c][j], outside);
+                for (int j = 0; j < 4; ++j) outside = fmaf(acc[c][j], x[c][j], outside);
 #pragma unroll
-                for (int i = 0; i < C / 16; ++i) {
-                    const int col = 16 * i + 4 * g;
+            for (int i = 0; i < C / 16; ++i) {
+                const int col = 16 * i + 4 * g;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) inside = fmaf(other[i][j], col + j == row ? 0.f : pr[i][j], inside);
-                }
-                outside = lin_sum_groups(outside) * scale;
-                inside = lin_sum_groups(inside) * scale;
-                if (g == 0) {
-                    lds_put(sums + ((1 + ct0) * C + row) * 4, outside);
-                    if (ct0 == 0) lds_put(sums + row * 4, inside);
-                }
+                for (int j = 0; j < 4; ++j) inside = fmaf(other[i][j], col + j == row ? 0.f : pr[i][j], inside);
+            }
+            outside = lin_sum_groups(outside) * scale;
+            inside = lin_sum_groups(inside) * scale;
+            if (g == 0) {
+                lds_put(sums + ((1 + ct0) * C + row) * 4, outside);
+                if (ct0 == 0) lds_put(sums + row * 4, inside);
             }
         }
         // What a row may not see it has times 0, which is not 0 of an infinite or
@@ -1009,7 +1018,8 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 // Workgroups: the tiles of a unit (a head of a sequence, or a segment of one)
 // beside each other on one XCD, whose L2 then holds the rows that they share;
 // neighbouring units too, whose heads may share queries and keys.
-enum LinSet { kLinSetFwd, kLinSetQk, kLinSetV, kLinSetAll, kLinSetSum, kLinSetSums };
+// (with the decay's gradient dk comes first, and dv with it or after)
+enum LinSet { kLinSetFwd, kLinSetQk, kLinSetV, kLinSetAll, kLinSetKSums, kLinSetKvSums, kLinSetQSums, kLinSetSum, kLinSetSums };
 constexpr int kXcds = 8;
 
 constexpr int lin_most(int a, int b) { return a > b ? a : b; }
@@ -1017,22 +1027,22 @@ constexpr int lin_most(int a, int b) { return a > b ? a : b; }
 template <bool BF, int NK, int SET>
 struct LinBytes {
     static constexpr int C = lin_chunk(BF, NK);
-    static constexpr int kGrad = LinPlan<BF, NK, C, kLinDq>::kBytes;
     static constexpr int kRows = LinPlan<BF, NK, C, kLinFwd>::kBytes;
-    static constexpr int kSum = LinPlan<BF, NK, C, kLinSum>::kBytes;
-    static constexpr int value = SET == kLinSetFwd || SET == kLinSetV     ? kRows
-                                 : SET == kLinSetSum || SET == kLinSetSums ? kSum
-                                 : SET == kLinSetQk                        ? kGrad
-                                                                           : lin_most(kGrad, kRows);
-    static_assert(kGrad == LinPlan<BF, NK, C, kLinDk>::kBytes && kRows == LinPlan<BF, NK, C, kLinDv>::kBytes, "");
-    static_assert(kSum == LinPlan<BF, NK, C, kLinSumD>::kBytes, "");
+    static constexpr int kDq = LinPlan<BF, NK, C, kLinDqSums>::kBytes, kDk = LinPlan<BF, NK, C, kLinDkSums>::kBytes;
+    static constexpr int value = SET == kLinSetSum || SET == kLinSetSums ? LinPlan<BF, NK, C, kLinSum>::kBytes
+                                 : SET == kLinSetKSums                   ? kDk
+                                 : SET == kLinSetKvSums                  ? lin_most(kDk, kRows)
+                                 : SET == kLinSetQSums                   ? kDq
+                                                                         : kRows;
+    static_assert(LinPlan<BF, NK, C, kLinDq>::kBytes == kRows && LinPlan<BF, NK, C, kLinDk>::kBytes == kRows, "");
+    static_assert(LinPlan<BF, NK, C, kLinDv>::kBytes == kRows && LinPlan<BF, NK, C, kLinSum>::kBytes == LinPlan<BF, NK, C, kLinSumD>::kBytes, "");
 };
 
 template <bool BF, int NK, int SET>
 __global__ __launch_bounds__(kLinThreads) void gdn_lin_kernel(LinParams p) {
     __shared__ __align__(256) char lin_lds[LinBytes<BF, NK, SET>::value];
     constexpr int C = lin_chunk(BF, NK);
-    constexpr int kRoles = SET == kLinSetAll ? 3 : SET == kLinSetQk || SET == kLinSetSums ? 2 : 1;
+    constexpr int kRoles = SET == kLinSetAll ? 3 : SET == kLinSetQk || SET == kLinSetKvSums || SET == kLinSetSums ? 2 : 1;
     int tiles = 0;
 #pragma unroll
     for (int i = 0; i < kRoles; ++i) tiles += p.r[i].tiles;
@@ -1041,25 +1051,25 @@ __global__ __launch_bounds__(kLinThreads) void gdn_lin_kernel(LinParams p) {
     const int64_t unit = (blockIdx.x % kXcds) * per + at / tiles;
     int tile = (int)(at % tiles);
     if (at / tiles >= per || unit >= p.units) return;
-    if constexpr (SET == kLinSetFwd) {
-        lin_pass<BF, NK, C, kLinFwd>(p, p.r[0], unit, tile, lin_lds);
-    } else if constexpr (SET == kLinSetV) {
-        lin_pass<BF, NK, C, kLinDv>(p, p.r[0], unit, tile, lin_lds);
-    } else if constexpr (SET == kLinSetSum) {
-        lin_pass<BF, NK, C, kLinSum>(p, p.r[0], unit, tile, lin_lds);
-    } else {
-        if (tile < p.r[0].tiles) {
-            if constexpr (SET == kLinSetSums) lin_pass<BF, NK, C, kLinSum>(p, p.r[0], unit, tile, lin_lds);
-            else lin_pass<BF, NK, C, kLinDq>(p, p.r[0], unit, tile, lin_lds);
-            return;
-        }
+    // (the modes of a set's roles)
+    constexpr LinMode k0 = SET == kLinSetFwd                               ? kLinFwd
+                           : SET == kLinSetV                               ? kLinDv
+                           : SET == kLinSetKSums || SET == kLinSetKvSums   ? kLinDkSums
+                           : SET == kLinSetQSums                           ? kLinDqSums
+                           : SET == kLinSetSum || SET == kLinSetSums       ? kLinSum
+                                                                           : kLinDq;
+    constexpr LinMode k1 = SET == kLinSetSums ? kLinSumD : SET == kLinSetKvSums ? kLinDv : kLinDk;
+    if (kRoles == 1 || tile < p.r[0].tiles) {
+        lin_pass<BF, NK, C, k0>(p, p.r[0], unit, tile, lin_lds);
+        return;
+    }
+    if constexpr (kRoles > 1) {
         tile -= p.r[0].tiles;
-        if (tile < p.r[1].tiles) {
-            if constexpr (SET == kLinSetSums) lin_pass<BF, NK, C, kLinSumD>(p, p.r[1], unit, tile, lin_lds);
-            else lin_pass<BF, NK, C, kLinDk>(p, p.r[1], unit, tile, lin_lds);
+        if (kRoles == 2 || tile < p.r[1].tiles) {
+            lin_pass<BF, NK, C, k1>(p, p.r[1], unit, tile, lin_lds);
             return;
         }
-        if constexpr (SET == kLinSetAll) lin_pass<BF, NK, C, kLinDv>(p, p.r[2], unit, tile - p.r[1].tiles, lin_lds);
+        if constexpr (kRoles > 2) lin_pass<BF, NK, C, kLinDv>(p, p.r[2], unit, tile - p.r[1].tiles, lin_lds);
     }
 }
 
@@ -1091,9 +1101,7 @@ struct LinDecayParams {
     const float* sum_x;
     const float* sum_v;     // of the pass of dk
     const float* sum_y;
-    const float* chunk_x;   // [tiles, B H, chunks]
-    const float* chunk_y;
-    const float* end_share; // [tiles, B H] or null
+    const float* sum_f;     // [tiles, B H, chunks]
     const float* log_alpha;
     int64_t lsb, lsh, lst;
     const int32_t* lens;
@@ -1119,10 +1127,7 @@ static __global__ __launch_bounds__(256) void gdn_lin_decay_kernel(LinDecayParam
                 x += p.sum_x[row * p.T + t];
                 y += p.sum_y[row * p.T + t];
             }
-            // <D, S> behind this chunk
-            for (int c = ch + 1 + lane; c < chunks; c += 64) F += (double)p.chunk_x[row * per + c] - p.chunk_y[row * per + c];
-            if (lane == 0 && p.end_share) F += p.end_share[row];
-            if (lane == 0) F -= p.chunk_y[row * per + ch];
+            F += p.sum_f[row * per + ch];
         }
     }
     double before = y;      // sums of y up to a token, of w + x from it on
@@ -1130,7 +1135,6 @@ static __global__ __launch_bounds__(256) void gdn_lin_decay_kernel(LinDecayParam
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
         const double u = __shfl_up(before, d), v = __shfl_down(behind, d);
-        F += __shfl_xor(F, d);
         if (lane >= d) before += u;
         if (lane + d < 64) behind += v;
     }

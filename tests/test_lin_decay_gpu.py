@@ -1,0 +1,72 @@
+"""The gradient of linear attention's decays by each token's own measure: every
+number within half a step and 2^-16 of the sum of its own terms' absolute values
+(`mix_ref`: the same gradient on absolute inputs), however large the gradients of
+other tokens of the row are."""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_13_amd as gdn
+from tests import layer_ref as ref
+from tests import mix_ref as mix
+from tests.gpu_helpers import say
+from tests.test_lin_gpu import BF, F32, SCALE, inputs
+from tests.test_lin_rounding_gpu import once
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(a, dO, dS):
+    """The exact gradient of log_alpha, and the sums of its terms' absolute values."""
+    w = ref.wide(a)
+    fn = lambda **k: mix.lin(**k, scale=SCALE)  # noqa: E731
+    size = {n: x if n in ("log_alpha", "lens") or x is None else x.abs() for n, x in w.items()}
+    absolute = lambda x: None if x is None else x.double().abs()  # noqa: E731
+    return [ref.gradients(fn, *args)["log_alpha"] for args in ((w, ["log_alpha"], (dO, dS)),
+                                                              (size, ["log_alpha"], (absolute(dO), absolute(dS))))]
+
+
+def check(a, dO, dS=None):
+    want, bound = reference(a, dO, dS)
+    got = gdn.gdn_lin_bwd(dO.cuda(), **ref.dev(a), dS_final=None if dS is None else dS.cuda(), scale=SCALE)["dlog_alpha"]
+    once("dlog_alpha", got, want, bound)
+    return got
+
+
+def row(dtype, T, dk, dv, seed, strong=0.02, H=2):
+    a = inputs(1, H, H, H, T, dk, dv, dtype, seed, "token", False, None, strong)
+    return a, ref.rand(ref.gen(seed + 1), 1, H, T, dv, dtype=dtype)
+
+
+@pytest.mark.parametrize("small", [0.0])
+@pytest.mark.parametrize("dtype,T,dk,dv,start", [(BF, 2100, 64, 64, 1280), (F32, 1000, 40, 64, 512), (BF, 600, 256, 128, 320)])
+def test_documents_of_a_row(dtype, T, dk, dv, start, small):
+    """Two documents packed into a row, the first with a gradient of 0 or a small
+    one (its own tokens' alone)."""
+    say(f"case: lin decays of documents {dtype} T{T} {dk}x{dv} from {start} {small}")
+    a, dO = row(dtype, T, dk, dv, T)
+    a["log_alpha"][..., start] = -math.inf
+    dO[:, :, :start] *= small
+    got = check(a, dO)
+    assert bool((got[:, :, 1:start].abs().amax(-1) > 0).all()) == (small > 0) and bool((got[:, :, start:].abs() > 0).any())
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [(BF, 128, 128), (BF, 64, 40), (F32, 64, 64), (F32, 256, 32)])
+@pytest.mark.parametrize("strong", [0.05])
+def test_loss_on_the_last_tokens(dtype, dk, dv, strong):
+    """A prompt whose own tokens have no loss: what reaches them decays."""
+    say(f"case: lin decays of a prompt {dtype} {dk}x{dv} {strong}")
+    T = 900
+    a, dO = row(dtype, T, dk, dv, dk + dv, strong)
+    dO[:, :, :T - 100] = 0
+    check(a, dO)
+
+
+@pytest.mark.parametrize("dtype,T,dk,dv,decay,state,lens", [
+    (BF, 700, 128, 128, "token", True, None), (BF, 1100, 40, 64, "resets", True, [1100, 517]), (F32, 500, 72, 40, "token", True, [77, 500]),
+    (F32, 200, 256, 256, "resets", True, None), (BF, 130, 33, 1, "token", True, [130, 64])])
+def test_by_its_own_measure(dtype, T, dk, dv, decay, state, lens):
+    say(f"case: lin decays {dtype} T{T} {dk}x{dv} {decay}")
+    a = inputs(2, 2, 1, 2, T, dk, dv, dtype, T, decay, state, lens)
+    check(a, ref.rand(ref.gen(1), 2, 2, T, dv, dtype=dtype), ref.rand(ref.gen(2), 2, 2, dv, dk) if state else None)
