@@ -59,7 +59,7 @@ int64_t lin_blocks(int64_t units, int tiles) { return ceil_div(units, kXcds) * k
 struct LinPlanSizes {
     int nseg, seg_len;
     int64_t units;
-    size_t sum, sum_d, decay, w, x, v, y, f, hold, dla, dq, dk, bytes;
+    size_t sum, sum_d, decay, sums_q, sums_k, hold, dla, dq, dk, bytes;
 };
 LinPlanSizes lin_plan(const gdn_lin_shape& s, bool grad) {
     LinPlanSizes pl{};
@@ -82,11 +82,8 @@ LinPlanSizes lin_plan(const gdn_lin_shape& s, bool grad) {
     pl.decay = take(pl.nseg > 1, pl.units);
     if (grad) {
         pl.sum_d = take(pl.nseg > 1, pl.units * plane);
-        pl.w = take(true, tiles * tokens);
-        pl.x = take(true, tiles * tokens);
-        pl.v = take(true, tiles * tokens);
-        pl.y = take(true, tiles * tokens);
-        pl.f = take(true, tiles * bh * ceil_div(s.T, C));
+        pl.sums_q = take(true, tiles * tokens);
+        pl.sums_k = take(true, tiles * tokens);
         pl.hold = take(true, tiles * bh * ceil_div(s.T, C) * lin_rows(s.d_v) * kLinTile);
         pl.dla = take(s.per_head, tokens);
         pl.dq = take(s.Hq < s.H, tokens * s.d_k);
@@ -101,7 +98,7 @@ gdn_status lin_fits(const gdn_lin_shape& s, bool grad) {
     const int tiles = lin_tiles(s.d_v) + (grad ? 2 * lin_tiles(s.d_k) : 0);
     bool ok = threads_ok((long double)lin_blocks(pl.units, tiles) * kLinThreads);
     if (grad) {
-        ok = ok && threads_ok((long double)bh * ceil_div(ceil_div(s.T, 32), 4) * 256);
+        ok = ok && threads_ok((long double)bh * s.T + 256);
         if (s.Hq < s.H) ok = ok && threads_ok((long double)s.B * s.Hq * s.T * s.d_k + 256);
         if (s.Hk < s.H) ok = ok && threads_ok((long double)s.B * s.Hk * s.T * s.d_k + 256);
         ok = ok && threads_ok((long double)s.H * 1024);
@@ -346,16 +343,13 @@ gdn_status gdn_lin_bwd(const gdn_lin_shape* s, const void* dO, const void* q, co
     rq.x = tq;
     rq.first = S0;
     rq.carry = carry;
-    rq.sum_w = sum(pl.w);
-    rq.sum_x = sum(pl.x);
-    rq.sum_f = sum(pl.f);
+    rq.sums = sum(pl.sums_q);
     rq.hold = sum(pl.hold);
     LinRole rk = lin_role(tv, td, tq, s->d_v, s->d_k, gk ? ws + pl.dk : dk, bf && !gk);
     rk.x = tk;
     rk.first = dS_final;
     rk.carry = carry_d;
-    rk.sum_w = sum(pl.v);
-    rk.sum_x = sum(pl.y);
+    rk.sums = sum(pl.sums_k);
     rk.hold = sum(pl.hold);
     LinRole rv = lin_role(tk, tq, td, s->d_k, s->d_v, dv, bf);
     rv.first = dS_final;
@@ -396,24 +390,19 @@ gdn_status gdn_lin_bwd(const gdn_lin_shape* s, const void* dO, const void* q, co
     groups(gk, pl.dk, dk, s->Hk);
     if (dlog_alpha) {
         LinDecayParams d{};
-        d.sum_w = rq.sum_w;
-        d.sum_x = rq.sum_x;
-        d.sum_v = rk.sum_w;
-        d.sum_y = rk.sum_x;
-        d.sum_f = rq.sum_f;
+        d.sums_q = rq.sums;
+        d.sums_k = rk.sums;
         d.log_alpha = log_alpha;
         d.lsb = p.lsb;
         d.lsh = p.lsh;
         d.lst = p.lst;
         d.lens = lens;
         d.out = s->per_head ? reinterpret_cast<float*>(ws + pl.dla) : dlog_alpha;
-        d.bhs = (int64_t)s->B * s->H;
+        d.tokens = (int64_t)s->B * s->H * s->T;
         d.H = s->H;
         d.T = s->T;
-        d.C = lin_chunk(bf, lin_rows(s->d_v));
         d.tiles = rq.tiles;
-        const int64_t blocks = d.bhs * ceil_div(ceil_div(s->T, d.C), 4);
-        hipLaunchKernelGGL(gdn_lin_decay_kernel, dim3((unsigned)blocks), dim3(256), 0, hs, d);
+        hipLaunchKernelGGL(gdn_lin_decay_kernel, dim3((unsigned)ceil_div(d.tokens, 256)), dim3(256), 0, hs, d);
         if (s->per_head)
             hipLaunchKernelGGL(gdn_lin_head_sum_kernel, dim3((unsigned)s->H), dim3(1024), 0, hs, d.out, dlog_alpha, s->B, s->H, s->T);
     }

@@ -15,14 +15,16 @@
 // contribute rows `c`.
 //
 // The decay's gradient a_t <D_t, S_{t-1}> is a sum over pairs of tokens, one
-// that reads at or after t and one that writes before t.  Pairs inside t's chunk:
-// their products M_ri, summed over rows and columns; pairs with one token
-// outside: q_r . dq_r and k_i . dk_i without their chunk's part; pairs with both
-// outside: e^{G_C} <D, S> of the states on the chunk's two sides.  The pass of dk
-// leaves D behind each chunk for that of dq, which runs after it: 32 KB to and fro
-// for a chunk and 32 columns at 128 (written as differences of sums over all
-// later tokens, as q . dq - k . dk would allow, an early token's gradient holds
-// the rounding of every later one's, also where a document lies between them).
+// that reads at or after t and one that writes before t.  Pairs around t's chunk:
+// e^{G_C} <D, S> of the states on its two sides, for which the pass of dk leaves
+// D behind each chunk and that of dq, which runs after it, reads it (32 KB to and
+// fro for a chunk and 32 columns at 128); pairs with one token outside: q_r . dq_r
+// for r >= t and k_i . dk_i for i < t without their chunk's part; pairs inside:
+// their products M_ri, in t's tile of 16 tokens summed as a rectangle, with one
+// token in another tile by rows (dq) and columns (dk), around the tile by whole
+// tiles.  Every sum holds terms of the result alone: as differences of sums over
+// q . dq and k . dk an early token's gradient would hold the rounding of every
+// later one's, also where a document lies between them.
 //
 // Products on the matrix units: bf16 rows as they lie, and what is computed (the
 // state, decayed values, products of rows times their decay) in two or three bf16
@@ -65,9 +67,7 @@ struct LinRole {
     void* out;              // [B, H, T, nv]
     int out_bf16, out_wide;
     // gradient of the decay
-    float* sum_w;           // [tiles, B H, T]: a row's pairs inside its chunk
-    float* sum_x;           // [tiles, B H, T]: its pairs with tokens outside
-    float* sum_f;           // [tiles, B H, chunks]: pairs around a chunk (dq)
+    float* sums;            // [tiles, B H, T]: this pass's part of it
     float* hold;            // [B H, chunks, tiles, NK * 32]: D behind each chunk, as
                             // the waves that keep it have it (dk writes, dq reads)
 };
@@ -385,16 +385,28 @@ __device__ __forceinline__ double lin_row_shr(double x) {
     const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), 0x110 + N, 0xf, 0xf, false);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+template <int N>
+__device__ __forceinline__ float lin_row_shr(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x110 + N, 0xf, 0xf, false));
+}
+// Inclusive sums over rows of 16 lanes.
+template <typename F>
+__device__ __forceinline__ F lin_row_scan(F x) {
+    x += lin_row_shr<1>(x);
+    x += lin_row_shr<2>(x);
+    x += lin_row_shr<4>(x);
+    return x + lin_row_shr<8>(x);
+}
+__device__ __forceinline__ float lin_lane(float x, int l) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
+}
 __device__ __forceinline__ double lin_lane(double x, int l) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);
     const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, l), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ double lin_scan(double x, int lane) {
-    x += lin_row_shr<1>(x);
-    x += lin_row_shr<2>(x);
-    x += lin_row_shr<4>(x);
-    x += lin_row_shr<8>(x);
+    x = lin_row_scan(x);
     const double a = lin_lane(x, 15), b = a + lin_lane(x, 31), c = b + lin_lane(x, 47);
     const int row = lane >> 4;
     return x + (row == 0 ? 0. : row == 1 ? a : row == 2 ? b : c);
@@ -424,8 +436,8 @@ struct LinPlan {
     static constexpr int kVec = 0;                                  // of two chunks: see LinDecays
     static constexpr int kVecBytes = (6 * C + 4) * 4;
     static constexpr int kLog = kVec + 2 * kVecBytes;               // log_alpha of four chunks
-    static constexpr int kSums = kLog + 4 * 64 * 4;                 // of two: pairs inside, outside by column tile, around
-    static constexpr int kSumBytes = kGrad ? (3 * C + 4) * 4 : 0;
+    static constexpr int kSums = kLog + 4 * 64 * 4;                 // of two: see LinSums
+    static constexpr int kSumBytes = kGrad ? (4 * C + 20) * 4 : 0;
     static constexpr int kState = (kSums + 2 * kSumBytes + 255) / 256 * 256;
     static constexpr int kStage = kState + (kOut ? 2 * kStateBytes : 0);
     static constexpr int kRoom = 160 * 1024 - kStage;
@@ -434,6 +446,16 @@ struct LinPlan {
     static_assert(kBytes <= 160 * 1024, "");
 };
 
+// Sum over lanes 16 g + n of the groups before g.
+__device__ __forceinline__ float lin_groups_before(float v, int g) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t even = r[0], odd = r[1];
+    const uint32_t both = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, even) + __builtin_bit_cast(float, odd));
+    const auto q = __builtin_amdgcn_permlane32_swap(both, both, false, false);
+    const uint32_t low = q[0];
+    return ((g & 1) ? __builtin_bit_cast(float, even) : 0.f) + (g >= 2 ? __builtin_bit_cast(float, low) : 0.f);
+}
 // Sum over lanes 16 g + n of all g, in each.
 __device__ __forceinline__ float lin_sum_groups(float v) {
     v = swap16_add(v, v);
@@ -446,6 +468,11 @@ __device__ __forceinline__ float lin_sum_groups(float v) {
 // difference of G, which is kept in two numbers.
 enum LinDecays { kLinOut, kLinIn, kLinGh, kLinGl, kLinFirst, kLinState, kLinWhole };
 constexpr float kLinSpan = 48.f;
+// The sums that a chunk leaves for the decay's gradient, C numbers each: pairs of
+// a row with other tiles of its chunk, with tokens outside (by tile of columns),
+// and of dq pairs around a token in its tile; then [reader's tile][token's tile]
+// pairs around a tile, and the state's four waves' parts of those around the chunk.
+enum LinSums { kLinOther, kLinOutside, kLinTileSum = 3, kLinAcross };
 
 template <bool BF, int NK, int C, int MODE>
 __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, int64_t unit, int tile, char* shared) {
@@ -573,17 +600,37 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             if constexpr (L::kGrad) {
                 if (wave != 1) return;
                 const lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
-                const int ch = number(it), t = t0 + ch * C + lane;
-                if (lane < C && t < tl) {
-                    float x = lds_get<float>(sums + (C + lane) * 4);
-                    if constexpr (RT == 2) x += lds_get<float>(sums + (2 * C + lane) * 4);
-                    R.sum_x[part * p.T + t] = x;
-                    R.sum_w[part * p.T + t] = lds_get<float>(sums + lane * 4);
+                // (of dq lane 0 has the last token: sums from it on; of dk the
+                // first, and sums up to the one before)
+                const int c = kRev ? lane : C - 1 - lane, t = t0 + number(it) * C + c;
+                float own = 0.f, x = 0.f;
+                if (lane < C) {
+                    x = lds_get<float>(sums + (kLinOutside * C + c) * 4);
+                    if constexpr (RT == 2) x += lds_get<float>(sums + (kLinOutside * C + C + c) * 4);
+                    own = lds_get<float>(sums + (kLinOther * C + c) * 4);
                 }
-                if (MODE == kLinDqSums && lane == 0) {
-                    const f32x4 f = lds_get<f32x4>(sums + 3 * C * 4);
-                    R.sum_f[part * ((p.T + C - 1) / C) + t0 / C + ch] = (f[0] + f[1]) + (f[2] + f[3]);
+                // (a tile is a row of lanes)
+                float r = lin_row_scan(x + own);
+                x = lin_row_scan(x);
+                if constexpr (kRev) r = lin_row_shr<1>(r);
+                float before = 0.f;
+#pragma unroll
+                for (int i = 0; i + 1 < RT; ++i) {
+                    const float whole = lin_lane(x, 16 * i + 15);
+                    if (lane >= 16 * i + 16) before += whole;
                 }
+                r += before;
+                if constexpr (!kRev) {
+                    if (lane < C) r += lds_get<float>(sums + (kLinTileSum * C + c) * 4);
+#pragma unroll
+                    for (int i = 2; i < RT; ++i)
+#pragma unroll
+                        for (int m = 1; m < i; ++m)
+                            if (c / 16 == m) r += lds_get<float>(sums + (kLinAcross * C + 4 * i + m) * 4);
+                    const f32x4 f = lds_get<f32x4>(sums + (kLinAcross * C + 16) * 4);
+                    r += (f[0] + f[1]) + (f[2] + f[3]);
+                }
+                if (lane < C && t < tl) R.sums[part * p.T + t] = r;
             }
         };
         if (fill) lin_wait<0>();
@@ -765,7 +812,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             if constexpr (L::kOut) publish((it + 1) & 1);
             if constexpr (MODE == kLinDqSums) {
                 const float f = lanes_sum<64>(around) * whole;
-                if (lane == 0) lds_put(lds + L::kSums + (it & 1) * L::kSumBytes + (3 * C + wave) * 4, f);
+                if (lane == 0) lds_put(lds + L::kSums + (it & 1) * L::kSumBytes + (kLinAcross * C + 16 + wave) * 4, f);
             }
             sides(it + 1);
         }
@@ -945,9 +992,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         if constexpr (L::kGrad) {
             const LinRows<BF, L::kRowC, 1> rx(at_x, stage);
             const LinFrag<BF> mine = rx.get(L::kX, rt * 16, 0);
-            f32x4 other[C / 16], x[CT];
-#pragma unroll
-            for (int i = 0; i < C / 16; ++i) other[i] = lin_mma(rx.get(L::kC, 16 * i, 0), mine, zero4());
+            f32x4 x[CT];
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 const int col = (ct0 + c) * 16 + 4 * g;
@@ -955,22 +1000,51 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 if constexpr (BF) x[c] = __builtin_convertvector(lds_get<bf16x4>(at), f32x4);
                 else x[c] = lds_get<f32x4>(at);
             }
-            float outside = 0.f, inside = 0.f;
+            // (pairs in the row's own tile in the pass of dq, with other tiles in
+            // both; what is no pair is left out, not multiplied by 0)
+            float outside = 0.f, others = 0.f, across[RT] = {};
+            f32x4 tile_sum = zero4();
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                if constexpr (MODE == kLinDqSums) {
+                    // (tiles before this one, of the row's tile)
+                    if (i > 0) across[i] = others;
+                }
+                if (kRev ? i <= rt : i > rt) continue;
+                const f32x4 m = lin_mma(rx.get(L::kC, 16 * i, 0), mine, zero4()) * pr[i];
+                if (kRev || i < rt) {
+                    others += (m[0] + m[1]) + (m[2] + m[3]);
+                } else {
+                    float e[4], sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        e[j] = sum;
+                        sum += 4 * g + j < n ? m[j] : 0.f;
+                    }
+                    const float before_g = lin_groups_before(sum, g);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) tile_sum[j] = lanes_sum<16>(4 * g + j <= n ? (before_g + e[j]) * scale : 0.f);
+                }
+            }
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) outside = fmaf(acc[c][j], x[c][j], outside);
-#pragma unroll
-            for (int i = 0; i < C / 16; ++i) {
-                const int col = 16 * i + 4 * g;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) inside = fmaf(other[i][j], col + j == row ? 0.f : pr[i][j], inside);
-            }
             outside = lin_sum_groups(outside) * scale;
-            inside = lin_sum_groups(inside) * scale;
-            if (g == 0) {
-                lds_put(sums + ((1 + ct0) * C + row) * 4, outside);
-                if (ct0 == 0) lds_put(sums + row * 4, inside);
+            if (g == 0) lds_put(sums + ((kLinOutside + ct0) * C + row) * 4, outside);
+            if (ct0 == 0) {
+                others *= scale;
+                const float row_others = lin_sum_groups(others);
+                if (g == 0) lds_put(sums + (kLinOther * C + row) * 4, row_others);
+                if constexpr (MODE == kLinDqSums) {
+                    if (n == 0) lds_put(sums + (kLinTileSum * C + rt * 16 + 4 * g) * 4, tile_sum);
+#pragma unroll
+                    for (int i = 1; i < RT; ++i) {
+                        if (i >= rt) break;
+                        const float a = lanes_sum<64>(across[i] * scale);
+                        if (lane == 0) lds_put(sums + (kLinAcross * C + 4 * rt + i) * 4, a);
+                    }
+                }
             }
         }
         // What a row may not see it has times 0, which is not 0 of an infinite or
@@ -1095,56 +1169,30 @@ static __global__ __launch_bounds__(256) void gdn_lin_chain_kernel(LinChainParam
     }
 }
 
-// The decay's gradient from the passes' sums: a wave to a chunk.
+// The decay's gradient: the sums of the passes of dq and dk by tiles of columns.
 struct LinDecayParams {
-    const float* sum_w;     // [tiles, B H, T]: of the pass of dq
-    const float* sum_x;
-    const float* sum_v;     // of the pass of dk
-    const float* sum_y;
-    const float* sum_f;     // [tiles, B H, chunks]
+    const float* sums_q;    // [tiles, B H, T]
+    const float* sums_k;
     const float* log_alpha;
     int64_t lsb, lsh, lst;
     const int32_t* lens;
     float* out;             // [B, H, T]
-    int64_t bhs;
-    int H, T, C, tiles;
+    int64_t tokens;         // B H T
+    int H, T, tiles;
 };
 static __global__ __launch_bounds__(256) void gdn_lin_decay_kernel(LinDecayParams p) {
-    const int per = (p.T + p.C - 1) / p.C;
-    const int groups = (per + 3) / 4;
-    const int64_t bh = blockIdx.x / groups;
-    const int ch = (int)(blockIdx.x % groups) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (ch >= per) return;
-    const int b = (int)(bh / p.H), h = (int)(bh % p.H);
-    const int len = seq_len(p.lens, b, p.T), chunks = (len + p.C - 1) / p.C;
-    const int t = ch * p.C + lane;
-    double w = 0, x = 0, y = 0, F = 0;
-    if (ch < chunks) {
-        for (int i = 0; i < p.tiles; ++i) {
-            const int64_t row = i * p.bhs + bh;
-            if (lane < p.C && t < len) {
-                w += (double)p.sum_w[row * p.T + t] - p.sum_v[row * p.T + t];
-                x += p.sum_x[row * p.T + t];
-                y += p.sum_y[row * p.T + t];
-            }
-            F += p.sum_f[row * per + ch];
-        }
+    const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+    if (i >= p.tokens) return;
+    const int64_t bh = i / p.T;
+    const int t = (int)(i - bh * p.T), b = (int)(bh / p.H), h = (int)(bh % p.H);
+    float r = 0.f;
+    // (behind a decay of 0 nothing is left to have a gradient)
+    if (t < seq_len(p.lens, b, p.T) && !(p.log_alpha[b * p.lsb + h * p.lsh + t * p.lst] < -150.f / kLog2e)) {
+        double s = 0;
+        for (int k = 0; k < p.tiles; ++k) s += (double)p.sums_q[k * p.tokens + i] + p.sums_k[k * p.tokens + i];
+        r = (float)s;
     }
-    double before = y;      // sums of y up to a token, of w + x from it on
-    double behind = w + x;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const double u = __shfl_up(before, d), v = __shfl_down(behind, d);
-        if (lane >= d) before += u;
-        if (lane + d < 64) behind += v;
-    }
-    if (lane < p.C && t < p.T) {
-        const float la = p.log_alpha[b * p.lsb + h * p.lsh + t * p.lst];
-        float r = (float)(behind + (before - y) + F);
-        // (behind a decay of 0 nothing is left to have a gradient)
-        if (t >= len || la < -150.f / kLog2e) r = 0.f;
-        p.out[bh * p.T + t] = r;
-    }
+    p.out[i] = r;
 }
 
 // Sums over sequences and tokens of one head's [B, H, T] numbers, in a fixed

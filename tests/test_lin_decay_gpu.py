@@ -39,8 +39,9 @@ def row(dtype, T, dk, dv, seed, strong=0.02, H=2):
     return a, ref.rand(ref.gen(seed + 1), 1, H, T, dv, dtype=dtype)
 
 
-@pytest.mark.parametrize("small", [0.0])
-@pytest.mark.parametrize("dtype,T,dk,dv,start", [(BF, 2100, 64, 64, 1280), (F32, 1000, 40, 64, 512), (BF, 600, 256, 128, 320)])
+@pytest.mark.parametrize("small", [0.0, 2.0 ** -17])
+@pytest.mark.parametrize("dtype,T,dk,dv,start", [(BF, 2100, 64, 64, 1280), (F32, 1000, 40, 64, 512), (BF, 600, 256, 128, 320),
+                                                 (BF, 700, 128, 64, 300), (F32, 500, 96, 32, 333)])
 def test_documents_of_a_row(dtype, T, dk, dv, start, small):
     """Two documents packed into a row, the first with a gradient of 0 or a small
     one (its own tokens' alone)."""
@@ -53,7 +54,7 @@ def test_documents_of_a_row(dtype, T, dk, dv, start, small):
 
 
 @pytest.mark.parametrize("dtype,dk,dv", [(BF, 128, 128), (BF, 64, 40), (F32, 64, 64), (F32, 256, 32)])
-@pytest.mark.parametrize("strong", [0.05])
+@pytest.mark.parametrize("strong", [0.05, 1.0])
 def test_loss_on_the_last_tokens(dtype, dk, dv, strong):
     """A prompt whose own tokens have no loss: what reaches them decays."""
     say(f"case: lin decays of a prompt {dtype} {dk}x{dv} {strong}")
@@ -65,8 +66,35 @@ def test_loss_on_the_last_tokens(dtype, dk, dv, strong):
 
 @pytest.mark.parametrize("dtype,T,dk,dv,decay,state,lens", [
     (BF, 700, 128, 128, "token", True, None), (BF, 1100, 40, 64, "resets", True, [1100, 517]), (F32, 500, 72, 40, "token", True, [77, 500]),
-    (F32, 200, 256, 256, "resets", True, None), (BF, 130, 33, 1, "token", True, [130, 64])])
+    (BF, 300, 200, 256, "token", False, None), (F32, 200, 256, 256, "resets", True, None), (BF, 130, 33, 1, "token", True, [130, 64])])
 def test_by_its_own_measure(dtype, T, dk, dv, decay, state, lens):
     say(f"case: lin decays {dtype} T{T} {dk}x{dv} {decay}")
     a = inputs(2, 2, 1, 2, T, dk, dv, dtype, T, decay, state, lens)
     check(a, ref.rand(ref.gen(1), 2, 2, T, dv, dtype=dtype), ref.rand(ref.gen(2), 2, 2, dv, dk) if state else None)
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [(BF, 64, 128), (F32, 40, 32)])
+@pytest.mark.parametrize("name,at", [(n, t) for n in ("q", "k", "v", "dO") for t in (0, 30, 75, 127)])
+def test_infinities(dtype, dk, dv, name, at):
+    """An infinite row written at a token reaches the decays behind it, one read
+    there those up to it: the others keep their values, in the token's tile and
+    chunk too."""
+    T = 200
+    a, dO = row(dtype, T, dk, dv, at)
+    want, bound = reference(a, dO, None)
+    d = {**ref.dev(a), "dO": dO.cuda()}
+    d[name] = d[name].clone()
+    d[name][0, 1, at, 5] = math.inf
+    got = gdn.gdn_lin_bwd(**d, scale=SCALE)["dlog_alpha"]
+    keep = slice(0, at + 1) if name in ("k", "v") else slice(at + 1, T)
+    once("head without", got[:, 0], want[:, 0], bound[:, 0])
+    once("tokens without", got[:, 1, keep], want[:, 1, keep], bound[:, 1, keep])
+    rest = got[:, 1, at + 1:] if name in ("k", "v") else got[:, 1, 1:at + 1]
+    assert not torch.isfinite(rest).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_decay_for_each_head(dtype):
+    """Its gradient sums over tokens and sequences: by the terms' sum too."""
+    a = inputs(3, 4, 2, 4, 700, 64, 32, dtype, 3, "head", True, [700, 0, 333])
+    check(a, ref.rand(ref.gen(1), 3, 4, 700, 32, dtype=dtype), ref.rand(ref.gen(2), 3, 4, 32, 64))
