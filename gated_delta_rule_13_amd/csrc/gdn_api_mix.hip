@@ -150,7 +150,7 @@ LinRole lin_role(const LinTensor& a, const LinTensor& b, const LinTensor& c, int
     r.tiles = lin_tiles(nv);
     r.out = out;
     r.out_bf16 = out_bf16;
-    r.out_wide = rows4(out, out_bf16 ? GDN_BF16 : GDN_F32, {nv});
+    r.out_wide = out_bf16 && rows16(out, GDN_BF16, {nv}) ? 8 : rows4(out, out_bf16 ? GDN_BF16 : GDN_F32, {nv}) ? 4 : 1;
     return r;
 }
 // What the segments add to the state (and to its gradient), and the states that

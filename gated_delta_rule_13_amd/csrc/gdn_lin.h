@@ -65,7 +65,7 @@ struct LinRole {
     const float* carry;     // states that segments start from [B H, nseg, d_v, d_k]
     float* last;            // state at the end, or null
     void* out;              // [B, H, T, nv]
-    int out_bf16, out_wide;
+    int out_bf16, out_wide; // out_wide: rows of pieces of 1, 4 or (bf16) 8 numbers
     // gradient of the decay
     float* sums;            // [tiles, B H, T]: this pass's part of it
     float* hold;            // [B H, chunks, tiles, NK * 32]: D behind each chunk, as
@@ -862,7 +862,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         // (rows behind the sequence's end inside its last chunk are 0)
         const bool live = done_at < tl;
         const int64_t first = (int64_t)done_at * R.nv;
-        if (BF && CT == 2 && R.out_wide && R.out_bf16 && cols == kLinTile && R.nv % 8 == 0) {
+        if (BF && CT == 2 && R.out_wide == 8 && cols == kLinTile) {
             // 16 bytes a lane: lanes of even g take their neighbour's columns of
             // the first tile, those of odd g theirs of the second
             const f32x4 a = live ? done.c[0] * done_scale : zero4(), b = live ? done.c[CT - 1] * done_scale : zero4();
@@ -876,7 +876,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             const int col = (ct0 + c) * 16 + 4 * g;
             const f32x4 o = live ? done.c[c] * done_scale : zero4();
             const int64_t at = first + col;
-            if (R.out_wide) {
+            if (R.out_wide >= 4) {
                 if (col < cols) {
                     if (R.out_bf16) *reinterpret_cast<bf16x4*>(out_base + at * 2) = __builtin_convertvector(o, bf16x4);
                     else *reinterpret_cast<f32x4*>(out_base + at * 4) = o;

@@ -23,6 +23,12 @@ def once(name, got, want, bound):
     off = (g - w).abs() - half * w.abs() - mix.LIN_TOL * bound.detach() * (1 + half)
     worst = float(off.max())
     assert worst <= 1e-30, f"{name}: off by {worst:.3e} more than allowed (largest number {float(w.abs().max()):.3e})"
+    if got.dtype is BF and g.numel() >= 4096:
+        # One rounding and no more, in the mean: that of numbers off by the terms'
+        # error is as large as that of the exact ones to a per cent (the mean square
+        # of n uniform errors varies by 0.9 / sqrt(n)).
+        rms = lambda x: float((x * x).mean()) ** 0.5  # noqa: E731
+        assert rms(g - w) <= 1.05 * rms(w.to(BF).double() - w) + mix.LIN_TOL * rms(bound.detach()), (name, rms(g - w))
 
 
 CASES = [  # B, H, Hq, Hk, T, dk, dv, decay, state, lens
@@ -77,3 +83,17 @@ def test_step_in_another_type(rows, out, B, H, Hq, Hk, dk, dv):
     mine = torch.full_like(O, float("nan"))
     S = d["S0"].clone()
     assert gdn.gdn_lin_step(*tok, S, scale=SCALE, O=mine) is mine and torch.equal(mine, O)
+
+
+@pytest.mark.parametrize("off", [0, 1, 2, 4, 8])
+@pytest.mark.parametrize("rows,out", [(BF, BF), (F32, BF), (BF, F32)])
+def test_outputs_off_their_places(rows, out, off):
+    """O anywhere that its type allows (8 bytes off a 16-byte place, 2 off a 4-byte
+    one): the same bits, and nothing around it written."""
+    a = ref.dev(inputs(1, 3, 3, 3, 150, 64, 64, rows, 21, "token", True))
+    want, _ = gdn.gdn_lin_fwd(**a, scale=SCALE, o_dtype=out)
+    n = want.numel()
+    buf = torch.full((n + 16,), 7.0, dtype=out, device="cuda")
+    got, _ = gdn.gdn_lin_fwd(**a, scale=SCALE, O=buf[off:off + n].view(want.shape))
+    assert torch.equal(got, want)
+    assert bool((buf[:off] == 7).all()) and bool((buf[off + n:] == 7).all())
