@@ -12,6 +12,7 @@
 #include "gdn_error.h"
 #include "gdn_launch.h"
 #include "gdn_lin.h"
+#include "gdn_lin_join.h"
 
 using namespace gdn;
 
