@@ -15,25 +15,22 @@ template <int L, int K, int V>
 void bwd(const BlockBwdParams& q, int64_t blocks, hipStream_t st) {
     hipLaunchKernelGGL((gdn_block_bwd_kernel<kXb, kOb, L, K, V>), dim3((unsigned)blocks), dim3(block_threads<L>()), 0, st, q);
 }
+// Q: fours of numbers to a lane
+template <int L, int Q>
+BlockLaunchers fours(bool wide) {
+    return wide ? BlockLaunchers{fwd<L, Q, 4>, bwd<L, Q, 4>} : BlockLaunchers{fwd<L, 4 * Q, 1>, bwd<L, 4 * Q, 1>};
+}
+// (rows that fewer lanes hold are theirs)
 template <int L>
-BlockLaunchers pick(int numbers, bool wide) {
-    BlockLaunchers r{};
-    if (wide) {
-        switch ((numbers + 3) / 4) {
-            case 1: r.fwd = fwd<L, 1, 4>; r.bwd = bwd<L, 1, 4>; break;
-            case 2: r.fwd = fwd<L, 2, 4>; r.bwd = bwd<L, 2, 4>; break;
-            case 3: r.fwd = fwd<L, 3, 4>; r.bwd = bwd<L, 3, 4>; break;
-            default: r.fwd = fwd<L, 4, 4>; r.bwd = bwd<L, 4, 4>; break;
-        }
-    } else {
-        switch ((numbers + 3) / 4) {
-            case 1: r.fwd = fwd<L, 4, 1>; r.bwd = bwd<L, 4, 1>; break;
-            case 2: r.fwd = fwd<L, 8, 1>; r.bwd = bwd<L, 8, 1>; break;
-            case 3: r.fwd = fwd<L, 12, 1>; r.bwd = bwd<L, 12, 1>; break;
-            default: r.fwd = fwd<L, 16, 1>; r.bwd = bwd<L, 16, 1>; break;
-        }
+BlockLaunchers pick(int D, bool wide) {
+    const int q = ((D + L - 1) / L + 3) / 4;
+    if constexpr (L == 64) {
+        if (q <= 1) return fours<L, 1>(wide);
     }
-    return r;
+    if constexpr (L <= 256) {
+        if (q <= 2) return fours<L, 2>(wide);
+    }
+    return q <= 3 ? fours<L, 3>(wide) : fours<L, 4>(wide);
 }
 }  // namespace
 
@@ -42,12 +39,13 @@ BlockLaunchers pick(int numbers, bool wide) {
 BlockLaunchers GDN_BLOCK_NAME(GDN_BLOCK_XB, GDN_BLOCK_OB)(int D, bool wide) {
     // the fewest lanes that hold a row with at most sixteen numbers each (a
     // thousand lanes leave the gradient too few registers: 4096 rows of 8192, bf16
-    // on an fp32 stream, take 529 us, and with 512 lanes 257; forward 68 and 78)
+    // on an fp32 stream, gated, take 532 us, and with 512 lanes 255; forward 91 and
+    // 94)
     switch (block_lanes(D)) {
-        case 64: return pick<64>((D + 63) / 64, wide);
-        case 256: return pick<256>((D + 255) / 256, wide);
-        case 512: return pick<512>((D + 511) / 512, wide);
-        default: return pick<1024>((D + 1023) / 1024, wide);
+        case 64: return pick<64>(D, wide);
+        case 256: return pick<256>(D, wide);
+        case 512: return pick<512>(D, wide);
+        default: return pick<1024>(D, wide);
     }
 }
 
