@@ -423,8 +423,9 @@ struct LinPlan {
     // state and the products of rows two, whose errors of 2^-17 a bf16 output's
     // own rounding hides (with one, 17 us less at 4 x 4096 x 16 x 128, every term
     // would be off by a rounding like the output's: 2.3e-3 in the mean for
-    // 1.7e-3).
-    static constexpr int kParts = BF ? 2 : 1;
+    // 1.7e-3); the state three where the decay's gradient is taken from it, which
+    // is fp32 (1.6e-7 off in the mean, and 1.5e-6 with two).
+    static constexpr int kParts = !BF ? 1 : kGrad ? 3 : 2;
     static constexpr int kRowParts = 2;
     static constexpr int kValueParts = 3;
     static constexpr int kStateBytes = kParts * kLinTile * kRowA;
@@ -439,7 +440,14 @@ struct LinPlan {
     static constexpr int kSums = kLog + 4 * 64 * 4;                 // of two: see LinSums
     static constexpr int kSumBytes = kGrad ? (4 * C + 20) * 4 : 0;
     static constexpr int kState = (kSums + 2 * kSumBytes + 255) / 256 * 256;
-    static constexpr int kStage = kState + (kOut ? 2 * kStateBytes : 0);
+    // The state lies in LDS twice, or once where only so two chunks' rows fit
+    // beside it (bf16 rows of 256 numbers with the decay's gradient: 1038 us at
+    // 2 x 16 x 4096 for 1690 with one chunk's); it is then written behind a barrier
+    // of its own, which where both fit costs more than a third chunk's rows win
+    // (4 x 16 x 4096 of 128: 446 us, and 421 with two states and two chunks).
+    static constexpr bool fits(int states) { return kState + states * kStateBytes + 2 * kStageBytes <= 160 * 1024; }
+    static constexpr int kStates = kOut && !fits(2) && fits(1) ? 1 : 2;
+    static constexpr int kStage = kState + (kOut ? kStates * kStateBytes : 0);
     static constexpr int kRoom = 160 * 1024 - kStage;
     static constexpr int kStages = kRoom >= 3 * kStageBytes ? 3 : kRoom >= 2 * kStageBytes ? 2 : 1;
     static constexpr int kBytes = kStage + kStages * kStageBytes;
@@ -662,6 +670,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 load(it + kAhead);
             }
             if constexpr (kAhead <= 1) decays(it + 1);
+            if constexpr (L::kStates == 1) lin_wait_lds();
             if (it > 0) emit(it - 1);
         }
         if constexpr (L::kGrad) {
@@ -702,7 +711,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                 }
         }
         auto publish = [&](int buf) __attribute__((always_inline)) {
-            lds_char* at = lds + L::kState + buf * L::kStateBytes;
+            lds_char* at = lds + L::kState + buf % L::kStates * L::kStateBytes;
             const int row = nvt * 16 + n;
             if constexpr (BF) {
                 f32x4 x[KT];
@@ -809,7 +818,8 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 #pragma unroll
                     for (int t = 0; t < KT; ++t) S[t] = lin_mma(keys[m][t], fc.part[k], S[t]);
             }
-            if constexpr (L::kOut) publish((it + 1) & 1);
+            if constexpr (L::kStates == 1) lin_wait_lds();
+            if constexpr (L::kOut) publish(it + 1);
             if constexpr (MODE == kLinDqSums) {
                 const float f = lanes_sum<64>(around) * whole;
                 if (lane == 0) lds_put(lds + L::kSums + (it & 1) * L::kSumBytes + (kLinAcross * C + 16 + wave) * 4, f);
@@ -846,6 +856,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     const int row = rt * 16 + n;
     // (steps whose reads go out together)
     constexpr int KB = KS < 4 ? KS : BF || NK <= 128 ? 4 : 2;
+    constexpr int KBS = L::kParts == 3 && KB > 2 ? 2 : KB;
     const LinRows<BF, L::kRowA, KS> at_a(n, g);
     const LinRows<BF, L::kRowC, 1> at_x(n, g);
     const LinCols<BF, L::kRowC, CT> at_c(ct0 * 16, n, g);
@@ -899,7 +910,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
         const lds_char* vec = lds + L::kVec + (it & 1) * L::kVecBytes;
         lds_char* sums = lds + L::kSums + (it & 1) * L::kSumBytes;
         const uint32_t stage = stage_of(it);
-        const LinRows<BF, L::kRowA, KS> ra(at_a, stage), rs(at_a, lds0 + L::kState + (it & 1) * L::kStateBytes);
+        const LinRows<BF, L::kRowA, KS> ra(at_a, stage), rs(at_a, lds0 + L::kState + it % L::kStates * L::kStateBytes);
         const LinCols<BF, L::kRowC, CT> rc(at_c, stage);
         // Reads go out together, as many as registers hold (KB steps), before
         // the products that wait for them.
@@ -909,10 +920,10 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[c] = zero4();
 #pragma unroll
-        for (int k0 = 0; k0 < KS; k0 += KB) {
-            LinFrag<BF> fs[L::kParts][CT][KB];
+        for (int k0 = 0; k0 < KS; k0 += KBS) {
+            LinFrag<BF> fs[L::kParts][CT][KBS];
 #pragma unroll
-            for (int ks = 0; ks < KB; ++ks) {
+            for (int ks = 0; ks < KBS; ++ks) {
                 if (k0 + ks >= KS) break;
                 fa[k0 + ks] = ra.get(L::kA, rt * 16, k0 + ks);
 #pragma unroll
@@ -923,7 +934,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
             __builtin_amdgcn_sched_barrier(0);
             if (k0 == 0 && it > 0) store();
 #pragma unroll
-            for (int ks = 0; ks < KB; ++ks) {
+            for (int ks = 0; ks < KBS; ++ks) {
                 if (k0 + ks >= KS) break;
 #pragma unroll
                 for (int k = 0; k < L::kParts; ++k)
@@ -931,6 +942,7 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
                     for (int c = 0; c < CT; ++c) acc[c] = lin_mma(fs[k][c][ks], fa[k0 + ks], acc[c]);
             }
         }
+        if constexpr (L::kStates == 1) lin_wait_lds();
         // products of the rows with the pairs of tiles that hold any row on their
         // side of the diagonal, and what their decays need
         f32x4 pr[C / 16];

@@ -98,3 +98,21 @@ def test_one_decay_for_each_head(dtype):
     """Its gradient sums over tokens and sequences: by the terms' sum too."""
     a = inputs(3, 4, 2, 4, 700, 64, 32, dtype, 3, "head", True, [700, 0, 333])
     check(a, ref.rand(ref.gen(1), 3, 4, 700, 32, dtype=dtype), ref.rand(ref.gen(2), 3, 4, 32, 64))
+
+
+@pytest.mark.parametrize("dtype,T,dk,dv", [(BF, 37, 64, 128), (BF, 200, 128, 128), (BF, 100, 256, 64), (F32, 150, 64, 64)])
+def test_as_exact_as_fp32_arithmetic(dtype, T, dk, dv):
+    """In the mean no further from the exact gradient than twice what the
+    recurrence in fp32, a token at a time, with its gradient by autograd is."""
+    say(f"case: lin decays in fp32 {dtype} T{T} {dk}x{dv}")
+    a, dO = row(dtype, T, dk, dv, T, 0.05)
+    want, _ = reference(a, dO, None)
+    a32 = {n: x.float() if torch.is_tensor(x) and x.is_floating_point() else x for n, x in a.items()}
+    la = a32["log_alpha"].clone().requires_grad_(True)
+    O, _ = mix.lin(**{**a32, "log_alpha": la}, scale=SCALE)
+    plain, = torch.autograd.grad((O * dO.float()).sum(), [la])
+    assert plain.dtype is F32
+    got = gdn.gdn_lin_bwd(dO.cuda(), **ref.dev(a), scale=SCALE)["dlog_alpha"].cpu()
+    off, plain_off = (float((x.double() - want).norm() / want.norm()) for x in (got, plain))
+    say(f"off {off:.2e}, fp32 {plain_off:.2e}")
+    assert off <= 2 * plain_off
