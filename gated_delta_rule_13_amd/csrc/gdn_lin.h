@@ -856,7 +856,8 @@ __device__ __forceinline__ void lin_pass(const LinParams& p, const LinRole& R, i
     const int row = rt * 16 + n;
     // (steps whose reads go out together)
     constexpr int KB = KS < 4 ? KS : BF || NK <= 128 ? 4 : 2;
-    constexpr int KBS = L::kParts == 3 && KB > 2 ? 2 : KB;
+    // (of a state in parts one step, which is as many: prompts 107 us for 111)
+    constexpr int KBS = L::kParts > 1 ? 1 : KB;
     const LinRows<BF, L::kRowA, KS> at_a(n, g);
     const LinRows<BF, L::kRowC, 1> at_x(n, g);
     const LinCols<BF, L::kRowC, CT> at_c(ct0 * 16, n, g);
