@@ -2,12 +2,14 @@
 number within half a step and 2^-16 of the sum of its own terms' absolute values
 (`mix_ref`: the same gradient on absolute inputs), however large the gradients of
 other tokens of the row are."""
+import ctypes
 import math
 
 import pytest
 import torch
 
 import gated_delta_rule_13_amd as gdn
+from gated_delta_rule_13_amd import _lib, _mix
 from tests import layer_ref as ref
 from tests import mix_ref as mix
 from tests.gpu_helpers import say
@@ -116,3 +118,24 @@ def test_as_exact_as_fp32_arithmetic(dtype, T, dk, dv):
     off, plain_off = (float((x.double() - want).norm() / want.norm()) for x in (got, plain))
     say(f"off {off:.2e}, fp32 {plain_off:.2e}")
     assert off <= 2 * plain_off
+
+
+@pytest.mark.parametrize("dtype,T,lens", [(BF, 150, [150, 70, 0]), (BF, 900, [900, 0, 513]), (F32, 700, [1, 700, 320]), (BF, 64, [0, 0, 0])])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 40), (40, 256)])
+def test_nothing_of_a_workspace_is_read_before_it_is_written(dtype, T, lens, dk, dv):
+    """A workspace full of NaN, with and without segments and empty sequences: the
+    same bits as any other."""
+    say(f"case: lin bwd on a workspace of NaN {dtype} T{T} {lens} {dk}x{dv}")
+    a = ref.dev(inputs(3, 2, 1, 2, T, dk, dv, dtype, T, "token", True, lens))
+    dO, dS = ref.rand(ref.gen(1), 3, 2, T, dv, dtype=dtype).cuda(), ref.rand(ref.gen(2), 3, 2, dv, dk).cuda()
+    want = gdn.gdn_lin_bwd(dO, **a, dS_final=dS, scale=SCALE)
+    assert all(torch.isfinite(x).all() for x in want.values())
+    got = {n: torch.full_like(x, math.nan) for n, x in want.items()}
+    s = _mix._lin_shape(a["q"], a["k"], a["v"], a["log_alpha"], SCALE, dtype)
+    nbytes = gdn.gdn_lin_bwd_workspace_bytes(s)
+    ws = torch.full((nbytes,), 0xff, dtype=torch.uint8, device="cuda")
+    _lib.check(_lib.load().gdn_lin_bwd(
+        ctypes.byref(s), dO.data_ptr(), a["q"].data_ptr(), a["k"].data_ptr(), a["v"].data_ptr(), a["log_alpha"].data_ptr(),
+        a["S0"].data_ptr(), dS.data_ptr(), a["lens"].data_ptr(), *(got[n].data_ptr() for n in ("dq", "dk", "dv", "dlog_alpha", "dS0")),
+        ws.data_ptr(), nbytes, torch.cuda.current_stream().cuda_stream))
+    assert all(torch.equal(got[n], want[n]) for n in want)
