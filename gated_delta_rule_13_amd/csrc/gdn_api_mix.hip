@@ -55,8 +55,9 @@ int64_t lin_blocks(int64_t units, int tiles) { return ceil_div(units, kXcds) * k
 // cut, into 256 each at least, so that they have about two workgroups each, or in
 // the gradient those of its smallest launch (the tiles of dq) one each.  They
 // cost a pass over the rows for their sums, and win by the units that work:
-// 1 x 8 x 32768 of 128/128 take 140 us, the same tokens as 64 heads 86 without.
-// (Aiming at 256 or 1024 workgroups measures alike.)
+// 1 x 8 x 32768 of 128/128 take 156 us, the same tokens as 64 heads 101 without;
+// their gradient with decays 529 us, and 623 where its launches aim at two
+// workgroups each together.  (Forward, 256 or 1024 workgroups measure alike.)
 struct LinPlanSizes {
     int nseg, seg_len;
     int64_t units;

@@ -35,12 +35,13 @@
 // the tiles of a head read the same rows a and b, from one XCD's L2, and the more
 // columns a tile had, the fewer workgroups there were for 256 compute units.
 // What bounds the passes is the chain of a chunk (reads from LDS, products,
-// rounding, barrier: about 2600 clocks), with the matrix units busy a quarter of
-// the time: 4 x 16 x 4096 of 128/128 in bf16 take 86 us (274 MB, 57 us at a
-// copy's rate), 1 x 8 x 32768 140 (of them 57 for the segments' sums and 8 for
-// their chain), 32 x 16 x 256 of 64/64 27 (84 MB, 18), the gradient of
-// 4 x 16 x 4096 324 (472 MB, 98); 3 x 6 x 1021 of 72/40 in fp32 39, in three
-// launches that each wait for few rows.
+// rounding, barrier: about 3000 clocks), with the matrix units busy 28 % of
+// the time: 4 x 16 x 4096 of 128/128 in bf16 take 101 us (274 MB, 56 us at a
+// copy's rate; 117 in calls without a pause), 1 x 8 x 32768 156 (of them 57 for
+// the segments' sums and 8 for their chain), 32 x 16 x 256 of 64/64 33 (84 MB, 17),
+// the gradient of 4 x 16 x 4096 406 (472 MB, 96; 240 for dk and dv, 160 for dq,
+// of which moving D behind the chunks to and fro is some 60);
+// 3 x 6 x 1021 of 72/40 in fp32 39, in three launches that each wait for few rows.
 #pragma once
 #include <type_traits>
 
