@@ -139,3 +139,35 @@ def test_nothing_of_a_workspace_is_read_before_it_is_written(dtype, T, lens, dk,
         a["S0"].data_ptr(), dS.data_ptr(), a["lens"].data_ptr(), *(got[n].data_ptr() for n in ("dq", "dk", "dv", "dlog_alpha", "dS0")),
         ws.data_ptr(), nbytes, torch.cuda.current_stream().cuda_stream))
     assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [(BF, 64, 128), (F32, 40, 64)])
+@pytest.mark.parametrize("kind", ["growing", "both ways", "of all sizes"])
+def test_decays_of_all_kinds(dtype, dk, dv, kind):
+    """States that grow (by e^6 a chunk), that grow and decay, and decays from none
+    to all of it beside each other: outputs and every gradient by their own
+    terms."""
+    say(f"case: lin decays {kind} {dtype} {dk}x{dv}")
+    T = 330
+    a = inputs(1, 2, 2, 2, T, dk, dv, dtype, 5, "token", True)
+    g = ref.gen(6)
+    if kind == "growing":
+        a["log_alpha"] = 0.1 * torch.rand(1, 2, T, generator=g)
+    elif kind == "both ways":
+        a["log_alpha"] = 0.5 * torch.randn(1, 2, T, generator=g)
+    else:
+        pool = torch.tensor([0.0, -1e-4, -0.1, -3.0, -20.0, -60.0, -95.0, -math.inf])
+        a["log_alpha"] = pool[torch.randint(0, 8, (1, 2, T), generator=g) * (torch.rand(1, 2, T, generator=g) < 0.3)]
+    dO, dS = ref.rand(g, 1, 2, T, dv, dtype=dtype), ref.rand(g, 1, 2, dv, dk)
+    w = ref.wide(a)
+    (wo, ws), (bo, bs) = mix.lin(**w, scale=SCALE), mix.lin_bound(w, scale=SCALE)
+    O, S = gdn.gdn_lin_fwd(**ref.dev(a), scale=SCALE)
+    once("O", O, wo, bo)
+    once("S", S, ws, bs)
+    names = ["q", "k", "v", "log_alpha", "S0"]
+    size = {n: x if n in ("log_alpha", "lens") or x is None else x.abs() for n, x in w.items()}
+    fn = lambda **k: mix.lin(**k, scale=SCALE)  # noqa: E731
+    want, bound = ref.gradients(fn, w, names, (dO, dS)), ref.gradients(fn, size, names, (dO.double().abs(), dS.double().abs()))
+    got = gdn.gdn_lin_bwd(dO.cuda(), **ref.dev(a), dS_final=dS.cuda(), scale=SCALE)
+    for n in names:
+        once("d" + n, got["d" + n], want[n], bound[n])
